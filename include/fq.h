@@ -207,6 +207,82 @@ fq_status fq_decode_step_all_logits(const fq_model* m, fq_kv* kv, const int32_t*
 fq_status fq_decode_greedy(const fq_model* m, fq_kv* const* caches, uint32_t n, const int32_t* first_tokens,
                            uint32_t n_steps, int32_t* tokens_out, float* logits, void* stream);
 
+/* ---- prompt and shared-prompt attention over caller-held rows ----
+ *
+ * The attention of a prompt (and of many answers to one prompt) as operators on device
+ * buffers, next to the decode steps above, which fuse theirs.  head_dim is 128, K and V are
+ * bf16, query groups (num_attention_heads / num_key_value_heads) are 1, 2, 4 or 8, and a call
+ * takes up to 64 sequences.  Host arrays are read during the call only.  Nothing is allocated
+ * and nothing outlives a call but its outputs, so calls may be captured into CUDA graphs; a
+ * workspace belongs to one call at a time (calls, or replayed graphs, that overlap on
+ * different streams need workspaces of their own).  Outputs must not overlap inputs. */
+
+/* K and V rows on the device: element d of row r of kv head h is at k[r * row_stride +
+ * h * head_stride + d] (v alike), bf16.  k and v are 16-byte aligned, strides count elements and
+ * are multiples of 8 (row_stride at least 128).  `rows` rows per head belong to the view. */
+typedef struct fq_kv_view {
+    void *k, *v;
+    uint64_t rows, row_stride, head_stride;
+} fq_kv_view;
+
+/* The rows of one layer of a bf16 cache (rows = its capacity).  Valid until the cache is
+ * freed.  Errors: INVALID_ARGUMENT, UNSUPPORTED (f32 or q8_0 cache). */
+fq_status fq_kv_layer_view(const fq_kv* kv, uint32_t layer, fq_kv_view* out);
+
+/* The rows of raw projections made ready for attention, n_seq sequences packed one after the
+ * other: sequence s has len[s] rows (0 allowed) at positions pos0[s], pos0[s] + 1, ...  Each row
+ * of qkv (device f32, row stride qkv_stride elements, 0 = (Hq + 2 Hkv) * 128, a multiple of 4;
+ * 16-byte aligned) holds the heads q | k | v.  Every q and k head is RMS-normalised with its
+ * gain (q_norm, k_norm: device f32 [128]; eps) and rotated at its position (half-split pairing
+ * (i, i + 64); rope: device f32 [rope_rows][64][2], cos and sin); q goes to q_out (device bf16
+ * [rows][Hq][128], row stride q_stride elements, 0 = Hq * 128), k and v to rows kv_row0[s] + i of
+ * the sequence's view, all rounded to the nearest bf16.  views: n_views = 1 (all sequences) or
+ * n_seq entries.  Rows of the views and of q_out outside the call's stay as they were.
+ * Errors: INVALID_SEQUENCE_LENGTH (n_seq = 0, pos0 + len > rope_rows), KV_CACHE_OVERFLOW
+ * (kv_row0 + len > rows), INVALID_ARGUMENT (null, alignment, strides, n_seq > 64, two sequences
+ * writing the same rows), UNSUPPORTED (group). */
+fq_status fq_qk_norm_rope(const float* qkv, uint64_t qkv_stride, uint32_t n_seq, const uint32_t* len,
+                          const uint32_t* pos0, const fq_kv_view* views, uint32_t n_views, const uint32_t* kv_row0,
+                          uint32_t num_attention_heads, uint32_t num_key_value_heads, const float* q_norm,
+                          const float* k_norm, float eps, const float* rope, uint32_t rope_rows, void* q_out,
+                          uint64_t q_stride, void* stream);
+
+/* Causal grouped-query attention of n_seq packed sequences.  Sequence s has q_len[s] query rows,
+ * one sequence after the other in q (device bf16 [rows][Hq][128], row stride q_stride elements, a
+ * multiple of 8, 0 = Hq * 128), and the k_len[s] key rows kv_row0[s] .. of its view (n_views = 1 or
+ * n_seq views; kv_row0 NULL: with one view the sequences' keys follow one another, else 0).
+ * Query row i sees the keys j <= i + k_len - q_len: the last row sees all, so k_len = q_len is a
+ * whole prompt and k_len > q_len a chunk behind cached rows.
+ *   out[i] = sum_j softmax_j(scale * q[i].k[j]) v[j];  a row that sees no key gives zeros.
+ * Only the keys a row sees have an influence on it, whatever values the others hold (NaN and
+ * infinities included).  out: device [rows][Hq][128] bf16 or f32 (out_dtype), row stride
+ * out_stride elements (0 = Hq * 128).  Scores and sums are f32; the softmax weights are rounded to
+ * bf16 for the product with V (up to 2^-8 of each weight), for f32 outputs too.
+ * workspace: device, 16-byte aligned, at least the bytes fq_attn_prompt_workspace gives for the
+ * same lengths and heads (may be 0); its contents do not matter.
+ * Errors: INVALID_SEQUENCE_LENGTH (n_seq = 0), KV_CACHE_OVERFLOW (keys beyond the view),
+ * INVALID_ARGUMENT (null, alignment, strides, n_seq > 64, a non-finite scale, more than 2^30 rows,
+ * workspace too small), UNSUPPORTED (group, out_dtype). */
+fq_status fq_attn_prompt(const void* q, uint64_t q_stride, const fq_kv_view* views, uint32_t n_views, uint32_t n_seq,
+                         const uint32_t* q_len, const uint32_t* kv_row0, const uint32_t* k_len,
+                         uint32_t num_attention_heads, uint32_t num_key_value_heads, float scale, void* out,
+                         uint64_t out_stride, fq_dtype out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+fq_status fq_attn_prompt_workspace(uint32_t n_seq, const uint32_t* q_len, const uint32_t* k_len,
+                                   uint32_t num_attention_heads, uint32_t num_key_value_heads, size_t* bytes);
+
+/* One query token per sequence over a prefix that all n_seq sequences share (rows 0 ..
+ * prefix_len - 1 of `prefix`, read once for all of them; NULL with prefix_len = 0) and over the
+ * sequence's own tail (rows 0 .. tail_len[s] - 1 of tails[s], an array of n_seq views; tail_len[s]
+ * may be 0, and tails NULL when all are):
+ *   out[s] = sum over prefix and tail of softmax(scale * q[s].k) v;  no key at all gives zeros.
+ * q, out, scale, rounding, workspace (fq_attn_shared_workspace) and errors as in fq_attn_prompt. */
+fq_status fq_attn_shared(const void* q, uint64_t q_stride, uint32_t n_seq, const fq_kv_view* prefix,
+                         uint32_t prefix_len, const fq_kv_view* tails, const uint32_t* tail_len,
+                         uint32_t num_attention_heads, uint32_t num_key_value_heads, float scale, void* out,
+                         uint64_t out_stride, fq_dtype out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+fq_status fq_attn_shared_workspace(uint32_t n_seq, uint32_t prefix_len, const uint32_t* tail_len,
+                                   uint32_t num_attention_heads, uint32_t num_key_value_heads, size_t* bytes);
+
 /* ---- inspection (tests and tools; not the hot path) ---- */
 
 /* Same as fq_decode_step_batch, also writing the residual stream after every layer to

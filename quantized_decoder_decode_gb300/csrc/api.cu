@@ -17,6 +17,7 @@
 #include <string>
 #include <vector>
 
+#include "api_util.h"
 #include "fq.h"
 #include "kernels.h"
 
@@ -26,6 +27,10 @@ namespace {
 
 thread_local std::string g_err;
 constexpr uint32_t DESC_MAGIC = 0x51574633u;   // "QWF3"
+
+}  // namespace
+
+namespace fq {
 
 fq_status fail(fq_status s, const char* fmt, ...) {
     char buf[512];
@@ -37,21 +42,7 @@ fq_status fail(fq_status s, const char* fmt, ...) {
     return s;
 }
 
-#define CK(call)                                                                                       \
-    do {                                                                                               \
-        cudaError_t e_ = (call);                                                                       \
-        if (e_ != cudaSuccess)                                                                         \
-            return fail(e_ == cudaErrorMemoryAllocation ? FQ_ERR_OUT_OF_MEMORY : FQ_ERR_CUDA, "%s: %s", \
-                        #call, cudaGetErrorString(e_));                                                \
-    } while (0)
-
-#define TRY(call)                  \
-    do {                           \
-        fq_status s_ = (call);     \
-        if (s_ != FQ_OK) return s_; \
-    } while (0)
-
-}  // namespace
+}  // namespace fq
 
 // ---------------------------------------------------------------- model and cache objects
 
@@ -983,6 +974,19 @@ fq_status fq_kv_read(const fq_kv* kv, uint32_t layer, uint32_t pos, uint32_t n_p
     if ((uint64_t)pos + n_pos > kv->cap) return fail(FQ_ERR_INVALID_ARGUMENT, "range beyond capacity");
     if (n_pos == 0) return FQ_OK;
     return kv_copy(kv, layer, pos, n_pos, k, v, stream, false);
+}
+
+fq_status fq_kv_layer_view(const fq_kv* kv, uint32_t layer, fq_kv_view* out) {
+    if (!kv || !out) return fail(FQ_ERR_INVALID_ARGUMENT, "null argument");
+    if (layer >= kv->m->d.p.num_layers) return fail(FQ_ERR_INVALID_ARGUMENT, "layer %u out of range", layer);
+    if (kv->type != KV_BF16) return fail(FQ_ERR_UNSUPPORTED, "views are of bf16 caches");
+    const size_t plane = (size_t)kv->m->d.p.num_key_value_heads * kv->cap * HEAD_DIM;
+    out->k = (uint16_t*)kv->k + layer * plane;
+    out->v = (uint16_t*)kv->v + layer * plane;
+    out->rows = kv->cap;
+    out->row_stride = HEAD_DIM;
+    out->head_stride = (uint64_t)kv->cap * HEAD_DIM;
+    return FQ_OK;
 }
 
 fq_status fq_layer_step(const fq_model* m, uint32_t layer, fq_kv* kv, uint32_t pos, float* x, void* stream) {

@@ -250,6 +250,55 @@ void launch_moe_route(const float* logits, int E, int k, int n, int norm_topk, M
 void launch_moe_combine(float* x, const float* y, const MoeRoute* route, int n, int k, int H, cudaStream_t s,
                         bool pdl);
 
+// ---- prompt and shared-prompt attention (bf16 rows of head_dim 128)
+struct KvRows {                   // element d of row r of kv head h: [r * row_stride + h * head_stride + d]
+    uint16_t *k = nullptr, *v = nullptr;
+    int64_t row_stride = 0, head_stride = 0;
+};
+
+// QK-norm + rope of packed rows, q -> q_out, k and v -> cache rows (qk_rows.cu)
+struct QkRowsArgs {
+    const float* qkv;             // [rows][(Hq + 2 Hkv) * 128]
+    int64_t qkv_stride;
+    const float *q_norm, *k_norm; // [128]
+    const float2* rope;           // [positions][64] (cos, sin)
+    float eps;
+    int Hq, Hkv, n_seq, rows;
+    uint16_t* q_out;              // bf16 [rows][Hq * 128]
+    int64_t q_stride;
+    int32_t row0[MAX_SEQ], pos0[MAX_SEQ], kv_row0[MAX_SEQ];   // per sequence: first row, position, cache row
+    KvRows kv[MAX_SEQ];
+};
+void launch_qk_rows(const QkRowsArgs& a, cudaStream_t s);
+
+struct AttnIo {
+    const uint16_t* q;            // bf16 [rows][Hq][128]
+    int64_t q_stride;
+    void* out;                    // bf16 or f32 [rows][Hq][128]
+    int64_t out_stride;
+    int out_f32;
+    int Hq, Hkv;
+    float scale;
+};
+struct PromptSeq {
+    int32_t q_row0, q_len, k_row0, k_len;
+};
+struct PromptArgs {
+    AttnIo io;
+    int n_seq, q_rows;
+    PromptSeq seq[MAX_SEQ];
+    KvRows kv[MAX_SEQ];
+};
+void launch_prompt(const PromptArgs& a, cudaStream_t s);
+struct SharedArgs {
+    AttnIo io;
+    int n_seq, prefix_len;
+    KvRows prefix;
+    int32_t tail_len[MAX_SEQ];
+    KvRows tail[MAX_SEQ];
+};
+void launch_shared(const SharedArgs& a, cudaStream_t s);
+
 // Load-time helpers
 // Source row r lands in destination row (r / group) * group_stride + (r % group) * step + off
 // (fusing q/k/v, interleaving gate/up rows, stacking experts).

@@ -63,6 +63,12 @@ class fq_weight_src(ctypes.Structure):
                 ("layers", ctypes.POINTER(fq_layer_src))]
 
 
+class fq_kv_view(ctypes.Structure):
+    """K and V rows on the device: addresses, rows per head, row and head strides in elements."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("rows", ctypes.c_uint64),
+                ("row_stride", ctypes.c_uint64), ("head_stride", ctypes.c_uint64)]
+
+
 def lib():
     """The loaded ``libfq.so``; raises if it is missing (no fallback path exists)."""
     global _lib
@@ -97,6 +103,14 @@ def lib():
                 "fq_step_path": [vp, u32, ctypes.c_int, ctypes.POINTER(ctypes.c_int)],
                 "fq_step_kernels": [vp, vp, ctypes.POINTER(ctypes.c_uint32)],
                 "fq_layer_step_noalloc": [vp, u32, vp, u32, vp, vp],
+                "fq_kv_layer_view": [vp, u32, vp],
+                "fq_qk_norm_rope": [vp, u64, u32, vp, vp, vp, u32, vp, u32, u32, vp, vp, ctypes.c_float, vp, u32, vp, u64, vp],
+                "fq_attn_prompt": [vp, u64, vp, u32, u32, vp, vp, vp, u32, u32, ctypes.c_float, vp, u64, ctypes.c_int, vp,
+                                   ctypes.c_size_t, vp],
+                "fq_attn_prompt_workspace": [u32, vp, vp, u32, u32, vp],
+                "fq_attn_shared": [vp, u64, u32, vp, u32, vp, vp, u32, u32, ctypes.c_float, vp, u64, ctypes.c_int, vp,
+                                   ctypes.c_size_t, vp],
+                "fq_attn_shared_workspace": [u32, u32, vp, u32, u32, vp],
             }
             for name, args in sig.items():
                 fn = getattr(L, name)
@@ -122,7 +136,8 @@ EXPORTED = ("fq_desc_init", "fq_load_weights", "fq_model_free", "fq_kv_init", "f
             "fq_kv_capacity", "fq_kv_append", "fq_kv_commit", "fq_kv_rewind", "fq_kv_read", "fq_layer_step", "fq_decode_step",
             "fq_decode_step_batch", "fq_decode_step_all_logits", "fq_forward_step", "fq_decode_greedy", "fq_decode_step_trace", "fq_dequant_rows", "fq_quantize_q8_0", "fq_layer_step_trace",
             "fq_gemv", "fq_step_kernels", "fq_check_device", "fq_debug_wait_timeout", "fq_set_option", "fq_step_path", "fq_layer_step_noalloc", "fq_last_error",
-            "fq_status_str")
+            "fq_status_str", "fq_kv_layer_view", "fq_qk_norm_rope", "fq_attn_prompt", "fq_attn_prompt_workspace",
+            "fq_attn_shared", "fq_attn_shared_workspace")
 
 
 def _check(status: int, where: str) -> None:
@@ -332,3 +347,85 @@ def fq_debug_wait_timeout(model: int, stream: int = 0) -> None:
 def fq_layer_step_noalloc(model: int, layer: int, kv: int, pos: int, x_ptr: int, stream: int = 0) -> None:
     """fq_layer_step without any device allocation (scratch lives in a built-in array)."""
     _check(lib().fq_layer_step_noalloc(model, layer, kv, pos, x_ptr, stream), "fq_layer_step_noalloc")
+
+
+# ---------------------------------------------------------------- prompt and shared-prompt attention
+
+def u32_array(values):
+    """A host array of lengths or rows as the calls below take it; a program that calls again
+    with the same lengths keeps it."""
+    if isinstance(values, ctypes.Array) and values._type_ is ctypes.c_uint32:
+        return values
+    return (ctypes.c_uint32 * len(values))(*[int(v) for v in values])
+
+
+def kv_view_array(views):
+    """One view or a sequence of views as a host array of ``fq_kv_view``."""
+    if isinstance(views, fq_kv_view):
+        return (fq_kv_view * 1)(views)
+    if isinstance(views, ctypes.Array) and views._type_ is fq_kv_view:
+        return views
+    return (fq_kv_view * len(views))(*views)
+
+
+def _same_length(n: int, **arrays) -> None:
+    for name, a in arrays.items():
+        if a is not None and len(a) != n:
+            raise ValueError(f"{name} has {len(a)} entries for {n} sequences")
+
+
+def fq_kv_layer_view(kv: int, layer: int) -> fq_kv_view:
+    out = fq_kv_view()
+    _check(lib().fq_kv_layer_view(kv, layer, ctypes.byref(out)), "fq_kv_layer_view")
+    return out
+
+
+def fq_qk_norm_rope(qkv_ptr: int, lens, pos0, views, kv_row0, num_attention_heads: int, num_key_value_heads: int,
+                    q_norm_ptr: int, k_norm_ptr: int, eps: float, rope_ptr: int, rope_rows: int, q_out_ptr: int,
+                    stream: int = 0, qkv_stride: int = 0, q_stride: int = 0) -> None:
+    """RMSNorm and rotary embedding of packed raw projections: q to q_out (bf16), k and v to cache rows."""
+    n, p, r, w = u32_array(lens), u32_array(pos0), u32_array(kv_row0), kv_view_array(views)
+    _same_length(len(n), pos0=p, kv_row0=r)
+    _check(lib().fq_qk_norm_rope(qkv_ptr, qkv_stride, len(n), n, p, w, len(w), r, num_attention_heads,
+                                 num_key_value_heads, q_norm_ptr, k_norm_ptr, eps, rope_ptr, rope_rows, q_out_ptr,
+                                 q_stride, stream), "fq_qk_norm_rope")
+
+
+def fq_attn_prompt_workspace(q_len, k_len, num_attention_heads: int, num_key_value_heads: int) -> int:
+    a, b, out = u32_array(q_len), u32_array(k_len), ctypes.c_size_t(0)
+    _same_length(len(a), k_len=b)
+    _check(lib().fq_attn_prompt_workspace(len(a), a, b, num_attention_heads, num_key_value_heads, ctypes.byref(out)),
+           "fq_attn_prompt_workspace")
+    return int(out.value)
+
+
+def fq_attn_prompt(q_ptr: int, views, q_len, k_len, num_attention_heads: int, num_key_value_heads: int, scale: float,
+                   out_ptr: int, ws_ptr: int = 0, ws_bytes: int = 0, stream: int = 0, kv_row0=None, q_stride: int = 0,
+                   out_stride: int = 0, out_dtype: str = "bf16") -> None:
+    """Causal attention of packed sequences over K/V rows (one view, or one per sequence)."""
+    a, b, w = u32_array(q_len), u32_array(k_len), kv_view_array(views)
+    r = None if kv_row0 is None else u32_array(kv_row0)
+    _same_length(len(a), k_len=b, kv_row0=r)
+    _check(lib().fq_attn_prompt(q_ptr, q_stride, w, len(w), len(a), a, r, b, num_attention_heads, num_key_value_heads,
+                                scale, out_ptr, out_stride, DTYPES[out_dtype], ws_ptr, ws_bytes, stream),
+           "fq_attn_prompt")
+
+
+def fq_attn_shared_workspace(prefix_len: int, tail_len, num_attention_heads: int, num_key_value_heads: int) -> int:
+    a, out = u32_array(tail_len), ctypes.c_size_t(0)
+    _check(lib().fq_attn_shared_workspace(len(a), prefix_len, a, num_attention_heads, num_key_value_heads,
+                                          ctypes.byref(out)), "fq_attn_shared_workspace")
+    return int(out.value)
+
+
+def fq_attn_shared(q_ptr: int, prefix, prefix_len: int, tails, tail_len, num_attention_heads: int,
+                   num_key_value_heads: int, scale: float, out_ptr: int, ws_ptr: int = 0, ws_bytes: int = 0,
+                   stream: int = 0, q_stride: int = 0, out_stride: int = 0, out_dtype: str = "bf16") -> None:
+    """One query token per sequence over a shared prefix (a view or None) and per-sequence tails."""
+    a = u32_array(tail_len)
+    t = None if tails is None else kv_view_array(tails)
+    _same_length(len(a), tails=t)
+    p = None if prefix is None else ctypes.byref(prefix)
+    _check(lib().fq_attn_shared(q_ptr, q_stride, len(a), p, prefix_len, t, a, num_attention_heads, num_key_value_heads,
+                                scale, out_ptr, out_stride, DTYPES[out_dtype], ws_ptr, ws_bytes, stream),
+           "fq_attn_shared")
