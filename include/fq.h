@@ -283,6 +283,11 @@ fq_status fq_attn_shared(const void* q, uint64_t q_stride, uint32_t n_seq, const
 fq_status fq_attn_shared_workspace(uint32_t n_seq, uint32_t prefix_len, const uint32_t* tail_len,
                                    uint32_t num_attention_heads, uint32_t num_key_value_heads, size_t* bytes);
 
+/* Synchronise `stream` and report bounded device waits of the two attentions that gave up on the
+ * current device since the last check (DEVICE_TIMEOUT: the outputs of the calls since then are
+ * invalid); clears the record.  The counterpart of fq_check_device for calls without a model. */
+fq_status fq_attn_check(void* stream);
+
 /* ---- inspection (tests and tools; not the hot path) ---- */
 
 /* Same as fq_decode_step_batch, also writing the residual stream after every layer to

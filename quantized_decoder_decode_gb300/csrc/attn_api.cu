@@ -5,11 +5,15 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
+#include <mutex>
+#include <new>
+#include <vector>
 
 #include "api_util.h"
+#include "attn_plan.h"
 #include "fq.h"
-#include "kernels.h"
 
 using namespace fq;
 
@@ -68,6 +72,282 @@ KvRows rows_of(const fq_kv_view& v) {
     r.row_stride = (int64_t)v.row_stride;
     r.head_stride = (int64_t)v.head_stride;
     return r;
+}
+
+// ---------------------------------------------------------------- work lists
+
+// Keys a unit of attn_tiles.cu should have at least when keys are split, in tiles: a partial
+// result of a 128-row tile is 64 KB, as much as the K and V of one key tile.
+constexpr int SPLIT_TILES = 8;
+// Keys per chunk of attn_rows.cu at least, and chunks that fill the GPU once (three CTAs per SM)
+constexpr int64_t ROWS_CHUNK = 128;
+constexpr int64_t ROWS_CTAS = 3 * ATTN_SMS;
+
+struct Plan {
+    std::vector<TileEntry> tiles;     // longest first
+    std::vector<RowGroup> groups;
+    std::vector<int> group_view;      // sequence whose view a group reads (-1: the prefix)
+    std::vector<JoinEntry> join;
+    int64_t tile_slots = 0, row_slots = 0;
+    int row_items = 0;
+
+    size_t tile_bytes(uint32_t Hkv) const { return (size_t)tile_slots * Hkv * TILE_ROWS * HEAD_DIM * 4; }
+    size_t row_bytes(uint32_t Hkv) const { return (size_t)row_slots * Hkv * ROWS_MAX * HEAD_DIM * 4; }
+    size_t bytes(uint32_t Hkv) const {   // values, then (m, l) pairs: 2 of every 128 + 2 floats
+        return (tile_bytes(Hkv) + row_bytes(Hkv)) / HEAD_DIM * (HEAD_DIM + 2);
+    }
+    Partials at(void* ws, uint32_t Hkv) const {
+        Partials p;
+        char* b = (char*)ws;
+        p.a_o = (float*)b;
+        p.b_o = (float*)(b += tile_bytes(Hkv));
+        p.a_ml = (float2*)(b += row_bytes(Hkv));
+        p.b_ml = (float2*)(b + tile_bytes(Hkv) / HEAD_DIM * 2);
+        return p;
+    }
+    int add_slots(int64_t& n, int64_t k) {
+        n += k;
+        return (int)(n - k);
+    }
+};
+
+int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+// chunk the keys of the groups so that their CTAs fill the GPU about once
+void plan_groups(Plan& p, uint32_t Hkv, bool partial) {
+    int64_t keys = 0;
+    for (auto& g : p.groups) keys += g.k_len;
+    const int64_t per = std::max(ROWS_CHUNK, (keys * Hkv + ROWS_CTAS - 1) / ROWS_CTAS);
+    for (auto& g : p.groups) {
+        const int splits = std::max(1, ceil_div(g.k_len, per));
+        g.chunk = std::max(64, ceil_div(ceil_div(g.k_len, splits), 64) * 64);
+        const int n = std::max(1, ceil_div(g.k_len, g.chunk));
+        g.item0 = p.row_items;
+        p.row_items += n;
+        g.slot0 = partial || n > 1 ? p.add_slots(p.row_slots, n) : -1;
+    }
+}
+
+int splits_of(const Plan& p, size_t g) {
+    return (g + 1 < p.groups.size() ? p.groups[g + 1].item0 : p.row_items) - p.groups[g].item0;
+}
+
+struct Tiles {
+    int tok0, n_tok, nt;   // tokens and key tiles of a unit
+    int seq;
+    bool single;
+};
+
+void plan_prompt(Plan& p, uint32_t n_seq, const PromptSeq* seq, uint32_t G, uint32_t Hkv) {
+    const int tpt = TILE_ROWS / (int)G;
+    std::vector<Tiles> units;
+    int64_t total = 0;
+    for (uint32_t s = 0; s < n_seq; ++s) {
+        const PromptSeq& q = seq[s];
+        if (q.q_len == 0) continue;
+        if ((int64_t)q.q_len * G <= ROWS_MAX) {
+            p.groups.push_back(RowGroup{q.q_row0, q.q_len, q.k_row0, q.k_len, q.off, 0, 0, -1});
+            p.group_view.push_back((int)s);
+            continue;
+        }
+        const bool single = q.q_len <= tpt;
+        for (int t = 0; t < q.q_len; t += 2 * tpt) {
+            const int n_tok = std::min(2 * tpt, q.q_len - t);
+            const int nt = ceil_div(std::max(0, std::min(q.k_len, t + n_tok - 1 + q.off)), TILE_ROWS);
+            units.push_back(Tiles{t, n_tok, nt, (int)s, single});
+            total += nt;
+        }
+    }
+    plan_groups(p, Hkv, false);
+    for (size_t g = 0; g < p.groups.size(); ++g) {
+        const RowGroup& r = p.groups[g];
+        if (r.slot0 >= 0)
+            p.join.push_back(JoinEntry{r.q_row0, r.n_tok, r.k_len, r.off, 0, 0, 0, 0, r.slot0, splits_of(p, g), 0, 0, 0});
+    }
+    // units of more than a CTA's fair share are split along their keys
+    const int fair = std::max(SPLIT_TILES, ceil_div(total * Hkv, ATTN_SMS));
+    for (const Tiles& u : units) {
+        const int S = 2 * u.nt > 3 * fair ? ceil_div(u.nt, fair) : 1;
+        const uint32_t info = (uint32_t)u.seq | (u.single ? TILE_SINGLE : 0u);
+        if (S == 1) {
+            p.tiles.push_back(TileEntry{u.tok0, info, 0, u.nt});
+            continue;
+        }
+        const int blocks = u.single ? 1 : 2;
+        const int slot = p.add_slots(p.tile_slots, (int64_t)S * blocks);
+        for (int i = 0; i < S; ++i)
+            p.tiles.push_back(TileEntry{u.tok0, info | (uint32_t)(slot + i * blocks + 1) << 8, (int)((int64_t)u.nt * i / S),
+                                        (int)((int64_t)u.nt * (i + 1) / S)});
+        const PromptSeq& q = seq[u.seq];
+        for (int b = 0; b < blocks && b * tpt < u.n_tok; ++b)
+            p.join.push_back(JoinEntry{q.q_row0 + u.tok0 + b * tpt, std::min(tpt, u.n_tok - b * tpt), q.k_len,
+                                       q.off + u.tok0 + b * tpt, slot + b, S, blocks, 0, 0, 0, 0, 0, 0});
+    }
+    std::stable_sort(p.tiles.begin(), p.tiles.end(),
+                     [](const TileEntry& a, const TileEntry& b) { return a.j1 - a.j0 > b.j1 - b.j0; });
+}
+
+void plan_shared(Plan& p, uint32_t n_seq, uint32_t prefix_len, const uint32_t* tail_len, uint32_t G, uint32_t Hkv) {
+    const int tpt = TILE_ROWS / (int)G;
+    const int P = (int)prefix_len;
+    const bool tiled = P > 0 && n_seq * G > (uint32_t)ROWS_MAX;
+    if (P > 0 && !tiled) {   // few rows: the prefix is a row group of all sequences
+        p.groups.push_back(RowGroup{0, (int)n_seq, 0, P, SEES_ALL, 0, 0, -1});
+        p.group_view.push_back(-1);
+    }
+    std::vector<int> tail_group(n_seq, -1);
+    for (uint32_t s = 0; s < n_seq; ++s)
+        if (tail_len[s]) {
+            tail_group[s] = (int)p.groups.size();
+            p.groups.push_back(RowGroup{(int)s, 1, 0, (int)tail_len[s], SEES_ALL, 0, 0, -1});
+            p.group_view.push_back((int)s);
+        }
+    const bool tails = p.groups.size() > (P > 0 && !tiled ? 1u : 0u);
+    plan_groups(p, Hkv, tiled || (P > 0 && tails));
+    // the prefix as tiles: units (pairs of query tiles) x splits of the keys
+    int S = 1, blocks = 1, units = 0, slot = 0;
+    const bool single = (int)n_seq <= tpt;
+    if (tiled) {
+        units = ceil_div(n_seq, 2 * tpt);
+        blocks = single ? 1 : 2;
+        const int nt = ceil_div(P, TILE_ROWS);
+        S = std::max(1, std::min(nt / SPLIT_TILES, ATTN_SMS / (units * (int)Hkv)));
+        const bool partial = S > 1 || tails;
+        if (partial) slot = p.add_slots(p.tile_slots, (int64_t)S * blocks * units);
+        for (int u = 0; u < units; ++u)
+            for (int i = 0; i < S; ++i)
+                p.tiles.push_back(TileEntry{u * 2 * tpt,
+                                            (single ? TILE_SINGLE : 0u) |
+                                                (partial ? (uint32_t)(slot + (u * S + i) * blocks + 1) << 8 : 0u),
+                                            (int)((int64_t)nt * i / S), (int)((int64_t)nt * (i + 1) / S)});
+        if (!partial) return;
+    } else if (!(P > 0 && tails)) {
+        // finished by the row groups themselves, but for split groups and sequences without keys
+        for (uint32_t s = 0; s < n_seq; ++s) {
+            const int g = P > 0 ? 0 : tail_group[s];
+            if (g >= 0 && p.groups[g].slot0 < 0) continue;
+            JoinEntry e{(int)s, 1, g < 0 ? 0 : p.groups[g].k_len, SEES_ALL, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+            if (g >= 0) {
+                e.b0 = p.groups[g].slot0;
+                e.nB = splits_of(p, g);
+                e.b_row = P > 0 ? (int)(s * G) : 0;
+            }
+            p.join.push_back(e);
+        }
+        return;
+    }
+    for (uint32_t s = 0; s < n_seq; ++s) {
+        const int64_t keys = (int64_t)P + tail_len[s];
+        JoinEntry e{(int)s, 1, (int)std::min<int64_t>(keys, SEES_ALL), SEES_ALL, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+        if (tiled) {
+            const int b = (int)s / tpt;
+            e.a0 = slot + (b / blocks) * S * blocks + b % blocks;
+            e.nA = S;
+            e.a_step = blocks;
+            e.a_row = (int)(s % tpt) * (int)G;
+        } else {
+            e.b0 = p.groups[0].slot0;
+            e.nB = splits_of(p, 0);
+            e.b_row = (int)(s * G);
+        }
+        if (tail_group[s] >= 0) {
+            e.c0 = p.groups[tail_group[s]].slot0;
+            e.nC = splits_of(p, tail_group[s]);
+        }
+        p.join.push_back(e);
+    }
+}
+
+// ---------------------------------------------------------------- launches
+
+fq_status prepare_device() {
+    static std::mutex mu;
+    static bool done[64] = {};
+    int dev = 0;
+    CK(cudaGetDevice(&dev));
+    std::lock_guard<std::mutex> lk(mu);
+    if (dev < 64 && done[dev]) return FQ_OK;
+    CK(attn_tiles_prepare());
+    if (dev < 64) done[dev] = true;
+    return FQ_OK;
+}
+
+fq_status encode_rows(void* map_k, void* map_v, const KvRows& r, uint64_t rows, int Hkv) {
+    const uint64_t rs = (uint64_t)r.row_stride * 2, hs = Hkv > 1 ? (uint64_t)r.head_stride * 2 : rs;
+    const uint64_t dims[3] = {(uint64_t)HEAD_DIM, rows, (uint64_t)Hkv}, strides[3] = {2, rs, hs};
+    const uint32_t box[3] = {64, (uint32_t)TILE_ROWS, 1};
+    if (!encode_bf16_tiles(map_k, r.k, 3, dims, strides, box) || !encode_bf16_tiles(map_v, r.v, 3, dims, strides, box))
+        return fail(FQ_ERR_CUDA, "tensor map of K or V refused");
+    return FQ_OK;
+}
+
+// views[s]: the rows of sequence s (views[0] for all when one is given), used: rows it is read up to
+template <class Args>
+fq_status run_tiles(const Plan& p, const AttnIo& io, const Partials& part, const PromptSeq* seq, int n_seq, int q_rows,
+                    const KvRows* views, int n_views, const uint64_t* used, cudaStream_t s) {
+    TRY(prepare_device());
+    Args* a = new (std::nothrow) Args;
+    if (!a) return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
+    auto run = [&]() -> fq_status {
+        a->io = io;
+        a->c = std::max(std::fabs(io.scale) * 1.4426950408889634f, FLT_MIN);   // (a scale of 0: equal weights)
+        a->negate = io.scale < 0.f;
+        a->part = part;
+        std::copy(seq, seq + n_seq, a->seq);
+        const uint64_t G = io.Hq / io.Hkv;
+        const uint64_t qs = (uint64_t)io.q_stride * 2;
+        const uint64_t dims[4] = {(uint64_t)HEAD_DIM, G, (uint64_t)io.Hkv, (uint64_t)q_rows};
+        const uint64_t strides[4] = {2, HEAD_DIM * 2, G * HEAD_DIM * 2, qs};
+        const uint32_t box[4] = {64, (uint32_t)G, 1, (uint32_t)(TILE_ROWS / G)};
+        if (!encode_bf16_tiles(a->map_q, io.q, 4, dims, strides, box)) return fail(FQ_ERR_CUDA, "tensor map of q refused");
+        for (int v = 0; v < n_views; ++v)
+            if (used[v]) TRY(encode_rows(a->map_k[v], a->map_v[v], views[v], used[v], io.Hkv));
+        constexpr size_t NE = sizeof a->e / sizeof a->e[0];
+        for (size_t e0 = 0; e0 < p.tiles.size(); e0 += NE) {
+            a->n_entries = (int)std::min(NE, p.tiles.size() - e0);
+            std::copy(p.tiles.begin() + e0, p.tiles.begin() + e0 + a->n_entries, a->e);
+            launch_tiles(*a, s);
+            CK(cudaGetLastError());
+        }
+        return FQ_OK;
+    };
+    const fq_status st = run();
+    delete a;
+    return st;
+}
+
+fq_status run_groups(const Plan& p, const AttnIo& io, const Partials& part, const KvRows* views, const KvRows* prefix,
+                     cudaStream_t s) {
+    if (p.groups.empty()) return FQ_OK;
+    RowsArgs a;
+    a.io = io;
+    a.c = io.scale * 1.4426950408889634f;
+    a.part = part;
+    a.n_groups = (int)p.groups.size();
+    a.n_items = p.row_items;
+    for (size_t g = 0; g < p.groups.size(); ++g) {
+        a.g[g] = p.groups[g];
+        a.kv[g] = p.group_view[g] < 0 ? *prefix : views[p.group_view[g]];
+    }
+    launch_attn_rows(a, s);
+    CK(cudaGetLastError());
+    return FQ_OK;
+}
+
+fq_status run_join(const Plan& p, const AttnIo& io, const Partials& part, cudaStream_t s) {
+    if (p.join.empty()) return FQ_OK;
+    JoinArgs a;
+    a.io = io;
+    a.part = part;
+    a.n_entries = (int)p.join.size();
+    a.max_tok = 0;
+    for (size_t i = 0; i < p.join.size(); ++i) {
+        a.e[i] = p.join[i];
+        a.max_tok = std::max(a.max_tok, p.join[i].n_tok);
+    }
+    launch_attn_join(a, s);
+    CK(cudaGetLastError());
+    return FQ_OK;
 }
 
 // the checks that both attentions share, and the common part of their arguments
@@ -149,12 +429,47 @@ fq_status fq_qk_norm_rope(const float* qkv, uint64_t qkv_stride, uint32_t n_seq,
     return FQ_OK;
 }
 
+// Row ranges of the sequences of a prompt call; views may be null (lengths only).
+static fq_status prompt_sequences(uint32_t n_seq, const uint32_t* q_len, const uint32_t* kv_row0, const uint32_t* k_len,
+                                  const fq_kv_view* views, uint32_t n_views, uint32_t Hkv, PromptSeq* seq, KvRows* kv,
+                                  uint64_t* used, uint64_t* q_rows) {
+    uint64_t qr = 0, kr = 0;
+    for (uint32_t s = 0; s < n_seq; ++s) {
+        if (q_len[s] > MAX_ROWS || k_len[s] > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 rows");
+        uint64_t r0 = 0;
+        if (views) {
+            const uint32_t w = n_views == 1 ? 0 : s;
+            r0 = kv_row0 ? kv_row0[s] : n_views == 1 ? kr : 0;
+            TRY(check_view(views[w], Hkv, r0, k_len[s], "sequence", s));
+            kv[s] = rows_of(views[w]);
+            if (s == w) used[w] = 0;
+            if (k_len[s]) used[w] = std::max(used[w], r0 + k_len[s]);
+        }
+        seq[s] = PromptSeq{(int32_t)qr, (int32_t)q_len[s], (int32_t)r0, (int32_t)k_len[s],
+                           (int32_t)k_len[s] - (int32_t)q_len[s] + 1};
+        qr += q_len[s];
+        kr += k_len[s];
+        if (qr > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 query rows");
+    }
+    *q_rows = qr;
+    return FQ_OK;
+}
+
 fq_status fq_attn_prompt_workspace(uint32_t n_seq, const uint32_t* q_len, const uint32_t* k_len,
                                    uint32_t num_attention_heads, uint32_t num_key_value_heads, size_t* bytes) {
     TRY(check_heads(num_attention_heads, num_key_value_heads));
     TRY(check_count(n_seq));
     if (!q_len || !k_len || !bytes) return fail(FQ_ERR_INVALID_ARGUMENT, "null argument");
-    *bytes = 0;
+    PromptSeq seq[MAX_SEQ];
+    uint64_t q_rows;
+    TRY(prompt_sequences(n_seq, q_len, nullptr, k_len, nullptr, 0, num_key_value_heads, seq, nullptr, nullptr, &q_rows));
+    try {
+        Plan p;
+        plan_prompt(p, n_seq, seq, num_attention_heads / num_key_value_heads, num_key_value_heads);
+        *bytes = p.bytes(num_key_value_heads);
+    } catch (const std::bad_alloc&) {
+        return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
+    }
     return FQ_OK;
 }
 
@@ -167,26 +482,27 @@ fq_status fq_attn_prompt(const void* q, uint64_t q_stride, const fq_kv_view* vie
     TRY(check_count(n_seq));
     if (!q_len || !k_len || !views) return fail(FQ_ERR_INVALID_ARGUMENT, "null argument");
     if (n_views != 1 && n_views != n_seq) return fail(FQ_ERR_INVALID_ARGUMENT, "%u views for %u sequences", n_views, n_seq);
-    PromptArgs a;
-    a.n_seq = (int)n_seq;
-    uint64_t qr = 0, kr = 0;
-    for (uint32_t s = 0; s < n_seq; ++s) {
-        const fq_kv_view& v = views[n_views == 1 ? 0 : s];
-        const uint64_t r0 = kv_row0 ? kv_row0[s] : n_views == 1 ? kr : 0;
-        TRY(check_view(v, Hkv, r0, k_len[s], "sequence", s));
-        if (q_len[s] > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 query rows");
-        a.seq[s] = PromptSeq{(int32_t)qr, (int32_t)q_len[s], (int32_t)r0, (int32_t)k_len[s]};
-        a.kv[s] = rows_of(v);
-        qr += q_len[s];
-        kr += k_len[s];
-        if (qr > MAX_ROWS || kr > (uint64_t)MAX_SEQ * MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 query rows");
+    PromptSeq seq[MAX_SEQ];
+    KvRows kv[MAX_SEQ];
+    uint64_t used[MAX_SEQ], q_rows = 0;
+    TRY(prompt_sequences(n_seq, q_len, kv_row0, k_len, views, n_views, Hkv, seq, kv, used, &q_rows));
+    try {
+        Plan p;
+        plan_prompt(p, n_seq, seq, Hq / Hkv, Hkv);
+        AttnIo io;
+        TRY(attn_common(q, q_stride, Hq, Hkv, scale, out, out_stride, out_dtype, q_rows, workspace, workspace_bytes,
+                        p.bytes(Hkv), io));
+        if (q_rows == 0) return FQ_OK;
+        const Partials part = p.at(workspace, Hkv);
+        cudaStream_t s = (cudaStream_t)stream;
+        if (!p.tiles.empty())
+            TRY(n_views == 1 ? run_tiles<TileArgs1>(p, io, part, seq, (int)n_seq, (int)q_rows, kv, 1, used, s)
+                             : run_tiles<TileArgsN>(p, io, part, seq, (int)n_seq, (int)q_rows, kv, (int)n_views, used, s));
+        TRY(run_groups(p, io, part, kv, nullptr, s));
+        return run_join(p, io, part, s);
+    } catch (const std::bad_alloc&) {
+        return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
     }
-    TRY(attn_common(q, q_stride, Hq, Hkv, scale, out, out_stride, out_dtype, qr, workspace, workspace_bytes, 0, a.io));
-    if (qr == 0) return FQ_OK;
-    a.q_rows = (int)qr;
-    launch_prompt(a, (cudaStream_t)stream);
-    CK(cudaGetLastError());
-    return FQ_OK;
 }
 
 fq_status fq_attn_shared_workspace(uint32_t n_seq, uint32_t prefix_len, const uint32_t* tail_len,
@@ -194,7 +510,16 @@ fq_status fq_attn_shared_workspace(uint32_t n_seq, uint32_t prefix_len, const ui
     TRY(check_heads(num_attention_heads, num_key_value_heads));
     TRY(check_count(n_seq));
     if (!tail_len || !bytes) return fail(FQ_ERR_INVALID_ARGUMENT, "null argument");
-    *bytes = 0;
+    if (prefix_len > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 rows");
+    for (uint32_t s = 0; s < n_seq; ++s)
+        if (tail_len[s] > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 rows");
+    try {
+        Plan p;
+        plan_shared(p, n_seq, prefix_len, tail_len, num_attention_heads / num_key_value_heads, num_key_value_heads);
+        *bytes = p.bytes(num_key_value_heads);
+    } catch (const std::bad_alloc&) {
+        return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
+    }
     return FQ_OK;
 }
 
@@ -206,24 +531,42 @@ fq_status fq_attn_shared(const void* q, uint64_t q_stride, uint32_t n_seq, const
     TRY(check_heads(Hq, Hkv));
     TRY(check_count(n_seq));
     if (!tail_len) return fail(FQ_ERR_INVALID_ARGUMENT, "null argument");
-    SharedArgs a;
+    KvRows first, kv[MAX_SEQ];
     if (prefix_len) {
         if (!prefix) return fail(FQ_ERR_INVALID_ARGUMENT, "null prefix");
         TRY(check_view(*prefix, Hkv, 0, prefix_len, "prefix", 0));
-        a.prefix = rows_of(*prefix);
+        first = rows_of(*prefix);
     }
-    a.prefix_len = (int)prefix_len;
     for (uint32_t s = 0; s < n_seq; ++s) {
-        a.tail_len[s] = (int32_t)tail_len[s];
         if (!tail_len[s]) continue;
         if (!tails) return fail(FQ_ERR_INVALID_ARGUMENT, "null tails");
         TRY(check_view(tails[s], Hkv, 0, tail_len[s], "tail", s));
-        a.tail[s] = rows_of(tails[s]);
+        kv[s] = rows_of(tails[s]);
     }
-    TRY(attn_common(q, q_stride, Hq, Hkv, scale, out, out_stride, out_dtype, n_seq, workspace, workspace_bytes, 0, a.io));
-    a.n_seq = (int)n_seq;
-    launch_shared(a, (cudaStream_t)stream);
-    CK(cudaGetLastError());
+    try {
+        Plan p;
+        plan_shared(p, n_seq, prefix_len, tail_len, Hq / Hkv, Hkv);
+        AttnIo io;
+        TRY(attn_common(q, q_stride, Hq, Hkv, scale, out, out_stride, out_dtype, n_seq, workspace, workspace_bytes,
+                        p.bytes(Hkv), io));
+        const Partials part = p.at(workspace, Hkv);
+        cudaStream_t s = (cudaStream_t)stream;
+        if (!p.tiles.empty()) {
+            const PromptSeq all{0, (int32_t)n_seq, 0, (int32_t)prefix_len, SEES_ALL};
+            const uint64_t used = prefix_len;
+            TRY(run_tiles<TileArgs1>(p, io, part, &all, 1, (int)n_seq, &first, 1, &used, s));
+        }
+        TRY(run_groups(p, io, part, kv, &first, s));
+        return run_join(p, io, part, s);
+    } catch (const std::bad_alloc&) {
+        return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
+    }
+}
+
+fq_status fq_attn_check(void* stream) {
+    uint32_t n = 0;
+    CK(attn_wait_record(&n, (cudaStream_t)stream));
+    if (n) return fail(FQ_ERR_DEVICE_TIMEOUT, "a bounded device wait of an attention operator gave up (%u waits)", n);
     return FQ_OK;
 }
 

@@ -1,0 +1,99 @@
+// Work lists of the prompt and shared-prompt attention kernels, made on the host
+// (attn_api.cu) and passed by value to attn_tiles.cu, attn_rows.cu and its join kernel.
+//
+// "Packed rows": a kv head's query rows are (token, head of its group) with the head running
+// fastest, so G heads x tokens fill the 128 (or 16) rows of a matrix product.
+#pragma once
+
+#include "kernels.h"
+
+namespace fq {
+
+constexpr int ATTN_SMS = 152;         // SMs that the work lists are made for
+constexpr int TILE_ROWS = 128;        // packed rows of a query tile = keys of a key tile
+constexpr int ROWS_MAX = 16;          // packed rows that attn_rows.cu takes
+constexpr int32_t SEES_ALL = 1 << 30; // PromptSeq::off of rows that see every key
+
+// Row i (token) of a sequence sees keys [0, min(k_len, i + off)), off = k_len - q_len + 1.
+struct PromptSeq {
+    int32_t q_row0, q_len, k_row0, k_len, off;
+};
+
+// One unit of attn_tiles.cu per kv head: two query tiles (pair) over the same keys, or one tile
+// whose key tiles alternate between the two softmax warpgroups.
+struct TileEntry {
+    int32_t tok0;         // first token (of its sequence)
+    uint32_t info;        // sequence | single tile << 6 | (slot + 1) << 8; slot: partial blocks (a
+                          // pair uses slot, slot + 1), 0 = finished outputs
+    int32_t j0, j1;       // key tiles [j0, j1) (clipped to what the rows see)
+};
+constexpr uint32_t TILE_SINGLE = 1u << 6;
+
+// A row group of attn_rows.cu: up to ROWS_MAX packed rows over keys [0, k_len) in `splits`
+// chunks, one CTA per chunk and kv head.
+struct RowGroup {
+    int32_t q_row0, n_tok, k_row0, k_len, off;
+    int32_t item0;        // first work item (chunk) of the group
+    int32_t chunk;        // keys per item, a multiple of 64
+    int32_t slot0;        // first partial block, or -1: one item that writes finished outputs
+};
+
+// Rows whose output is joined from partial results: nA blocks of attn_tiles.cu (slots a0, a0 +
+// a_step, ..; row of token t: a_row + t * G), nB and nC blocks of attn_rows.cu (slots b0 .. and
+// c0 .., rows from b_row and 0).  Token t sees min(k_len, t + off) keys in all.
+struct JoinEntry {
+    int32_t q_row0, n_tok, k_len, off, a0, nA, a_step, a_row, b0, nB, b_row, c0, nC;
+};
+
+// Partial results: sums and values unnormalised against the row's reference maximum m (base 2).
+//   tiles: o [slot][kv head][128 rows][128] f32, ml [slot][kv head][128] (m, l)
+//   rows:  o [slot][kv head][16 rows][128],      ml [slot][kv head][16]
+struct Partials {
+    float *a_o = nullptr, *b_o = nullptr;
+    float2 *a_ml = nullptr, *b_ml = nullptr;
+};
+
+constexpr int MAX_JOIN = 512;
+constexpr int MAX_GROUPS = MAX_SEQ + 1;
+
+template <int NV, int NE>
+struct TileArgs {
+    alignas(64) unsigned long long map_q[16];
+    alignas(64) unsigned long long map_k[NV][16], map_v[NV][16];
+    AttnIo io;
+    int n_entries;
+    float c;              // |scale| log2(e)
+    int negate;           // scale < 0
+    Partials part;
+    PromptSeq seq[MAX_SEQ];
+    TileEntry e[NE];
+};
+// every sequence over one view, or a view per sequence
+using TileArgs1 = TileArgs<1, 1536>;
+using TileArgsN = TileArgs<MAX_SEQ, 768>;
+static_assert(sizeof(TileArgs1) <= 32764 && sizeof(TileArgsN) <= 32764, "kernel parameters");
+void launch_tiles(const TileArgs1& a, cudaStream_t s);
+void launch_tiles(const TileArgsN& a, cudaStream_t s);
+cudaError_t attn_tiles_prepare();     // per device, before the first launch
+cudaError_t attn_wait_record(uint32_t* host, cudaStream_t s);
+
+struct RowsArgs {
+    AttnIo io;
+    int n_groups, n_items;
+    float c;              // scale log2(e)
+    Partials part;
+    RowGroup g[MAX_GROUPS];
+    KvRows kv[MAX_GROUPS];
+};
+void launch_attn_rows(const RowsArgs& a, cudaStream_t s);
+
+struct JoinArgs {
+    AttnIo io;
+    int n_entries, max_tok;
+    Partials part;
+    JoinEntry e[MAX_JOIN];
+};
+static_assert(sizeof(JoinArgs) <= 32764, "kernel parameters");
+void launch_attn_join(const JoinArgs& a, cudaStream_t s);
+
+}  // namespace fq

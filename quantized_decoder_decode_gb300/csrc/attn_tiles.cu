@@ -1,0 +1,591 @@
+// Attention of query tiles on the 5th-generation tensor cores (tcgen05, sm_103a): prompts, chunks
+// of prompts behind cached rows, and the shared prefix of a decode batch.
+//
+// One pass over the keys per query tile of 128 packed rows (token, head of the kv head's group):
+//   S = Q K^T (f32, tensor memory),  p = 2^(c S - c m),  O += bf16(p) V,  l += p,
+// c = scale log2(e), m a reference maximum per row.  m follows the running maximum only when that
+// has grown by more than 2^8 = 256 (then O and l of the warp's rows are rescaled); until then
+// p <= 256, which bf16 and the f32 sums carry at the same relative precision.
+//
+// A work unit is a pair of query tiles over the same keys, or (few rows) one tile whose key tiles
+// alternate between the two softmax warpgroups, which are joined at the end.  Either way the
+// tensor cores work for one warpgroup while the other turns scores into weights:
+//   S_A | S_B | PV_A S_A' | PV_B S_B' | ...
+// Tensor memory: S_A, S_B (128 columns each; the weights P overwrite the first 64 as bf16 pairs
+// and are the A operand of P V straight from there), O_A, O_B (128 columns each): all 512.
+// Shared memory: Q (2 x 32 KB), a ring of five 32 KB stages for K and V tiles of 128 keys.
+//
+// Roles (384 threads, one CTA per SM, looping over its units):
+//   warps 0-3, 4-7  softmax of tile A / B, one row per thread, and the outputs
+//   warp 8          one thread issues the products
+//   warp 9          one thread loads Q, K, V by TMA
+//   warp 10         V tiles whose keys some row does not see: a weight of 0 times NaN would
+//                   still be NaN, so values that are not finite are taken out of the tile and
+//                   noted per column with their first key; the rows that see that key get them back
+//                   in their output.  (Tiles of finite values, the rule, are only scanned.)
+//   warp 11         idle
+// Every wait is bounded; one that gives up records it, and all roles leave.
+
+#include "attn_plan.h"
+#include "common.cuh"
+#include "tc.cuh"
+
+namespace fq {
+
+namespace {
+
+constexpr int AT_THREADS = 384;
+constexpr int AT_STAGES = 5;
+constexpr int AT_TILE_BYTES = TILE_ROWS * HEAD_DIM * 2;   // 32 KB
+constexpr int AT_PANEL = AT_TILE_BYTES / 2;               // 64 dims of 128 rows
+constexpr uint32_t AT_S = 0, AT_O = 256;                  // tensor-memory columns (+ 128 for tile B)
+
+struct AtShared {
+    uint64_t q_full, q_empty, item_done, join;
+    uint64_t full[AT_STAGES], empty[AT_STAGES], raw[AT_STAGES];
+    uint64_t s_full[2], p_full[2], o_done[2];
+    uint32_t tmem, abort;
+    uint32_t poison_unit[2];              // unit number + 1 whose notes the buffer holds
+    float exchange[2][TILE_ROWS];
+    uint16_t poison[2][3][HEAD_DIM];      // first key (from the unit's first partly seen tile) of +inf, -inf, NaN
+};
+constexpr int AT_SMEM = (2 + AT_STAGES) * AT_TILE_BYTES + 3072;
+static_assert(sizeof(AtShared) <= 3072, "shared memory");
+static_assert(AT_SMEM <= 232448, "shared memory");
+
+__device__ uint32_t g_attn_waits;   // waits that gave up, since the last check
+
+// One unit as every role sees it.
+struct Unit {
+    int seq, head, slot;          // slot: first partial block + 1, or 0
+    bool single;
+    int tok[2], n_tok[2];         // tokens of tile A / B
+    int j0;                       // first key tile
+    int n[2];                     // key tiles of warpgroup A / B
+    int nt;                       // key tiles of the unit
+    int jm;                       // first key tile with a key that some row does not see
+    int step;
+};
+
+template <class Args>
+FQ_DEV Unit unit_of(const Args& a, int w) {
+    Unit u;
+    const TileEntry& e = a.e[w / a.io.Hkv];
+    const int G = a.io.Hq / a.io.Hkv, tpt = TILE_ROWS / G;
+    u.head = w % a.io.Hkv;
+    u.seq = e.info & 63;
+    u.single = (e.info & TILE_SINGLE) != 0;
+    u.slot = (int)(e.info >> 8);
+    const PromptSeq& s = a.seq[u.seq];
+    u.tok[0] = e.tok0;
+    u.tok[1] = e.tok0 + (u.single ? 0 : tpt);
+    u.j0 = e.j0;
+    u.step = u.single ? 2 : 1;
+    int tiles[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        u.n_tok[x] = max(0, min(tpt, s.q_len - u.tok[x]));
+        const int last = min(s.k_len, u.tok[x] + u.n_tok[x] - 1 + s.off);   // keys the tile's last row sees
+        tiles[x] = u.n_tok[x] > 0 && last > 0 ? max(0, min(e.j1, (last + TILE_ROWS - 1) / TILE_ROWS) - e.j0) : 0;
+    }
+    if (u.single) {
+        u.nt = tiles[0];
+        u.n[0] = (u.nt + 1) / 2;
+        u.n[1] = u.nt / 2;
+    } else {
+        u.n[0] = tiles[0];
+        u.n[1] = tiles[1];
+        u.nt = max(tiles[0], tiles[1]);
+    }
+    u.jm = max(0, min(s.k_len, u.tok[0] + s.off)) / TILE_ROWS;
+    return u;
+}
+
+// Ring position of V tile t of a unit (loads: pair K0 V0 K1 V1 ..; single K0 K1 V0 K2 V1 ..)
+FQ_DEV int v_at(const Unit& u, int t) { return u.single ? min(2 + 2 * t, 2 * u.nt - 1) : 1 + 2 * t; }
+
+FQ_DEV bool at_wait(uint64_t* bar, uint32_t parity, AtShared* sh) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*(volatile uint32_t*)&sh->abort) return false;
+        if (clock64() - t0 > WAIT_BUDGET_CYCLES) {
+            *(volatile uint32_t*)&sh->abort = 1;
+            atomicAdd(&g_attn_waits, 1u);
+            return false;
+        }
+    }
+    return true;
+}
+
+// The same by a whole warp, with one answer for all lanes.
+FQ_DEV bool at_wait_warp(uint64_t* bar, uint32_t parity, AtShared* sh) {
+    return __all_sync(0xFFFFFFFFu, at_wait(bar, parity, sh));
+}
+template <int N>
+FQ_DEV void set_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+FQ_DEV void set_regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+template <class Args, int NV>
+__global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_constant__ Args a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* q_sm = smem;
+    uint8_t* ring = smem + 2 * AT_TILE_BYTES;
+    AtShared* sh = reinterpret_cast<AtShared*>(ring + AT_STAGES * AT_TILE_BYTES);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int units = a.n_entries * a.io.Hkv;
+    const int G = a.io.Hq / a.io.Hkv;
+
+    if (tid == 0) {
+        mbar_init(&sh->q_full, 1);
+        mbar_init(&sh->q_empty, 1);
+        mbar_init(&sh->item_done, 8);
+        mbar_init(&sh->join, 8);
+        for (int s = 0; s < AT_STAGES; ++s) {
+            mbar_init(&sh->full[s], 1);
+            mbar_init(&sh->empty[s], 1);
+            mbar_init(&sh->raw[s], 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&sh->s_full[x], 1);
+            mbar_init(&sh->p_full[x], 4);
+            mbar_init(&sh->o_done[x], 1);
+            sh->poison_unit[x] = 0;
+        }
+        // the 128-byte swizzle wants 1024-byte aligned tiles
+        sh->abort = (smem_u32(smem) & 1023) ? 1 : 0;
+        if (sh->abort) atomicAdd(&g_attn_waits, 1u);
+        mbar_fence_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(&sh->tmem, 512);
+        tmem_relinquish();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = sh->tmem;
+
+    // registers: 384 x 168 at launch = 256 x 216 (softmax: a row's 128 scores) + 128 x 72
+    const bool broken = *(volatile uint32_t*)&sh->abort != 0;   // (only with a misaligned base)
+    if (warp >= 8) {
+    set_regs_down<72>();
+    if (broken) {
+    } else if (warp == 9) {
+        if (lane == 0) {
+            // ---------------- loads
+            uint64_t* last[AT_STAGES];     // where each stage's last load arrives, and its parity
+            uint32_t last_par = 0, used = 0;
+            uint32_t pos = 0, qn = 0, it = 0, raw_ph = 0;
+            bool ok = true;
+            for (int w = blockIdx.x; w < units && ok; w += gridDim.x, ++it) {
+                const Unit u = unit_of(a, w);
+                const PromptSeq& sq = a.seq[u.seq];
+                if (it >= 2 && !(ok = at_wait(&sh->item_done, it & 1, sh))) break;   // unit it - 2 finished
+                if (u.nt == 0) continue;
+                if (!(ok = at_wait(&sh->q_empty, (qn & 1) ^ 1, sh))) break;
+                const int n_q = (u.single || u.n[1] == 0) ? 1 : 2, q0 = u.n[0] > 0 ? 0 : 1;
+                mbar_arrive_expect_tx(&sh->q_full, (uint32_t)((n_q - q0) * AT_TILE_BYTES));
+                for (int x = q0; x < n_q; ++x)
+                    for (int h = 0; h < 2; ++h)
+                        tma_load_4d(q_sm + x * AT_TILE_BYTES + h * AT_PANEL, a.map_q, 64 * h, 0, u.head, sq.q_row0 + u.tok[x],
+                                    &sh->q_full);
+                ++qn;
+                const int vw = NV == 1 ? 0 : u.seq;
+                auto load = [&](bool v, int t) {
+                    const int s = pos % AT_STAGES;
+                    if (!(ok = at_wait(&sh->empty[s], ((pos / AT_STAGES) & 1) ^ 1, sh))) return;
+                    const bool look = v && u.j0 + t >= u.jm;
+                    uint64_t* bar = look ? &sh->raw[s] : &sh->full[s];
+                    mbar_arrive_expect_tx(bar, AT_TILE_BYTES);
+                    uint8_t* dst = ring + s * AT_TILE_BYTES;
+                    const int row = sq.k_row0 + (u.j0 + t) * TILE_ROWS;
+                    const void* map = v ? a.map_v[vw] : a.map_k[vw];
+                    tma_load_3d(dst, map, 0, row, u.head, bar);
+                    tma_load_3d(dst + AT_PANEL, map, 64, row, u.head, bar);
+                    const uint32_t par = look ? (raw_ph >> s) & 1 : (pos / AT_STAGES) & 1;
+                    if (look) raw_ph ^= 1u << s;
+                    last[s] = bar;
+                    last_par = (last_par & ~(1u << s)) | par << s;
+                    used |= 1u << s;
+                    ++pos;
+                };
+                if (u.single) {
+                    load(false, 0);
+                    if (ok && u.nt > 1) load(false, 1);
+                    for (int t = 0; t < u.nt && ok; ++t) {
+                        load(true, t);
+                        if (ok && t + 2 < u.nt) load(false, t + 2);
+                    }
+                } else {
+                    for (int t = 0; t < u.nt && ok; ++t) {
+                        load(false, t);
+                        if (ok) load(true, t);
+                    }
+                }
+            }
+            if (!ok) {   // no copy may still be landing when the CTA exits
+                for (int s = 0; s < AT_STAGES; ++s)
+                    if (used >> s & 1) mbar_wait(last[s], last_par >> s & 1);
+                if (qn) mbar_wait(&sh->q_full, (qn - 1) & 1);
+            }
+        }
+    } else if (warp == 8) {
+        if (lane == 0) {
+            // ---------------- products
+            const uint32_t id_qk = idesc_bf16_f32(TILE_ROWS, TILE_ROWS, false, a.negate != 0);
+            const uint32_t id_pv = idesc_bf16_f32(TILE_ROWS, HEAD_DIM, true, false);
+            const uint32_t q_addr = smem_u32(q_sm), r_addr = smem_u32(ring);
+            uint32_t pos = 0, qn = 0, pc[2] = {0, 0};
+            bool ok = true;
+            auto stage_of = [&](uint32_t p) -> int {
+                const int s = p % AT_STAGES;
+                ok = ok && at_wait(&sh->full[s], (p / AT_STAGES) & 1, sh);
+                return s;
+            };
+            auto qk = [&](int x, int qt, int s) {
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t off = (k >> 2) * AT_PANEL + (k & 3) * 32;
+                    mma_f16(tm + AT_S + 128 * x, sdesc_sw128(q_addr + qt * AT_TILE_BYTES + off),
+                            sdesc_sw128(r_addr + s * AT_TILE_BYTES + off), id_qk, k > 0);
+                }
+                mma_commit(&sh->s_full[x]);
+            };
+            auto pv = [&](int x, int i, int s) {
+                ok = ok && at_wait(&sh->p_full[x], pc[x] & 1, sh);
+                ++pc[x];
+                if (!ok) return;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_f16_ta(tm + AT_O + 128 * x, tm + AT_S + 128 * x + 8 * k,
+                               sdesc_sw128_mn(r_addr + s * AT_TILE_BYTES + k * 2048, AT_PANEL), id_pv, (i > 0 || k > 0) ? 1u : 0u);
+                mma_commit(&sh->o_done[x]);
+            };
+            for (int w = blockIdx.x; w < units && ok; w += gridDim.x) {
+                const Unit u = unit_of(a, w);
+                if (u.nt == 0) continue;
+                if (!(ok = at_wait(&sh->q_full, qn & 1, sh))) break;
+                ++qn;
+                if (u.single) {
+                    for (int x = 0; x < 2 && x < u.nt; ++x) {
+                        const int s = stage_of(pos++);
+                        if (!ok) break;
+                        qk(x, 0, s);
+                        mma_commit(&sh->empty[s]);
+                    }
+                    if (u.nt <= 2) mma_commit(&sh->q_empty);
+                    for (int t = 0; t < u.nt && ok; ++t) {
+                        const int x = t & 1;
+                        int s = stage_of(pos++);
+                        pv(x, t >> 1, s);
+                        if (!ok) break;
+                        mma_commit(&sh->empty[s]);
+                        if (t + 2 < u.nt) {
+                            s = stage_of(pos++);
+                            if (!ok) break;
+                            qk(x, 0, s);
+                            mma_commit(&sh->empty[s]);
+                            if (t + 3 == u.nt) mma_commit(&sh->q_empty);
+                        }
+                    }
+                } else {
+                    int s = stage_of(pos++);
+                    if (!ok) break;
+                    for (int x = 0; x < 2; ++x)
+                        if (u.n[x] > 0) qk(x, x, s);
+                    mma_commit(&sh->empty[s]);
+                    if (u.nt == 1) mma_commit(&sh->q_empty);
+                    for (int i = 0; i < u.nt && ok; ++i) {
+                        const int sv = stage_of(pos++);
+                        int sk = 0;
+                        const bool more = i + 1 < u.nt;
+                        for (int x = 0; x < 2 && ok; ++x) {
+                            if (i < u.n[x]) pv(x, i, sv);
+                            if (x == 0 && more) sk = stage_of(pos++);
+                            if (ok && i + 1 < u.n[x]) qk(x, x, sk);
+                        }
+                        if (!ok) break;
+                        mma_commit(&sh->empty[sv]);
+                        if (more) mma_commit(&sh->empty[sk]);
+                        if (i + 2 == u.nt) mma_commit(&sh->q_empty);
+                    }
+                }
+            }
+        }
+    } else if (warp == 10) {
+        // ---------------- partly seen V tiles
+        uint32_t pos0 = 0, it = 0, raw_ph = 0;
+        bool ok = true;
+        for (int w = blockIdx.x; w < units && ok; w += gridDim.x, ++it) {
+            const Unit u = unit_of(a, w);
+            const int k_len = a.seq[u.seq].k_len;
+            for (int t = max(0, u.jm - u.j0); t < u.nt; ++t) {
+                const int s = (pos0 + v_at(u, t)) % AT_STAGES;
+                if (!(ok = at_wait_warp(&sh->raw[s], (raw_ph >> s) & 1, sh))) break;
+                raw_ph ^= 1u << s;
+                uint8_t* tile = ring + s * AT_TILE_BYTES;
+                // largest magnitude, NaN kept: bf16 bits without the sign order like integers
+                uint32_t hi = 0, lo = 0;
+#pragma unroll 8
+                for (int i = lane; i < AT_TILE_BYTES / 16; i += 32) {
+                    const uint4 v = reinterpret_cast<const uint4*>(tile)[i];
+                    hi = max(hi, max(max(v.x & 0x7FFF0000u, v.y & 0x7FFF0000u), max(v.z & 0x7FFF0000u, v.w & 0x7FFF0000u)));
+                    lo = max(lo, max(max(v.x & 0x7FFFu, v.y & 0x7FFFu), max(v.z & 0x7FFFu, v.w & 0x7FFFu)));
+                }
+                if (__any_sync(0xFFFFFFFFu, hi >= 0x7F800000u || lo >= 0x7F80u)) {
+                    const int buf = it & 1;
+                    uint16_t(*note)[HEAD_DIM] = sh->poison[buf];
+                    if (sh->poison_unit[buf] != it + 1) {
+                        for (int i = lane; i < 3 * HEAD_DIM; i += 32) note[0][i] = 0xFFFFu;
+                        __syncwarp();
+                    }
+                    // lane l owns columns 4l .. 4l+3: 8 bytes of every row
+                    uint8_t* col = tile + (lane >> 4) * AT_PANEL;
+                    for (int r = 0; r < TILE_ROWS; ++r) {
+                        uint16_t* p = reinterpret_cast<uint16_t*>(col + sw128_offset(r, (lane & 15) >> 1) + (lane & 1) * 8);
+                        const int key = (u.j0 + t) * TILE_ROWS + r;
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t b = p[c];
+                            if ((b & 0x7F80u) != 0x7F80u) continue;
+                            p[c] = 0;
+                            if (key >= k_len) continue;   // seen by no row
+                            uint16_t& f = note[(b & 0x7Fu) ? 2 : (b & 0x8000u) ? 1 : 0][4 * lane + c];
+                            const uint16_t k16 = (uint16_t)(key - u.jm * TILE_ROWS);
+                            if (k16 < f) f = k16;
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) *(volatile uint32_t*)&sh->poison_unit[buf] = it + 1;
+                    __threadfence_block();
+                    fence_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->full[s]);
+            }
+            pos0 += 2 * u.nt;
+        }
+    }
+    } else {
+    set_regs_up<216>();
+    if (!broken) {
+        // ---------------- softmax and outputs: thread = row
+        const int x = warp >> 2, row = tid & 127;
+        const uint32_t lane_base = (uint32_t)(warp & 3) << 21;      // 32 lanes per warp, lane in bits 16..
+        const uint32_t tS = tm + AT_S + 128 * x + lane_base, tO = tm + AT_O + 128 * x + lane_base;
+        const float c = a.c;
+        uint32_t sc = 0, it = 0, jc = 0;   // scores seen (of all units); units; joins
+        bool ok = true;
+        // both warpgroups meet (a bounded wait, unlike a named barrier)
+        auto join = [&]() -> bool {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->join);
+            const bool met = at_wait_warp(&sh->join, jc++ & 1, sh);
+            tc_fence_after();
+            return met;
+        };
+        for (int w = blockIdx.x; w < units && ok; w += gridDim.x, ++it) {
+            const Unit u = unit_of(a, w);
+            const PromptSeq& sq = a.seq[u.seq];
+            const int tok = u.tok[x] + row / G;
+            const bool valid = row / G < u.n_tok[x];
+            const int limit = valid ? max(0, min(sq.k_len, tok + sq.off)) : 0;   // keys the row sees
+            float m = -INFINITY, l = 0.f;
+            for (int i = 0; i < u.n[x]; ++i) {
+                if (!(ok = at_wait_warp(&sh->s_full[x], sc & 1, sh))) break;
+                tc_fence_after();
+                float s[TILE_ROWS];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) tmem_ld32(tS + 32 * h, reinterpret_cast<uint32_t*>(s) + 32 * h);
+                tmem_wait_ld();
+                const int left = limit - (u.j0 + (u.single ? 2 * i + x : i)) * TILE_ROWS;   // keys of this tile that the row sees
+                if (__any_sync(0xFFFFFFFFu, left < TILE_ROWS)) {
+#pragma unroll
+                    for (int k = 0; k < TILE_ROWS; ++k) s[k] = k < left ? s[k] : -INFINITY;
+                }
+                float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int k = 4; k < TILE_ROWS; ++k) mx[k & 3] = fmaxf(mx[k & 3], s[k]);
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                // (a row without a key so far has m = -inf and moves at its first one)
+                const bool move = (top - m) * c > 8.f;
+                if (__any_sync(0xFFFFFFFFu, move)) {
+                    const float mn = move ? top : m;
+                    const float f = move ? ex2((m - mn) * c) : 1.f;
+                    m = mn;
+                    l *= f;
+                    if (i > 0) {
+                        if (!(ok = at_wait_warp(&sh->o_done[x], (sc - 1) & 1, sh))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int h = 0; h < 8; ++h) {
+                            uint32_t o[16];
+                            tmem_ld16(tO + 16 * h, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_st16(tO + 16 * h, o);
+                        }
+                    }
+                }
+                const float mc = m == -INFINITY ? 0.f : m * c;
+                float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float p0 = ex2(fmaf(s[32 * h + 2 * k], c, -mc)), p1 = ex2(fmaf(s[32 * h + 2 * k + 1], c, -mc));
+                        ls[(2 * k) & 3] += p0;
+                        ls[(2 * k + 1) & 3] += p1;
+                        p[k] = bf16x2(p0, p1);
+                    }
+                    tmem_st16(tS + 16 * h, p);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->p_full[x]);
+                l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                ++sc;
+            }
+            if (!ok) break;
+            if (u.n[x] > 0) {
+                if (!(ok = at_wait_warp(&sh->o_done[x], (sc - 1) & 1, sh))) break;
+                tc_fence_after();
+            }
+            // weights of the tile's accumulator(s): single units join A and B here, A's threads
+            // writing dims 0-63 and B's 64-127 of the same rows
+            float f0 = 1.f, f1 = 0.f, lsum = l, mref = m;
+            if (u.single) {
+                sh->exchange[x][row] = m;
+                if (!(ok = join())) break;
+                const float mo = sh->exchange[x ^ 1][row];
+                if (!(ok = join())) break;
+                mref = fmaxf(m, mo);
+                const float own = m == mref ? 1.f : ex2((m - mref) * c), other = mo == mref ? 1.f : ex2((mo - mref) * c);
+                sh->exchange[x][row] = l * own;
+                if (!(ok = join())) break;
+                lsum = l * own + sh->exchange[x ^ 1][row];
+                f0 = x == 0 ? own : other;    // weight of O_A
+                f1 = x == 0 ? other : own;    // weight of O_B
+                if (u.nt == 1) f1 = 0.f;
+            }
+            const bool noted = *(volatile uint32_t*)&sh->poison_unit[it & 1] == it + 1;
+            const int seen = limit - u.jm * TILE_ROWS;   // noted keys below this are the row's
+            const int d0 = u.single ? 64 * x : 0, dn = u.single ? 64 : HEAD_DIM;
+            const uint32_t tA = tm + AT_O + lane_base + (u.single ? 0 : 128 * x);
+            const float inv = u.slot ? 1.f : (limit > 0 ? 1.f / lsum : 0.f);
+            const int64_t o_row = (int64_t)(sq.q_row0 + tok);
+            const int64_t o_col = (int64_t)(u.head * G + row % G) * HEAD_DIM;
+            const int64_t blk = ((int64_t)(u.slot - 1 + (u.single ? 0 : x)) * a.io.Hkv + u.head) * TILE_ROWS + row;
+            const bool have = u.single ? u.nt > 0 : u.n[x] > 0;
+            for (int d = d0; d < d0 + dn; d += 16) {
+                uint32_t o[16];
+                __syncwarp();
+                if (have) {
+                    tmem_ld16(tA + d, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] = 0;
+                }
+                float y[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) y[k] = __uint_as_float(o[k]);
+                if (u.single) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) y[k] *= f0;
+                    if (u.nt > 1) {
+                        tmem_ld16(tA + 128 + d, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) y[k] = fmaf(__uint_as_float(o[k]), f1, y[k]);
+                    }
+                }
+                if (noted) {
+                    for (int k = 0; k < 16; ++k) {
+                        const bool pos_inf = sh->poison[it & 1][0][d + k] < seen, neg_inf = sh->poison[it & 1][1][d + k] < seen;
+                        if (sh->poison[it & 1][2][d + k] < seen) y[k] = NAN;
+                        if (pos_inf) y[k] += INFINITY;
+                        if (neg_inf) y[k] -= INFINITY;
+                    }
+                }
+                if (limit > 0) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) y[k] *= inv;
+                }
+                if (valid) {
+                    if (u.slot) {
+                        float4* dst = reinterpret_cast<float4*>(a.part.a_o + blk * HEAD_DIM + d);
+    #pragma unroll
+                        for (int k = 0; k < 4; ++k) dst[k] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+                    } else if (a.io.out_f32) {
+                        float4* dst = reinterpret_cast<float4*>((float*)a.io.out + o_row * a.io.out_stride + o_col + d);
+    #pragma unroll
+                        for (int k = 0; k < 4; ++k) dst[k] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+                    } else {
+                        uint4* dst = reinterpret_cast<uint4*>((uint16_t*)a.io.out + o_row * a.io.out_stride + o_col + d);
+    #pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            dst[k] = make_uint4(bf16x2(y[8 * k], y[8 * k + 1]), bf16x2(y[8 * k + 2], y[8 * k + 3]),
+                                                bf16x2(y[8 * k + 4], y[8 * k + 5]), bf16x2(y[8 * k + 6], y[8 * k + 7]));
+                    }
+                }
+            }
+            if (u.slot && valid && (!u.single || x == 0)) a.part.a_ml[blk] = make_float2(mref * c, lsum);
+            // the next unit's products may overwrite O once both warpgroups have read it
+            tc_fence_before();
+            if (u.single && !(ok = join())) break;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->item_done);
+        }
+    }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tm, 512);
+}
+
+constexpr int AT_REGS = 168;   // what the register split above draws on
+
+template <class Args, int NV>
+cudaError_t prepare_t() {
+    cudaFuncAttributes fa;
+    cudaError_t e = cudaFuncGetAttributes(&fa, attn_tiles_kernel<Args, NV>);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != AT_REGS) return cudaErrorInvalidKernelImage;   // the split would wait for registers that are not there
+    return cudaFuncSetAttribute(attn_tiles_kernel<Args, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_SMEM);
+}
+
+template <class Args, int NV>
+void launch_t(const Args& a, cudaStream_t s) {
+    const int64_t units = (int64_t)a.n_entries * a.io.Hkv;
+    const int grid = (int)(units < ATTN_SMS ? units : ATTN_SMS);
+    attn_tiles_kernel<Args, NV><<<grid, AT_THREADS, AT_SMEM, s>>>(a);
+}
+
+}  // namespace
+
+cudaError_t attn_tiles_prepare() {
+    const cudaError_t e = prepare_t<TileArgs1, 1>();
+    return e != cudaSuccess ? e : prepare_t<TileArgsN, MAX_SEQ>();
+}
+void launch_tiles(const TileArgs1& a, cudaStream_t s) { launch_t<TileArgs1, 1>(a, s); }
+void launch_tiles(const TileArgsN& a, cudaStream_t s) { launch_t<TileArgsN, MAX_SEQ>(a, s); }
+
+// Waits that gave up on the current device, read (and cleared) after the work queued on s.
+cudaError_t attn_wait_record(uint32_t* host, cudaStream_t s) {
+    cudaError_t e = cudaMemcpyFromSymbolAsync(host, g_attn_waits, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess || *host == 0) return e;
+    const uint32_t zero = 0;
+    e = cudaMemcpyToSymbolAsync(g_attn_waits, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s);
+    return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
+}
+
+}  // namespace fq

@@ -70,6 +70,19 @@ FQ_DEV float bf2f(unsigned short h) { return __uint_as_float((uint32_t)h << 16);
 FQ_DEV float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 FQ_DEV float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// two floats rounded to a bf16 pair (lo in the low half)
+FQ_DEV uint32_t bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// 2^x, relative error about 2^-22, results below the normal range flushed to zero
+FQ_DEV float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Four int8 codes of one 32-bit word to exact floats: bias each byte to unsigned, place it
 // in the low mantissa bits of 2^23 (byte permute: selector nibble 0 picks source byte k of
 // u, nibbles 1-2 pick zero bytes and nibble 3 the 0x4B exponent byte of the constant),

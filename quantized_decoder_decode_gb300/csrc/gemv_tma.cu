@@ -411,6 +411,21 @@ bool encode_f16_rows_sw128(void* map, const void* base, uint64_t K, uint64_t row
                   CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+bool encode_bf16_tiles(void* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
+                       const uint32_t* box) {
+    if (!load_encoder()) return false;
+    cuuint64_t d[5], st[5];
+    cuuint32_t b[5], es[5] = {1, 1, 1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i) st[i - 1] = strides_bytes[i];
+    }
+    return g_encode(reinterpret_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
+                    const_cast<void*>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool launch_gemv_tma(const GemvArgs& a, cudaStream_t s, bool pdl) {
     if (a.route || a.B > 4 || a.W.K % 256 != 0 || g_sms_t == 0 || !a.W.tm || !a.W.tm->ok) return false;
     const bool one = a.B == 1;

@@ -121,6 +121,11 @@ bool make_tma_maps(const QMat& W, TmaMaps* out);
 // tensor map over f16 rows [rows][K], box 64 halves x box_rows, 128-byte swizzle
 bool encode_f16_rows_sw128(void* map, const void* base, uint64_t K, uint64_t rows, uint32_t box_rows);
 
+// tensor map over bf16 values of rank 3 or 4 (strides[0] is not read), 128-byte swizzle, zero
+// fill outside
+bool encode_bf16_tiles(void* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
+                       const uint32_t* box);
+
 // tcgen05 GEMM for lockstep batches of TC_MIN_BATCH..32 rows over Q8_0 weights: a prep
 // kernel (RMSNorm + f16 hi/lo split into xh, 64 x K halves) and the GEMM
 constexpr int TC_MIN_BATCH = 8;
@@ -280,25 +285,6 @@ struct AttnIo {
     int Hq, Hkv;
     float scale;
 };
-struct PromptSeq {
-    int32_t q_row0, q_len, k_row0, k_len;
-};
-struct PromptArgs {
-    AttnIo io;
-    int n_seq, q_rows;
-    PromptSeq seq[MAX_SEQ];
-    KvRows kv[MAX_SEQ];
-};
-void launch_prompt(const PromptArgs& a, cudaStream_t s);
-struct SharedArgs {
-    AttnIo io;
-    int n_seq, prefix_len;
-    KvRows prefix;
-    int32_t tail_len[MAX_SEQ];
-    KvRows tail[MAX_SEQ];
-};
-void launch_shared(const SharedArgs& a, cudaStream_t s);
-
 // Load-time helpers
 // Source row r lands in destination row (r / group) * group_stride + (r % group) * step + off
 // (fusing q/k/v, interleaving gate/up rows, stacking experts).

@@ -20,11 +20,6 @@ namespace {
 constexpr int QR_HEADS = 4;      // heads per warp
 constexpr int QR_THREADS = 256;
 
-FQ_DEV uint2 pack_bf16x4(const float v[4]) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-    return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
-
 __global__ void __launch_bounds__(QR_THREADS) qk_rows_kernel(const __grid_constant__ QkRowsArgs a, int groups) {
     const int lane = threadIdx.x & 31;
     const int64_t w = ((int64_t)blockIdx.x * QR_THREADS + threadIdx.x) >> 5;
@@ -75,7 +70,7 @@ __global__ void __launch_bounds__(QR_THREADS) qk_rows_kernel(const __grid_consta
         } else {
             dst = kv.v + at + (int64_t)(h - a.Hq - a.Hkv) * kv.head_stride;
         }
-        *reinterpret_cast<uint2*>(dst) = pack_bf16x4(v);
+        *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
     }
 }
 

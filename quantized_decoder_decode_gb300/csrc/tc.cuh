@@ -33,6 +33,15 @@ FQ_DEV void mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t id
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// the same with A in tensor memory (row = lane, two 16-bit K elements per column)
+FQ_DEV void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
 // arrive once on bar when every MMA issued so far by this thread has completed
 FQ_DEV void mma_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
@@ -44,6 +53,11 @@ FQ_DEV void mma_commit(uint64_t* bar) {
 //   15 / 16 A / B major (0 = K); 17-22 N >> 3; 24-28 M >> 4.
 FQ_HD constexpr uint32_t idesc_f16_f32(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// The same with bf16 operands; B may be MN-major (bit 16), A negated (bit 13).
+FQ_HD constexpr uint32_t idesc_bf16_f32(int M, int N, bool b_mn_major, bool negate_a) {
+    return idesc_f16_f32(M, N) | (1u << 7) | (1u << 10) | (negate_a ? 1u << 13 : 0u) | (b_mn_major ? 1u << 16 : 0u);
 }
 
 // Shared-memory matrix descriptor for a K-major operand in the 128-byte swizzled canonical
@@ -61,6 +75,14 @@ FQ_DEV uint64_t sdesc_sw128(uint32_t saddr) {
     return d;
 }
 
+// The same for an MN-major operand in the 128-byte swizzled layout: atoms of 64 MN elements
+// (one 128-byte row) x 8 K rows; the next 8 K rows 1024 bytes further (stride byte offset),
+// the next 64 MN elements `panel` bytes further (leading byte offset).
+FQ_DEV uint64_t sdesc_sw128_mn(uint32_t saddr, uint32_t panel) {
+    uint64_t d = sdesc_sw128(saddr) & ~((uint64_t)0x3FFF << 16);
+    return d | (uint64_t)(panel >> 4) << 16;
+}
+
 // byte offset of (row, 16-byte chunk j of its 128-byte K slice) in the swizzled layout
 FQ_DEV uint32_t sw128_offset(int row, int j) {
     return (uint32_t)((row >> 3) * 1024 + (row & 7) * 128 + ((j ^ (row & 7)) << 4));
@@ -75,6 +97,26 @@ FQ_DEV void tmem_ld16(uint32_t taddr, uint32_t* r) {
         : "r"(taddr)
         : "memory");
 }
+FQ_DEV void tmem_ld32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+// registers -> TMEM
+FQ_DEV void tmem_st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+FQ_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 FQ_DEV void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 }  // namespace fq

@@ -111,6 +111,7 @@ def lib():
                 "fq_attn_shared": [vp, u64, u32, vp, u32, vp, vp, u32, u32, ctypes.c_float, vp, u64, ctypes.c_int, vp,
                                    ctypes.c_size_t, vp],
                 "fq_attn_shared_workspace": [u32, u32, vp, u32, u32, vp],
+                "fq_attn_check": [vp],
             }
             for name, args in sig.items():
                 fn = getattr(L, name)
@@ -137,7 +138,7 @@ EXPORTED = ("fq_desc_init", "fq_load_weights", "fq_model_free", "fq_kv_init", "f
             "fq_decode_step_batch", "fq_decode_step_all_logits", "fq_forward_step", "fq_decode_greedy", "fq_decode_step_trace", "fq_dequant_rows", "fq_quantize_q8_0", "fq_layer_step_trace",
             "fq_gemv", "fq_step_kernels", "fq_check_device", "fq_debug_wait_timeout", "fq_set_option", "fq_step_path", "fq_layer_step_noalloc", "fq_last_error",
             "fq_status_str", "fq_kv_layer_view", "fq_qk_norm_rope", "fq_attn_prompt", "fq_attn_prompt_workspace",
-            "fq_attn_shared", "fq_attn_shared_workspace")
+            "fq_attn_shared", "fq_attn_shared_workspace", "fq_attn_check")
 
 
 def _check(status: int, where: str) -> None:
@@ -429,3 +430,7 @@ def fq_attn_shared(q_ptr: int, prefix, prefix_len: int, tails, tail_len, num_att
     _check(lib().fq_attn_shared(q_ptr, q_stride, len(a), p, prefix_len, t, a, num_attention_heads, num_key_value_heads,
                                 scale, out_ptr, out_stride, DTYPES[out_dtype], ws_ptr, ws_bytes, stream),
            "fq_attn_shared")
+
+
+def fq_attn_check(stream: int = 0) -> None:
+    _check(lib().fq_attn_check(stream), "fq_attn_check")

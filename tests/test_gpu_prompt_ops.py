@@ -46,7 +46,7 @@ def run_prompt(q, views, q_len, k_len, hq, hkv, kv_row0=None, out=None, out_dtyp
         out = torch.full((sum(q_len), hq, D), NAN, device=DEV, dtype=torch.bfloat16 if out_dtype == "bf16" else torch.float32)
     fq.fq_attn_prompt(q.data_ptr(), views, q_len, k_len, hq, hkv, scale, out.data_ptr(), ws.data_ptr(), ws.numel() * 4,
                       stream(), kv_row0=kv_row0, q_stride=q_stride, out_stride=out_stride, out_dtype=out_dtype)
-    torch.cuda.synchronize()
+    fq.fq_attn_check(stream())
     return out
 
 
@@ -203,7 +203,7 @@ def run_shared(q, prefix, prefix_len, tails, tail_len, hq, hkv, out=None, out_dt
         out = torch.full((len(tail_len), hq, D), NAN, device=DEV, dtype=torch.bfloat16 if out_dtype == "bf16" else torch.float32)
     fq.fq_attn_shared(q.data_ptr(), prefix, prefix_len, tails, tail_len, hq, hkv, scale, out.data_ptr(), ws.data_ptr(),
                       ws.numel() * 4, stream(), out_dtype=out_dtype, **kw)
-    torch.cuda.synchronize()
+    fq.fq_attn_check(stream())
     return out
 
 
