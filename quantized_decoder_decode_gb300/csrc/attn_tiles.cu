@@ -38,12 +38,12 @@ constexpr int AT_THREADS = 384;
 constexpr int AT_STAGES = 5;
 constexpr int AT_TILE_BYTES = TILE_ROWS * HEAD_DIM * 2;   // 32 KB
 constexpr int AT_PANEL = AT_TILE_BYTES / 2;               // 64 dims of 128 rows
-constexpr uint32_t AT_S = 0, AT_O = 256;                  // tensor-memory columns (+ 128 for tile B)
+constexpr uint32_t AT_S = 0, AT_P = 128, AT_O = 256;      // tensor-memory columns: S, P_A, P_B (64 each), O_A, O_B
 
 struct AtShared {
     uint64_t q_full, q_empty, item_done, join;
     uint64_t full[AT_STAGES], empty[AT_STAGES], raw[AT_STAGES];
-    uint64_t s_full[2], p_full[2], o_done[2];
+    uint64_t s_full[2], p_full[2], o_done[2], s_free;
     uint32_t tmem, abort;
     uint32_t poison_unit[2];              // unit number + 1 whose notes the buffer holds
     float exchange[2][TILE_ROWS];
@@ -66,6 +66,10 @@ struct Unit {
     int jm;                       // first key tile with a key that some row does not see
     int step;
 };
+
+// The unit of a CTA in its round r: forth and back over the list (longest first), so that the
+// CTAs' sums come out nearly even (8192 tokens, 32 / 8 heads: 2% over the mean instead of 14%).
+FQ_DEV int unit_at(int r) { return r * (int)gridDim.x + (int)(r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x); }
 
 template <class Args>
 FQ_DEV Unit unit_of(const Args& a, int w) {
@@ -101,8 +105,10 @@ FQ_DEV Unit unit_of(const Args& a, int w) {
     return u;
 }
 
-// Ring position of V tile t of a unit (loads: pair K0 V0 K1 V1 ..; single K0 K1 V0 K2 V1 ..)
-FQ_DEV int v_at(const Unit& u, int t) { return u.single ? min(2 + 2 * t, 2 * u.nt - 1) : 1 + 2 * t; }
+// Ring position of V tile t of a unit: each follows the K tile whose scores are made before its
+// product (pair: K0 K1 V0 K2 V1 ..; single: K0 K1 K2 V0 K3 V1 ..)
+FQ_DEV int k_at(const Unit& u, int t) { return t + max(0, t - u.step); }
+FQ_DEV int v_at(const Unit& u, int t) { return t + min(t + 1 + u.step, u.nt); }
 
 FQ_DEV bool at_wait(uint64_t* bar, uint32_t parity, AtShared* sh) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -142,6 +148,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
         mbar_init(&sh->q_empty, 1);
         mbar_init(&sh->item_done, 8);
         mbar_init(&sh->join, 8);
+        mbar_init(&sh->s_free, 4);
         for (int s = 0; s < AT_STAGES; ++s) {
             mbar_init(&sh->full[s], 1);
             mbar_init(&sh->empty[s], 1);
@@ -178,7 +185,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
             uint32_t last_par = 0, used = 0;
             uint32_t pos = 0, qn = 0, it = 0, raw_ph = 0;
             bool ok = true;
-            for (int w = blockIdx.x; w < units && ok; w += gridDim.x, ++it) {
+            for (int w; (w = unit_at(it)) < units && ok; ++it) {
                 const Unit u = unit_of(a, w);
                 const PromptSeq& sq = a.seq[u.seq];
                 if (it >= 2 && !(ok = at_wait(&sh->item_done, it & 1, sh))) break;   // unit it - 2 finished
@@ -210,18 +217,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
                     used |= 1u << s;
                     ++pos;
                 };
-                if (u.single) {
-                    load(false, 0);
-                    if (ok && u.nt > 1) load(false, 1);
-                    for (int t = 0; t < u.nt && ok; ++t) {
-                        load(true, t);
-                        if (ok && t + 2 < u.nt) load(false, t + 2);
-                    }
-                } else {
-                    for (int t = 0; t < u.nt && ok; ++t) {
-                        load(false, t);
-                        if (ok) load(true, t);
-                    }
+                for (int t = 0; t < u.step && t < u.nt && ok; ++t) load(false, t);
+                for (int t = 0; t < u.nt && ok; ++t) {
+                    if (t + u.step < u.nt) load(false, t + u.step);
+                    if (ok) load(true, t);
                 }
             }
             if (!ok) {   // no copy may still be landing when the CTA exits
@@ -231,95 +230,84 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
             }
         }
     } else if (warp == 8) {
-        if (lane == 0) {
-            // ---------------- products
-            const uint32_t id_qk = idesc_bf16_f32(TILE_ROWS, TILE_ROWS, false, a.negate != 0);
-            const uint32_t id_pv = idesc_bf16_f32(TILE_ROWS, HEAD_DIM, true, false);
-            const uint32_t q_addr = smem_u32(q_sm), r_addr = smem_u32(ring);
-            uint32_t pos = 0, qn = 0, pc[2] = {0, 0};
-            bool ok = true;
-            auto stage_of = [&](uint32_t p) -> int {
-                const int s = p % AT_STAGES;
-                ok = ok && at_wait(&sh->full[s], (p / AT_STAGES) & 1, sh);
-                return s;
-            };
-            auto qk = [&](int x, int qt, int s) {
-                tc_fence_after();
+        // ---------------- scores
+        const uint32_t idesc = idesc_bf16_f32(TILE_ROWS, TILE_ROWS, false, a.negate != 0);
+        const uint64_t dq0 = sdesc_sw128(smem_u32(q_sm)), dk0 = sdesc_sw128(smem_u32(ring));
+        uint32_t pos0 = 0, qn = 0, sn = 0, it = 0;   // sn: score tiles
+        bool ok = true;
+        for (int w; (w = unit_at(it)) < units && ok; ++it) {
+            const Unit u = unit_of(a, w);
+            if (u.nt == 0) continue;
+            if (!(ok = at_wait_warp(&sh->q_full, qn++ & 1, sh))) break;
+            for (int t = 0; t < u.nt && ok; ++t) {
+                const uint32_t pos = pos0 + k_at(u, t);
+                const int s = pos % AT_STAGES;
+                if (!(ok = at_wait_warp(&sh->full[s], (pos / AT_STAGES) & 1, sh))) break;
+                for (int x = 0; x < 2; ++x) {
+                    if (u.single ? x != (t & 1) : t >= u.n[x]) continue;
+                    // the scores before are in registers
+                    if (!(ok = at_wait_warp(&sh->s_free, (sn++ & 1) ^ 1, sh))) break;
+                    tc_fence_after();
+                    const uint64_t dq = dq0 + (uint32_t)((u.single ? 0 : x) * (AT_TILE_BYTES >> 4));
+                    const uint64_t dk = dk0 + (uint32_t)(s * (AT_TILE_BYTES >> 4));
+                    if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t off = (k >> 2) * AT_PANEL + (k & 3) * 32;
-                    mma_f16(tm + AT_S + 128 * x, sdesc_sw128(q_addr + qt * AT_TILE_BYTES + off),
-                            sdesc_sw128(r_addr + s * AT_TILE_BYTES + off), id_qk, k > 0);
-                }
-                mma_commit(&sh->s_full[x]);
-            };
-            auto pv = [&](int x, int i, int s) {
-                ok = ok && at_wait(&sh->p_full[x], pc[x] & 1, sh);
-                ++pc[x];
-                if (!ok) return;
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_f16_ta(tm + AT_O + 128 * x, tm + AT_S + 128 * x + 8 * k,
-                               sdesc_sw128_mn(r_addr + s * AT_TILE_BYTES + k * 2048, AT_PANEL), id_pv, (i > 0 || k > 0) ? 1u : 0u);
-                mma_commit(&sh->o_done[x]);
-            };
-            for (int w = blockIdx.x; w < units && ok; w += gridDim.x) {
-                const Unit u = unit_of(a, w);
-                if (u.nt == 0) continue;
-                if (!(ok = at_wait(&sh->q_full, qn & 1, sh))) break;
-                ++qn;
-                if (u.single) {
-                    for (int x = 0; x < 2 && x < u.nt; ++x) {
-                        const int s = stage_of(pos++);
-                        if (!ok) break;
-                        qk(x, 0, s);
-                        mma_commit(&sh->empty[s]);
-                    }
-                    if (u.nt <= 2) mma_commit(&sh->q_empty);
-                    for (int t = 0; t < u.nt && ok; ++t) {
-                        const int x = t & 1;
-                        int s = stage_of(pos++);
-                        pv(x, t >> 1, s);
-                        if (!ok) break;
-                        mma_commit(&sh->empty[s]);
-                        if (t + 2 < u.nt) {
-                            s = stage_of(pos++);
-                            if (!ok) break;
-                            qk(x, 0, s);
-                            mma_commit(&sh->empty[s]);
-                            if (t + 3 == u.nt) mma_commit(&sh->q_empty);
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t off = (k >> 2) * (AT_PANEL >> 4) + (k & 3) * 2;
+                            mma_f16(tm + AT_S, dq + off, dk + off, idesc, k > 0);
                         }
+                        mma_commit(&sh->s_full[x]);
                     }
-                } else {
-                    int s = stage_of(pos++);
-                    if (!ok) break;
-                    for (int x = 0; x < 2; ++x)
-                        if (u.n[x] > 0) qk(x, x, s);
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (elect_one()) {
                     mma_commit(&sh->empty[s]);
-                    if (u.nt == 1) mma_commit(&sh->q_empty);
-                    for (int i = 0; i < u.nt && ok; ++i) {
-                        const int sv = stage_of(pos++);
-                        int sk = 0;
-                        const bool more = i + 1 < u.nt;
-                        for (int x = 0; x < 2 && ok; ++x) {
-                            if (i < u.n[x]) pv(x, i, sv);
-                            if (x == 0 && more) sk = stage_of(pos++);
-                            if (ok && i + 1 < u.n[x]) qk(x, x, sk);
-                        }
-                        if (!ok) break;
-                        mma_commit(&sh->empty[sv]);
-                        if (more) mma_commit(&sh->empty[sk]);
-                        if (i + 2 == u.nt) mma_commit(&sh->q_empty);
-                    }
+                    if (t + 1 == u.nt) mma_commit(&sh->q_empty);
                 }
+                __syncwarp();
             }
+            pos0 += 2 * u.nt;
+        }
+    } else if (warp == 11) {
+        // ---------------- values
+        const uint32_t idesc = idesc_bf16_f32(TILE_ROWS, HEAD_DIM, true, false);
+        const uint64_t dv0 = sdesc_sw128_mn(smem_u32(ring), AT_PANEL);
+        uint32_t pos0 = 0, pc = 0, it = 0;   // pc: parities of p_full
+        bool ok = true;
+        for (int w; (w = unit_at(it)) < units && ok; ++it) {
+            const Unit u = unit_of(a, w);
+            for (int t = 0; t < u.nt && ok; ++t) {
+                const uint32_t pos = pos0 + v_at(u, t);
+                const int s = pos % AT_STAGES;
+                if (!(ok = at_wait_warp(&sh->full[s], (pos / AT_STAGES) & 1, sh))) break;
+                for (int x = 0; x < 2; ++x) {
+                    if (u.single ? x != (t & 1) : t >= u.n[x]) continue;
+                    if (!(ok = at_wait_warp(&sh->p_full[x], (pc >> x) & 1, sh))) break;
+                    pc ^= 1u << x;
+                    tc_fence_after();
+                    const uint64_t dv = dv0 + (uint32_t)(s * (AT_TILE_BYTES >> 4));
+                    const uint32_t first = t < u.step ? 0u : 1u;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mma_f16_ta(tm + AT_O + 128 * x, tm + AT_P + 64 * x + 8 * k, dv + (uint32_t)(k * (2048 >> 4)), idesc,
+                                       k > 0 ? 1u : first);
+                        mma_commit(&sh->o_done[x]);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (elect_one()) mma_commit(&sh->empty[s]);
+                __syncwarp();
+            }
+            pos0 += 2 * u.nt;
         }
     } else if (warp == 10) {
         // ---------------- partly seen V tiles
         uint32_t pos0 = 0, it = 0, raw_ph = 0;
         bool ok = true;
-        for (int w = blockIdx.x; w < units && ok; w += gridDim.x, ++it) {
+        for (int w; (w = unit_at(it)) < units && ok; ++it) {
             const Unit u = unit_of(a, w);
             const int k_len = a.seq[u.seq].k_len;
             for (int t = max(0, u.jm - u.j0); t < u.nt; ++t) {
@@ -374,9 +362,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
         // ---------------- softmax and outputs: thread = row
         const int x = warp >> 2, row = tid & 127;
         const uint32_t lane_base = (uint32_t)(warp & 3) << 21;      // 32 lanes per warp, lane in bits 16..
-        const uint32_t tS = tm + AT_S + 128 * x + lane_base, tO = tm + AT_O + 128 * x + lane_base;
+        const uint32_t tS = tm + AT_S + lane_base, tP = tm + AT_P + 64 * x + lane_base, tO = tm + AT_O + 128 * x + lane_base;
         const float c = a.c;
-        uint32_t sc = 0, it = 0, jc = 0;   // scores seen (of all units); units; joins
+        uint32_t sc = 0, it = 0, jc = 0, oc = 0;   // score tiles, units, joins, products with V
         bool ok = true;
         // both warpgroups meet (a bounded wait, unlike a named barrier)
         auto join = [&]() -> bool {
@@ -387,7 +375,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
             tc_fence_after();
             return met;
         };
-        for (int w = blockIdx.x; w < units && ok; w += gridDim.x, ++it) {
+        for (int w; (w = unit_at(it)) < units && ok; ++it) {
             const Unit u = unit_of(a, w);
             const PromptSeq& sq = a.seq[u.seq];
             const int tok = u.tok[x] + row / G;
@@ -401,60 +389,80 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
 #pragma unroll
                 for (int h = 0; h < 4; ++h) tmem_ld32(tS + 32 * h, reinterpret_cast<uint32_t*>(s) + 32 * h);
                 tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->s_free);   // the other tile's scores may come
                 const int left = limit - (u.j0 + (u.single ? 2 * i + x : i)) * TILE_ROWS;   // keys of this tile that the row sees
                 if (__any_sync(0xFFFFFFFFu, left < TILE_ROWS)) {
 #pragma unroll
                     for (int k = 0; k < TILE_ROWS; ++k) s[k] = k < left ? s[k] : -INFINITY;
                 }
-                float mx[4] = {s[0], s[1], s[2], s[3]};
+                // One pass over the scores: weights against the reference m, while the maximum is
+                // taken for the check of m; the rare tile whose maximum is too far above goes
+                // through twice.  A unit's first tile takes its maximum first.
+                if (i == 0) {
+                    float mx[4];
 #pragma unroll
-                for (int k = 4; k < TILE_ROWS; ++k) mx[k & 3] = fmaxf(mx[k & 3], s[k]);
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                // (a row without a key so far has m = -inf and moves at its first one)
-                const bool move = (top - m) * c > 8.f;
-                if (__any_sync(0xFFFFFFFFu, move)) {
-                    const float mn = move ? top : m;
-                    const float f = move ? ex2((m - mn) * c) : 1.f;
-                    m = mn;
-                    l *= f;
-                    if (i > 0) {
-                        if (!(ok = at_wait_warp(&sh->o_done[x], (sc - 1) & 1, sh))) break;
-                        tc_fence_after();
+                    for (int k = 0; k < 4; ++k) mx[k] = fmaxf(s[k], s[4 + k]);
 #pragma unroll
-                        for (int h = 0; h < 8; ++h) {
-                            uint32_t o[16];
-                            tmem_ld16(tO + 16 * h, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                            tmem_st16(tO + 16 * h, o);
-                        }
-                    }
+                    for (int k = 8; k < TILE_ROWS; k += 2) mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], s[k], s[k + 1]);
+                    m = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
                 }
-                const float mc = m == -INFINITY ? 0.f : m * c;
-                float ls[4] = {0.f, 0.f, 0.f, 0.f};
+                if (i > 0) {   // P V of the tile before has read P and written O
+                    if (!(ok = at_wait_warp(&sh->o_done[x], oc++ & 1, sh))) break;
+                    tc_fence_after();
+                }
+                uint64_t ls[2];
+                for (;;) {
+                    const float mc = m == -INFINITY ? 0.f : m * c;
+                    const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
+                    float mx[2] = {-INFINITY, -INFINITY};
+                    ls[0] = ls[1] = 0;   // two pairs of partial sums
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t p[16];
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t p[16];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float p0 = ex2(fmaf(s[32 * h + 2 * k], c, -mc)), p1 = ex2(fmaf(s[32 * h + 2 * k + 1], c, -mc));
-                        ls[(2 * k) & 3] += p0;
-                        ls[(2 * k + 1) & 3] += p1;
-                        p[k] = bf16x2(p0, p1);
+                        for (int k = 0; k < 16; ++k) {
+                            const float s0 = s[32 * h + 2 * k], s1 = s[32 * h + 2 * k + 1];
+                            float p0, p1;
+                            unpair(fma2(pair(s0, s1), c2, mc2), p0, p1);
+                            p0 = ex2(p0);
+                            p1 = ex2(p1);
+                            mx[k & 1] = max3(mx[k & 1], s0, s1);
+                            ls[k & 1] = add2(ls[k & 1], pair(p0, p1));
+                            p[k] = bf16x2(p0, p1);
+                        }
+                        tmem_st16(tP + 16 * h, p);
                     }
-                    tmem_st16(tS + 16 * h, p);
+                    // (a row without a key so far has m = -inf and moves at its first one)
+                    const float top = fmaxf(mx[0], mx[1]);
+                    const bool move = (top - m) * c > 8.f;
+                    if (!__any_sync(0xFFFFFFFFu, move)) break;
+                    const float f = move ? ex2((m - top) * c) : 1.f;
+                    if (move) m = top;
+                    l *= f;
+#pragma unroll
+                    for (int h = 0; h < 8; ++h) {
+                        uint32_t o[16];
+                        tmem_ld16(tO + 16 * h, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        tmem_st16(tO + 16 * h, o);
+                    }
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh->p_full[x]);
-                l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                float l0, l1;
+                unpair(add2(ls[0], ls[1]), l0, l1);
+                l += l0 + l1;
                 ++sc;
             }
             if (!ok) break;
             if (u.n[x] > 0) {
-                if (!(ok = at_wait_warp(&sh->o_done[x], (sc - 1) & 1, sh))) break;
+                if (!(ok = at_wait_warp(&sh->o_done[x], oc++ & 1, sh))) break;
                 tc_fence_after();
             }
             // weights of the tile's accumulator(s): single units join A and B here, A's threads

@@ -24,6 +24,14 @@ FQ_DEV void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" 
 // generic-proxy shared-memory writes -> visible to the async proxy (tensor core reads)
 FQ_DEV void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// One lane of the (converged) warp: the one that issues.  Around tcgen05 instructions this keeps
+// their operands in uniform registers, which a test of the lane number does not.
+FQ_DEV bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
 // ---- MMA: D[tmem] (+)= A[smem] x B[smem], kind::f16, one thread issues
 FQ_DEV void mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
