@@ -115,9 +115,19 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 // chunk the keys of the groups so that their CTAs fill the GPU about once
 void plan_groups(Plan& p, uint32_t Hkv, bool partial) {
-    int64_t keys = 0;
-    for (auto& g : p.groups) keys += g.k_len;
-    const int64_t per = std::max(ROWS_CHUNK, (keys * Hkv + ROWS_CTAS - 1) / ROWS_CTAS);
+    auto ctas = [&](int64_t per) {
+        int64_t n = 0;
+        for (auto& g : p.groups) n += std::max(1, ceil_div(g.k_len, per));
+        return n * Hkv;
+    };
+    int64_t keys = 0, longest = 0;
+    for (auto& g : p.groups) {
+        keys += g.k_len;
+        longest = std::max<int64_t>(longest, g.k_len);
+    }
+    // the shortest chunks that still give one wave of CTAs
+    int64_t per = std::max(ROWS_CHUNK, (keys * Hkv + ROWS_CTAS - 1) / ROWS_CTAS / 64 * 64);
+    while (per < longest && ctas(per) > ROWS_CTAS) per += std::max<int64_t>(64, per / 32 / 64 * 64);
     for (auto& g : p.groups) {
         const int splits = std::max(1, ceil_div(g.k_len, per));
         g.chunk = std::max(64, ceil_div(ceil_div(g.k_len, splits), 64) * 64);
@@ -302,7 +312,7 @@ fq_status run_tiles(const Plan& p, const AttnIo& io, const Partials& part, const
         if (!encode_bf16_tiles(a->map_q, io.q, 4, dims, strides, box)) return fail(FQ_ERR_CUDA, "tensor map of q refused");
         for (int v = 0; v < n_views; ++v)
             if (used[v]) TRY(encode_rows(a->map_k[v], a->map_v[v], views[v], used[v], io.Hkv));
-        constexpr size_t NE = sizeof a->e / sizeof a->e[0];
+        constexpr size_t NE = Args::ENTRIES;
         for (size_t e0 = 0; e0 < p.tiles.size(); e0 += NE) {
             a->n_entries = (int)std::min(NE, p.tiles.size() - e0);
             std::copy(p.tiles.begin() + e0, p.tiles.begin() + e0 + a->n_entries, a->e);
@@ -314,6 +324,12 @@ fq_status run_tiles(const Plan& p, const AttnIo& io, const Partials& part, const
     const fq_status st = run();
     delete a;
     return st;
+}
+
+fq_status run_one_view(const Plan& p, const AttnIo& io, const Partials& part, const PromptSeq* seq, int n_seq, int q_rows,
+                       const KvRows* view, const uint64_t* used, cudaStream_t s) {
+    return p.tiles.size() <= (size_t)TileArgsS::ENTRIES ? run_tiles<TileArgsS>(p, io, part, seq, n_seq, q_rows, view, 1, used, s)
+                                                        : run_tiles<TileArgs1>(p, io, part, seq, n_seq, q_rows, view, 1, used, s);
 }
 
 fq_status run_groups(const Plan& p, const AttnIo& io, const Partials& part, const KvRows* views, const KvRows* prefix,
@@ -329,14 +345,14 @@ fq_status run_groups(const Plan& p, const AttnIo& io, const Partials& part, cons
         a.g[g] = p.groups[g];
         a.kv[g] = p.group_view[g] < 0 ? *prefix : views[p.group_view[g]];
     }
-    launch_attn_rows(a, s);
+    launch_attn_rows(a, !p.tiles.empty(), s);
     CK(cudaGetLastError());
     return FQ_OK;
 }
 
-fq_status run_join(const Plan& p, const AttnIo& io, const Partials& part, cudaStream_t s) {
-    if (p.join.empty()) return FQ_OK;
-    JoinArgs a;
+template <class Args>
+fq_status run_join_t(const Plan& p, const AttnIo& io, const Partials& part, cudaStream_t s) {
+    Args a;
     a.io = io;
     a.part = part;
     a.n_entries = (int)p.join.size();
@@ -348,6 +364,11 @@ fq_status run_join(const Plan& p, const AttnIo& io, const Partials& part, cudaSt
     launch_attn_join(a, s);
     CK(cudaGetLastError());
     return FQ_OK;
+}
+
+fq_status run_join(const Plan& p, const AttnIo& io, const Partials& part, cudaStream_t s) {
+    if (p.join.empty()) return FQ_OK;
+    return p.join.size() <= (size_t)JoinArgsS::ENTRIES ? run_join_t<JoinArgsS>(p, io, part, s) : run_join_t<JoinArgsL>(p, io, part, s);
 }
 
 // the checks that both attentions share, and the common part of their arguments
@@ -363,8 +384,8 @@ fq_status attn_common(const void* q, uint64_t q_stride, uint32_t Hq, uint32_t Hk
     if (q_rows) {
         if (!q || !out) return fail(FQ_ERR_INVALID_ARGUMENT, "null q or out");
         if (!aligned16(q) || !aligned16(out)) return fail(FQ_ERR_INVALID_ARGUMENT, "q or out not 16-byte aligned");
-        if (need > ws_bytes || (need && (!ws || !aligned16(ws))))
-            return fail(FQ_ERR_INVALID_ARGUMENT, "workspace of %zu bytes, 16-byte aligned, needed (%zu given)", need, ws_bytes);
+        if (need > ws_bytes || (need && (!ws || (reinterpret_cast<uintptr_t>(ws) & 31))))
+            return fail(FQ_ERR_INVALID_ARGUMENT, "workspace of %zu bytes, 32-byte aligned, needed (%zu given)", need, ws_bytes);
     }
     io.q = (const uint16_t*)q;
     io.out = out;
@@ -496,7 +517,7 @@ fq_status fq_attn_prompt(const void* q, uint64_t q_stride, const fq_kv_view* vie
         const Partials part = p.at(workspace, Hkv);
         cudaStream_t s = (cudaStream_t)stream;
         if (!p.tiles.empty())
-            TRY(n_views == 1 ? run_tiles<TileArgs1>(p, io, part, seq, (int)n_seq, (int)q_rows, kv, 1, used, s)
+            TRY(n_views == 1 ? run_one_view(p, io, part, seq, (int)n_seq, (int)q_rows, kv, used, s)
                              : run_tiles<TileArgsN>(p, io, part, seq, (int)n_seq, (int)q_rows, kv, (int)n_views, used, s));
         TRY(run_groups(p, io, part, kv, nullptr, s));
         return run_join(p, io, part, s);
@@ -554,7 +575,7 @@ fq_status fq_attn_shared(const void* q, uint64_t q_stride, uint32_t n_seq, const
         if (!p.tiles.empty()) {
             const PromptSeq all{0, (int32_t)n_seq, 0, (int32_t)prefix_len, SEES_ALL};
             const uint64_t used = prefix_len;
-            TRY(run_tiles<TileArgs1>(p, io, part, &all, 1, (int)n_seq, &first, 1, &used, s));
+            TRY(run_one_view(p, io, part, &all, 1, (int)n_seq, &first, &used, s));
         }
         TRY(run_groups(p, io, part, kv, &first, s));
         return run_join(p, io, part, s);

@@ -58,6 +58,7 @@ constexpr int MAX_GROUPS = MAX_SEQ + 1;
 
 template <int NV, int NE>
 struct TileArgs {
+    static constexpr int VIEWS = NV, ENTRIES = NE;
     alignas(64) unsigned long long map_q[16];
     alignas(64) unsigned long long map_k[NV][16], map_v[NV][16];
     AttnIo io;
@@ -68,12 +69,14 @@ struct TileArgs {
     PromptSeq seq[MAX_SEQ];
     TileEntry e[NE];
 };
-// every sequence over one view, or a view per sequence
+// Every sequence over one view, or a view per sequence.  The parameters of a launch travel with
+// it, so the common short list has a type of its own.
+using TileArgsS = TileArgs<1, 64>;
 using TileArgs1 = TileArgs<1, 1536>;
 using TileArgsN = TileArgs<MAX_SEQ, 768>;
 static_assert(sizeof(TileArgs1) <= 32764 && sizeof(TileArgsN) <= 32764, "kernel parameters");
-void launch_tiles(const TileArgs1& a, cudaStream_t s);
-void launch_tiles(const TileArgsN& a, cudaStream_t s);
+template <class Args>
+void launch_tiles(const Args& a, cudaStream_t s);
 cudaError_t attn_tiles_prepare();     // per device, before the first launch
 cudaError_t attn_wait_record(uint32_t* host, cudaStream_t s);
 
@@ -85,15 +88,22 @@ struct RowsArgs {
     RowGroup g[MAX_GROUPS];
     KvRows kv[MAX_GROUPS];
 };
-void launch_attn_rows(const RowsArgs& a, cudaStream_t s);
+// dependent: behind launch_tiles of the same call, whose CTAs it may run beside
+void launch_attn_rows(const RowsArgs& a, bool dependent, cudaStream_t s);
 
+template <int NE>
 struct JoinArgs {
+    static constexpr int ENTRIES = NE;
     AttnIo io;
     int n_entries, max_tok;
     Partials part;
-    JoinEntry e[MAX_JOIN];
+    JoinEntry e[NE];
 };
-static_assert(sizeof(JoinArgs) <= 32764, "kernel parameters");
-void launch_attn_join(const JoinArgs& a, cudaStream_t s);
+using JoinArgsS = JoinArgs<64>;
+using JoinArgsL = JoinArgs<MAX_JOIN>;
+static_assert(sizeof(JoinArgsL) <= 32764, "kernel parameters");
+// behind launch_tiles or launch_attn_rows of the same call
+template <class Args>
+void launch_attn_join(const Args& a, cudaStream_t s);
 
 }  // namespace fq

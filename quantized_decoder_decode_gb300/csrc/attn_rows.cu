@@ -44,6 +44,7 @@ FQ_DEV uint32_t finite_pair(uint32_t w) {
 __global__ void __launch_bounds__(AR_THREADS, 3) attn_rows_kernel(const __grid_constant__ RowsArgs a) {
     __shared__ float so[AR_WARPS][ROWS_MAX][AR_OPAD];
     __shared__ float2 sml[AR_WARPS][ROWS_MAX];
+    pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int Hkv = a.io.Hkv, G = a.io.Hq / Hkv;
     const int item = blockIdx.x / Hkv, head = blockIdx.x % Hkv;
@@ -247,18 +248,23 @@ __global__ void __launch_bounds__(AR_THREADS, 3) attn_rows_kernel(const __grid_c
             else reinterpret_cast<uint2*>((uint16_t*)a.io.out + at)[lane] = make_uint2(bf16x2(y.x, y.y), bf16x2(y.z, y.w));
         }
     }
+    pdl_wait();   // this grid ends after the one it may run beside, so what waits for it waits for both
 }
 
 // out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i over the partial results of a (token, head);
 // one warp each.  Up to 32 of them have their weights made by one lane each.
 constexpr int AJ_WARPS = 8;
 
-__global__ void __launch_bounds__(AJ_WARPS * 32) attn_join_kernel(const __grid_constant__ JoinArgs a) {
+template <class Args>
+__global__ void __launch_bounds__(AJ_WARPS * 32) attn_join_kernel(const __grid_constant__ Args a) {
     const int lane = threadIdx.x & 31;
-    const JoinEntry& e = a.e[blockIdx.x];
+    const JoinEntry e = a.e[blockIdx.x];
     const int Hq = a.io.Hq, Hkv = a.io.Hkv, G = Hq / Hkv;
     const int idx = blockIdx.y * AJ_WARPS + (threadIdx.x >> 5);
-    if (idx >= e.n_tok * Hq) return;
+    if (idx >= e.n_tok * Hq) {
+        pdl_wait();
+        return;
+    }
     const int t = idx / Hq, h = idx % Hq, kh = h / G, gh = h % G;
     const int n = e.nA + e.nB + e.nC;
     auto where = [&](int i, const float*& o) -> const float2* {
@@ -273,6 +279,7 @@ __global__ void __launch_bounds__(AJ_WARPS * 32) attn_join_kernel(const __grid_c
         o = a.part.b_o + b * HEAD_DIM;
         return a.part.b_ml + b;
     };
+    pdl_wait();   // the partial results are written
     float M = -INFINITY;
     for (int i = lane; i < n; i += 32) {
         const float* o;
@@ -290,13 +297,13 @@ __global__ void __launch_bounds__(AJ_WARPS * 32) attn_join_kernel(const __grid_c
             lw = w * ml.y;   // (a NaN sum stays one)
         }
         L += warp_sum(lw);
-#pragma unroll 4
+#pragma unroll 8
         for (int i = 0; i < min(32, n - i0); ++i) {
             const float f = __shfl_sync(0xFFFFFFFFu, w, i);
-            if (f == 0.f) continue;
             const float* o;
             where(i0 + i, o);
-            const float4 v = reinterpret_cast<const float4*>(o)[lane];
+            // (a weight of 0 drops what may not be finite)
+            const float4 v = f == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : reinterpret_cast<const float4*>(o)[lane];
             y.x = fmaf(v.x, f, y.x);
             y.y = fmaf(v.y, f, y.y);
             y.z = fmaf(v.z, f, y.z);
@@ -317,13 +324,32 @@ __global__ void __launch_bounds__(AJ_WARPS * 32) attn_join_kernel(const __grid_c
 
 }  // namespace
 
-void launch_attn_rows(const RowsArgs& a, cudaStream_t s) {
-    attn_rows_kernel<<<(unsigned)((int64_t)a.n_items * a.io.Hkv), AR_THREADS, 0, s>>>(a);
+static cudaLaunchConfig_t config(dim3 grid, int threads, bool dependent, cudaLaunchAttribute* attr, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = dependent ? 1 : 0;
+    return cfg;
 }
 
-void launch_attn_join(const JoinArgs& a, cudaStream_t s) {
-    const int y = (a.max_tok * a.io.Hq + AJ_WARPS - 1) / AJ_WARPS;
-    attn_join_kernel<<<dim3((unsigned)a.n_entries, (unsigned)y), AJ_WARPS * 32, 0, s>>>(a);
+void launch_attn_rows(const RowsArgs& a, bool dependent, cudaStream_t s) {
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = config(dim3((unsigned)((int64_t)a.n_items * a.io.Hkv)), AR_THREADS, dependent, attr, s);
+    cudaLaunchKernelEx(&cfg, attn_rows_kernel, a);
 }
+
+template <class Args>
+void launch_attn_join(const Args& a, cudaStream_t s) {
+    cudaLaunchAttribute attr[1];
+    const unsigned y = (unsigned)((a.max_tok * a.io.Hq + AJ_WARPS - 1) / AJ_WARPS);
+    const cudaLaunchConfig_t cfg = config(dim3((unsigned)a.n_entries, y), AJ_WARPS * 32, true, attr, s);
+    cudaLaunchKernelEx(&cfg, attn_join_kernel<Args>, a);
+}
+template void launch_attn_join<JoinArgsS>(const JoinArgsS&, cudaStream_t);
+template void launch_attn_join<JoinArgsL>(const JoinArgsL&, cudaStream_t);
 
 }  // namespace fq

@@ -128,12 +128,38 @@ FQ_DEV bool at_wait(uint64_t* bar, uint32_t parity, AtShared* sh) {
 FQ_DEV bool at_wait_warp(uint64_t* bar, uint32_t parity, AtShared* sh) {
     return __all_sync(0xFFFFFFFFu, at_wait(bar, parity, sh));
 }
+constexpr long long DRAIN_CYCLES = 1 << 20;   // half a millisecond
+FQ_DEV uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+// 32 bytes to a 32-byte aligned address
+FQ_DEV void st_global32(void* p, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+// N words (a multiple of 8) to a 16-byte aligned address, 32 bytes at a time where that is aligned
+template <int N>
+FQ_DEV void st_row(void* p, const uint32_t* v, bool wide) {
+#pragma unroll
+    for (int k = 0; k < N; k += 8) {
+        uint32_t* d = (uint32_t*)p + k;
+        if (wide) {
+            st_global32(d, v + k);
+        } else {
+            reinterpret_cast<uint4*>(d)[0] = make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+            reinterpret_cast<uint4*>(d)[1] = make_uint4(v[k + 4], v[k + 5], v[k + 6], v[k + 7]);
+        }
+    }
+}
 template <int N>
 FQ_DEV void set_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 FQ_DEV void set_regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-template <class Args, int NV>
+template <class Args>
 __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_constant__ Args a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* q_sm = smem;
@@ -142,6 +168,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int units = a.n_entries * a.io.Hkv;
     const int G = a.io.Hq / a.io.Hkv;
+    // the first unit, worked out while the barriers and tensor memory are set up: its entry is a
+    // chain of reads of kernel parameters that no cache holds yet
+    const Unit u0 = unit_of(a, blockIdx.x);
+    pdl_trigger();   // the kernels behind this one in the call may start beside it
 
     if (tid == 0) {
         mbar_init(&sh->q_full, 1);
@@ -179,54 +209,53 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
     set_regs_down<72>();
     if (broken) {
     } else if (warp == 9) {
-        if (lane == 0) {
-            // ---------------- loads
-            uint64_t* last[AT_STAGES];     // where each stage's last load arrives, and its parity
-            uint32_t last_par = 0, used = 0;
-            uint32_t pos = 0, qn = 0, it = 0, raw_ph = 0;
-            bool ok = true;
-            for (int w; (w = unit_at(it)) < units && ok; ++it) {
-                const Unit u = unit_of(a, w);
-                const PromptSeq& sq = a.seq[u.seq];
-                if (it >= 2 && !(ok = at_wait(&sh->item_done, it & 1, sh))) break;   // unit it - 2 finished
-                if (u.nt == 0) continue;
-                if (!(ok = at_wait(&sh->q_empty, (qn & 1) ^ 1, sh))) break;
-                const int n_q = (u.single || u.n[1] == 0) ? 1 : 2, q0 = u.n[0] > 0 ? 0 : 1;
+        // ---------------- loads
+        uint32_t pos = 0, qn = 0, it = 0;
+        bool ok = true;
+        for (int w; (w = unit_at(it)) < units && ok; ++it) {
+            const Unit u = it == 0 ? u0 : unit_of(a, w);
+            const PromptSeq& sq = a.seq[u.seq];
+            if (it >= 2 && !(ok = at_wait_warp(&sh->item_done, it & 1, sh))) break;   // unit it - 2 finished
+            if (u.nt == 0) continue;
+            if (!(ok = at_wait_warp(&sh->q_empty, (qn & 1) ^ 1, sh))) break;
+            ++qn;
+            const int n_q = (u.single || u.n[1] == 0) ? 1 : 2, q0 = u.n[0] > 0 ? 0 : 1;
+            if (elect_one()) {
                 mbar_arrive_expect_tx(&sh->q_full, (uint32_t)((n_q - q0) * AT_TILE_BYTES));
-                for (int x = q0; x < n_q; ++x)
-                    for (int h = 0; h < 2; ++h)
-                        tma_load_4d(q_sm + x * AT_TILE_BYTES + h * AT_PANEL, a.map_q, 64 * h, 0, u.head, sq.q_row0 + u.tok[x],
-                                    &sh->q_full);
-                ++qn;
-                const int vw = NV == 1 ? 0 : u.seq;
-                auto load = [&](bool v, int t) {
-                    const int s = pos % AT_STAGES;
-                    if (!(ok = at_wait(&sh->empty[s], ((pos / AT_STAGES) & 1) ^ 1, sh))) return;
-                    const bool look = v && u.j0 + t >= u.jm;
-                    uint64_t* bar = look ? &sh->raw[s] : &sh->full[s];
-                    mbar_arrive_expect_tx(bar, AT_TILE_BYTES);
-                    uint8_t* dst = ring + s * AT_TILE_BYTES;
-                    const int row = sq.k_row0 + (u.j0 + t) * TILE_ROWS;
-                    const void* map = v ? a.map_v[vw] : a.map_k[vw];
-                    tma_load_3d(dst, map, 0, row, u.head, bar);
-                    tma_load_3d(dst + AT_PANEL, map, 64, row, u.head, bar);
-                    const uint32_t par = look ? (raw_ph >> s) & 1 : (pos / AT_STAGES) & 1;
-                    if (look) raw_ph ^= 1u << s;
-                    last[s] = bar;
-                    last_par = (last_par & ~(1u << s)) | par << s;
-                    used |= 1u << s;
-                    ++pos;
-                };
-                for (int t = 0; t < u.step && t < u.nt && ok; ++t) load(false, t);
-                for (int t = 0; t < u.nt && ok; ++t) {
-                    if (t + u.step < u.nt) load(false, t + u.step);
-                    if (ok) load(true, t);
+                for (int x = q0; x < n_q; ++x) {
+                    const int row = sq.q_row0 + u.tok[x];
+                    tma_load_4d(q_sm + x * AT_TILE_BYTES, a.map_q, 0, 0, u.head, row, &sh->q_full);
+                    tma_load_4d(q_sm + x * AT_TILE_BYTES + AT_PANEL, a.map_q, 64, 0, u.head, row, &sh->q_full);
                 }
             }
-            if (!ok) {   // no copy may still be landing when the CTA exits
-                for (int s = 0; s < AT_STAGES; ++s)
-                    if (used >> s & 1) mbar_wait(last[s], last_par >> s & 1);
-                if (qn) mbar_wait(&sh->q_full, (qn - 1) & 1);
+            __syncwarp();
+            const int vw = Args::VIEWS == 1 ? 0 : u.seq;
+            auto load = [&](bool v, int t) {
+                const int s = pos % AT_STAGES;
+                if (!(ok = at_wait_warp(&sh->empty[s], ((pos / AT_STAGES) & 1) ^ 1, sh))) return;
+                ++pos;
+                uint64_t* bar = v && u.j0 + t >= u.jm ? &sh->raw[s] : &sh->full[s];
+                const void* map = v ? a.map_v[vw] : a.map_k[vw];
+                uint8_t* dst = ring + s * AT_TILE_BYTES;
+                const int row = sq.k_row0 + (u.j0 + t) * TILE_ROWS;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(bar, AT_TILE_BYTES);
+                    tma_load_3d(dst, map, 0, row, u.head, bar);
+                    tma_load_3d(dst + AT_PANEL, map, 64, row, u.head, bar);
+                }
+                __syncwarp();
+            };
+            for (int t = 0; t < u.step && t < u.nt && ok; ++t) load(false, t);
+            for (int t = 0; t < u.nt && ok; ++t) {
+                if (t + u.step < u.nt) load(false, t + u.step);
+                if (ok) load(true, t);
+            }
+        }
+        if (!ok) {
+            // No copy may still be landing when the CTA exits.  A role gave up after a quarter
+            // second of waiting; copies that were issued land within microseconds of that.
+            const long long t0 = clock64();
+            while (clock64() - t0 < DRAIN_CYCLES) {
             }
         }
     } else if (warp == 8) {
@@ -236,7 +265,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
         uint32_t pos0 = 0, qn = 0, sn = 0, it = 0;   // sn: score tiles
         bool ok = true;
         for (int w; (w = unit_at(it)) < units && ok; ++it) {
-            const Unit u = unit_of(a, w);
+            const Unit u = it == 0 ? u0 : unit_of(a, w);
             if (u.nt == 0) continue;
             if (!(ok = at_wait_warp(&sh->q_full, qn++ & 1, sh))) break;
             for (int t = 0; t < u.nt && ok; ++t) {
@@ -276,7 +305,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
         uint32_t pos0 = 0, pc = 0, it = 0;   // pc: parities of p_full
         bool ok = true;
         for (int w; (w = unit_at(it)) < units && ok; ++it) {
-            const Unit u = unit_of(a, w);
+            const Unit u = it == 0 ? u0 : unit_of(a, w);
             for (int t = 0; t < u.nt && ok; ++t) {
                 const uint32_t pos = pos0 + v_at(u, t);
                 const int s = pos % AT_STAGES;
@@ -308,22 +337,30 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
         uint32_t pos0 = 0, it = 0, raw_ph = 0;
         bool ok = true;
         for (int w; (w = unit_at(it)) < units && ok; ++it) {
-            const Unit u = unit_of(a, w);
+            const Unit u = it == 0 ? u0 : unit_of(a, w);
             const int k_len = a.seq[u.seq].k_len;
             for (int t = max(0, u.jm - u.j0); t < u.nt; ++t) {
                 const int s = (pos0 + v_at(u, t)) % AT_STAGES;
                 if (!(ok = at_wait_warp(&sh->raw[s], (raw_ph >> s) & 1, sh))) break;
                 raw_ph ^= 1u << s;
                 uint8_t* tile = ring + s * AT_TILE_BYTES;
-                // largest magnitude, NaN kept: bf16 bits without the sign order like integers
-                uint32_t hi = 0, lo = 0;
-#pragma unroll 8
-                for (int i = lane; i < AT_TILE_BYTES / 16; i += 32) {
-                    const uint4 v = reinterpret_cast<const uint4*>(tile)[i];
-                    hi = max(hi, max(max(v.x & 0x7FFF0000u, v.y & 0x7FFF0000u), max(v.z & 0x7FFF0000u, v.w & 0x7FFF0000u)));
-                    lo = max(lo, max(max(v.x & 0x7FFFu, v.y & 0x7FFFu), max(v.z & 0x7FFFu, v.w & 0x7FFFu)));
+                // x * 0 is NaN where x is not finite (rows before `from` are seen by every row)
+                const int from = max(0, min(k_len, u.tok[0] + a.seq[u.seq].off) - (u.j0 + t) * TILE_ROWS);
+                uint32_t z[4] = {0, 0, 0, 0};
+                for (int i = from * 8 + lane; i < TILE_ROWS * 8; i += 32) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 v = reinterpret_cast<const uint4*>(tile + h * AT_PANEL)[i];
+                        z[0] = fma_bf16x2(v.x, 0u, z[0]);
+                        z[1] = fma_bf16x2(v.y, 0u, z[1]);
+                        z[2] = fma_bf16x2(v.z, 0u, z[2]);
+                        z[3] = fma_bf16x2(v.w, 0u, z[3]);
+                    }
                 }
-                if (__any_sync(0xFFFFFFFFu, hi >= 0x7F800000u || lo >= 0x7F80u)) {
+                bool odd = false;
+#pragma unroll
+                for (int h = 0; h < 4; ++h) odd |= (z[h] & 0x7FFFu) != 0 || (z[h] & 0x7FFF0000u) != 0;
+                if (__any_sync(0xFFFFFFFFu, odd)) {
                     const int buf = it & 1;
                     uint16_t(*note)[HEAD_DIM] = sh->poison[buf];
                     if (sh->poison_unit[buf] != it + 1) {
@@ -332,7 +369,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
                     }
                     // lane l owns columns 4l .. 4l+3: 8 bytes of every row
                     uint8_t* col = tile + (lane >> 4) * AT_PANEL;
-                    for (int r = 0; r < TILE_ROWS; ++r) {
+                    for (int r = from; r < TILE_ROWS; ++r) {
                         uint16_t* p = reinterpret_cast<uint16_t*>(col + sw128_offset(r, (lane & 15) >> 1) + (lane & 1) * 8);
                         const int key = (u.j0 + t) * TILE_ROWS + r;
                         for (int c = 0; c < 4; ++c) {
@@ -364,6 +401,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
         const uint32_t lane_base = (uint32_t)(warp & 3) << 21;      // 32 lanes per warp, lane in bits 16..
         const uint32_t tS = tm + AT_S + lane_base, tP = tm + AT_P + 64 * x + lane_base, tO = tm + AT_O + 128 * x + lane_base;
         const float c = a.c;
+        const bool wide = ((reinterpret_cast<uintptr_t>(a.io.out) | (uintptr_t)(a.io.out_stride * (a.io.out_f32 ? 4 : 2))) & 31) == 0;
         uint32_t sc = 0, it = 0, jc = 0, oc = 0;   // score tiles, units, joins, products with V
         bool ok = true;
         // both warpgroups meet (a bounded wait, unlike a named barrier)
@@ -376,7 +414,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
             return met;
         };
         for (int w; (w = unit_at(it)) < units && ok; ++it) {
-            const Unit u = unit_of(a, w);
+            const Unit u = it == 0 ? u0 : unit_of(a, w);
             const PromptSeq& sq = a.seq[u.seq];
             const int tok = u.tok[x] + row / G;
             const bool valid = row / G < u.n_tok[x];
@@ -484,65 +522,61 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
             }
             const bool noted = *(volatile uint32_t*)&sh->poison_unit[it & 1] == it + 1;
             const int seen = limit - u.jm * TILE_ROWS;   // noted keys below this are the row's
-            const int d0 = u.single ? 64 * x : 0, dn = u.single ? 64 : HEAD_DIM;
-            const uint32_t tA = tm + AT_O + lane_base + (u.single ? 0 : 128 * x);
-            const float inv = u.slot ? 1.f : (limit > 0 ? 1.f / lsum : 0.f);
+            const float inv = u.slot || limit == 0 ? 1.f : 1.f / lsum;
             const int64_t o_row = (int64_t)(sq.q_row0 + tok);
             const int64_t o_col = (int64_t)(u.head * G + row % G) * HEAD_DIM;
             const int64_t blk = ((int64_t)(u.slot - 1 + (u.single ? 0 : x)) * a.io.Hkv + u.head) * TILE_ROWS + row;
             const bool have = u.single ? u.nt > 0 : u.n[x] > 0;
-            for (int d = d0; d < d0 + dn; d += 16) {
-                uint32_t o[16];
-                __syncwarp();
-                if (have) {
-                    tmem_ld16(tA + d, o);
-                    tmem_wait_ld();
-                } else {
+            float o[TILE_ROWS];   // pair: the row's 128 dims; single: 64 dims of O_A, then of O_B
+            __syncwarp();
+            if (have) {
+                const uint32_t t0 = tm + AT_O + lane_base + (u.single ? 64 * x : 128 * x);
+                const uint32_t t1 = t0 + (u.single ? 128 : 64);
+                tmem_ld32(t0, reinterpret_cast<uint32_t*>(o));
+                tmem_ld32(t0 + 32, reinterpret_cast<uint32_t*>(o) + 32);
+                tmem_ld32(t1, reinterpret_cast<uint32_t*>(o) + 64);
+                tmem_ld32(t1 + 32, reinterpret_cast<uint32_t*>(o) + 96);
+                tmem_wait_ld();
+            } else {
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) o[k] = 0;
-                }
-                float y[16];
+                for (int k = 0; k < TILE_ROWS; ++k) o[k] = 0.f;
+            }
+            if (u.single) {
+                f0 *= inv;
+                f1 *= inv;
 #pragma unroll
-                for (int k = 0; k < 16; ++k) y[k] = __uint_as_float(o[k]);
-                if (u.single) {
+                for (int k = 0; k < 64; ++k) o[k] = u.nt > 1 ? fmaf(o[64 + k], f1, o[k] * f0) : o[k] * f0;
+            } else {
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) y[k] *= f0;
-                    if (u.nt > 1) {
-                        tmem_ld16(tA + 128 + d, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) y[k] = fmaf(__uint_as_float(o[k]), f1, y[k]);
-                    }
-                }
+                for (int k = 0; k < TILE_ROWS; ++k) o[k] *= inv;
+            }
+            auto store = [&](float* y, int d) {   // 32 dims from d
                 if (noted) {
-                    for (int k = 0; k < 16; ++k) {
-                        const bool pos_inf = sh->poison[it & 1][0][d + k] < seen, neg_inf = sh->poison[it & 1][1][d + k] < seen;
-                        if (sh->poison[it & 1][2][d + k] < seen) y[k] = NAN;
-                        if (pos_inf) y[k] += INFINITY;
-                        if (neg_inf) y[k] -= INFINITY;
-                    }
-                }
-                if (limit > 0) {
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) y[k] *= inv;
-                }
-                if (valid) {
-                    if (u.slot) {
-                        float4* dst = reinterpret_cast<float4*>(a.part.a_o + blk * HEAD_DIM + d);
-    #pragma unroll
-                        for (int k = 0; k < 4; ++k) dst[k] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-                    } else if (a.io.out_f32) {
-                        float4* dst = reinterpret_cast<float4*>((float*)a.io.out + o_row * a.io.out_stride + o_col + d);
-    #pragma unroll
-                        for (int k = 0; k < 4; ++k) dst[k] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-                    } else {
-                        uint4* dst = reinterpret_cast<uint4*>((uint16_t*)a.io.out + o_row * a.io.out_stride + o_col + d);
-    #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            dst[k] = make_uint4(bf16x2(y[8 * k], y[8 * k + 1]), bf16x2(y[8 * k + 2], y[8 * k + 3]),
-                                                bf16x2(y[8 * k + 4], y[8 * k + 5]), bf16x2(y[8 * k + 6], y[8 * k + 7]));
+                    for (int k = 0; k < 32; ++k) {
+                        if (sh->poison[it & 1][2][d + k] < seen) y[k] = NAN;
+                        if (sh->poison[it & 1][0][d + k] < seen) y[k] += INFINITY;
+                        if (sh->poison[it & 1][1][d + k] < seen) y[k] -= INFINITY;
                     }
                 }
+                if (!valid) return;
+                if (u.slot) {
+                    st_row<32>(a.part.a_o + blk * HEAD_DIM + d, reinterpret_cast<uint32_t*>(y), true);
+                } else if (a.io.out_f32) {
+                    st_row<32>((float*)a.io.out + o_row * a.io.out_stride + o_col + d, reinterpret_cast<uint32_t*>(y), wide);
+                } else {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) p[k] = bf16x2(y[2 * k], y[2 * k + 1]);
+                    st_row<16>((uint16_t*)a.io.out + o_row * a.io.out_stride + o_col + d, p, wide);
+                }
+            };
+            if (u.single) {
+                store(o, 64 * x);
+                store(o + 32, 64 * x + 32);
+            } else {
+#pragma unroll
+                for (int h = 0; h < 4; ++h) store(o + 32 * h, 32 * h);
             }
             if (u.slot && valid && (!u.single || x == 0)) a.part.a_ml[blk] = make_float2(mref * c, lsum);
             // the next unit's products may overwrite O once both warpgroups have read it
@@ -561,30 +595,32 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
 
 constexpr int AT_REGS = 168;   // what the register split above draws on
 
-template <class Args, int NV>
+template <class Args>
 cudaError_t prepare_t() {
     cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, attn_tiles_kernel<Args, NV>);
+    cudaError_t e = cudaFuncGetAttributes(&fa, attn_tiles_kernel<Args>);
     if (e != cudaSuccess) return e;
     if (fa.numRegs != AT_REGS) return cudaErrorInvalidKernelImage;   // the split would wait for registers that are not there
-    return cudaFuncSetAttribute(attn_tiles_kernel<Args, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_SMEM);
-}
-
-template <class Args, int NV>
-void launch_t(const Args& a, cudaStream_t s) {
-    const int64_t units = (int64_t)a.n_entries * a.io.Hkv;
-    const int grid = (int)(units < ATTN_SMS ? units : ATTN_SMS);
-    attn_tiles_kernel<Args, NV><<<grid, AT_THREADS, AT_SMEM, s>>>(a);
+    return cudaFuncSetAttribute(attn_tiles_kernel<Args>, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_SMEM);
 }
 
 }  // namespace
 
 cudaError_t attn_tiles_prepare() {
-    const cudaError_t e = prepare_t<TileArgs1, 1>();
-    return e != cudaSuccess ? e : prepare_t<TileArgsN, MAX_SEQ>();
+    cudaError_t e = prepare_t<TileArgsS>();
+    if (e == cudaSuccess) e = prepare_t<TileArgs1>();
+    return e != cudaSuccess ? e : prepare_t<TileArgsN>();
 }
-void launch_tiles(const TileArgs1& a, cudaStream_t s) { launch_t<TileArgs1, 1>(a, s); }
-void launch_tiles(const TileArgsN& a, cudaStream_t s) { launch_t<TileArgsN, MAX_SEQ>(a, s); }
+
+template <class Args>
+void launch_tiles(const Args& a, cudaStream_t s) {
+    const int64_t units = (int64_t)a.n_entries * a.io.Hkv;
+    const int grid = (int)(units < ATTN_SMS ? units : ATTN_SMS);
+    attn_tiles_kernel<Args><<<grid, AT_THREADS, AT_SMEM, s>>>(a);
+}
+template void launch_tiles<TileArgsS>(const TileArgsS&, cudaStream_t);
+template void launch_tiles<TileArgs1>(const TileArgs1&, cudaStream_t);
+template void launch_tiles<TileArgsN>(const TileArgsN&, cudaStream_t);
 
 // Waits that gave up on the current device, read (and cleared) after the work queued on s.
 cudaError_t attn_wait_record(uint32_t* host, cudaStream_t s) {

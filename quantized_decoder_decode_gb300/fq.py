@@ -352,27 +352,39 @@ def fq_layer_step_noalloc(model: int, layer: int, kv: int, pos: int, x_ptr: int,
 
 # ---------------------------------------------------------------- prompt and shared-prompt attention
 
+_U32Array = {}   # array types by length
+
+
 def u32_array(values):
     """A host array of lengths or rows as the calls below take it; a program that calls again
     with the same lengths keeps it."""
     if isinstance(values, ctypes.Array) and values._type_ is ctypes.c_uint32:
         return values
-    return (ctypes.c_uint32 * len(values))(*[int(v) for v in values])
+    n = len(values)
+    t = _U32Array.get(n)
+    if t is None:
+        t = _U32Array[n] = ctypes.c_uint32 * n
+    return t(*[int(v) for v in values])
 
 
 def kv_view_array(views):
-    """One view or a sequence of views as a host array of ``fq_kv_view``."""
-    if isinstance(views, fq_kv_view):
-        return (fq_kv_view * 1)(views)
+    """A sequence of views as a host array of ``fq_kv_view``."""
     if isinstance(views, ctypes.Array) and views._type_ is fq_kv_view:
         return views
     return (fq_kv_view * len(views))(*views)
 
 
-def _same_length(n: int, **arrays) -> None:
-    for name, a in arrays.items():
-        if a is not None and len(a) != n:
-            raise ValueError(f"{name} has {len(a)} entries for {n} sequences")
+def _views(views):
+    """(argument, count) of one view or several."""
+    if type(views) is fq_kv_view:
+        return ctypes.byref(views), 1
+    w = kv_view_array(views)
+    return w, len(w)
+
+
+def _same_length(n: int, name: str, a) -> None:
+    if len(a) != n:
+        raise ValueError(f"{name} has {len(a)} entries for {n} sequences")
 
 
 def fq_kv_layer_view(kv: int, layer: int) -> fq_kv_view:
@@ -385,16 +397,20 @@ def fq_qk_norm_rope(qkv_ptr: int, lens, pos0, views, kv_row0, num_attention_head
                     q_norm_ptr: int, k_norm_ptr: int, eps: float, rope_ptr: int, rope_rows: int, q_out_ptr: int,
                     stream: int = 0, qkv_stride: int = 0, q_stride: int = 0) -> None:
     """RMSNorm and rotary embedding of packed raw projections: q to q_out (bf16), k and v to cache rows."""
-    n, p, r, w = u32_array(lens), u32_array(pos0), u32_array(kv_row0), kv_view_array(views)
-    _same_length(len(n), pos0=p, kv_row0=r)
-    _check(lib().fq_qk_norm_rope(qkv_ptr, qkv_stride, len(n), n, p, w, len(w), r, num_attention_heads,
-                                 num_key_value_heads, q_norm_ptr, k_norm_ptr, eps, rope_ptr, rope_rows, q_out_ptr,
-                                 q_stride, stream), "fq_qk_norm_rope")
+    L = _lib or lib()
+    n, p, r = u32_array(lens), u32_array(pos0), u32_array(kv_row0)
+    w, n_w = _views(views)
+    _same_length(len(n), "pos0", p)
+    _same_length(len(n), "kv_row0", r)
+    st = L.fq_qk_norm_rope(qkv_ptr, qkv_stride, len(n), n, p, w, n_w, r, num_attention_heads, num_key_value_heads,
+                           q_norm_ptr, k_norm_ptr, eps, rope_ptr, rope_rows, q_out_ptr, q_stride, stream)
+    if st:
+        _check(st, "fq_qk_norm_rope")
 
 
 def fq_attn_prompt_workspace(q_len, k_len, num_attention_heads: int, num_key_value_heads: int) -> int:
     a, b, out = u32_array(q_len), u32_array(k_len), ctypes.c_size_t(0)
-    _same_length(len(a), k_len=b)
+    _same_length(len(a), "k_len", b)
     _check(lib().fq_attn_prompt_workspace(len(a), a, b, num_attention_heads, num_key_value_heads, ctypes.byref(out)),
            "fq_attn_prompt_workspace")
     return int(out.value)
@@ -404,12 +420,18 @@ def fq_attn_prompt(q_ptr: int, views, q_len, k_len, num_attention_heads: int, nu
                    out_ptr: int, ws_ptr: int = 0, ws_bytes: int = 0, stream: int = 0, kv_row0=None, q_stride: int = 0,
                    out_stride: int = 0, out_dtype: str = "bf16") -> None:
     """Causal attention of packed sequences over K/V rows (one view, or one per sequence)."""
-    a, b, w = u32_array(q_len), u32_array(k_len), kv_view_array(views)
-    r = None if kv_row0 is None else u32_array(kv_row0)
-    _same_length(len(a), k_len=b, kv_row0=r)
-    _check(lib().fq_attn_prompt(q_ptr, q_stride, w, len(w), len(a), a, r, b, num_attention_heads, num_key_value_heads,
-                                scale, out_ptr, out_stride, DTYPES[out_dtype], ws_ptr, ws_bytes, stream),
-           "fq_attn_prompt")
+    L = _lib or lib()
+    a, b = u32_array(q_len), u32_array(k_len)
+    w, n_w = _views(views)
+    _same_length(len(a), "k_len", b)
+    r = None
+    if kv_row0 is not None:
+        r = u32_array(kv_row0)
+        _same_length(len(a), "kv_row0", r)
+    st = L.fq_attn_prompt(q_ptr, q_stride, w, n_w, len(a), a, r, b, num_attention_heads, num_key_value_heads, scale,
+                          out_ptr, out_stride, DTYPES[out_dtype], ws_ptr, ws_bytes, stream)
+    if st:
+        _check(st, "fq_attn_prompt")
 
 
 def fq_attn_shared_workspace(prefix_len: int, tail_len, num_attention_heads: int, num_key_value_heads: int) -> int:
@@ -423,13 +445,17 @@ def fq_attn_shared(q_ptr: int, prefix, prefix_len: int, tails, tail_len, num_att
                    num_key_value_heads: int, scale: float, out_ptr: int, ws_ptr: int = 0, ws_bytes: int = 0,
                    stream: int = 0, q_stride: int = 0, out_stride: int = 0, out_dtype: str = "bf16") -> None:
     """One query token per sequence over a shared prefix (a view or None) and per-sequence tails."""
+    L = _lib or lib()
     a = u32_array(tail_len)
-    t = None if tails is None else kv_view_array(tails)
-    _same_length(len(a), tails=t)
+    t = None
+    if tails is not None:
+        t = kv_view_array(tails)
+        _same_length(len(a), "tails", t)
     p = None if prefix is None else ctypes.byref(prefix)
-    _check(lib().fq_attn_shared(q_ptr, q_stride, len(a), p, prefix_len, t, a, num_attention_heads, num_key_value_heads,
-                                scale, out_ptr, out_stride, DTYPES[out_dtype], ws_ptr, ws_bytes, stream),
-           "fq_attn_shared")
+    st = L.fq_attn_shared(q_ptr, q_stride, len(a), p, prefix_len, t, a, num_attention_heads, num_key_value_heads,
+                          scale, out_ptr, out_stride, DTYPES[out_dtype], ws_ptr, ws_bytes, stream)
+    if st:
+        _check(st, "fq_attn_shared")
 
 
 def fq_attn_check(stream: int = 0) -> None:
