@@ -46,8 +46,9 @@ struct JoinEntry {
 };
 
 // Partial results: sums and values unnormalised against the row's reference maximum m (base 2).
-//   tiles: o [slot][kv head][128 rows][128] f32, ml [slot][kv head][128] (m, l)
-//   rows:  o [slot][kv head][16 rows][128],      ml [slot][kv head][16]
+//   tiles: o [slot][kv head][16 dim chunks][128 rows][8] f32 (a warp with a row per lane writes
+//          neighbouring rows), ml [slot][kv head][128] (m, l)
+//   rows:  o [slot][kv head][16 rows][128],          ml [slot][kv head][16]
 struct Partials {
     float *a_o = nullptr, *b_o = nullptr;
     float2 *a_ml = nullptr, *b_ml = nullptr;

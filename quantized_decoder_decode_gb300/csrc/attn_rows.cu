@@ -251,8 +251,11 @@ __global__ void __launch_bounds__(AR_THREADS, 3) attn_rows_kernel(const __grid_c
     pdl_wait();   // this grid ends after the one it may run beside, so what waits for it waits for both
 }
 
-// out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i over the partial results of a (token, head);
-// one warp each.  Up to 32 of them have their weights made by one lane each.
+// out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i over the partial results of the rows of an
+// entry.  A kv head's G rows of a token are joined by G warps: a lane takes one row and four dims
+// (one 16-byte load per partial result, eight in flight), so that a warp reads G x 32 bytes at a
+// time from the chunked layout of the tiles and whole 32-byte sectors from the rows.  The reads
+// are what it costs: it starts early (its index work overlaps the kernels before) and is short.
 constexpr int AJ_WARPS = 8;
 
 template <class Args>
@@ -261,54 +264,55 @@ __global__ void __launch_bounds__(AJ_WARPS * 32) attn_join_kernel(const __grid_c
     const JoinEntry e = a.e[blockIdx.x];
     const int Hq = a.io.Hq, Hkv = a.io.Hkv, G = Hq / Hkv;
     const int idx = blockIdx.y * AJ_WARPS + (threadIdx.x >> 5);
-    if (idx >= e.n_tok * Hq) {
-        pdl_wait();
-        return;
-    }
-    const int t = idx / Hq, h = idx % Hq, kh = h / G, gh = h % G;
+    const int t = idx / Hq, kh = idx % Hq / G;
+    const int gh = (lane >> 1) % G, row = t * G + gh;
+    const int d = ((idx % G) * (16 / G) + (lane >> 1) / G) * 8 + (lane & 1) * 4;   // dims d .. d + 3
     const int n = e.nA + e.nB + e.nC;
-    auto where = [&](int i, const float*& o) -> const float2* {
-        if (i < e.nA) {
-            const int64_t b = ((int64_t)(e.a0 + i * e.a_step) * Hkv + kh) * TILE_ROWS + e.a_row + t * G + gh;
-            o = a.part.a_o + b * HEAD_DIM;
-            return a.part.a_ml + b;
-        }
+    const float* a_o = a.part.a_o + ((int64_t)e.a0 * Hkv + kh) * TILE_ROWS * HEAD_DIM + ((d >> 3) * TILE_ROWS + e.a_row + row) * 8 + (d & 7);
+    const float2* a_ml = a.part.a_ml + ((int64_t)e.a0 * Hkv + kh) * TILE_ROWS + e.a_row + row;
+    const int64_t a_step = (int64_t)e.a_step * Hkv * TILE_ROWS;
+    const int64_t b_blk = ((int64_t)e.b0 * Hkv + kh) * ROWS_MAX + e.b_row + row, c_blk = ((int64_t)e.c0 * Hkv + kh) * ROWS_MAX + row;
+    const int64_t b_step = (int64_t)Hkv * ROWS_MAX;
+    // partial result i of this row: (m, l) and the values
+    auto ml_at = [&](int i) -> const float2* {
+        if (i < e.nA) return a_ml + i * a_step;
         i -= e.nA;
-        const int64_t b = i < e.nB ? ((int64_t)(e.b0 + i) * Hkv + kh) * ROWS_MAX + e.b_row + t * G + gh
-                                   : ((int64_t)(e.c0 + i - e.nB) * Hkv + kh) * ROWS_MAX + t * G + gh;
-        o = a.part.b_o + b * HEAD_DIM;
-        return a.part.b_ml + b;
+        return a.part.b_ml + (i < e.nB ? b_blk + i * b_step : c_blk + (i - e.nB) * b_step);
+    };
+    auto o_at = [&](int i) -> const float4* {
+        if (i < e.nA) return reinterpret_cast<const float4*>(a_o + i * a_step * HEAD_DIM);
+        i -= e.nA;
+        return reinterpret_cast<const float4*>(a.part.b_o + (i < e.nB ? b_blk + i * b_step : c_blk + (i - e.nB) * b_step) * HEAD_DIM + d);
     };
     pdl_wait();   // the partial results are written
+    if (idx >= e.n_tok * Hq) return;
     float M = -INFINITY;
-    for (int i = lane; i < n; i += 32) {
-        const float* o;
-        M = fmaxf(M, where(i, o)->x);
-    }
-    M = warp_max(M);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) M = fmaxf(M, ml_at(i)->x);
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
     float L = 0.f;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-        float w = 0.f, lw = 0.f;
-        if (i0 + lane < n) {
-            const float* o;
-            const float2 ml = *where(i0 + lane, o);
-            if (!(ml.x == -INFINITY && ml.y == 0.f)) w = ml.x == M ? 1.f : ex2(ml.x - M);   // (else it saw no key)
-            lw = w * ml.y;   // (a NaN sum stays one)
-        }
-        L += warp_sum(lw);
-#pragma unroll 8
-        for (int i = 0; i < min(32, n - i0); ++i) {
-            const float f = __shfl_sync(0xFFFFFFFFu, w, i);
-            const float* o;
-            where(i0 + i, o);
-            // (a weight of 0 drops what may not be finite)
-            const float4 v = f == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : reinterpret_cast<const float4*>(o)[lane];
-            y.x = fmaf(v.x, f, y.x);
-            y.y = fmaf(v.y, f, y.y);
-            y.z = fmaf(v.z, f, y.z);
-            y.w = fmaf(v.w, f, y.w);
-        }
+    constexpr int BATCH = 8;
+    for (int i0 = 0; i0 < n; i0 += BATCH) {
+        float4 v[BATCH];
+        float2 ml[BATCH];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k)
+            if (i0 + k < n) {
+                v[k] = *o_at(i0 + k);
+                ml[k] = *ml_at(i0 + k);
+            }
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k)
+            if (i0 + k < n) {
+                // (a part that saw no key, or only scores of -inf, weighs nothing; a NaN sum stays one)
+                const float f = ml[k].x == -INFINITY && ml[k].y == 0.f ? 0.f : ml[k].x == M ? 1.f : ex2(ml[k].x - M);
+                L = fmaf(ml[k].y, f, L);
+                if (f == 0.f) continue;   // its values may not be finite
+                y.x = fmaf(v[k].x, f, y.x);
+                y.y = fmaf(v[k].y, f, y.y);
+                y.z = fmaf(v[k].z, f, y.z);
+                y.w = fmaf(v[k].w, f, y.w);
+            }
     }
     if (min(e.k_len, t + e.off) > 0) {
         const float inv = 1.f / L;
@@ -317,9 +321,9 @@ __global__ void __launch_bounds__(AJ_WARPS * 32) attn_join_kernel(const __grid_c
         y.z *= inv;
         y.w *= inv;
     }
-    const int64_t at = (int64_t)(e.q_row0 + t) * a.io.out_stride + (int64_t)h * HEAD_DIM;
-    if (a.io.out_f32) reinterpret_cast<float4*>((float*)a.io.out + at)[lane] = y;
-    else reinterpret_cast<uint2*>((uint16_t*)a.io.out + at)[lane] = make_uint2(bf16x2(y.x, y.y), bf16x2(y.z, y.w));
+    const int64_t at = (int64_t)(e.q_row0 + t) * a.io.out_stride + (int64_t)(kh * G + gh) * HEAD_DIM + d;
+    if (a.io.out_f32) *reinterpret_cast<float4*>((float*)a.io.out + at) = y;
+    else *reinterpret_cast<uint2*>((uint16_t*)a.io.out + at) = make_uint2(bf16x2(y.x, y.y), bf16x2(y.z, y.w));
 }
 
 }  // namespace

@@ -41,10 +41,11 @@ constexpr int AT_PANEL = AT_TILE_BYTES / 2;               // 64 dims of 128 rows
 constexpr uint32_t AT_S = 0, AT_P = 128, AT_O = 256;      // tensor-memory columns: S, P_A, P_B (64 each), O_A, O_B
 
 struct AtShared {
-    uint64_t q_full, q_empty, item_done, join;
+    uint64_t q_full, q_empty, join;
     uint64_t full[AT_STAGES], empty[AT_STAGES], raw[AT_STAGES];
     uint64_t s_full[2], p_full[2], o_done[2], s_free;
-    uint32_t tmem, abort;
+    uint32_t tmem, abort, preloaded;
+    uint32_t done[8];                     // units that each softmax warp has finished
     uint32_t poison_unit[2];              // unit number + 1 whose notes the buffer holds
     float exchange[2][TILE_ROWS];
     uint16_t poison[2][3][HEAD_DIM];      // first key (from the unit's first partly seen tile) of +inf, -inf, NaN
@@ -110,6 +111,23 @@ FQ_DEV Unit unit_of(const Args& a, int w) {
 FQ_DEV int k_at(const Unit& u, int t) { return t + max(0, t - u.step); }
 FQ_DEV int v_at(const Unit& u, int t) { return t + min(t + 1 + u.step, u.nt); }
 
+// By one thread: the unit's query tiles; one K or V tile.
+template <class Args>
+FQ_DEV void load_q(const Args& a, const Unit& u, const PromptSeq& sq, uint8_t* q_sm, AtShared* sh) {
+    const int q0 = u.n[0] > 0 ? 0 : 1, q1 = u.single || u.n[1] == 0 ? 1 : 2;
+    mbar_arrive_expect_tx(&sh->q_full, (uint32_t)((q1 - q0) * AT_TILE_BYTES));
+    for (int x = q0; x < q1; ++x) {
+        const int row = sq.q_row0 + u.tok[x];
+        tma_load_4d(q_sm + x * AT_TILE_BYTES, a.map_q, 0, 0, u.head, row, &sh->q_full);
+        tma_load_4d(q_sm + x * AT_TILE_BYTES + AT_PANEL, a.map_q, 64, 0, u.head, row, &sh->q_full);
+    }
+}
+FQ_DEV void load_kv(const void* map, uint8_t* dst, int row, int head, uint64_t* bar) {
+    mbar_arrive_expect_tx(bar, AT_TILE_BYTES);
+    tma_load_3d(dst, map, 0, row, head, bar);
+    tma_load_3d(dst + AT_PANEL, map, 64, row, head, bar);
+}
+
 FQ_DEV bool at_wait(uint64_t* bar, uint32_t parity, AtShared* sh) {
     if (mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
@@ -127,6 +145,22 @@ FQ_DEV bool at_wait(uint64_t* bar, uint32_t parity, AtShared* sh) {
 // The same by a whole warp, with one answer for all lanes.
 FQ_DEV bool at_wait_warp(uint64_t* bar, uint32_t parity, AtShared* sh) {
     return __all_sync(0xFFFFFFFFu, at_wait(bar, parity, sh));
+}
+// All softmax warps have finished n units (a count each: a warpgroup whose tile is empty may be
+// units ahead of the other one, which no phase bit could tell).
+FQ_DEV bool units_done(uint32_t n, int lane, AtShared* sh) {
+    const long long t0 = clock64();
+    while (!__all_sync(0xFFFFFFFFu, *(volatile uint32_t*)&sh->done[lane & 7] >= n)) {
+        const bool late = clock64() - t0 > WAIT_BUDGET_CYCLES;
+        if (__any_sync(0xFFFFFFFFu, late || *(volatile uint32_t*)&sh->abort)) {
+            if (lane == 0 && late) {
+                *(volatile uint32_t*)&sh->abort = 1;
+                atomicAdd(&g_attn_waits, 1u);
+            }
+            return false;
+        }
+    }
+    return true;
 }
 constexpr long long DRAIN_CYCLES = 1 << 20;   // half a millisecond
 FQ_DEV uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
@@ -168,34 +202,43 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int units = a.n_entries * a.io.Hkv;
     const int G = a.io.Hq / a.io.Hkv;
-    // the first unit, worked out while the barriers and tensor memory are set up: its entry is a
-    // chain of reads of kernel parameters that no cache holds yet
-    const Unit u0 = unit_of(a, blockIdx.x);
     pdl_trigger();   // the kernels behind this one in the call may start beside it
-
-    if (tid == 0) {
-        mbar_init(&sh->q_full, 1);
-        mbar_init(&sh->q_empty, 1);
-        mbar_init(&sh->item_done, 8);
-        mbar_init(&sh->join, 8);
-        mbar_init(&sh->s_free, 4);
-        for (int s = 0; s < AT_STAGES; ++s) {
-            mbar_init(&sh->full[s], 1);
-            mbar_init(&sh->empty[s], 1);
-            mbar_init(&sh->raw[s], 1);
+    if (warp == 9) {
+        // (the loads of the first unit start before the CTA meets)
+        if (lane == 0) {
+            mbar_init(&sh->q_full, 1);
+            mbar_init(&sh->q_empty, 1);
+            for (int i = 0; i < 8; ++i) sh->done[i] = 0;
+            mbar_init(&sh->join, 8);
+            mbar_init(&sh->s_free, 4);
+            for (int s = 0; s < AT_STAGES; ++s) {
+                mbar_init(&sh->full[s], 1);
+                mbar_init(&sh->empty[s], 1);
+                mbar_init(&sh->raw[s], 1);
+            }
+            for (int x = 0; x < 2; ++x) {
+                mbar_init(&sh->s_full[x], 1);
+                mbar_init(&sh->p_full[x], 4);
+                mbar_init(&sh->o_done[x], 1);
+                sh->poison_unit[x] = 0;
+            }
+            // the 128-byte swizzle wants 1024-byte aligned tiles
+            sh->abort = (smem_u32(smem) & 1023) ? 1 : 0;
+            if (sh->abort) atomicAdd(&g_attn_waits, 1u);
+            mbar_fence_init();
         }
-        for (int x = 0; x < 2; ++x) {
-            mbar_init(&sh->s_full[x], 1);
-            mbar_init(&sh->p_full[x], 4);
-            mbar_init(&sh->o_done[x], 1);
-            sh->poison_unit[x] = 0;
+        __syncwarp();
+        const Unit u = unit_of(a, blockIdx.x);
+        const PromptSeq& sq = a.seq[u.seq];
+        const int vw = Args::VIEWS == 1 ? 0 : u.seq;
+        const bool pre = u.nt > 0 && sh->abort == 0;
+        if (pre && elect_one()) {
+            load_q(a, u, sq, q_sm, sh);
+            load_kv(a.map_k[vw], ring, sq.k_row0 + u.j0 * TILE_ROWS, u.head, &sh->full[0]);
         }
-        // the 128-byte swizzle wants 1024-byte aligned tiles
-        sh->abort = (smem_u32(smem) & 1023) ? 1 : 0;
-        if (sh->abort) atomicAdd(&g_attn_waits, 1u);
-        mbar_fence_init();
-    }
-    if (warp == 8) {
+        if (lane == 0) sh->preloaded = pre;
+        __syncwarp();
+    } else if (warp == 8) {
         tmem_alloc(&sh->tmem, 512);
         tmem_relinquish();
     }
@@ -210,25 +253,22 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
     if (broken) {
     } else if (warp == 9) {
         // ---------------- loads
-        uint32_t pos = 0, qn = 0, it = 0;
+        // Q and the first K tile of the first unit are on their way: neither is waited for again
+        // here (their release may come before this warp gets to it)
+        uint32_t pos = sh->preloaded, qn = sh->preloaded, it = 0;
         bool ok = true;
         for (int w; (w = unit_at(it)) < units && ok; ++it) {
-            const Unit u = it == 0 ? u0 : unit_of(a, w);
+            const Unit u = unit_of(a, w);
             const PromptSeq& sq = a.seq[u.seq];
-            if (it >= 2 && !(ok = at_wait_warp(&sh->item_done, it & 1, sh))) break;   // unit it - 2 finished
+            if (it >= 2 && !(ok = units_done(it - 1, lane, sh))) break;   // all but the unit before
             if (u.nt == 0) continue;
-            if (!(ok = at_wait_warp(&sh->q_empty, (qn & 1) ^ 1, sh))) break;
-            ++qn;
-            const int n_q = (u.single || u.n[1] == 0) ? 1 : 2, q0 = u.n[0] > 0 ? 0 : 1;
-            if (elect_one()) {
-                mbar_arrive_expect_tx(&sh->q_full, (uint32_t)((n_q - q0) * AT_TILE_BYTES));
-                for (int x = q0; x < n_q; ++x) {
-                    const int row = sq.q_row0 + u.tok[x];
-                    tma_load_4d(q_sm + x * AT_TILE_BYTES, a.map_q, 0, 0, u.head, row, &sh->q_full);
-                    tma_load_4d(q_sm + x * AT_TILE_BYTES + AT_PANEL, a.map_q, 64, 0, u.head, row, &sh->q_full);
-                }
+            const bool pre = it == 0;
+            if (!pre) {
+                if (!(ok = at_wait_warp(&sh->q_empty, (qn & 1) ^ 1, sh))) break;
+                ++qn;
+                if (elect_one()) load_q(a, u, sq, q_sm, sh);
+                __syncwarp();
             }
-            __syncwarp();
             const int vw = Args::VIEWS == 1 ? 0 : u.seq;
             auto load = [&](bool v, int t) {
                 const int s = pos % AT_STAGES;
@@ -236,16 +276,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
                 ++pos;
                 uint64_t* bar = v && u.j0 + t >= u.jm ? &sh->raw[s] : &sh->full[s];
                 const void* map = v ? a.map_v[vw] : a.map_k[vw];
-                uint8_t* dst = ring + s * AT_TILE_BYTES;
-                const int row = sq.k_row0 + (u.j0 + t) * TILE_ROWS;
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(bar, AT_TILE_BYTES);
-                    tma_load_3d(dst, map, 0, row, u.head, bar);
-                    tma_load_3d(dst + AT_PANEL, map, 64, row, u.head, bar);
-                }
+                if (elect_one()) load_kv(map, ring + s * AT_TILE_BYTES, sq.k_row0 + (u.j0 + t) * TILE_ROWS, u.head, bar);
                 __syncwarp();
             };
-            for (int t = 0; t < u.step && t < u.nt && ok; ++t) load(false, t);
+            for (int t = pre ? 1 : 0; t < u.step && t < u.nt && ok; ++t) load(false, t);
             for (int t = 0; t < u.nt && ok; ++t) {
                 if (t + u.step < u.nt) load(false, t + u.step);
                 if (ok) load(true, t);
@@ -265,7 +299,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
         uint32_t pos0 = 0, qn = 0, sn = 0, it = 0;   // sn: score tiles
         bool ok = true;
         for (int w; (w = unit_at(it)) < units && ok; ++it) {
-            const Unit u = it == 0 ? u0 : unit_of(a, w);
+            const Unit u = unit_of(a, w);
             if (u.nt == 0) continue;
             if (!(ok = at_wait_warp(&sh->q_full, qn++ & 1, sh))) break;
             for (int t = 0; t < u.nt && ok; ++t) {
@@ -305,7 +339,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
         uint32_t pos0 = 0, pc = 0, it = 0;   // pc: parities of p_full
         bool ok = true;
         for (int w; (w = unit_at(it)) < units && ok; ++it) {
-            const Unit u = it == 0 ? u0 : unit_of(a, w);
+            const Unit u = unit_of(a, w);
             for (int t = 0; t < u.nt && ok; ++t) {
                 const uint32_t pos = pos0 + v_at(u, t);
                 const int s = pos % AT_STAGES;
@@ -337,7 +371,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
         uint32_t pos0 = 0, it = 0, raw_ph = 0;
         bool ok = true;
         for (int w; (w = unit_at(it)) < units && ok; ++it) {
-            const Unit u = it == 0 ? u0 : unit_of(a, w);
+            const Unit u = unit_of(a, w);
             const int k_len = a.seq[u.seq].k_len;
             for (int t = max(0, u.jm - u.j0); t < u.nt; ++t) {
                 const int s = (pos0 + v_at(u, t)) % AT_STAGES;
@@ -414,7 +448,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
             return met;
         };
         for (int w; (w = unit_at(it)) < units && ok; ++it) {
-            const Unit u = it == 0 ? u0 : unit_of(a, w);
+            const Unit u = unit_of(a, w);
             const PromptSeq& sq = a.seq[u.seq];
             const int tok = u.tok[x] + row / G;
             const bool valid = row / G < u.n_tok[x];
@@ -561,7 +595,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
                 }
                 if (!valid) return;
                 if (u.slot) {
-                    st_row<32>(a.part.a_o + blk * HEAD_DIM + d, reinterpret_cast<uint32_t*>(y), true);
+                    float* dst = a.part.a_o + (blk - row) * HEAD_DIM + ((d >> 3) * TILE_ROWS + row) * 8;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) st_global32(dst + k * TILE_ROWS * 8, reinterpret_cast<uint32_t*>(y) + 8 * k);
                 } else if (a.io.out_f32) {
                     st_row<32>((float*)a.io.out + o_row * a.io.out_stride + o_col + d, reinterpret_cast<uint32_t*>(y), wide);
                 } else {
@@ -582,8 +618,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
             // the next unit's products may overwrite O once both warpgroups have read it
             tc_fence_before();
             if (u.single && !(ok = join())) break;
+            __threadfence_block();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->item_done);
+            if (lane == 0) *(volatile uint32_t*)&sh->done[warp] = it + 1;
         }
     }
     }

@@ -182,6 +182,26 @@ def test_prompt_growing_scores():
     assert_within(got, ref, bound, True)
 
 
+def test_prompt_many_calls_in_a_row():
+    """Calls queued behind one another: the same bits every time and no wait that gave up.  Lengths whose
+    last units have an empty second tile, single tokens, one-tile units and splits among them."""
+    g, hq, hkv = gen(29), 32, 8
+    q_len = [1, 37, 129, 255, 64, 640, 771, 901, 65, 1187]
+    rows, T = sum(q_len), sum(q_len)
+    k, v = normal(g, hkv, rows, D), normal(g, hkv, rows, D)
+    qs = [normal(g, T, hq, D) for _ in range(2)]
+    ws = workspace(fq.fq_attn_prompt_workspace(q_len, q_len, hq, hkv))
+    outs = [torch.empty_like(qs[0]) for _ in range(4)]
+    for i in range(400):
+        fq.fq_attn_prompt(qs[i & 1].data_ptr(), view_of(k, v, rows, D, rows * D), q_len, q_len, hq, hkv, SCALE,
+                          outs[i & 1 if i < 2 else 2 + (i & 1)].data_ptr(), ws.data_ptr(), ws.numel() * 4, stream())
+    fq.fq_attn_check(stream())
+    assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
+    k0 = [sum(q_len[:s]) for s in range(len(q_len))]
+    ref, bound = reference_prompt(qs[1], lambda s, h: (k[h, k0[s]:k0[s] + q_len[s]], v[h, k0[s]:k0[s] + q_len[s]]), q_len, q_len, hq, hkv)
+    assert_within(outs[3], ref, bound, True)
+
+
 def test_prompt_long_cache_offsets():
     """Rows and heads whose element offsets pass 2^32."""
     g, hq, hkv = gen(23), 4, 2
