@@ -76,12 +76,15 @@ KvRows rows_of(const fq_kv_view& v) {
 
 // ---------------------------------------------------------------- work lists
 
-// Keys a unit of attn_tiles.cu should have at least when keys are split, in tiles: a partial
-// result of a 128-row tile is 64 KB, as much as the K and V of one key tile.
-constexpr int SPLIT_TILES = 8;
-// Keys per chunk of attn_rows.cu at least, and chunks that fill the GPU once (three CTAs per SM)
+// Times of attn_tiles.cu in microseconds (measured at head_dim 128 on one GB300) that the choices
+// below weigh: a key tile of a pair of query tiles and of a single one, a unit's own cost (loads
+// before its first scores, outputs), what a unit with partial results costs more, and joining
+// them: a launch and the reads.
+constexpr float T_PAIR = 1.45f, T_SINGLE = 0.85f, T_UNIT = 4.f, T_PARTIAL = 0.7f, T_JOIN = 3.f, T_JOIN_MB = 0.4f;
+// .. and of attn_rows.cu: a CTA's own cost, and megabytes of keys and values per SM
+constexpr float T_ROWS = 4.f, T_ROWS_MB = 26.f;
+// Keys per chunk of attn_rows.cu at least
 constexpr int64_t ROWS_CHUNK = 128;
-constexpr int64_t ROWS_CTAS = 3 * ATTN_SMS;
 
 struct Plan {
     std::vector<TileEntry> tiles;     // longest first
@@ -148,25 +151,50 @@ struct Tiles {
     bool single;
 };
 
+// Units of sequence s: pairs of query tiles, or single ones.
+void add_units(std::vector<Tiles>& units, const PromptSeq& q, int s, int tpt, bool singles) {
+    const bool single = singles || q.q_len <= tpt;
+    const int step = single ? tpt : 2 * tpt;
+    for (int t = 0; t < q.q_len; t += step) {
+        const int n_tok = std::min(step, q.q_len - t);
+        units.push_back(Tiles{t, n_tok, ceil_div(std::max(0, std::min(q.k_len, t + n_tok - 1 + q.off)), TILE_ROWS), s, single});
+    }
+}
+
+// Estimated time of the units with at most `cap` key tiles each (longer ones split): the longest
+// unit, or as many average ones as the fullest CTA gets.
+float estimate(const std::vector<Tiles>& units, int cap, int G, int Hkv) {
+    float total = 0.f, longest = 0.f, joined_mb = 0.f;
+    int64_t n = 0;
+    for (const Tiles& u : units) {
+        const int S = std::max(1, ceil_div(u.nt, cap));
+        const float one = (u.single ? T_SINGLE : T_PAIR) * ceil_div(u.nt, S) + T_UNIT + (S > 1 ? T_PARTIAL : 0.f);
+        total += S * one * Hkv;
+        longest = std::max(longest, one);
+        n += (int64_t)S * Hkv;
+        if (S > 1) joined_mb += S * (float)u.n_tok * G * Hkv * (HEAD_DIM * 4e-6f);
+    }
+    const float even = total / n * ceil_div(n, ATTN_SMS);
+    // many units per CTA even out
+    return std::max(longest, n > 4 * ATTN_SMS ? total / ATTN_SMS : even) + (joined_mb > 0.f ? T_JOIN + T_JOIN_MB * joined_mb : 0.f);
+}
+
 void plan_prompt(Plan& p, uint32_t n_seq, const PromptSeq* seq, uint32_t G, uint32_t Hkv) {
     const int tpt = TILE_ROWS / (int)G;
-    std::vector<Tiles> units;
-    int64_t total = 0;
+    // Sequences of a few rows go to attn_rows.cu, but for short ones beside others that need tiles:
+    // a unit more costs less than a launch more (1024 keys: 11 us of one CTA).
+    bool tiled = false;
+    for (uint32_t s = 0; s < n_seq; ++s) tiled |= (int64_t)seq[s].q_len * G > ROWS_MAX;
+    std::vector<Tiles> units, other;
     for (uint32_t s = 0; s < n_seq; ++s) {
         const PromptSeq& q = seq[s];
         if (q.q_len == 0) continue;
-        if ((int64_t)q.q_len * G <= ROWS_MAX) {
-            p.groups.push_back(RowGroup{q.q_row0, q.q_len, q.k_row0, q.k_len, q.off, 0, 0, -1});
-            p.group_view.push_back((int)s);
+        if ((int64_t)q.q_len * G > ROWS_MAX || (tiled && q.k_len <= 1024)) {
+            add_units(units, q, (int)s, tpt, false);
             continue;
         }
-        const bool single = q.q_len <= tpt;
-        for (int t = 0; t < q.q_len; t += 2 * tpt) {
-            const int n_tok = std::min(2 * tpt, q.q_len - t);
-            const int nt = ceil_div(std::max(0, std::min(q.k_len, t + n_tok - 1 + q.off)), TILE_ROWS);
-            units.push_back(Tiles{t, n_tok, nt, (int)s, single});
-            total += nt;
-        }
+        p.groups.push_back(RowGroup{q.q_row0, q.q_len, q.k_row0, q.k_len, q.off, 0, 0, -1});
+        p.group_view.push_back((int)s);
     }
     plan_groups(p, Hkv, false);
     for (size_t g = 0; g < p.groups.size(); ++g) {
@@ -174,10 +202,32 @@ void plan_prompt(Plan& p, uint32_t n_seq, const PromptSeq* seq, uint32_t G, uint
         if (r.slot0 >= 0)
             p.join.push_back(JoinEntry{r.q_row0, r.n_tok, r.k_len, r.off, 0, 0, 0, 0, r.slot0, splits_of(p, g), 0, 0, 0});
     }
-    // units of more than a CTA's fair share are split along their keys
-    const int fair = std::max(SPLIT_TILES, ceil_div(total * Hkv, ATTN_SMS));
+    if (units.empty()) return;
+    // Pairs of query tiles share their K and V tiles, single ones give shorter units, and units may
+    // be split along the keys: with few units per SM the estimate chooses (2048 tokens, 16 / 8
+    // heads: single tiles 19 us, pairs 27, split pairs 33).
+    int longest = 0;
+    for (const Tiles& u : units) longest = std::max(longest, u.nt);
+    int cap = std::max(1, longest);
+    if ((int64_t)units.size() * Hkv < 3 * ATTN_SMS) {
+        for (const Tiles& u : units)
+            if (u.tok0 == 0) add_units(other, seq[u.seq], u.seq, tpt, true);
+        float best = 0.f;
+        bool singles = false;
+        for (int mode = 0; mode < 2; ++mode)
+            for (int k = 1; k <= 24 && (k == 1 || longest / k >= 4); ++k) {
+                const int c = std::max(1, ceil_div(longest, k));
+                const float t = estimate(mode ? other : units, c, (int)G, (int)Hkv);
+                if ((mode == 0 && k == 1) || t < best) {
+                    best = t;
+                    cap = c;
+                    singles = mode == 1;
+                }
+            }
+        if (singles) units.swap(other);
+    }
     for (const Tiles& u : units) {
-        const int S = 2 * u.nt > 3 * fair ? ceil_div(u.nt, fair) : 1;
+        const int S = std::max(1, ceil_div(u.nt, cap));
         const uint32_t info = (uint32_t)u.seq | (u.single ? TILE_SINGLE : 0u);
         if (S == 1) {
             p.tiles.push_back(TileEntry{u.tok0, info, 0, u.nt});
@@ -193,8 +243,35 @@ void plan_prompt(Plan& p, uint32_t n_seq, const PromptSeq* seq, uint32_t G, uint
             p.join.push_back(JoinEntry{q.q_row0 + u.tok0 + b * tpt, std::min(tpt, u.n_tok - b * tpt), q.k_len,
                                        q.off + u.tok0 + b * tpt, slot + b, S, blocks, 0, 0, 0, 0, 0, 0});
     }
-    std::stable_sort(p.tiles.begin(), p.tiles.end(),
-                     [](const TileEntry& a, const TileEntry& b) { return a.j1 - a.j0 > b.j1 - b.j0; });
+    std::stable_sort(p.tiles.begin(), p.tiles.end(), [](const TileEntry& a, const TileEntry& b) {
+        const float ca = (a.j1 - a.j0) * (a.info & TILE_SINGLE ? T_SINGLE : T_PAIR);
+        return ca > (b.j1 - b.j0) * (b.info & TILE_SINGLE ? T_SINGLE : T_PAIR);
+    });
+}
+
+// Splits of a shared prefix of nt key tiles (rows packed query rows, `units` units per kv head)
+// while row groups with `tail_mb` of keys and values run on the SMs that the units leave.
+int prefix_splits(int nt, int units, int rows, bool single, float tail_mb, int Hkv) {
+    int best_S = 1;
+    float best = 0.f;
+    for (int S = 1; S <= nt; ++S) {
+        const int ctas = units * Hkv * S;
+        const float tiles = ((single ? T_SINGLE : T_PAIR) * ceil_div(nt, S) + T_UNIT + T_PARTIAL) * ceil_div(ctas, ATTN_SMS);
+        float t = tiles;
+        if (tail_mb > 0.f) {
+            const int free = ATTN_SMS - std::min(ctas, ATTN_SMS);
+            const float alone = T_ROWS + T_ROWS_MB * tail_mb / ATTN_SMS;
+            t = tiles + alone;
+            if (free > 0) t = std::min(t, std::max(tiles, T_ROWS + T_ROWS_MB * tail_mb / free));
+        }
+        t += T_JOIN + T_JOIN_MB * (S + (tail_mb > 0.f ? 1 : 0)) * rows * Hkv * (HEAD_DIM * 4e-6f);
+        if (S == 1 || t < best) {
+            best = t;
+            best_S = S;
+        }
+        if (ctas >= 2 * ATTN_SMS) break;
+    }
+    return best_S;
 }
 
 void plan_shared(Plan& p, uint32_t n_seq, uint32_t prefix_len, const uint32_t* tail_len, uint32_t G, uint32_t Hkv) {
@@ -221,7 +298,9 @@ void plan_shared(Plan& p, uint32_t n_seq, uint32_t prefix_len, const uint32_t* t
         units = ceil_div(n_seq, 2 * tpt);
         blocks = single ? 1 : 2;
         const int nt = ceil_div(P, TILE_ROWS);
-        S = std::max(1, std::min(nt / SPLIT_TILES, ATTN_SMS / (units * (int)Hkv)));
+        float mb = 0.f;
+        for (uint32_t s = 0; s < n_seq; ++s) mb += (float)tail_len[s] * Hkv * (HEAD_DIM * 4e-6f);
+        S = prefix_splits(nt, units, (int)(n_seq * G), single, mb, (int)Hkv);
         const bool partial = S > 1 || tails;
         if (partial) slot = p.add_slots(p.tile_slots, (int64_t)S * blocks * units);
         for (int u = 0; u < units; ++u)
@@ -343,6 +422,7 @@ fq_status run_groups(const Plan& p, const AttnIo& io, const Partials& part, cons
     a.n_items = p.row_items;
     for (size_t g = 0; g < p.groups.size(); ++g) {
         a.g[g] = p.groups[g];
+        std::fill(a.group + p.groups[g].item0, a.group + p.groups[g].item0 + splits_of(p, g), (uint8_t)g);
         a.kv[g] = p.group_view[g] < 0 ? *prefix : views[p.group_view[g]];
     }
     launch_attn_rows(a, !p.tiles.empty(), s);
@@ -355,14 +435,17 @@ fq_status run_join_t(const Plan& p, const AttnIo& io, const Partials& part, cuda
     Args a;
     a.io = io;
     a.part = part;
-    a.n_entries = (int)p.join.size();
-    a.max_tok = 0;
-    for (size_t i = 0; i < p.join.size(); ++i) {
-        a.e[i] = p.join[i];
-        a.max_tok = std::max(a.max_tok, p.join[i].n_tok);
+    for (size_t e0 = 0; e0 < p.join.size(); e0 += Args::ENTRIES) {
+        a.n_entries = (int)std::min<size_t>(Args::ENTRIES, p.join.size() - e0);
+        a.max_tok = 0;
+        for (int i = 0; i < a.n_entries; ++i) {
+            a.e[i] = p.join[e0 + i];
+            a.max_tok = std::max(a.max_tok, a.e[i].n_tok);
+        }
+        // (a second launch waits for the first, which waits for the partial results)
+        launch_attn_join(a, s);
+        CK(cudaGetLastError());
     }
-    launch_attn_join(a, s);
-    CK(cudaGetLastError());
     return FQ_OK;
 }
 

@@ -2,7 +2,7 @@
 // (attn_api.cu) and passed by value to attn_tiles.cu, attn_rows.cu and its join kernel.
 //
 // "Packed rows": a kv head's query rows are (token, head of its group) with the head running
-// fastest, so G heads x tokens fill the 128 (or 16) rows of a matrix product.
+// fastest, so G heads x tokens fill the 128 rows (or 8 columns) of a matrix product.
 #pragma once
 
 #include "kernels.h"
@@ -11,7 +11,7 @@ namespace fq {
 
 constexpr int ATTN_SMS = 152;         // SMs that the work lists are made for
 constexpr int TILE_ROWS = 128;        // packed rows of a query tile = keys of a key tile
-constexpr int ROWS_MAX = 16;          // packed rows that attn_rows.cu takes
+constexpr int ROWS_MAX = 8;           // packed rows that attn_rows.cu takes
 constexpr int32_t SEES_ALL = 1 << 30; // PromptSeq::off of rows that see every key
 
 // Row i (token) of a sequence sees keys [0, min(k_len, i + off)), off = k_len - q_len + 1.
@@ -48,7 +48,7 @@ struct JoinEntry {
 // Partial results: sums and values unnormalised against the row's reference maximum m (base 2).
 //   tiles: o [slot][kv head][16 dim chunks][128 rows][8] f32 (a warp with a row per lane writes
 //          neighbouring rows), ml [slot][kv head][128] (m, l)
-//   rows:  o [slot][kv head][16 rows][128],          ml [slot][kv head][16]
+//   rows:  o [slot][kv head][8 rows][128],           ml [slot][kv head][8]
 struct Partials {
     float *a_o = nullptr, *b_o = nullptr;
     float2 *a_ml = nullptr, *b_ml = nullptr;
@@ -56,6 +56,9 @@ struct Partials {
 
 constexpr int MAX_JOIN = 512;
 constexpr int MAX_GROUPS = MAX_SEQ + 1;
+constexpr int ROWS_CTAS_SM = 3;                     // CTAs of attn_rows.cu per SM (156 registers x 128)
+constexpr int ROWS_CTAS = ROWS_CTAS_SM * ATTN_SMS;  // ..  that run at once
+constexpr int MAX_ITEMS = ROWS_CTAS + MAX_GROUPS;   // (a group is one item at least)
 
 template <int NV, int NE>
 struct TileArgs {
@@ -86,6 +89,7 @@ struct RowsArgs {
     int n_groups, n_items;
     float c;              // scale log2(e)
     Partials part;
+    uint8_t group[MAX_ITEMS];   // of an item
     RowGroup g[MAX_GROUPS];
     KvRows kv[MAX_GROUPS];
 };

@@ -2,15 +2,16 @@
 // batch behind a shared prefix, short prompts.  And the kernel that joins partial results.
 //
 // Memory bound: every K and V row is read once per kv head for all G heads (x tokens) of the
-// group, up to 16 packed rows, straight from global memory into the operand registers of
-// mma.sync m16n8k16 (bf16, f32 sums): at 16 rows the tensor work is far below the memory time,
-// and no shared memory or barrier stands between a load and its use.
-//   S = Q K^T: the sum over the 128 dims may run in any order as long as Q and K agree, so a
-//     thread's 16-byte piece of a K row (8 neighbouring dims) serves as the operand's pairs of
-//     two k-steps.
-//   O = P V: the weights leave S in the layout the second product takes them in; V rows 2c, 2c+1
-//     (keys) are paired per dim by byte permutes, and the dims of a 16-byte piece go to eight
-//     different n-tiles, so again every load is 16 bytes.
+// group, up to 8 packed rows, straight from global memory into the operand registers of
+// mma.sync m16n8k16 (bf16, f32 sums), with the query rows as the 8 columns: the tensor work is far
+// below the memory time, and no shared memory or barrier stands between a load and its use.
+//   S' = K Q' (16 keys x 8 rows): the sum over the 128 dims may run in any order as long as Q and
+//     K agree, so a thread's 16-byte piece of a K row (8 neighbouring dims) serves as the
+//     operand's pairs of two k-steps.
+//   O' = V' P' (dims x 8 rows): the weights, rounded to bf16 pairs, are transposed between the
+//     lanes (movmatrix); V rows 2c, 2c+1 (keys) are paired per dim by byte permutes, and the
+//     dims of a thread's 16-byte pieces go to eight different tiles, so that every load is 16
+//     bytes again and a thread ends up with 8 neighbouring dims of two rows.
 // A CTA of four warps takes a chunk of the keys of one (row group, kv head); the warps take
 // blocks of 16 keys in turn with a running reference maximum (moved only when the maximum has
 // grown by more than 2^8) and are joined in shared memory.
@@ -33,6 +34,12 @@ FQ_DEV void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint3
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// 8 x 8 matrix of 16-bit values, two neighbours of row lane / 4 per lane, transposed
+FQ_DEV uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 
 FQ_DEV bool odd_pair(uint32_t w) { return (w & 0x7F800000u) == 0x7F800000u || (w & 0x7F80u) == 0x7F80u; }
 FQ_DEV uint32_t finite_pair(uint32_t w) {
@@ -40,56 +47,41 @@ FQ_DEV uint32_t finite_pair(uint32_t w) {
     if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
     return w;
 }
+FQ_DEV float max_over_rows(float v) {   // over the lanes with the same lane % 4
+    v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+    v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+    return fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+}
 
-__global__ void __launch_bounds__(AR_THREADS, 3) attn_rows_kernel(const __grid_constant__ RowsArgs a) {
+__global__ void __launch_bounds__(AR_THREADS, ROWS_CTAS_SM) attn_rows_kernel(const __grid_constant__ RowsArgs a) {
     __shared__ float so[AR_WARPS][ROWS_MAX][AR_OPAD];
     __shared__ float2 sml[AR_WARPS][ROWS_MAX];
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int Hkv = a.io.Hkv, G = a.io.Hq / Hkv;
     const int item = blockIdx.x / Hkv, head = blockIdx.x % Hkv;
-    int lo = 0, hi = a.n_groups;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.g[mid].item0 <= item) lo = mid;
-        else hi = mid;
-    }
-    const RowGroup& g = a.g[lo];
-    const KvRows& kv = a.kv[lo];
+    const RowGroup& g = a.g[a.group[item]];
+    const KvRows& kv = a.kv[a.group[item]];
     const int rows = g.n_tok * G;
     const int c0 = (item - g.item0) * g.chunk;
     const int c1 = max(0, min(min(g.k_len, g.n_tok - 1 + g.off), c0 + g.chunk));
     const int first = max(0, min(g.k_len, g.off));   // keys that every row sees
     const int r = lane >> 2, c = lane & 3;
-    int limit[2];
-    const uint16_t* qrow[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int row = r + 8 * j, tok = row / G;
-        limit[j] = row < rows ? max(0, min(g.k_len, tok + g.off)) : 0;
-        qrow[j] = a.io.q + (int64_t)(g.q_row0 + tok) * a.io.q_stride + (int64_t)(head * G + row % G) * HEAD_DIM + 8 * c;
-    }
-    uint4 q[2][4];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            q[j][i] = r + 8 * j < rows ? __ldg(reinterpret_cast<const uint4*>(qrow[j] + 32 * i)) : make_uint4(0, 0, 0, 0);
 
-    const uint16_t* kb = kv.k + (int64_t)g.k_row0 * kv.row_stride + (int64_t)head * kv.head_stride;
-    const uint16_t* vb = kv.v + (int64_t)g.k_row0 * kv.row_stride + (int64_t)head * kv.head_stride;
     const int64_t rs = kv.row_stride;
+    const uint16_t* kb = kv.k + (int64_t)g.k_row0 * rs + (int64_t)head * kv.head_stride + 8 * c;
+    const uint16_t* vb = kv.v + (int64_t)g.k_row0 * rs + (int64_t)head * kv.head_stride;
     uint4 kr[2][4], vr[4][2];
-    auto load_k = [&](int k0) {
+    auto load_k = [&](int k0) {   // keys k0 + r, k0 + 8 + r: dims 32i + 8c ..
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int key = k0 + 8 * j + r;
-            const uint16_t* p = kb + (int64_t)key * rs + 8 * c;
+            const uint16_t* p = kb + (int64_t)key * rs;
 #pragma unroll
             for (int i = 0; i < 4; ++i) kr[j][i] = key < c1 ? ld_stream16(p + 32 * i) : make_uint4(0, 0, 0, 0);
         }
     };
-    auto load_v = [&](int k0) {
+    auto load_v = [&](int k0) {   // keys k0 + 2c, + 1, + 8, + 9: dims 64h + 8r ..
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int key = k0 + 2 * c + (j & 1) + 8 * (j >> 1);
@@ -98,66 +90,61 @@ __global__ void __launch_bounds__(AR_THREADS, 3) attn_rows_kernel(const __grid_c
             for (int h = 0; h < 2; ++h) vr[j][h] = key < c1 ? ld_stream16(p + 64 * h) : make_uint4(0, 0, 0, 0);
         }
     };
-    float o[16][4];
-#pragma unroll
-    for (int t = 0; t < 16; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     int k0 = c0 + 16 * warp;
     if (k0 < c1) load_k(k0);
+    uint4 q[4];   // packed row r: dims 32i + 8c ..
+    {
+        const uint16_t* p = a.io.q + (int64_t)(g.q_row0 + r / G) * a.io.q_stride + (int64_t)(head * G + r % G) * HEAD_DIM + 8 * c;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = r < rows ? __ldg(reinterpret_cast<const uint4*>(p + 32 * i)) : make_uint4(0, 0, 0, 0);
+    }
+    int limit[2];   // keys of this chunk's range that rows 2c, 2c + 1 see
+#pragma unroll
+    for (int e = 0; e < 2; ++e) limit[e] = 2 * c + e < rows ? min(c1, max(0, (2 * c + e) / G + g.off)) : 0;
+    float o[8][4];   // dims 8r + t (rows 2c, 2c + 1), 64 + 8r + t
+#pragma unroll
+    for (int t = 0; t < 8; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     for (; k0 < c1; k0 += 16 * AR_WARPS) {
         load_v(k0);
-        float s[2][4];
+        float s[4] = {0.f, 0.f, 0.f, 0.f};   // (key r, rows 2c, 2c + 1), (key 8 + r, ..)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                mma16816(s[j], q[0][i].x, q[1][i].x, q[0][i].y, q[1][i].y, kr[j][i].x, kr[j][i].y);
-                mma16816(s[j], q[0][i].z, q[1][i].z, q[0][i].w, q[1][i].w, kr[j][i].z, kr[j][i].w);
-            }
+        for (int i = 0; i < 4; ++i) {
+            mma16816(s, kr[0][i].x, kr[1][i].x, kr[0][i].y, kr[1][i].y, q[i].x, q[i].y);
+            mma16816(s, kr[0][i].z, kr[1][i].z, kr[0][i].w, kr[1][i].w, q[i].z, q[i].w);
         }
         if (k0 + 16 * AR_WARPS < c1) load_k(k0 + 16 * AR_WARPS);
-        // scores of row r (s[j][0..1]) and r + 8 (s[j][2..3]), keys k0 + 8j + 2c + {0, 1}
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                s[j][e] = k0 + 8 * j + 2 * c + (e & 1) < min(limit[e >> 1], c1) ? s[j][e] * a.c : -INFINITY;
+        for (int e = 0; e < 4; ++e) s[e] = k0 + 8 * (e >> 1) + r < limit[e & 1] ? s[e] * a.c : -INFINITY;
         float f[2];
         bool move = false;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float top = fmaxf(fmaxf(s[0][2 * j], s[0][2 * j + 1]), fmaxf(s[1][2 * j], s[1][2 * j + 1]));
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            const bool mv = top - m[j] > 8.f;   // (not at -inf - -inf)
-            f[j] = mv ? ex2(m[j] - top) : 1.f;
-            if (mv) m[j] = top;
+        for (int e = 0; e < 2; ++e) {
+            const float top = max_over_rows(fmaxf(s[e], s[2 + e]));
+            const bool mv = top - m[e] > 8.f;   // (not at -inf - -inf)
+            f[e] = mv ? ex2(m[e] - top) : 1.f;
+            if (mv) m[e] = top;
             move |= mv;
         }
         if (__any_sync(0xFFFFFFFFu, move)) {
-            l[0] *= f[0];
-            l[1] *= f[1];
 #pragma unroll
-            for (int t = 0; t < 16; ++t) {
-                o[t][0] *= f[0];
-                o[t][1] *= f[0];
-                o[t][2] *= f[1];
-                o[t][3] *= f[1];
+            for (int e = 0; e < 2; ++e) {
+                l[e] *= f[e];
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    o[t][e] *= f[e];
+                    o[t][2 + e] *= f[e];
+                }
             }
         }
-        const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            s[j][0] = ex2(s[j][0] - m0);
-            s[j][1] = ex2(s[j][1] - m0);
-            s[j][2] = ex2(s[j][2] - m1);
-            s[j][3] = ex2(s[j][3] - m1);
-            l[0] += s[j][0] + s[j][1];
-            l[1] += s[j][2] + s[j][3];
+        for (int e = 0; e < 2; ++e) {
+            const float mm = m[e] == -INFINITY ? 0.f : m[e];
+            s[e] = ex2(s[e] - mm);
+            s[2 + e] = ex2(s[2 + e] - mm);
+            l[e] += s[e] + s[2 + e];
         }
-        const uint32_t p0 = bf16x2(s[0][0], s[0][1]), p1 = bf16x2(s[0][2], s[0][3]), p2 = bf16x2(s[1][0], s[1][1]),
-                       p3 = bf16x2(s[1][2], s[1][3]);
+        const uint32_t p0 = transpose8(bf16x2(s[0], s[1])), p1 = transpose8(bf16x2(s[2], s[3]));
         bool odd = false;
         if (k0 + 16 > first) {   // some row does not see all of these keys
 #pragma unroll
@@ -175,41 +162,45 @@ __global__ void __launch_bounds__(AR_THREADS, 3) attn_rows_kernel(const __grid_c
                                               finite_pair(vr[j][h].w));
             }
         }
-        // dim 64h + 8r + e of the pieces is column r of n-tile 8h + e
+        {
+            const uint32_t w[4][2][4] = {
+                {{vr[0][0].x, vr[0][0].y, vr[0][0].z, vr[0][0].w}, {vr[0][1].x, vr[0][1].y, vr[0][1].z, vr[0][1].w}},
+                {{vr[1][0].x, vr[1][0].y, vr[1][0].z, vr[1][0].w}, {vr[1][1].x, vr[1][1].y, vr[1][1].z, vr[1][1].w}},
+                {{vr[2][0].x, vr[2][0].y, vr[2][0].z, vr[2][0].w}, {vr[2][1].x, vr[2][1].y, vr[2][1].z, vr[2][1].w}},
+                {{vr[3][0].x, vr[3][0].y, vr[3][0].z, vr[3][0].w}, {vr[3][1].x, vr[3][1].y, vr[3][1].z, vr[3][1].w}}};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t w0[4] = {vr[0][h].x, vr[0][h].y, vr[0][h].z, vr[0][h].w}, w1[4] = {vr[1][h].x, vr[1][h].y, vr[1][h].z, vr[1][h].w};
-            const uint32_t w2[4] = {vr[2][h].x, vr[2][h].y, vr[2][h].z, vr[2][h].w}, w3[4] = {vr[3][h].x, vr[3][h].y, vr[3][h].z, vr[3][h].w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t sel = e & 1 ? 0x7632u : 0x5410u;
-                mma16816(o[8 * h + e], p0, p1, p2, p3, __byte_perm(w0[e >> 1], w1[e >> 1], sel), __byte_perm(w2[e >> 1], w3[e >> 1], sel));
+            for (int t = 0; t < 8; ++t) {
+                const uint32_t sel = t & 1 ? 0x7632u : 0x5410u;
+                mma16816(o[t], __byte_perm(w[0][0][t >> 1], w[1][0][t >> 1], sel), __byte_perm(w[0][1][t >> 1], w[1][1][t >> 1], sel),
+                         __byte_perm(w[2][0][t >> 1], w[3][0][t >> 1], sel), __byte_perm(w[2][1][t >> 1], w[3][1][t >> 1], sel), p0, p1);
             }
         }
         if (odd) {
             for (int k = 0; k < 16 && k0 + k < c1; ++k) {
-                const uint16_t* p = vb + (int64_t)(k0 + k) * rs;
+                const uint16_t* p = vb + (int64_t)(k0 + k) * rs + 8 * r;
 #pragma unroll
-                for (int t = 0; t < 16; ++t)
+                for (int t = 0; t < 8; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const uint16_t b = p[64 * (t >> 3) + 8 * (2 * c + (e & 1)) + (t & 7)];
-                        if ((b & 0x7F80u) == 0x7F80u && k0 + k < limit[e >> 1]) o[t][e] += bf2f(b);
+                        const uint16_t b = p[64 * (e >> 1) + t];
+                        if ((b & 0x7F80u) == 0x7F80u && k0 + k < limit[e & 1]) o[t][e] += bf2f(b);
                     }
             }
         }
     }
     // ---- join the warps
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        l[j] += __shfl_xor_sync(0xFFFFFFFFu, l[j], 1);
-        l[j] += __shfl_xor_sync(0xFFFFFFFFu, l[j], 2);
-        if (c == 0) sml[warp][r + 8 * j] = make_float2(m[j], l[j]);
-        if (r + 8 * j < rows)
+    for (int e = 0; e < 2; ++e) {
+        l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 4);
+        l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 8);
+        l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 16);
+        if (r == 0) sml[warp][2 * c + e] = make_float2(m[e], l[e]);
+        if (2 * c + e < rows)
 #pragma unroll
-            for (int t = 0; t < 16; ++t) {
-                so[warp][r + 8 * j][64 * (t >> 3) + 16 * c + (t & 7)] = o[t][2 * j];
-                so[warp][r + 8 * j][64 * (t >> 3) + 16 * c + 8 + (t & 7)] = o[t][2 * j + 1];
+            for (int h = 0; h < 2; ++h) {
+                float4* d = reinterpret_cast<float4*>(&so[warp][2 * c + e][64 * h + 8 * r]);
+                d[0] = make_float4(o[0][2 * h + e], o[1][2 * h + e], o[2][2 * h + e], o[3][2 * h + e]);
+                d[1] = make_float4(o[4][2 * h + e], o[5][2 * h + e], o[6][2 * h + e], o[7][2 * h + e]);
             }
     }
     __syncthreads();
@@ -221,8 +212,8 @@ __global__ void __launch_bounds__(AR_THREADS, 3) attn_rows_kernel(const __grid_c
 #pragma unroll
         for (int w = 0; w < AR_WARPS; ++w) {
             const float2 ml = sml[w][row];
-            const float f = ml.x == -INFINITY && M != -INFINITY ? 0.f : ml.x == M ? 1.f : ex2(ml.x - M);
-            if (ml.x == -INFINITY && ml.y == 0.f) continue;   // saw no key (its sums are zero)
+            if (ml.x == -INFINITY && ml.y == 0.f) continue;   // saw no key, or only scores of -inf
+            const float f = ml.x == M ? 1.f : ex2(ml.x - M);
             const float4 v = *reinterpret_cast<const float4*>(&so[w][row][4 * lane]);
             L = fmaf(ml.y, f, L);
             y.x = fmaf(v.x, f, y.x);
@@ -236,8 +227,8 @@ __global__ void __launch_bounds__(AR_THREADS, 3) attn_rows_kernel(const __grid_c
             reinterpret_cast<float4*>(a.part.b_o + blk * HEAD_DIM)[lane] = y;
             if (lane == 0) a.part.b_ml[blk] = make_float2(M, L);
         } else {
-            const float inv = min(g.k_len, tok + g.off) > 0 ? 1.f / L : 0.f;
             if (min(g.k_len, tok + g.off) > 0) {
+                const float inv = 1.f / L;
                 y.x *= inv;
                 y.y *= inv;
                 y.z *= inv;
