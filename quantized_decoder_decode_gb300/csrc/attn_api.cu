@@ -77,148 +77,114 @@ KvRows rows_of(const fq_kv_view& v) {
 // ---------------------------------------------------------------- work lists
 
 // Times of attn_tiles.cu in microseconds (measured at head_dim 128 on one GB300) that the choices
-// below weigh: a key tile of a pair of query tiles and of a single one, a unit's own cost (loads
-// before its first scores, outputs), what a unit with partial results costs more, and joining
-// them: a launch and the reads.
-constexpr float T_PAIR = 1.45f, T_SINGLE = 0.85f, T_UNIT = 4.f, T_PARTIAL = 0.7f, T_JOIN = 3.f, T_JOIN_MB = 0.4f;
-// .. and of attn_rows.cu: a CTA's own cost, and megabytes of keys and values per SM
-constexpr float T_ROWS = 4.f, T_ROWS_MB = 26.f;
-// Keys per chunk of attn_rows.cu at least
-constexpr int64_t ROWS_CHUNK = 128;
+// below weigh: a key tile of a pair of query tiles and of a single one, a unit's own cost (what of
+// its loads, joins and outputs nothing hides), what partial results cost more, and
+// joining them (a launch, the reads); and reading K and V rows from memory.
+constexpr float T_PAIR = 1.45f, T_SINGLE = 0.85f, T_UNIT = 2.5f, T_PARTIAL = 0.5f, T_JOIN = 3.f,
+                T_JOIN_MB = 0.4f, T_READ_MB = 0.16f;
+constexpr int MIN_SPLIT = 4;   // key tiles of a split unit, at least
 
 struct Plan {
     std::vector<TileEntry> tiles;     // longest first
-    std::vector<RowGroup> groups;
-    std::vector<int> group_view;      // sequence whose view a group reads (-1: the prefix)
     std::vector<JoinEntry> join;
-    int64_t tile_slots = 0, row_slots = 0;
-    int row_items = 0;
+    int64_t a_slots = 0, b_slots = 0;   // partial blocks of 128 and of 8 rows
 
-    size_t tile_bytes(uint32_t Hkv) const { return (size_t)tile_slots * Hkv * TILE_ROWS * HEAD_DIM * 4; }
-    size_t row_bytes(uint32_t Hkv) const { return (size_t)row_slots * Hkv * ROWS_MAX * HEAD_DIM * 4; }
+    size_t a_bytes(uint32_t Hkv) const { return (size_t)a_slots * Hkv * TILE_ROWS * HEAD_DIM * 4; }
+    size_t b_bytes(uint32_t Hkv) const { return (size_t)b_slots * Hkv * SMALL_ROWS * HEAD_DIM * 4; }
     size_t bytes(uint32_t Hkv) const {   // values, then (m, l) pairs: 2 of every 128 + 2 floats
-        return (tile_bytes(Hkv) + row_bytes(Hkv)) / HEAD_DIM * (HEAD_DIM + 2);
+        return (a_bytes(Hkv) + b_bytes(Hkv)) / HEAD_DIM * (HEAD_DIM + 2);
     }
     Partials at(void* ws, uint32_t Hkv) const {
         Partials p;
         char* b = (char*)ws;
         p.a_o = (float*)b;
-        p.b_o = (float*)(b += tile_bytes(Hkv));
-        p.a_ml = (float2*)(b += row_bytes(Hkv));
-        p.b_ml = (float2*)(b + tile_bytes(Hkv) / HEAD_DIM * 2);
+        p.b_o = (float*)(b += a_bytes(Hkv));
+        p.a_ml = (float2*)(b += b_bytes(Hkv));
+        p.b_ml = (float2*)(b + a_bytes(Hkv) / HEAD_DIM * 2);
         return p;
-    }
-    int add_slots(int64_t& n, int64_t k) {
-        n += k;
-        return (int)(n - k);
     }
 };
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// chunk the keys of the groups so that their CTAs fill the GPU about once
-void plan_groups(Plan& p, uint32_t Hkv, bool partial) {
-    auto ctas = [&](int64_t per) {
-        int64_t n = 0;
-        for (auto& g : p.groups) n += std::max(1, ceil_div(g.k_len, per));
-        return n * Hkv;
-    };
-    int64_t keys = 0, longest = 0;
-    for (auto& g : p.groups) {
-        keys += g.k_len;
-        longest = std::max<int64_t>(longest, g.k_len);
+struct Unit {
+    int seq, tok0, n_tok, nt;   // tokens and key tiles
+    bool single, small;
+    int splits;                 // chosen
+    int slot;                   // first partial block, or -1
+    float cost(int S, bool partial) const {
+        return (single ? T_SINGLE : T_PAIR) * ceil_div(nt, S) + T_UNIT + (partial ? T_PARTIAL : 0.f);
     }
-    // the shortest chunks that still give one wave of CTAs
-    int64_t per = std::max(ROWS_CHUNK, (keys * Hkv + ROWS_CTAS - 1) / ROWS_CTAS / 64 * 64);
-    while (per < longest && ctas(per) > ROWS_CTAS) per += std::max<int64_t>(64, per / 32 / 64 * 64);
-    for (auto& g : p.groups) {
-        const int splits = std::max(1, ceil_div(g.k_len, per));
-        g.chunk = std::max(64, ceil_div(ceil_div(g.k_len, splits), 64) * 64);
-        const int n = std::max(1, ceil_div(g.k_len, g.chunk));
-        g.item0 = p.row_items;
-        p.row_items += n;
-        g.slot0 = partial || n > 1 ? p.add_slots(p.row_slots, n) : -1;
-    }
-}
-
-int splits_of(const Plan& p, size_t g) {
-    return (g + 1 < p.groups.size() ? p.groups[g + 1].item0 : p.row_items) - p.groups[g].item0;
-}
-
-struct Tiles {
-    int tok0, n_tok, nt;   // tokens and key tiles of a unit
-    int seq;
-    bool single;
 };
 
 // Units of sequence s: pairs of query tiles, or single ones.
-void add_units(std::vector<Tiles>& units, const PromptSeq& q, int s, int tpt, bool singles) {
+void add_units(std::vector<Unit>& units, const AttnSeq& q, int s, int G, bool singles) {
+    const int tpt = TILE_ROWS / G;
     const bool single = singles || q.q_len <= tpt;
     const int step = single ? tpt : 2 * tpt;
     for (int t = 0; t < q.q_len; t += step) {
         const int n_tok = std::min(step, q.q_len - t);
-        units.push_back(Tiles{t, n_tok, ceil_div(std::max(0, std::min(q.k_len, t + n_tok - 1 + q.off)), TILE_ROWS), s, single});
+        const int nt = ceil_div(std::max(0, std::min(q.k_len, t + n_tok - 1 + q.off)), TILE_ROWS);
+        units.push_back(Unit{s, t, n_tok, nt, single, q.q_len * (int64_t)G <= SMALL_ROWS, 1, -1});
     }
 }
 
-// Estimated time of the units with at most `cap` key tiles each (longer ones split): the longest
-// unit, or as many average ones as the fullest CTA gets.
-float estimate(const std::vector<Tiles>& units, int cap, int G, int Hkv) {
+// Estimated time of the units with at most `cap` key tiles each (longer ones are split): the fullest CTA
+// as the kernel deals them out, and the join.  Gives up (returns `best`) once it cannot be below that.
+float estimate(const std::vector<Unit>& units, int cap, int G, int Hkv, bool partial, float best) {
     float total = 0.f, longest = 0.f, joined_mb = 0.f;
+    struct Run { float cost; int n; };
+    Run run[256];
+    int n_runs = 0;
     int64_t n = 0;
-    for (const Tiles& u : units) {
+    for (const Unit& u : units) {
         const int S = std::max(1, ceil_div(u.nt, cap));
-        const float one = (u.single ? T_SINGLE : T_PAIR) * ceil_div(u.nt, S) + T_UNIT + (S > 1 ? T_PARTIAL : 0.f);
+        const float one = u.cost(S, partial || S > 1);
         total += S * one * Hkv;
         longest = std::max(longest, one);
         n += (int64_t)S * Hkv;
-        if (S > 1) joined_mb += S * (float)u.n_tok * G * Hkv * (HEAD_DIM * 4e-6f);
+        if (partial || S > 1) joined_mb += S * (float)u.n_tok * G * Hkv * (HEAD_DIM * 4e-6f);
+        if (n_runs && run[n_runs - 1].cost == one) run[n_runs - 1].n += S * Hkv;
+        else if (n_runs < 256) run[n_runs++] = Run{one, S * Hkv};
     }
-    const float even = total / n * ceil_div(n, ATTN_SMS);
-    // many units per CTA even out
-    return std::max(longest, n > 4 * ATTN_SMS ? total / ATTN_SMS : even) + (joined_mb > 0.f ? T_JOIN + T_JOIN_MB * joined_mb : 0.f);
+    const float join = joined_mb > 0.f ? T_JOIN + T_JOIN_MB * joined_mb : 0.f;
+    float t = std::max(longest, total / ATTN_SMS) + join;
+    if (t >= best || n <= ATTN_SMS || n > 6 * ATTN_SMS || n_runs == 256) return t;
+    std::sort(run, run + n_runs, [](const Run& a, const Run& b) { return a.cost > b.cost; });
+    float sum[ATTN_SMS] = {};
+    int i = 0, dir = 1, c = 0;
+    for (int k = 0; k < n_runs; ++k)
+        for (int e = 0; e < run[k].n; ++e, ++i) {
+            sum[c] += run[k].cost;
+            if (c + dir < 0 || c + dir >= ATTN_SMS) dir = -dir;   // forth and back
+            else c += dir;
+        }
+    return std::max(t, *std::max_element(sum, sum + ATTN_SMS) + join);
 }
 
-void plan_prompt(Plan& p, uint32_t n_seq, const PromptSeq* seq, uint32_t G, uint32_t Hkv) {
-    const int tpt = TILE_ROWS / (int)G;
-    // Sequences of a few rows go to attn_rows.cu, but for short ones beside others that need tiles:
-    // a unit more costs less than a launch more (1024 keys: 11 us of one CTA).
-    bool tiled = false;
-    for (uint32_t s = 0; s < n_seq; ++s) tiled |= (int64_t)seq[s].q_len * G > ROWS_MAX;
-    std::vector<Tiles> units, other;
-    for (uint32_t s = 0; s < n_seq; ++s) {
-        const PromptSeq& q = seq[s];
-        if (q.q_len == 0) continue;
-        if ((int64_t)q.q_len * G > ROWS_MAX || (tiled && q.k_len <= 1024)) {
-            add_units(units, q, (int)s, tpt, false);
-            continue;
-        }
-        p.groups.push_back(RowGroup{q.q_row0, q.q_len, q.k_row0, q.k_len, q.off, 0, 0, -1});
-        p.group_view.push_back((int)s);
-    }
-    plan_groups(p, Hkv, false);
-    for (size_t g = 0; g < p.groups.size(); ++g) {
-        const RowGroup& r = p.groups[g];
-        if (r.slot0 >= 0)
-            p.join.push_back(JoinEntry{r.q_row0, r.n_tok, r.k_len, r.off, 0, 0, 0, 0, r.slot0, splits_of(p, g), 0, 0, 0});
-    }
+// Pairs of query tiles share their K and V tiles, single ones give shorter units, and units may be
+// split along the keys.  Where there are few units per SM an estimate chooses (2048 tokens, 16 / 8
+// heads: single tiles 21 us, pairs 27, split pairs 33).  kv_mb: keys and values read from memory,
+// which bounds what splitting can give.
+void choose(std::vector<Unit>& units, const AttnSeq* seq, int G, int Hkv, bool partial, float kv_mb) {
     if (units.empty()) return;
-    // Pairs of query tiles share their K and V tiles, single ones give shorter units, and units may
-    // be split along the keys: with few units per SM the estimate chooses (2048 tokens, 16 / 8
-    // heads: single tiles 19 us, pairs 27, split pairs 33).
-    int longest = 0;
-    for (const Tiles& u : units) longest = std::max(longest, u.nt);
-    int cap = std::max(1, longest);
+    int longest = 1;
+    for (const Unit& u : units) longest = std::max(longest, u.nt);
+    int cap = longest;
     if ((int64_t)units.size() * Hkv < 3 * ATTN_SMS) {
-        for (const Tiles& u : units)
-            if (u.tok0 == 0) add_units(other, seq[u.seq], u.seq, tpt, true);
-        float best = 0.f;
-        bool singles = false;
-        for (int mode = 0; mode < 2; ++mode)
-            for (int k = 1; k <= 24 && (k == 1 || longest / k >= 4); ++k) {
+        std::vector<Unit> other;
+        bool pairs = false, singles = false;
+        for (const Unit& u : units) {
+            if (u.tok0 == 0) add_units(other, seq[u.seq], u.seq, G, true);
+            pairs |= !u.single;
+        }
+        const float floor = T_READ_MB * kv_mb;
+        float best = 1e30f;
+        for (int mode = 0; mode < (pairs ? 2 : 1); ++mode)
+            for (int k = 1; k <= 64 && (k == 1 || longest >= MIN_SPLIT * k); k += k < 8 ? 1 : k / 4) {
                 const int c = std::max(1, ceil_div(longest, k));
-                const float t = estimate(mode ? other : units, c, (int)G, (int)Hkv);
-                if ((mode == 0 && k == 1) || t < best) {
+                const float t = std::max(floor, estimate(mode ? other : units, c, G, Hkv, partial, best));
+                if (t < best) {
                     best = t;
                     cap = c;
                     singles = mode == 1;
@@ -226,125 +192,105 @@ void plan_prompt(Plan& p, uint32_t n_seq, const PromptSeq* seq, uint32_t G, uint
             }
         if (singles) units.swap(other);
     }
-    for (const Tiles& u : units) {
-        const int S = std::max(1, ceil_div(u.nt, cap));
-        const uint32_t info = (uint32_t)u.seq | (u.single ? TILE_SINGLE : 0u);
-        if (S == 1) {
-            p.tiles.push_back(TileEntry{u.tok0, info, 0, u.nt});
-            continue;
-        }
+    for (Unit& u : units) u.splits = std::max(1, ceil_div(u.nt, cap));
+}
+
+// Entries of the units, longest first; partial results where a unit is split or `partial` says so.
+void emit(Plan& p, std::vector<Unit>& units, bool partial) {
+    for (Unit& u : units) {
+        uint32_t info = (uint32_t)u.seq | (u.single ? TILE_SINGLE : 0u) | (u.small ? TILE_SMALL : 0u);
         const int blocks = u.single ? 1 : 2;
-        const int slot = p.add_slots(p.tile_slots, (int64_t)S * blocks);
-        for (int i = 0; i < S; ++i)
-            p.tiles.push_back(TileEntry{u.tok0, info | (uint32_t)(slot + i * blocks + 1) << 8, (int)((int64_t)u.nt * i / S),
-                                        (int)((int64_t)u.nt * (i + 1) / S)});
-        const PromptSeq& q = seq[u.seq];
-        for (int b = 0; b < blocks && b * tpt < u.n_tok; ++b)
-            p.join.push_back(JoinEntry{q.q_row0 + u.tok0 + b * tpt, std::min(tpt, u.n_tok - b * tpt), q.k_len,
-                                       q.off + u.tok0 + b * tpt, slot + b, S, blocks, 0, 0, 0, 0, 0, 0});
+        if (partial || u.splits > 1) {
+            int64_t& n = u.small ? p.b_slots : p.a_slots;
+            u.slot = (int)n;
+            n += (int64_t)u.splits * blocks;
+        }
+        for (int i = 0; i < u.splits; ++i)
+            p.tiles.push_back(TileEntry{u.tok0, info | (u.slot >= 0 ? (uint32_t)(u.slot + i * blocks + 1) << TILE_SLOT_SHIFT : 0u),
+                                        (int)((int64_t)u.nt * i / u.splits), (int)((int64_t)u.nt * (i + 1) / u.splits)});
     }
-    std::stable_sort(p.tiles.begin(), p.tiles.end(), [](const TileEntry& a, const TileEntry& b) {
-        const float ca = (a.j1 - a.j0) * (a.info & TILE_SINGLE ? T_SINGLE : T_PAIR);
-        return ca > (b.j1 - b.j0) * (b.info & TILE_SINGLE ? T_SINGLE : T_PAIR);
-    });
+    auto cost = [](const TileEntry& e) { return (e.j1 - e.j0) * (e.info & TILE_SINGLE ? T_SINGLE : T_PAIR); };
+    std::stable_sort(p.tiles.begin(), p.tiles.end(), [&](const TileEntry& a, const TileEntry& b) { return cost(a) > cost(b); });
 }
 
-// Splits of a shared prefix of nt key tiles (rows packed query rows, `units` units per kv head)
-// while row groups with `tail_mb` of keys and values run on the SMs that the units leave.
-int prefix_splits(int nt, int units, int rows, bool single, float tail_mb, int Hkv) {
-    int best_S = 1;
-    float best = 0.f;
-    for (int S = 1; S <= nt; ++S) {
-        const int ctas = units * Hkv * S;
-        const float tiles = ((single ? T_SINGLE : T_PAIR) * ceil_div(nt, S) + T_UNIT + T_PARTIAL) * ceil_div(ctas, ATTN_SMS);
-        float t = tiles;
-        if (tail_mb > 0.f) {
-            const int free = ATTN_SMS - std::min(ctas, ATTN_SMS);
-            const float alone = T_ROWS + T_ROWS_MB * tail_mb / ATTN_SMS;
-            t = tiles + alone;
-            if (free > 0) t = std::min(t, std::max(tiles, T_ROWS + T_ROWS_MB * tail_mb / free));
-        }
-        t += T_JOIN + T_JOIN_MB * (S + (tail_mb > 0.f ? 1 : 0)) * rows * Hkv * (HEAD_DIM * 4e-6f);
-        if (S == 1 || t < best) {
-            best = t;
-            best_S = S;
-        }
-        if (ctas >= 2 * ATTN_SMS) break;
-    }
-    return best_S;
-}
-
-void plan_shared(Plan& p, uint32_t n_seq, uint32_t prefix_len, const uint32_t* tail_len, uint32_t G, uint32_t Hkv) {
+void plan_prompt(Plan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G, uint32_t Hkv) {
     const int tpt = TILE_ROWS / (int)G;
-    const int P = (int)prefix_len;
-    const bool tiled = P > 0 && n_seq * G > (uint32_t)ROWS_MAX;
-    if (P > 0 && !tiled) {   // few rows: the prefix is a row group of all sequences
-        p.groups.push_back(RowGroup{0, (int)n_seq, 0, P, SEES_ALL, 0, 0, -1});
-        p.group_view.push_back(-1);
+    std::vector<Unit> units;
+    float kv_mb = 0.f;
+    for (uint32_t s = 0; s < n_seq; ++s) {
+        add_units(units, seq[s], (int)s, (int)G, false);
+        if (seq[s].q_len) kv_mb += (float)seq[s].k_len * Hkv * (HEAD_DIM * 4e-6f);
     }
-    std::vector<int> tail_group(n_seq, -1);
-    for (uint32_t s = 0; s < n_seq; ++s)
-        if (tail_len[s]) {
-            tail_group[s] = (int)p.groups.size();
-            p.groups.push_back(RowGroup{(int)s, 1, 0, (int)tail_len[s], SEES_ALL, 0, 0, -1});
-            p.group_view.push_back((int)s);
-        }
-    const bool tails = p.groups.size() > (P > 0 && !tiled ? 1u : 0u);
-    plan_groups(p, Hkv, tiled || (P > 0 && tails));
-    // the prefix as tiles: units (pairs of query tiles) x splits of the keys
-    int S = 1, blocks = 1, units = 0, slot = 0;
-    const bool single = (int)n_seq <= tpt;
-    if (tiled) {
-        units = ceil_div(n_seq, 2 * tpt);
-        blocks = single ? 1 : 2;
-        const int nt = ceil_div(P, TILE_ROWS);
-        float mb = 0.f;
-        for (uint32_t s = 0; s < n_seq; ++s) mb += (float)tail_len[s] * Hkv * (HEAD_DIM * 4e-6f);
-        S = prefix_splits(nt, units, (int)(n_seq * G), single, mb, (int)Hkv);
-        const bool partial = S > 1 || tails;
-        if (partial) slot = p.add_slots(p.tile_slots, (int64_t)S * blocks * units);
-        for (int u = 0; u < units; ++u)
-            for (int i = 0; i < S; ++i)
-                p.tiles.push_back(TileEntry{u * 2 * tpt,
-                                            (single ? TILE_SINGLE : 0u) |
-                                                (partial ? (uint32_t)(slot + (u * S + i) * blocks + 1) << 8 : 0u),
-                                            (int)((int64_t)nt * i / S), (int)((int64_t)nt * (i + 1) / S)});
-        if (!partial) return;
-    } else if (!(P > 0 && tails)) {
-        // finished by the row groups themselves, but for split groups and sequences without keys
-        for (uint32_t s = 0; s < n_seq; ++s) {
-            const int g = P > 0 ? 0 : tail_group[s];
-            if (g >= 0 && p.groups[g].slot0 < 0) continue;
-            JoinEntry e{(int)s, 1, g < 0 ? 0 : p.groups[g].k_len, SEES_ALL, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-            if (g >= 0) {
-                e.b0 = p.groups[g].slot0;
-                e.nB = splits_of(p, g);
-                e.b_row = P > 0 ? (int)(s * G) : 0;
+    choose(units, seq, (int)G, (int)Hkv, false, kv_mb);
+    emit(p, units, false);
+    for (const Unit& u : units) {
+        if (u.slot < 0) continue;
+        const AttnSeq& q = seq[u.seq];
+        const int blocks = u.single ? 1 : 2;
+        for (int b = 0; b < blocks && b * tpt < u.n_tok; ++b) {
+            JoinEntry e{q.q_row0 + u.tok0 + b * tpt, std::min(tpt, u.n_tok - b * tpt), q.k_len, q.off + u.tok0 + b * tpt,
+                        0, 0, 0, 0, 0, 0, 0, 0, 0};
+            if (u.small) {
+                e.b0 = u.slot;
+                e.nB = u.splits;
+            } else {
+                e.a0 = u.slot + b;
+                e.nA = u.splits;
+                e.a_step = blocks;
             }
             p.join.push_back(e);
         }
-        return;
     }
+}
+
+// Sequences 0 .. n_seq - 1: the tails, n_seq: all query rows over the prefix.
+void plan_shared(Plan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G, uint32_t Hkv) {
+    const int tpt = TILE_ROWS / (int)G;
+    const AttnSeq& all = seq[n_seq];
+    std::vector<Unit> units;
+    float kv_mb = (float)all.k_len * Hkv * (HEAD_DIM * 4e-6f);
+    bool tails = false, empty = false;
+    if (all.k_len) add_units(units, all, (int)n_seq, (int)G, false);
     for (uint32_t s = 0; s < n_seq; ++s) {
-        const int64_t keys = (int64_t)P + tail_len[s];
-        JoinEntry e{(int)s, 1, (int)std::min<int64_t>(keys, SEES_ALL), SEES_ALL, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-        if (tiled) {
-            const int b = (int)s / tpt;
-            e.a0 = slot + (b / blocks) * S * blocks + b % blocks;
-            e.nA = S;
-            e.a_step = blocks;
-            e.a_row = (int)(s % tpt) * (int)G;
-        } else {
-            e.b0 = p.groups[0].slot0;
-            e.nB = splits_of(p, 0);
-            e.b_row = (int)(s * G);
-        }
-        if (tail_group[s] >= 0) {
-            e.c0 = p.groups[tail_group[s]].slot0;
-            e.nC = splits_of(p, tail_group[s]);
-        }
-        p.join.push_back(e);
+        if (seq[s].k_len) add_units(units, seq[s], (int)s, (int)G, false);
+        kv_mb += (float)seq[s].k_len * Hkv * (HEAD_DIM * 4e-6f);
+        tails |= seq[s].k_len > 0;
+        empty |= seq[s].k_len == 0;
     }
+    const bool partial = all.k_len && tails;   // both: joined
+    choose(units, seq, (int)G, (int)Hkv, partial, kv_mb);
+    emit(p, units, partial);
+    // where the partial results of each sequence are
+    std::vector<JoinEntry> e(n_seq);
+    for (uint32_t s = 0; s < n_seq; ++s)
+        e[s] = JoinEntry{(int)s, 1, (int)std::min<int64_t>((int64_t)all.k_len + seq[s].k_len, SEES_ALL), SEES_ALL,
+                         0, 0, 0, 0, 0, 0, 0, 0, 0};
+    bool any = !all.k_len && empty;   // sequences without a key: zeros from the join
+    for (const Unit& u : units) {
+        if (u.slot < 0) continue;
+        any = true;
+        if (u.seq < (int)n_seq) {
+            e[u.seq].c0 = u.slot;
+            e[u.seq].nC = u.splits;
+            continue;
+        }
+        for (int i = 0; i < u.n_tok; ++i) {
+            JoinEntry& j = e[u.tok0 + i];
+            if (u.small) {
+                j.b0 = u.slot;
+                j.nB = u.splits;
+                j.b_row = i * (int)G;
+            } else {
+                j.a0 = u.slot + i / tpt;
+                j.nA = u.splits;
+                j.a_step = u.single ? 1 : 2;
+                j.a_row = i % tpt * (int)G;
+            }
+        }
+    }
+    if (!any) return;
+    for (const JoinEntry& j : e)   // (the units finished the others themselves)
+        if (j.nA || j.nB || j.nC || j.k_len == 0) p.join.push_back(j);
 }
 
 // ---------------------------------------------------------------- launches
@@ -370,10 +316,14 @@ fq_status encode_rows(void* map_k, void* map_v, const KvRows& r, uint64_t rows, 
     return FQ_OK;
 }
 
-// views[s]: the rows of sequence s (views[0] for all when one is given), used: rows it is read up to
+struct ViewUse {
+    KvRows rows;
+    uint64_t used = 0;   // rows it is read up to
+};
+
 template <class Args>
-fq_status run_tiles(const Plan& p, const AttnIo& io, const Partials& part, const PromptSeq* seq, int n_seq, int q_rows,
-                    const KvRows* views, int n_views, const uint64_t* used, cudaStream_t s) {
+fq_status run_tiles_t(const Plan& p, const AttnIo& io, const Partials& part, const AttnSeq* seq, int n_seq, int q_rows,
+                      const ViewUse* views, int n_views, cudaStream_t s) {
     TRY(prepare_device());
     Args* a = new (std::nothrow) Args;
     if (!a) return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
@@ -390,7 +340,7 @@ fq_status run_tiles(const Plan& p, const AttnIo& io, const Partials& part, const
         const uint32_t box[4] = {64, (uint32_t)G, 1, (uint32_t)(TILE_ROWS / G)};
         if (!encode_bf16_tiles(a->map_q, io.q, 4, dims, strides, box)) return fail(FQ_ERR_CUDA, "tensor map of q refused");
         for (int v = 0; v < n_views; ++v)
-            if (used[v]) TRY(encode_rows(a->map_k[v], a->map_v[v], views[v], used[v], io.Hkv));
+            if (views[v].used) TRY(encode_rows(a->map_k[v], a->map_v[v], views[v].rows, views[v].used, io.Hkv));
         constexpr size_t NE = Args::ENTRIES;
         for (size_t e0 = 0; e0 < p.tiles.size(); e0 += NE) {
             a->n_entries = (int)std::min(NE, p.tiles.size() - e0);
@@ -405,29 +355,13 @@ fq_status run_tiles(const Plan& p, const AttnIo& io, const Partials& part, const
     return st;
 }
 
-fq_status run_one_view(const Plan& p, const AttnIo& io, const Partials& part, const PromptSeq* seq, int n_seq, int q_rows,
-                       const KvRows* view, const uint64_t* used, cudaStream_t s) {
-    return p.tiles.size() <= (size_t)TileArgsS::ENTRIES ? run_tiles<TileArgsS>(p, io, part, seq, n_seq, q_rows, view, 1, used, s)
-                                                        : run_tiles<TileArgs1>(p, io, part, seq, n_seq, q_rows, view, 1, used, s);
-}
-
-fq_status run_groups(const Plan& p, const AttnIo& io, const Partials& part, const KvRows* views, const KvRows* prefix,
-                     cudaStream_t s) {
-    if (p.groups.empty()) return FQ_OK;
-    RowsArgs a;
-    a.io = io;
-    a.c = io.scale * 1.4426950408889634f;
-    a.part = part;
-    a.n_groups = (int)p.groups.size();
-    a.n_items = p.row_items;
-    for (size_t g = 0; g < p.groups.size(); ++g) {
-        a.g[g] = p.groups[g];
-        std::fill(a.group + p.groups[g].item0, a.group + p.groups[g].item0 + splits_of(p, g), (uint8_t)g);
-        a.kv[g] = p.group_view[g] < 0 ? *prefix : views[p.group_view[g]];
-    }
-    launch_attn_rows(a, !p.tiles.empty(), s);
-    CK(cudaGetLastError());
-    return FQ_OK;
+fq_status run_tiles(const Plan& p, const AttnIo& io, const Partials& part, const AttnSeq* seq, int n_seq, int q_rows,
+                    const ViewUse* views, int n_views, cudaStream_t s) {
+    if (p.tiles.empty()) return FQ_OK;
+    const size_t n = p.tiles.size();
+    auto run = n_views == 1 ? (n <= TileArgs1S::ENTRIES ? run_tiles_t<TileArgs1S> : run_tiles_t<TileArgs1>)
+                            : (n <= TileArgsNS::ENTRIES && n_views <= TileArgsNS::VIEWS ? run_tiles_t<TileArgsNS> : run_tiles_t<TileArgsN>);
+    return run(p, io, part, seq, n_seq, q_rows, views, n_views, s);
 }
 
 template <class Args>
@@ -535,22 +469,21 @@ fq_status fq_qk_norm_rope(const float* qkv, uint64_t qkv_stride, uint32_t n_seq,
 
 // Row ranges of the sequences of a prompt call; views may be null (lengths only).
 static fq_status prompt_sequences(uint32_t n_seq, const uint32_t* q_len, const uint32_t* kv_row0, const uint32_t* k_len,
-                                  const fq_kv_view* views, uint32_t n_views, uint32_t Hkv, PromptSeq* seq, KvRows* kv,
-                                  uint64_t* used, uint64_t* q_rows) {
+                                  const fq_kv_view* views, uint32_t n_views, uint32_t Hkv, AttnSeq* seq, ViewUse* use,
+                                  uint64_t* q_rows) {
     uint64_t qr = 0, kr = 0;
     for (uint32_t s = 0; s < n_seq; ++s) {
         if (q_len[s] > MAX_ROWS || k_len[s] > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 rows");
         uint64_t r0 = 0;
+        const uint32_t w = n_views == 1 ? 0 : s;
         if (views) {
-            const uint32_t w = n_views == 1 ? 0 : s;
             r0 = kv_row0 ? kv_row0[s] : n_views == 1 ? kr : 0;
             TRY(check_view(views[w], Hkv, r0, k_len[s], "sequence", s));
-            kv[s] = rows_of(views[w]);
-            if (s == w) used[w] = 0;
-            if (k_len[s]) used[w] = std::max(used[w], r0 + k_len[s]);
+            use[w].rows = rows_of(views[w]);
+            if (k_len[s]) use[w].used = std::max(use[w].used, r0 + k_len[s]);
         }
-        seq[s] = PromptSeq{(int32_t)qr, (int32_t)q_len[s], (int32_t)r0, (int32_t)k_len[s],
-                           (int32_t)k_len[s] - (int32_t)q_len[s] + 1};
+        seq[s] = AttnSeq{(int32_t)qr, (int32_t)q_len[s], (int32_t)r0, (int32_t)k_len[s],
+                         (int32_t)k_len[s] - (int32_t)q_len[s] + 1, (int32_t)w};
         qr += q_len[s];
         kr += k_len[s];
         if (qr > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 query rows");
@@ -564,9 +497,9 @@ fq_status fq_attn_prompt_workspace(uint32_t n_seq, const uint32_t* q_len, const 
     TRY(check_heads(num_attention_heads, num_key_value_heads));
     TRY(check_count(n_seq));
     if (!q_len || !k_len || !bytes) return fail(FQ_ERR_INVALID_ARGUMENT, "null argument");
-    PromptSeq seq[MAX_SEQ];
+    AttnSeq seq[MAX_SEQ];
     uint64_t q_rows;
-    TRY(prompt_sequences(n_seq, q_len, nullptr, k_len, nullptr, 0, num_key_value_heads, seq, nullptr, nullptr, &q_rows));
+    TRY(prompt_sequences(n_seq, q_len, nullptr, k_len, nullptr, 0, num_key_value_heads, seq, nullptr, &q_rows));
     try {
         Plan p;
         plan_prompt(p, n_seq, seq, num_attention_heads / num_key_value_heads, num_key_value_heads);
@@ -586,10 +519,10 @@ fq_status fq_attn_prompt(const void* q, uint64_t q_stride, const fq_kv_view* vie
     TRY(check_count(n_seq));
     if (!q_len || !k_len || !views) return fail(FQ_ERR_INVALID_ARGUMENT, "null argument");
     if (n_views != 1 && n_views != n_seq) return fail(FQ_ERR_INVALID_ARGUMENT, "%u views for %u sequences", n_views, n_seq);
-    PromptSeq seq[MAX_SEQ];
-    KvRows kv[MAX_SEQ];
-    uint64_t used[MAX_SEQ], q_rows = 0;
-    TRY(prompt_sequences(n_seq, q_len, kv_row0, k_len, views, n_views, Hkv, seq, kv, used, &q_rows));
+    AttnSeq seq[MAX_SEQ];
+    ViewUse use[MAX_SEQ];
+    uint64_t q_rows = 0;
+    TRY(prompt_sequences(n_seq, q_len, kv_row0, k_len, views, n_views, Hkv, seq, use, &q_rows));
     try {
         Plan p;
         plan_prompt(p, n_seq, seq, Hq / Hkv, Hkv);
@@ -599,14 +532,23 @@ fq_status fq_attn_prompt(const void* q, uint64_t q_stride, const fq_kv_view* vie
         if (q_rows == 0) return FQ_OK;
         const Partials part = p.at(workspace, Hkv);
         cudaStream_t s = (cudaStream_t)stream;
-        if (!p.tiles.empty())
-            TRY(n_views == 1 ? run_one_view(p, io, part, seq, (int)n_seq, (int)q_rows, kv, used, s)
-                             : run_tiles<TileArgsN>(p, io, part, seq, (int)n_seq, (int)q_rows, kv, (int)n_views, used, s));
-        TRY(run_groups(p, io, part, kv, nullptr, s));
+        TRY(run_tiles(p, io, part, seq, (int)n_seq, (int)q_rows, use, (int)n_views, s));
         return run_join(p, io, part, s);
     } catch (const std::bad_alloc&) {
         return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
     }
+}
+
+// The sequences of a shared call: the tails, then all query rows over the prefix.
+static fq_status shared_sequences(uint32_t n_seq, uint32_t prefix_len, const uint32_t* tail_len, AttnSeq* seq) {
+    if (prefix_len > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 rows");
+    int32_t view = 1;
+    for (uint32_t s = 0; s < n_seq; ++s) {
+        if (tail_len[s] > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 rows");
+        seq[s] = AttnSeq{(int32_t)s, 1, 0, (int32_t)tail_len[s], SEES_ALL, tail_len[s] ? view++ : 0};
+    }
+    seq[n_seq] = AttnSeq{0, (int32_t)n_seq, 0, (int32_t)prefix_len, SEES_ALL, 0};
+    return FQ_OK;
 }
 
 fq_status fq_attn_shared_workspace(uint32_t n_seq, uint32_t prefix_len, const uint32_t* tail_len,
@@ -614,12 +556,11 @@ fq_status fq_attn_shared_workspace(uint32_t n_seq, uint32_t prefix_len, const ui
     TRY(check_heads(num_attention_heads, num_key_value_heads));
     TRY(check_count(n_seq));
     if (!tail_len || !bytes) return fail(FQ_ERR_INVALID_ARGUMENT, "null argument");
-    if (prefix_len > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 rows");
-    for (uint32_t s = 0; s < n_seq; ++s)
-        if (tail_len[s] > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 rows");
+    AttnSeq seq[MAX_SEQS];
+    TRY(shared_sequences(n_seq, prefix_len, tail_len, seq));
     try {
         Plan p;
-        plan_shared(p, n_seq, prefix_len, tail_len, num_attention_heads / num_key_value_heads, num_key_value_heads);
+        plan_shared(p, n_seq, seq, num_attention_heads / num_key_value_heads, num_key_value_heads);
         *bytes = p.bytes(num_key_value_heads);
     } catch (const std::bad_alloc&) {
         return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
@@ -635,32 +576,32 @@ fq_status fq_attn_shared(const void* q, uint64_t q_stride, uint32_t n_seq, const
     TRY(check_heads(Hq, Hkv));
     TRY(check_count(n_seq));
     if (!tail_len) return fail(FQ_ERR_INVALID_ARGUMENT, "null argument");
-    KvRows first, kv[MAX_SEQ];
+    ViewUse use[MAX_SEQS];
+    int n_views = 1;   // the prefix is view 0
     if (prefix_len) {
         if (!prefix) return fail(FQ_ERR_INVALID_ARGUMENT, "null prefix");
         TRY(check_view(*prefix, Hkv, 0, prefix_len, "prefix", 0));
-        first = rows_of(*prefix);
+        use[0].rows = rows_of(*prefix);
+        use[0].used = prefix_len;
     }
     for (uint32_t s = 0; s < n_seq; ++s) {
         if (!tail_len[s]) continue;
         if (!tails) return fail(FQ_ERR_INVALID_ARGUMENT, "null tails");
         TRY(check_view(tails[s], Hkv, 0, tail_len[s], "tail", s));
-        kv[s] = rows_of(tails[s]);
+        use[n_views].rows = rows_of(tails[s]);
+        use[n_views++].used = tail_len[s];
     }
+    AttnSeq seq[MAX_SEQS];
+    TRY(shared_sequences(n_seq, prefix_len, tail_len, seq));
     try {
         Plan p;
-        plan_shared(p, n_seq, prefix_len, tail_len, Hq / Hkv, Hkv);
+        plan_shared(p, n_seq, seq, Hq / Hkv, Hkv);
         AttnIo io;
         TRY(attn_common(q, q_stride, Hq, Hkv, scale, out, out_stride, out_dtype, n_seq, workspace, workspace_bytes,
                         p.bytes(Hkv), io));
         const Partials part = p.at(workspace, Hkv);
         cudaStream_t s = (cudaStream_t)stream;
-        if (!p.tiles.empty()) {
-            const PromptSeq all{0, (int32_t)n_seq, 0, (int32_t)prefix_len, SEES_ALL};
-            const uint64_t used = prefix_len;
-            TRY(run_one_view(p, io, part, &all, 1, (int)n_seq, &first, &used, s));
-        }
-        TRY(run_groups(p, io, part, kv, &first, s));
+        TRY(run_tiles(p, io, part, seq, (int)n_seq + 1, (int)n_seq, use, n_views, s));
         return run_join(p, io, part, s);
     } catch (const std::bad_alloc&) {
         return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");

@@ -13,7 +13,7 @@
 //   S_A | S_B | PV_A S_A' | PV_B S_B' | ...
 // Tensor memory: S_A, S_B (128 columns each; the weights P overwrite the first 64 as bf16 pairs
 // and are the A operand of P V straight from there), O_A, O_B (128 columns each): all 512.
-// Shared memory: Q (2 x 32 KB), a ring of five 32 KB stages for K and V tiles of 128 keys.
+// Shared memory: Q (2 x 32 KB), three 32 KB stages for K tiles and two for V tiles of 128 keys.
 //
 // Roles (384 threads, one CTA per SM, looping over its units):
 //   warps 0-3, 4-7  softmax of tile A / B, one row per thread, and the outputs
@@ -35,14 +35,17 @@ namespace fq {
 namespace {
 
 constexpr int AT_THREADS = 384;
-constexpr int AT_STAGES = 5;
+constexpr int AT_KS = 3, AT_VS = 2, AT_STAGES = AT_KS + AT_VS;   // stages for K and for V tiles
 constexpr int AT_TILE_BYTES = TILE_ROWS * HEAD_DIM * 2;   // 32 KB
 constexpr int AT_PANEL = AT_TILE_BYTES / 2;               // 64 dims of 128 rows
 constexpr uint32_t AT_S = 0, AT_P = 128, AT_O = 256;      // tensor-memory columns: S, P_A, P_B (64 each), O_A, O_B
 
 struct AtShared {
     uint64_t q_full, q_empty, join;
-    uint64_t full[AT_STAGES], empty[AT_STAGES], raw[AT_STAGES];
+    // One warp consumes K tiles and another V tiles, and a phase bit tells a waiter only whether the
+    // phase it waits for or the one before is the current one: each has stages of its own, so that it
+    // has always seen the phase before.
+    uint64_t k_full[AT_KS], k_empty[AT_KS], v_full[AT_VS], v_empty[AT_VS], v_raw[AT_VS];
     uint64_t s_full[2], p_full[2], o_done[2], s_free;
     uint32_t tmem, abort, preloaded;
     uint32_t done[8];                     // units that each softmax warp has finished
@@ -59,7 +62,7 @@ __device__ uint32_t g_attn_waits;   // waits that gave up, since the last check
 // One unit as every role sees it.
 struct Unit {
     int seq, head, slot;          // slot: first partial block + 1, or 0
-    bool single;
+    bool single, small;
     int tok[2], n_tok[2];         // tokens of tile A / B
     int j0;                       // first key tile
     int n[2];                     // key tiles of warpgroup A / B
@@ -78,10 +81,11 @@ FQ_DEV Unit unit_of(const Args& a, int w) {
     const TileEntry& e = a.e[w / a.io.Hkv];
     const int G = a.io.Hq / a.io.Hkv, tpt = TILE_ROWS / G;
     u.head = w % a.io.Hkv;
-    u.seq = e.info & 63;
+    u.seq = e.info & 127;
     u.single = (e.info & TILE_SINGLE) != 0;
-    u.slot = (int)(e.info >> 8);
-    const PromptSeq& s = a.seq[u.seq];
+    u.small = (e.info & TILE_SMALL) != 0;
+    u.slot = (int)(e.info >> TILE_SLOT_SHIFT);
+    const AttnSeq& s = a.seq[u.seq];
     u.tok[0] = e.tok0;
     u.tok[1] = e.tok0 + (u.single ? 0 : tpt);
     u.j0 = e.j0;
@@ -106,14 +110,9 @@ FQ_DEV Unit unit_of(const Args& a, int w) {
     return u;
 }
 
-// Ring position of V tile t of a unit: each follows the K tile whose scores are made before its
-// product (pair: K0 K1 V0 K2 V1 ..; single: K0 K1 K2 V0 K3 V1 ..)
-FQ_DEV int k_at(const Unit& u, int t) { return t + max(0, t - u.step); }
-FQ_DEV int v_at(const Unit& u, int t) { return t + min(t + 1 + u.step, u.nt); }
-
 // By one thread: the unit's query tiles; one K or V tile.
 template <class Args>
-FQ_DEV void load_q(const Args& a, const Unit& u, const PromptSeq& sq, uint8_t* q_sm, AtShared* sh) {
+FQ_DEV void load_q(const Args& a, const Unit& u, const AttnSeq& sq, uint8_t* q_sm, AtShared* sh) {
     const int q0 = u.n[0] > 0 ? 0 : 1, q1 = u.single || u.n[1] == 0 ? 1 : 2;
     mbar_arrive_expect_tx(&sh->q_full, (uint32_t)((q1 - q0) * AT_TILE_BYTES));
     for (int x = q0; x < q1; ++x) {
@@ -211,10 +210,14 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
             for (int i = 0; i < 8; ++i) sh->done[i] = 0;
             mbar_init(&sh->join, 8);
             mbar_init(&sh->s_free, 4);
-            for (int s = 0; s < AT_STAGES; ++s) {
-                mbar_init(&sh->full[s], 1);
-                mbar_init(&sh->empty[s], 1);
-                mbar_init(&sh->raw[s], 1);
+            for (int s = 0; s < AT_KS; ++s) {
+                mbar_init(&sh->k_full[s], 1);
+                mbar_init(&sh->k_empty[s], 1);
+            }
+            for (int s = 0; s < AT_VS; ++s) {
+                mbar_init(&sh->v_full[s], 1);
+                mbar_init(&sh->v_empty[s], 1);
+                mbar_init(&sh->v_raw[s], 1);
             }
             for (int x = 0; x < 2; ++x) {
                 mbar_init(&sh->s_full[x], 1);
@@ -229,12 +232,12 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
         }
         __syncwarp();
         const Unit u = unit_of(a, blockIdx.x);
-        const PromptSeq& sq = a.seq[u.seq];
-        const int vw = Args::VIEWS == 1 ? 0 : u.seq;
+        const AttnSeq& sq = a.seq[u.seq];
+        const int vw = Args::VIEWS == 1 ? 0 : sq.view;
         const bool pre = u.nt > 0 && sh->abort == 0;
         if (pre && elect_one()) {
             load_q(a, u, sq, q_sm, sh);
-            load_kv(a.map_k[vw], ring, sq.k_row0 + u.j0 * TILE_ROWS, u.head, &sh->full[0]);
+            load_kv(a.map_k[vw], ring, sq.k_row0 + u.j0 * TILE_ROWS, u.head, &sh->k_full[0]);
         }
         if (lane == 0) sh->preloaded = pre;
         __syncwarp();
@@ -255,11 +258,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
         // ---------------- loads
         // Q and the first K tile of the first unit are on their way: neither is waited for again
         // here (their release may come before this warp gets to it)
-        uint32_t pos = sh->preloaded, qn = sh->preloaded, it = 0;
+        uint32_t kn = sh->preloaded, vn = 0, qn = sh->preloaded, it = 0;   // K and V tiles, Q tiles, units
         bool ok = true;
         for (int w; (w = unit_at(it)) < units && ok; ++it) {
             const Unit u = unit_of(a, w);
-            const PromptSeq& sq = a.seq[u.seq];
+            const AttnSeq& sq = a.seq[u.seq];
             if (it >= 2 && !(ok = units_done(it - 1, lane, sh))) break;   // all but the unit before
             if (u.nt == 0) continue;
             const bool pre = it == 0;
@@ -269,22 +272,39 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
                 if (elect_one()) load_q(a, u, sq, q_sm, sh);
                 __syncwarp();
             }
-            const int vw = Args::VIEWS == 1 ? 0 : u.seq;
-            auto load = [&](bool v, int t) {
-                const int s = pos % AT_STAGES;
-                if (!(ok = at_wait_warp(&sh->empty[s], ((pos / AT_STAGES) & 1) ^ 1, sh))) return;
-                ++pos;
-                uint64_t* bar = v && u.j0 + t >= u.jm ? &sh->raw[s] : &sh->full[s];
-                const void* map = v ? a.map_v[vw] : a.map_k[vw];
-                if (elect_one()) load_kv(map, ring + s * AT_TILE_BYTES, sq.k_row0 + (u.j0 + t) * TILE_ROWS, u.head, bar);
+            const int vw = Args::VIEWS == 1 ? 0 : sq.view;
+            auto load_k = [&](int t) {
+                const int s = kn % AT_KS;
+                if (!(ok = at_wait_warp(&sh->k_empty[s], ((kn / AT_KS) & 1) ^ 1, sh))) return;
+                ++kn;
+                if (elect_one())
+                    load_kv(a.map_k[vw], ring + s * AT_TILE_BYTES, sq.k_row0 + (u.j0 + t) * TILE_ROWS, u.head, &sh->k_full[s]);
                 __syncwarp();
             };
-            for (int t = pre ? 1 : 0; t < u.step && t < u.nt && ok; ++t) load(false, t);
+            auto load_v = [&](int t) {
+                const int s = vn % AT_VS;
+                if (!(ok = at_wait_warp(&sh->v_empty[s], ((vn / AT_VS) & 1) ^ 1, sh))) return;
+                ++vn;
+                if (elect_one())
+                    load_kv(a.map_v[vw], ring + (AT_KS + s) * AT_TILE_BYTES, sq.k_row0 + (u.j0 + t) * TILE_ROWS, u.head,
+                            u.j0 + t >= u.jm ? &sh->v_raw[s] : &sh->v_full[s]);
+                __syncwarp();
+            };
+            // in the order of their use: a pair makes the scores of one tile ahead of the values, a
+            // single unit of two
+            for (int t = pre ? 1 : 0; t < u.step && t < u.nt && ok; ++t) load_k(t);
             for (int t = 0; t < u.nt && ok; ++t) {
-                if (t + u.step < u.nt) load(false, t + u.step);
-                if (ok) load(true, t);
+                if (t + u.step < u.nt) load_k(t + u.step);
+                if (ok) load_v(t);
             }
         }
+        // The products' arrivals at these barriers come by themselves: the CTA's shared memory must
+        // not be given to another CTA before the last of them.
+        for (uint32_t n = kn > AT_KS ? kn - AT_KS : 0; n < kn && ok; ++n)
+            ok = at_wait_warp(&sh->k_empty[n % AT_KS], (n / AT_KS) & 1, sh);
+        for (uint32_t n = vn > AT_VS ? vn - AT_VS : 0; n < vn && ok; ++n)
+            ok = at_wait_warp(&sh->v_empty[n % AT_VS], (n / AT_VS) & 1, sh);
+        if (qn && ok) ok = at_wait_warp(&sh->q_empty, (qn - 1) & 1, sh);
         if (!ok) {
             // No copy may still be landing when the CTA exits.  A role gave up after a quarter
             // second of waiting; copies that were issued land within microseconds of that.
@@ -296,16 +316,16 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
         // ---------------- scores
         const uint32_t idesc = idesc_bf16_f32(TILE_ROWS, TILE_ROWS, false, a.negate != 0);
         const uint64_t dq0 = sdesc_sw128(smem_u32(q_sm)), dk0 = sdesc_sw128(smem_u32(ring));
-        uint32_t pos0 = 0, qn = 0, sn = 0, it = 0;   // sn: score tiles
+        uint32_t kn = 0, qn = 0, sn = 0, it = 0;   // K tiles, Q tiles, score tiles, units
         bool ok = true;
         for (int w; (w = unit_at(it)) < units && ok; ++it) {
             const Unit u = unit_of(a, w);
             if (u.nt == 0) continue;
             if (!(ok = at_wait_warp(&sh->q_full, qn++ & 1, sh))) break;
             for (int t = 0; t < u.nt && ok; ++t) {
-                const uint32_t pos = pos0 + k_at(u, t);
-                const int s = pos % AT_STAGES;
-                if (!(ok = at_wait_warp(&sh->full[s], (pos / AT_STAGES) & 1, sh))) break;
+                const int s = kn % AT_KS;
+                if (!(ok = at_wait_warp(&sh->k_full[s], (kn / AT_KS) & 1, sh))) break;
+                ++kn;
                 for (int x = 0; x < 2; ++x) {
                     if (u.single ? x != (t & 1) : t >= u.n[x]) continue;
                     // the scores before are in registers
@@ -325,25 +345,24 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
                 }
                 if (!ok) break;
                 if (elect_one()) {
-                    mma_commit(&sh->empty[s]);
+                    mma_commit(&sh->k_empty[s]);
                     if (t + 1 == u.nt) mma_commit(&sh->q_empty);
                 }
                 __syncwarp();
             }
-            pos0 += 2 * u.nt;
         }
     } else if (warp == 11) {
         // ---------------- values
         const uint32_t idesc = idesc_bf16_f32(TILE_ROWS, HEAD_DIM, true, false);
-        const uint64_t dv0 = sdesc_sw128_mn(smem_u32(ring), AT_PANEL);
-        uint32_t pos0 = 0, pc = 0, it = 0;   // pc: parities of p_full
+        const uint64_t dv0 = sdesc_sw128_mn(smem_u32(ring + AT_KS * AT_TILE_BYTES), AT_PANEL);
+        uint32_t vn = 0, pc = 0, it = 0;   // V tiles; pc: parities of p_full
         bool ok = true;
         for (int w; (w = unit_at(it)) < units && ok; ++it) {
             const Unit u = unit_of(a, w);
             for (int t = 0; t < u.nt && ok; ++t) {
-                const uint32_t pos = pos0 + v_at(u, t);
-                const int s = pos % AT_STAGES;
-                if (!(ok = at_wait_warp(&sh->full[s], (pos / AT_STAGES) & 1, sh))) break;
+                const int s = vn % AT_VS;
+                if (!(ok = at_wait_warp(&sh->v_full[s], (vn / AT_VS) & 1, sh))) break;
+                ++vn;
                 for (int x = 0; x < 2; ++x) {
                     if (u.single ? x != (t & 1) : t >= u.n[x]) continue;
                     if (!(ok = at_wait_warp(&sh->p_full[x], (pc >> x) & 1, sh))) break;
@@ -361,23 +380,22 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
                     __syncwarp();
                 }
                 if (!ok) break;
-                if (elect_one()) mma_commit(&sh->empty[s]);
+                if (elect_one()) mma_commit(&sh->v_empty[s]);
                 __syncwarp();
             }
-            pos0 += 2 * u.nt;
         }
     } else if (warp == 10) {
         // ---------------- partly seen V tiles
-        uint32_t pos0 = 0, it = 0, raw_ph = 0;
+        uint32_t vn = 0, it = 0, raw_ph = 0;
         bool ok = true;
         for (int w; (w = unit_at(it)) < units && ok; ++it) {
             const Unit u = unit_of(a, w);
             const int k_len = a.seq[u.seq].k_len;
             for (int t = max(0, u.jm - u.j0); t < u.nt; ++t) {
-                const int s = (pos0 + v_at(u, t)) % AT_STAGES;
-                if (!(ok = at_wait_warp(&sh->raw[s], (raw_ph >> s) & 1, sh))) break;
+                const int s = (vn + t) % AT_VS;
+                if (!(ok = at_wait_warp(&sh->v_raw[s], (raw_ph >> s) & 1, sh))) break;
                 raw_ph ^= 1u << s;
-                uint8_t* tile = ring + s * AT_TILE_BYTES;
+                uint8_t* tile = ring + (AT_KS + s) * AT_TILE_BYTES;
                 // x * 0 is NaN where x is not finite (rows before `from` are seen by every row)
                 const int from = max(0, min(k_len, u.tok[0] + a.seq[u.seq].off) - (u.j0 + t) * TILE_ROWS);
                 uint32_t z[4] = {0, 0, 0, 0};
@@ -422,9 +440,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
                     fence_async_smem();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->full[s]);
+                if (lane == 0) mbar_arrive(&sh->v_full[s]);
             }
-            pos0 += 2 * u.nt;
+            vn += u.nt;
         }
     }
     } else {
@@ -449,7 +467,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
         };
         for (int w; (w = unit_at(it)) < units && ok; ++it) {
             const Unit u = unit_of(a, w);
-            const PromptSeq& sq = a.seq[u.seq];
+            const AttnSeq& sq = a.seq[u.seq];
             const int tok = u.tok[x] + row / G;
             const bool valid = row / G < u.n_tok[x];
             const int limit = valid ? max(0, min(sq.k_len, tok + sq.off)) : 0;   // keys the row sees
@@ -559,7 +577,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
             const float inv = u.slot || limit == 0 ? 1.f : 1.f / lsum;
             const int64_t o_row = (int64_t)(sq.q_row0 + tok);
             const int64_t o_col = (int64_t)(u.head * G + row % G) * HEAD_DIM;
-            const int64_t blk = ((int64_t)(u.slot - 1 + (u.single ? 0 : x)) * a.io.Hkv + u.head) * TILE_ROWS + row;
+            const int64_t blk = (int64_t)(u.slot - 1 + (u.single ? 0 : x)) * a.io.Hkv + u.head;   // partial block
+            const int R = u.small ? SMALL_ROWS : TILE_ROWS;
             const bool have = u.single ? u.nt > 0 : u.n[x] > 0;
             float o[TILE_ROWS];   // pair: the row's 128 dims; single: 64 dims of O_A, then of O_B
             __syncwarp();
@@ -595,9 +614,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
                 }
                 if (!valid) return;
                 if (u.slot) {
-                    float* dst = a.part.a_o + (blk - row) * HEAD_DIM + ((d >> 3) * TILE_ROWS + row) * 8;
+                    float* dst = (u.small ? a.part.b_o : a.part.a_o) + (blk * HEAD_DIM + d) * R + row * 8;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) st_global32(dst + k * TILE_ROWS * 8, reinterpret_cast<uint32_t*>(y) + 8 * k);
+                    for (int k = 0; k < 4; ++k) st_global32(dst + k * R * 8, reinterpret_cast<uint32_t*>(y) + 8 * k);
                 } else if (a.io.out_f32) {
                     st_row<32>((float*)a.io.out + o_row * a.io.out_stride + o_col + d, reinterpret_cast<uint32_t*>(y), wide);
                 } else {
@@ -614,7 +633,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
 #pragma unroll
                 for (int h = 0; h < 4; ++h) store(o + 32 * h, 32 * h);
             }
-            if (u.slot && valid && (!u.single || x == 0)) a.part.a_ml[blk] = make_float2(mref * c, lsum);
+            if (u.slot && valid && (!u.single || x == 0))
+                (u.small ? a.part.b_ml : a.part.a_ml)[blk * R + row] = make_float2(mref * c, lsum);
             // the next unit's products may overwrite O once both warpgroups have read it
             tc_fence_before();
             if (u.single && !(ok = join())) break;
@@ -644,8 +664,9 @@ cudaError_t prepare_t() {
 }  // namespace
 
 cudaError_t attn_tiles_prepare() {
-    cudaError_t e = prepare_t<TileArgsS>();
+    cudaError_t e = prepare_t<TileArgs1S>();
     if (e == cudaSuccess) e = prepare_t<TileArgs1>();
+    if (e == cudaSuccess) e = prepare_t<TileArgsNS>();
     return e != cudaSuccess ? e : prepare_t<TileArgsN>();
 }
 
@@ -655,7 +676,8 @@ void launch_tiles(const Args& a, cudaStream_t s) {
     const int grid = (int)(units < ATTN_SMS ? units : ATTN_SMS);
     attn_tiles_kernel<Args><<<grid, AT_THREADS, AT_SMEM, s>>>(a);
 }
-template void launch_tiles<TileArgsS>(const TileArgsS&, cudaStream_t);
+template void launch_tiles<TileArgs1S>(const TileArgs1S&, cudaStream_t);
+template void launch_tiles<TileArgsNS>(const TileArgsNS&, cudaStream_t);
 template void launch_tiles<TileArgs1>(const TileArgs1&, cudaStream_t);
 template void launch_tiles<TileArgsN>(const TileArgsN&, cudaStream_t);
 
