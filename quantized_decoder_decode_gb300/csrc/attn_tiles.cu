@@ -173,17 +173,17 @@ FQ_DEV void st_global32(void* p, const uint32_t* v) {
                  "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
 }
-// N words (a multiple of 8) to a 16-byte aligned address, 32 bytes at a time where that is aligned
+// N pieces of 32 bytes, `step` bytes apart, at 32-byte (wide) or 16-byte aligned addresses
 template <int N>
-FQ_DEV void st_row(void* p, const uint32_t* v, bool wide) {
+FQ_DEV void st_pieces(uint8_t* p, int64_t step, const uint32_t* v, bool wide) {
 #pragma unroll
-    for (int k = 0; k < N; k += 8) {
-        uint32_t* d = (uint32_t*)p + k;
+    for (int k = 0; k < N; ++k) {
         if (wide) {
-            st_global32(d, v + k);
+            st_global32(p + k * step, v + 8 * k);
         } else {
-            reinterpret_cast<uint4*>(d)[0] = make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-            reinterpret_cast<uint4*>(d)[1] = make_uint4(v[k + 4], v[k + 5], v[k + 6], v[k + 7]);
+            uint4* d = reinterpret_cast<uint4*>(p + k * step);
+            d[0] = make_uint4(v[8 * k], v[8 * k + 1], v[8 * k + 2], v[8 * k + 3]);
+            d[1] = make_uint4(v[8 * k + 4], v[8 * k + 5], v[8 * k + 6], v[8 * k + 7]);
         }
     }
 }
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
                     const float f = move ? ex2((m - top) * c) : 1.f;
                     if (move) m = top;
                     l *= f;
-#pragma unroll
+#pragma unroll 1
                     for (int h = 0; h < 8; ++h) {
                         uint32_t o[16];
                         tmem_ld16(tO + 16 * h, o);
@@ -575,63 +575,67 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
             const bool noted = *(volatile uint32_t*)&sh->poison_unit[it & 1] == it + 1;
             const int seen = limit - u.jm * TILE_ROWS;   // noted keys below this are the row's
             const float inv = u.slot || limit == 0 ? 1.f : 1.f / lsum;
-            const int64_t o_row = (int64_t)(sq.q_row0 + tok);
-            const int64_t o_col = (int64_t)(u.head * G + row % G) * HEAD_DIM;
+            f0 *= inv;
+            f1 *= inv;
+            // where the row goes, 32 dims at a time: 32-byte pieces `step` bytes apart
             const int64_t blk = (int64_t)(u.slot - 1 + (u.single ? 0 : x)) * a.io.Hkv + u.head;   // partial block
             const int R = u.small ? SMALL_ROWS : TILE_ROWS;
-            const bool have = u.single ? u.nt > 0 : u.n[x] > 0;
-            float o[TILE_ROWS];   // pair: the row's 128 dims; single: 64 dims of O_A, then of O_B
-            __syncwarp();
-            if (have) {
-                const uint32_t t0 = tm + AT_O + lane_base + (u.single ? 64 * x : 128 * x);
-                const uint32_t t1 = t0 + (u.single ? 128 : 64);
-                tmem_ld32(t0, reinterpret_cast<uint32_t*>(o));
-                tmem_ld32(t0 + 32, reinterpret_cast<uint32_t*>(o) + 32);
-                tmem_ld32(t1, reinterpret_cast<uint32_t*>(o) + 64);
-                tmem_ld32(t1 + 32, reinterpret_cast<uint32_t*>(o) + 96);
-                tmem_wait_ld();
-            } else {
+            const int d0 = u.single ? 64 * x : 0;
+            const bool f32 = u.slot || a.io.out_f32;
+            uint8_t* dst = u.slot ? (uint8_t*)((u.small ? a.part.b_o : a.part.a_o) + (blk * HEAD_DIM + d0) * R + row * 8)
+                                  : (uint8_t*)a.io.out + ((int64_t)(sq.q_row0 + tok) * a.io.out_stride +
+                                                          (int64_t)(u.head * G + row % G) * HEAD_DIM + d0) * (f32 ? 4 : 2);
+            const int64_t step = u.slot ? R * 32 : 32;
+            const bool wide32 = u.slot || wide;
+            const bool have = u.single ? u.nt > 0 : u.n[x] > 0, two = u.single && u.nt > 1;
+            const uint32_t t0 = tm + AT_O + lane_base + (u.single ? 0 : 128 * x) + d0;
+            // (a short loop: its instructions are fetched anew for every unit)
+#pragma unroll 1
+            for (int h = 0; h < (u.single ? 2 : 4); ++h) {
+                uint32_t o[32];
+                __syncwarp();
+                if (have) {
+                    tmem_ld32(t0 + 32 * h, o);
+                    tmem_wait_ld();
+                    if (two) {
+                        uint32_t o1[32];
+                        tmem_ld32(t0 + 128 + 32 * h, o1);
+                        tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < TILE_ROWS; ++k) o[k] = 0.f;
-            }
-            if (u.single) {
-                f0 *= inv;
-                f1 *= inv;
+                        for (int k = 0; k < 32; ++k)
+                            o[k] = __float_as_uint(fmaf(__uint_as_float(o1[k]), f1, __uint_as_float(o[k]) * f0));
+                    } else {
 #pragma unroll
-                for (int k = 0; k < 64; ++k) o[k] = u.nt > 1 ? fmaf(o[64 + k], f1, o[k] * f0) : o[k] * f0;
-            } else {
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f0);
+                    }
+                } else {
 #pragma unroll
-                for (int k = 0; k < TILE_ROWS; ++k) o[k] *= inv;
-            }
-            auto store = [&](float* y, int d) {   // 32 dims from d
-                if (noted) {
+                    for (int k = 0; k < 32; ++k) o[k] = 0;
+                }
+                if (valid) {
+                    if (f32) {
+                        st_pieces<4>(dst, step, o, wide32);
+                        dst += 4 * step;
+                    } else {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        if (sh->poison[it & 1][2][d + k] < seen) y[k] = NAN;
-                        if (sh->poison[it & 1][0][d + k] < seen) y[k] += INFINITY;
-                        if (sh->poison[it & 1][1][d + k] < seen) y[k] -= INFINITY;
+                        for (int k = 0; k < 16; ++k) o[k] = bf16x2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
+                        st_pieces<2>(dst, step, o, wide32);
+                        dst += 2 * step;
                     }
                 }
-                if (!valid) return;
-                if (u.slot) {
-                    float* dst = (u.small ? a.part.b_o : a.part.a_o) + (blk * HEAD_DIM + d) * R + row * 8;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) st_global32(dst + k * R * 8, reinterpret_cast<uint32_t*>(y) + 8 * k);
-                } else if (a.io.out_f32) {
-                    st_row<32>((float*)a.io.out + o_row * a.io.out_stride + o_col + d, reinterpret_cast<uint32_t*>(y), wide);
-                } else {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) p[k] = bf16x2(y[2 * k], y[2 * k + 1]);
-                    st_row<16>((uint16_t*)a.io.out + o_row * a.io.out_stride + o_col + d, p, wide);
+            }
+            if (noted && valid) {   // values that are not finite, for the rows that see them
+                const int dn = u.single ? 64 : HEAD_DIM;
+                dst -= dn / 8 * step / (f32 ? 1 : 2);
+                for (int d = 0; d < dn; ++d) {
+                    const uint16_t(*note)[HEAD_DIM] = sh->poison[it & 1];
+                    const float add = (note[0][d0 + d] < seen ? INFINITY : 0.f) + (note[1][d0 + d] < seen ? -INFINITY : 0.f) +
+                                      (note[2][d0 + d] < seen ? NAN : 0.f);
+                    if (add == 0.f) continue;
+                    uint8_t* at = dst + (f32 ? (d >> 3) * step + (d & 7) * 4 : (d >> 4) * step + (d & 15) * 2);
+                    if (f32) *(float*)at += add;
+                    else *(__nv_bfloat16*)at = __float2bfloat16_rn(__bfloat162float(*(__nv_bfloat16*)at) + add);
                 }
-            };
-            if (u.single) {
-                store(o, 64 * x);
-                store(o + 32, 64 * x + 32);
-            } else {
-#pragma unroll
-                for (int h = 0; h < 4; ++h) store(o + 32 * h, 32 * h);
             }
             if (u.slot && valid && (!u.single || x == 0))
                 (u.small ? a.part.b_ml : a.part.a_ml)[blk * R + row] = make_float2(mref * c, lsum);
