@@ -207,12 +207,39 @@ fq_status fq_decode_step_all_logits(const fq_model* m, fq_kv* kv, const int32_t*
 fq_status fq_decode_greedy(const fq_model* m, fq_kv* const* caches, uint32_t n, const int32_t* first_tokens,
                            uint32_t n_steps, int32_t* tokens_out, float* logits, void* stream);
 
+/* forwardStep over the prompts (or parts of prompts) of n sequences at once: sequence s appends
+ * its len[s] >= 1 tokens (host; tokens holds the sequences' ids one after the other) at positions
+ * fq_kv_len(caches[s]) .. of caches[s], n <= 64 distinct bf16 caches of this model; the logits of
+ * each sequence's last row go to `logits` (device f32 [n][vocab]; NULL: append only).  Every cache
+ * advances by its len.  The rows run in passes of up to 2048: the projections read each weight
+ * from memory about once per pass, and the attention is fq_qk_norm_rope and fq_attn_prompt
+ * below (q rounded to bf16, tensor cores), so that a prompt's attention costs a small part of
+ * what it costs in fq_forward_step's passes of 32 rows.  Equal, up to rounding, to one
+ * fq_forward_step per sequence.  Errors (state unchanged): INVALID_SEQUENCE_LENGTH (n = 0,
+ * len[s] = 0), KV_CACHE_OVERFLOW, MISMATCHED_KV_CACHES, INVALID_ARGUMENT, UNSUPPORTED (f32 or q8_0
+ * caches).  After a CUDA error the cache lengths cover the passes enqueued. */
+fq_status fq_forward_step_packed(const fq_model* m, fq_kv* const* caches, uint32_t n, const int32_t* tokens,
+                                 const uint32_t* len, float* logits, void* stream);
+
+/* forwardStepBatch behind one prompt that all n sequences share: `prefix` (a bf16 cache of this
+ * model, read only) holds the positions 0 .. P - 1 of every sequence, P = its len, and caches[s]
+ * only what follows them: row i of caches[s] is position P + i.  One token per sequence (host
+ * tokens [n]) is appended to caches[s] at position P + len; logits: device f32 [n][vocab] or NULL.
+ * The attention is fq_qk_norm_rope and fq_attn_shared below, which read the prefix once for all
+ * sequences.  Equal, up to rounding, to fq_decode_step_batch on caches that hold copies of the
+ * prefix.  P must stay what it was when caches[s] was filled; a cache filled here is of use behind
+ * that prefix alone.  Errors (state unchanged): INVALID_SEQUENCE_LENGTH (n = 0, P + len at
+ * max_positions), KV_CACHE_OVERFLOW, MISMATCHED_KV_CACHES (also: the prefix among the caches),
+ * INVALID_ARGUMENT, UNSUPPORTED (f32 or q8_0 caches). */
+fq_status fq_decode_step_shared(const fq_model* m, const fq_kv* prefix, fq_kv* const* caches, uint32_t n,
+                                const int32_t* tokens, float* logits, void* stream);
+
 /* ---- prompt and shared-prompt attention over caller-held rows ----
  *
  * The attention of a prompt (and of many answers to one prompt) as operators on device
- * buffers, next to the decode steps above, which fuse theirs.  head_dim is 128, K and V are
- * bf16, query groups (num_attention_heads / num_key_value_heads) are 1, 2, 4 or 8, and a call
- * takes up to 64 sequences.  Host arrays are read during the call only.  Nothing is allocated
+ * buffers: what fq_forward_step_packed and fq_decode_step_shared are made of.  head_dim is 128,
+ * K and V are bf16, query groups (num_attention_heads / num_key_value_heads) are 1, 2, 4 or 8, and
+ * a call takes up to 64 sequences.  Host arrays are read during the call only.  Nothing is allocated
  * and nothing outlives a call but its outputs, so calls may be captured into CUDA graphs; a
  * workspace belongs to one call at a time (calls, or replayed graphs, that overlap on
  * different streams need workspaces of their own).  Outputs must not overlap inputs. */
@@ -285,7 +312,8 @@ fq_status fq_attn_shared_workspace(uint32_t n_seq, uint32_t prefix_len, const ui
 
 /* Synchronise `stream` and report bounded device waits of the two attentions that gave up on the
  * current device since the last check (DEVICE_TIMEOUT: the outputs of the calls since then are
- * invalid); clears the record.  The counterpart of fq_check_device for calls without a model. */
+ * invalid); clears the record.  fq_check_device reads (and clears) the same record next to its
+ * model's own. */
 fq_status fq_attn_check(void* stream);
 
 /* ---- inspection (tests and tools; not the hot path) ---- */
@@ -384,7 +412,8 @@ fq_status fq_step_kernels(const fq_model* m, void* stream, uint32_t* kernels);
  * FQ_ERR_DEVICE_TIMEOUT when a kernel's bounded wait on its own copy pipeline or on another
  * CTA gave up (the kernel returned early; results of that step are invalid).  Clears the
  * record and, on a timeout, zeroes the arrival counters and tickets of every workspace of
- * the model (on each workspace's own stream), so that later steps start from a clean state. */
+ * the model (on each workspace's own stream), so that later steps start from a clean state.
+ * Waits of the attention operators (fq_attn_check) are reported and cleared too. */
 fq_status fq_check_device(const fq_model* m, void* stream);
 
 /* Test hook for the failure path of the bounded device waits (no counterpart on the pages).

@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "api_util.h"
+#include "attn_plan.h"
 #include "fq.h"
 #include "kernels.h"
 
@@ -114,6 +115,18 @@ struct Workspace {
     };
     std::vector<Graph> graphs;
     uint32_t last_kernels = 0; // kernels of the step most recently replayed on this stream
+    // the rows of a packed or shared-prefix step (its own allocations; no graph holds them)
+    struct Rows {
+        int cap = 0;           // rows the buffers hold
+        size_t attn_cap = 0;   // bytes of attn_ws
+        float *x = nullptr, *qkv = nullptr, *attn = nullptr, *h = nullptr, *last = nullptr;
+        void *q = nullptr, *attn_ws = nullptr;
+        std::vector<void*> allocs;
+    } rows;
+    void drop_rows() {
+        for (void* p : rows.allocs) cudaFree(p);
+        rows = Rows();
+    }
     void drop_graphs() {
         for (auto& g : graphs) cudaGraphExecDestroy(g.exec);
         graphs.clear();
@@ -122,6 +135,7 @@ struct Workspace {
         drop_graphs();
         for (void* p : allocs) cudaFree(p);
         allocs.clear();
+        drop_rows();
     }
 };
 
@@ -247,6 +261,33 @@ fq_status rearm_ws(const fq_model* m, Workspace* w, cudaStream_t s) {
     return FQ_OK;
 }
 
+// Buffers for `rows` rows of a packed or shared-prefix step and its attention workspace.
+fq_status ensure_rows(const fq_model* m, Workspace* w, int rows, size_t attn_bytes, cudaStream_t s) {
+    Workspace::Rows& r = w->rows;
+    if (r.cap >= rows && r.attn_cap >= attn_bytes) return FQ_OK;
+    rows = std::max(rows, r.cap);
+    attn_bytes = std::max(attn_bytes, r.attn_cap);
+    CK(cudaStreamSynchronize(s));   // steps queued on the stream still use the old ones
+    w->drop_rows();
+    const auto& p = m->d.p;
+    const size_t n = rows;
+    auto& A = r.allocs;
+    uint16_t* q;
+    uint8_t* ws;
+    TRY(dalloc(A, &r.x, n * p.hidden_size));
+    TRY(dalloc(A, &r.qkv, n * m->qkv_rows()));
+    TRY(dalloc(A, &q, n * p.num_attention_heads * HEAD_DIM));
+    TRY(dalloc(A, &r.attn, n * p.num_attention_heads * HEAD_DIM));
+    if (!m->moe()) TRY(dalloc(A, &r.h, n * p.intermediate_size));
+    TRY(dalloc(A, &r.last, (size_t)MAX_SEQ * p.hidden_size));
+    TRY(dalloc(A, &ws, attn_bytes));
+    r.q = q;
+    r.attn_ws = ws;
+    r.cap = rows;
+    r.attn_cap = attn_bytes;
+    return FQ_OK;
+}
+
 enum Mode { MODE_DECODE = 1, MODE_GREEDY = 2 };
 
 struct Body {
@@ -276,6 +317,62 @@ bool stream_eligible(const Body& b, int kv_type) {
            b.head_row < 0 && kv_type == KV_BF16;
 }
 
+// Dense projection: tensor cores for lockstep batches, the GEMV kernels otherwise.
+template <class Pdl>
+void project(const fq_model* m, Workspace* w, GemvArgs& g, cudaStream_t s, Pdl&& pdl) {
+    g.err = m->err;
+    if (m->opt_tc && w->xh && gemm_tc_applicable(g)) {
+        const bool p0 = pdl();
+        launch_gemm_tc(g, w->xh, w->tc_part, TC_PART_FLOATS, w->tc_tickets, s, p0, m->opt_pdl != 0);
+    } else {
+        launch_gemv(g, s, pdl());
+    }
+}
+
+GemvArgs dense_args(const QMat& W, int n, const float* x, int x_stride, float* y, int y_stride, int epi) {
+    GemvArgs g;
+    g.W = W;
+    g.B = n;
+    g.x = x;
+    g.x_stride = x_stride;
+    g.y = y;
+    g.y_stride = y_stride;
+    g.epi = epi;
+    g.ksplit = choose_ksplit(W, rows_per_warp(W));
+    return g;
+}
+
+// The routed FFN of n rows of x, in place.
+template <class Pdl>
+void enqueue_moe(const fq_model* m, Workspace* w, const LayerW& lw, int n, float* x, cudaStream_t s, Pdl&& pdl) {
+    const auto& p = m->d.p;
+    const int H = p.hidden_size, E = p.num_experts, k = p.num_experts_used, Fe = p.moe_intermediate_size;
+    GemvArgs r;
+    r.W = lw.router; r.B = n; r.x = x; r.x_stride = H; r.norm_g = lw.ffn_norm; r.eps = p.rms_norm_eps;
+    r.y = w->rlogits; r.y_stride = E; r.epi = EPI_STORE; r.xn_out = w->xn; r.xn_stride = H;
+    r.ksplit = choose_ksplit(r.W, 4);
+    r.err = m->err;
+    launch_gemv(r, s, pdl());
+    launch_moe_route(w->rlogits, E, k, n, p.norm_topk_prob, w->route, s, pdl());
+
+    GemvArgs eg;
+    eg.W = lw.gate_up_exps; eg.x = w->xn; eg.x_stride = H; eg.y = w->he; eg.y_stride = Fe;
+    eg.epi = EPI_SWIGLU; eg.route = w->route; eg.moe_k = k; eg.rows_per_expert = 2 * Fe; eg.x_by_pair = 0;
+    eg.max_experts = std::min(E, n * k);
+    eg.ksplit = 1;
+    eg.err = m->err;
+    launch_gemv(eg, s, pdl());
+
+    GemvArgs ed;
+    ed.W = lw.down_exps; ed.x = w->he; ed.x_stride = Fe; ed.y = w->ye; ed.y_stride = H; ed.epi = EPI_STORE;
+    ed.route = w->route; ed.moe_k = k; ed.rows_per_expert = H; ed.x_by_pair = 1;
+    ed.max_experts = std::min(E, n * k);
+    ed.ksplit = 2;
+    ed.err = m->err;
+    launch_gemv(ed, s, pdl());
+    launch_moe_combine(x, w->ye, w->route, n, k, H, s, pdl());
+}
+
 // The kernels of one decode step, in order.  The first launch follows the set-up kernel
 // with ordinary stream order; every later one uses programmatic dependent launch.
 fq_status enqueue_step(const Body& b, cudaStream_t s, int kv_type, float* x_override, int layer_only) {
@@ -287,18 +384,8 @@ fq_status enqueue_step(const Body& b, cudaStream_t s, int kv_type, float* x_over
     // Programmatic dependent launch is an option (off by default: measured on GB300 the
     // early-resident CTAs of the next kernel slowed the step down)
     const bool use_pdl = m->opt_pdl != 0;
-    const bool no_tc = m->opt_tc == 0;
     auto pdl = [&]() { bool r = !first && use_pdl; first = false; return r; };
-    // dense projection: tensor cores for lockstep batches, the GEMV kernels otherwise
-    auto proj = [&](GemvArgs& g) {
-        g.err = m->err;
-        if (!no_tc && w->xh && gemm_tc_applicable(g)) {
-            const bool p0 = pdl();
-            launch_gemm_tc(g, w->xh, w->tc_part, TC_PART_FLOATS, w->tc_tickets, s, p0, use_pdl);
-        } else {
-            launch_gemv(g, s, pdl());
-        }
-    };
+    auto proj = [&](GemvArgs& g) { project(m, w, g, s, pdl); };
     float* x = x_override ? x_override : w->x;
 
     // batch 1 of a dense model: the whole step as one streamed persistent kernel
@@ -366,31 +453,8 @@ fq_status enqueue_step(const Body& b, cudaStream_t s, int kv_type, float* x_over
             dn.epi = EPI_ADD; dn.ksplit = choose_ksplit(dn.W, rows_per_warp(dn.W));
             proj(dn);
         } else {
-            const int E = p.num_experts, k = p.num_experts_used, Fe = p.moe_intermediate_size;
-            GemvArgs r;
-            r.W = lw.router; r.B = n; r.x = x; r.x_stride = H; r.norm_g = lw.ffn_norm; r.eps = p.rms_norm_eps;
-            r.y = w->rlogits; r.y_stride = E; r.epi = EPI_STORE; r.xn_out = w->xn; r.xn_stride = H;
-            r.ksplit = choose_ksplit(r.W, 4);
-            r.err = m->err;
-            launch_gemv(r, s, pdl());
-            launch_moe_route(w->rlogits, E, k, n, p.norm_topk_prob, w->route, s, pdl());
-
-            GemvArgs eg;
-            eg.W = lw.gate_up_exps; eg.x = w->xn; eg.x_stride = H; eg.y = w->he; eg.y_stride = Fe;
-            eg.epi = EPI_SWIGLU; eg.route = w->route; eg.moe_k = k; eg.rows_per_expert = 2 * Fe; eg.x_by_pair = 0;
-            eg.max_experts = std::min(E, n * k);
-            eg.ksplit = 1;
-            eg.err = m->err;
-            launch_gemv(eg, s, pdl());
-
-            GemvArgs ed;
-            ed.W = lw.down_exps; ed.x = w->he; ed.x_stride = Fe; ed.y = w->ye; ed.y_stride = H; ed.epi = EPI_STORE;
-            ed.route = w->route; ed.moe_k = k; ed.rows_per_expert = H; ed.x_by_pair = 1;
-            ed.max_experts = std::min(E, n * k);
-            ed.ksplit = 2;
-            ed.err = m->err;
-            launch_gemv(ed, s, pdl());
-            launch_moe_combine(x, w->ye, w->route, n, k, H, s, pdl());
+            const int E = p.num_experts, k = p.num_experts_used;
+            enqueue_moe(m, w, lw, n, x, s, pdl);
 
             if (b.route_idx) {
                 CK(cudaMemcpyAsync(b.route_idx + (size_t)L * n * k, w->route->idx, sizeof(int32_t) * n * k,
@@ -528,6 +592,118 @@ uint32_t max_cap(fq_kv* const* caches, uint32_t n) {
     uint32_t c = 0;
     for (uint32_t i = 0; i < n; ++i) c = std::max(c, caches[i]->cap);
     return c;
+}
+
+// ---------------------------------------------------------------- packed rows of several sequences
+
+// Rows of one pass of a packed step (buffers of about 200 MB for hidden 4096, FFN 12288), and
+// rows per launch of the projections: the lockstep batch that the tensor-core GEMM is built for.
+constexpr uint32_t PASS_ROWS = 2048;
+constexpr uint32_t PROJ_ROWS = 32;
+
+// One pass: sequence s has len[s] rows at positions pos[s] .., its K and V go to rows row0[s] .. of
+// kv[s], and it attends to rows 0 .. row0[s] + len[s] - 1 (behind `prefix` in a shared-prefix step,
+// where len[s] = 1).
+struct RowsPass {
+    const int32_t* tokens = nullptr;   // host, one per row
+    uint32_t n_seq = 0, rows = 0;
+    uint32_t len[MAX_SEQ], pos[MAX_SEQ], row0[MAX_SEQ], k_len[MAX_SEQ];
+    const fq_kv* kv[MAX_SEQ];
+    const fq_kv* prefix = nullptr;
+    void add(const fq_kv* c, uint32_t n, uint32_t at, uint32_t position) {
+        kv[n_seq] = c;
+        len[n_seq] = n;
+        row0[n_seq] = at;
+        pos[n_seq] = position;
+        k_len[n_seq] = at + n;
+        ++n_seq;
+        rows += n;
+    }
+};
+
+fq_status rows_attn_bytes(const fq_model* m, const RowsPass& r, size_t* bytes) {
+    const uint32_t Hq = m->d.p.num_attention_heads, Hkv = m->d.p.num_key_value_heads;
+    return r.prefix ? fq_attn_shared_workspace(r.n_seq, r.prefix->len, r.k_len, Hq, Hkv, bytes)
+                    : fq_attn_prompt_workspace(r.n_seq, r.len, r.k_len, Hq, Hkv, bytes);
+}
+
+// Embedding and every layer of one pass; the residual rows end up in w->rows.x.  Each projection
+// goes over all rows before the next one, so that its weights come from L2 after the first chunk.
+fq_status enqueue_rows(const fq_model* m, Workspace* w, const RowsPass& r, cudaStream_t s) {
+    const auto& p = m->d.p;
+    const Workspace::Rows& b = w->rows;
+    const int H = p.hidden_size, Hq = p.num_attention_heads, Hkv = p.num_key_value_heads, D = Hq * HEAD_DIM;
+    const int N3 = m->qkv_rows(), F = p.intermediate_size;
+    auto pdl = [] { return false; };
+    auto chunks = [&](auto&& f) {
+        for (uint32_t o = 0; o < r.rows; o += PROJ_ROWS) f((size_t)o, (int)std::min(PROJ_ROWS, r.rows - o));
+    };
+    chunks([&](size_t o, int n) {
+        SetupArgs a;
+        memset(&a, 0, sizeof a);
+        a.n = n;
+        for (int i = 0; i < n; ++i) a.token[i] = r.tokens[o + i];
+        launch_setup(w->st, a, s);
+        launch_embed(m->tok_embd, w->st, n, b.x + o * H, s, false);
+    });
+    const float scale = 1.f / sqrtf((float)HEAD_DIM);
+    for (uint32_t L = 0; L < p.num_layers; ++L) {
+        const LayerW& lw = m->layers[L];
+        chunks([&](size_t o, int n) {
+            GemvArgs g = dense_args(lw.qkv, n, b.x + o * H, H, b.qkv + o * N3, N3, EPI_STORE);
+            g.norm_g = lw.attn_norm;
+            g.eps = p.rms_norm_eps;
+            project(m, w, g, s, pdl);
+        });
+        fq_kv_view views[MAX_SEQ], shared;
+        for (uint32_t i = 0; i < r.n_seq; ++i) TRY(fq_kv_layer_view(r.kv[i], L, &views[i]));
+        TRY(fq_qk_norm_rope(b.qkv, N3, r.n_seq, r.len, r.pos, views, r.n_seq, r.row0, Hq, Hkv, lw.q_norm, lw.k_norm,
+                            p.rms_norm_eps, reinterpret_cast<const float*>(m->rope), (uint32_t)m->max_pos, b.q, 0, s));
+        if (r.prefix) {
+            TRY(fq_kv_layer_view(r.prefix, L, &shared));
+            TRY(fq_attn_shared(b.q, 0, r.n_seq, &shared, r.prefix->len, views, r.k_len, Hq, Hkv, scale, b.attn, 0, FQ_F32,
+                               b.attn_ws, b.attn_cap, s));
+        } else {
+            const uint32_t zero[MAX_SEQ] = {};
+            TRY(fq_attn_prompt(b.q, 0, views, r.n_seq, r.n_seq, r.len, zero, r.k_len, Hq, Hkv, scale, b.attn, 0, FQ_F32,
+                               b.attn_ws, b.attn_cap, s));
+        }
+        chunks([&](size_t o, int n) {
+            GemvArgs g = dense_args(lw.o, n, b.attn + o * D, D, b.x + o * H, H, EPI_ADD);
+            project(m, w, g, s, pdl);
+        });
+        if (m->moe()) {
+            chunks([&](size_t o, int n) { enqueue_moe(m, w, lw, n, b.x + o * H, s, pdl); });
+            continue;
+        }
+        chunks([&](size_t o, int n) {
+            GemvArgs g = dense_args(lw.gate_up, n, b.x + o * H, H, b.h + o * F, F, EPI_SWIGLU);
+            g.norm_g = lw.ffn_norm;
+            g.eps = p.rms_norm_eps;
+            project(m, w, g, s, pdl);
+        });
+        chunks([&](size_t o, int n) {
+            GemvArgs g = dense_args(lw.down, n, b.h + o * F, F, b.x + o * H, H, EPI_ADD);
+            project(m, w, g, s, pdl);
+        });
+    }
+    CK(cudaGetLastError());
+    return FQ_OK;
+}
+
+// LM head of n rows.
+fq_status enqueue_head(const fq_model* m, Workspace* w, const float* x, uint32_t n, float* logits, cudaStream_t s) {
+    const auto& p = m->d.p;
+    for (uint32_t o = 0; o < n; o += PROJ_ROWS) {
+        GemvArgs g = dense_args(m->output, (int)std::min(PROJ_ROWS, n - o), x + (size_t)o * p.hidden_size, p.hidden_size,
+                                logits + (size_t)o * p.vocab_size, p.vocab_size, EPI_STORE);
+        g.norm_g = m->output_norm;
+        g.eps = p.rms_norm_eps;
+        g.st = w->st;
+        project(m, w, g, s, [] { return false; });
+    }
+    CK(cudaGetLastError());
+    return FQ_OK;
 }
 
 // ---------------------------------------------------------------- loading
@@ -1054,6 +1230,99 @@ fq_status fq_forward_step(const fq_model* m, fq_kv* kv, const int32_t* tokens, u
     return FQ_OK;
 }
 
+fq_status fq_forward_step_packed(const fq_model* m, fq_kv* const* caches, uint32_t n, const int32_t* tokens,
+                                 const uint32_t* len, float* logits, void* stream) {
+    TRY(check_caches(m, caches, n, 0));
+    if (!len) return fail(FQ_ERR_INVALID_ARGUMENT, "null len");
+    if (logits && !m->output.q) return fail(FQ_ERR_INVALID_ARGUMENT, "model has no LM head");
+    if (caches[0]->type != KV_BF16) return fail(FQ_ERR_UNSUPPORTED, "packed steps take bf16 caches");
+    uint32_t total = 0, start[MAX_SEQ];
+    for (uint32_t i = 0; i < n; ++i) {
+        start[i] = caches[i]->len;
+        if (len[i] == 0) return fail(FQ_ERR_INVALID_SEQUENCE_LENGTH, "sequence %u has no tokens", i);
+        if ((uint64_t)caches[i]->len + len[i] > caches[i]->cap)
+            return fail(FQ_ERR_KV_CACHE_OVERFLOW, "cache %u: len %u + %u > capacity %u", i, caches[i]->len, len[i], caches[i]->cap);
+        total += len[i];   // at most 64 x max_positions
+    }
+    TRY(check_tokens(m, tokens, total));
+    cudaStream_t s = (cudaStream_t)stream;
+    Workspace* w;
+    TRY(ensure_ws(m, s, (int)std::min(total, PROJ_ROWS), 1, &w));
+    // f(pass, its first sequence, the first sequence whose last row is not in it)
+    auto passes = [&](auto&& f) -> fq_status {
+        uint32_t seq = 0, done = 0;   // the next row: of sequence `seq`, its row `done`
+        for (uint32_t off = 0; off < total;) {
+            RowsPass r;
+            r.tokens = tokens + off;
+            const uint32_t s0 = seq;
+            while (seq < n && r.rows < PASS_ROWS) {
+                const uint32_t take = std::min(len[seq] - done, PASS_ROWS - r.rows), at = start[seq] + done;
+                r.add(caches[seq], take, at, at);
+                done += take;
+                if (done < len[seq]) break;
+                ++seq;
+                done = 0;
+            }
+            TRY(f(r, s0, seq));
+            off += r.rows;
+        }
+        return FQ_OK;
+    };
+    size_t bytes = 0;
+    TRY(passes([&](const RowsPass& r, uint32_t, uint32_t) -> fq_status {
+        size_t need;
+        TRY(rows_attn_bytes(m, r, &need));
+        bytes = std::max(bytes, need);
+        return FQ_OK;
+    }));
+    TRY(ensure_rows(m, w, (int)std::min(total, PASS_ROWS), bytes, s));
+    const size_t H = m->d.p.hidden_size;
+    TRY(passes([&](const RowsPass& r, uint32_t s0, uint32_t s1) -> fq_status {
+        TRY(enqueue_rows(m, w, r, s));
+        uint32_t row = 0;
+        for (uint32_t i = 0; i < r.n_seq; ++i) {
+            caches[s0 + i]->len += r.len[i];
+            row += r.len[i];
+            if (logits && s0 + i < s1)
+                CK(cudaMemcpyAsync(w->rows.last + (s0 + i) * H, w->rows.x + (row - 1) * H, H * sizeof(float),
+                                   cudaMemcpyDeviceToDevice, s));
+        }
+        return FQ_OK;
+    }));
+    return logits ? enqueue_head(m, w, w->rows.last, n, logits, s) : FQ_OK;
+}
+
+fq_status fq_decode_step_shared(const fq_model* m, const fq_kv* prefix, fq_kv* const* caches, uint32_t n,
+                                const int32_t* tokens, float* logits, void* stream) {
+    TRY(check_caches(m, caches, n, 1));
+    if (!prefix) return fail(FQ_ERR_INVALID_ARGUMENT, "null prefix");
+    if (prefix->m != m) return fail(FQ_ERR_MISMATCHED_KV_CACHES, "prefix belongs to another model");
+    if (prefix->type != caches[0]->type) return fail(FQ_ERR_MISMATCHED_KV_CACHES, "cache dtypes differ");
+    if (prefix->type != KV_BF16) return fail(FQ_ERR_UNSUPPORTED, "shared-prefix steps take bf16 caches");
+    if (logits && !m->output.q) return fail(FQ_ERR_INVALID_ARGUMENT, "model has no LM head");
+    RowsPass r;
+    r.prefix = prefix;
+    r.tokens = tokens;
+    for (uint32_t i = 0; i < n; ++i) {
+        if (caches[i] == prefix) return fail(FQ_ERR_MISMATCHED_KV_CACHES, "cache %u is the prefix", i);
+        const uint64_t pos = (uint64_t)prefix->len + caches[i]->len;
+        if (pos >= (uint64_t)m->max_pos)
+            return fail(FQ_ERR_INVALID_SEQUENCE_LENGTH, "cache %u: position %llu of %d", i, (unsigned long long)pos, m->max_pos);
+        r.add(caches[i], 1, caches[i]->len, (uint32_t)pos);
+    }
+    TRY(check_tokens(m, tokens, n));
+    cudaStream_t s = (cudaStream_t)stream;
+    Workspace* w;
+    TRY(ensure_ws(m, s, (int)std::min(n, PROJ_ROWS), 1, &w));
+    size_t bytes;
+    TRY(rows_attn_bytes(m, r, &bytes));
+    TRY(ensure_rows(m, w, (int)n, bytes, s));
+    TRY(enqueue_rows(m, w, r, s));
+    if (logits) TRY(enqueue_head(m, w, w->rows.x, n, logits, s));
+    for (uint32_t i = 0; i < n; ++i) caches[i]->len += 1;
+    return FQ_OK;
+}
+
 fq_status fq_decode_step_all_logits(const fq_model* m, fq_kv* kv, const int32_t* tokens, uint32_t len, uint32_t pos0,
                                     float* logits, void* stream) {
     if (!m || !kv || !logits) return fail(FQ_ERR_INVALID_ARGUMENT, "null argument");
@@ -1209,6 +1478,8 @@ fq_status fq_check_device(const fq_model* m, void* stream) {
     uint32_t host = 0;
     CK(cudaMemcpyAsync(&host, m->err, sizeof host, cudaMemcpyDeviceToHost, s));
     CK(cudaStreamSynchronize(s));
+    uint32_t waits = 0;   // of the packed and shared-prefix steps' attention
+    CK(attn_wait_record(&waits, s));
     if (host) {
         // A CTA that gave up left its arrival counters and tickets half counted; every
         // workspace of the model is re-armed on its own stream (after the work queued there)
@@ -1219,6 +1490,7 @@ fq_status fq_check_device(const fq_model* m, void* stream) {
         CK(cudaMemsetAsync(m->err, 0, sizeof(uint32_t), s));
         return fail(FQ_ERR_DEVICE_TIMEOUT, "a bounded device wait gave up (code %u)", host);
     }
+    if (waits) return fail(FQ_ERR_DEVICE_TIMEOUT, "%u bounded waits of the attention operators gave up", waits);
     return FQ_OK;
 }
 

@@ -91,6 +91,8 @@ def lib():
                 "fq_decode_step_batch": [vp, vp, u32, vp, vp, vp],
                 "fq_decode_step_all_logits": [vp, vp, vp, u32, u32, vp, vp],
                 "fq_forward_step": [vp, vp, vp, u32, u32, vp, vp],
+                "fq_forward_step_packed": [vp, vp, u32, vp, vp, vp, vp],
+                "fq_decode_step_shared": [vp, vp, vp, u32, vp, vp, vp],
                 "fq_decode_greedy": [vp, vp, u32, vp, u32, vp, vp, vp],
                 "fq_decode_step_trace": [vp, vp, u32, vp, vp, vp, vp, vp, vp, vp],
                 "fq_dequant_rows": [vp, u32, ctypes.c_int, u64, u64, vp, vp],
@@ -138,7 +140,7 @@ EXPORTED = ("fq_desc_init", "fq_load_weights", "fq_model_free", "fq_kv_init", "f
             "fq_decode_step_batch", "fq_decode_step_all_logits", "fq_forward_step", "fq_decode_greedy", "fq_decode_step_trace", "fq_dequant_rows", "fq_quantize_q8_0", "fq_layer_step_trace",
             "fq_gemv", "fq_step_kernels", "fq_check_device", "fq_debug_wait_timeout", "fq_set_option", "fq_step_path", "fq_layer_step_noalloc", "fq_last_error",
             "fq_status_str", "fq_kv_layer_view", "fq_qk_norm_rope", "fq_attn_prompt", "fq_attn_prompt_workspace",
-            "fq_attn_shared", "fq_attn_shared_workspace", "fq_attn_check")
+            "fq_attn_shared", "fq_attn_shared_workspace", "fq_attn_check", "fq_forward_step_packed", "fq_decode_step_shared")
 
 
 def _check(status: int, where: str) -> None:
@@ -272,6 +274,25 @@ def fq_forward_step(model: int, kv: int, tokens, pos0: int, logits_ptr: int = 0,
     ([vocab], device) or, with logits_ptr 0, only the K/V appends (a prefill at pos0 = 0)."""
     toks, tp = _i32(tokens)
     _check(lib().fq_forward_step(model, kv, tp, len(toks), pos0, logits_ptr or None, stream), "fq_forward_step")
+
+
+def fq_forward_step_packed(model: int, kvs, tokens, lens, logits_ptr: int = 0, stream: int = 0) -> None:
+    """tokens: the sequences' token ids one after the other, lens[s] of them for sequence s."""
+    if len(lens) != len(kvs):
+        raise FqError(INVALID_ARGUMENT, "fq_forward_step_packed", f"{len(kvs)} caches, {len(lens)} lens")
+    if sum(lens) != len(tokens):
+        raise FqError(INVALID_ARGUMENT, "fq_forward_step_packed", f"{len(tokens)} tokens, lens add up to {sum(lens)}")
+    toks, tp = _i32(tokens)
+    _check(lib().fq_forward_step_packed(model, _caches(kvs), len(kvs), tp, u32_array(lens), logits_ptr or None, stream),
+           "fq_forward_step_packed")
+
+
+def fq_decode_step_shared(model: int, prefix: int, kvs, tokens, logits_ptr: int = 0, stream: int = 0) -> None:
+    if len(tokens) != len(kvs):
+        raise FqError(INVALID_ARGUMENT, "fq_decode_step_shared", f"{len(kvs)} caches, {len(tokens)} tokens")
+    toks, tp = _i32(tokens)
+    _check(lib().fq_decode_step_shared(model, prefix, _caches(kvs), len(kvs), tp, logits_ptr or None, stream),
+           "fq_decode_step_shared")
 
 
 def fq_decode_step_all_logits(model: int, kv: int, tokens, pos0: int, logits_ptr: int, stream: int = 0) -> None:
