@@ -331,6 +331,9 @@ fq_status run_tiles_t(const Plan& p, const AttnIo& io, const Partials& part, con
         a->io = io;
         a->c = std::max(std::fabs(io.scale) * 1.4426950408889634f, FLT_MIN);   // (a scale of 0: equal weights)
         a->negate = io.scale < 0.f;
+        a->g_shift = 0;
+        while (io.Hkv << a->g_shift < io.Hq) ++a->g_shift;
+        a->inv_hkv = (uint32_t)(((1ull << 31) + io.Hkv - 1) / io.Hkv);
         a->part = part;
         std::copy(seq, seq + n_seq, a->seq);
         const uint64_t G = io.Hq / io.Hkv;

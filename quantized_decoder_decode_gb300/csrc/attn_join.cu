@@ -44,11 +44,10 @@ __global__ void __launch_bounds__(AJ_WARPS * 32) attn_join_kernel(const __grid_c
     };
     pdl_wait();   // the partial results are written
     if (idx >= e.n_tok * Hq) return;
-    float M = -INFINITY;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) M = fmaxf(M, ml_at(i)->x);
+    // One pass: values and statistics of a batch of partial results are read together, what is
+    // summed so far follows the maximum.
+    float M = -INFINITY, L = 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    float L = 0.f;
     constexpr int BATCH = 8;
     for (int i0 = 0; i0 < n; i0 += BATCH) {
         float4 v[BATCH];
@@ -56,9 +55,22 @@ __global__ void __launch_bounds__(AJ_WARPS * 32) attn_join_kernel(const __grid_c
 #pragma unroll
         for (int k = 0; k < BATCH; ++k)
             if (i0 + k < n) {
-                v[k] = *o_at(i0 + k);
                 ml[k] = *ml_at(i0 + k);
+                v[k] = *o_at(i0 + k);
             }
+        float top = M;
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k)
+            if (i0 + k < n) top = fmaxf(top, ml[k].x);
+        if (M != top) {
+            const float f = ex2(M - top);   // (0 from -inf)
+            L *= f;
+            y.x *= f;
+            y.y *= f;
+            y.z *= f;
+            y.w *= f;
+            M = top;
+        }
 #pragma unroll
         for (int k = 0; k < BATCH; ++k)
             if (i0 + k < n) {

@@ -56,6 +56,8 @@ struct TileArgs {
     int n_entries;
     float c;              // |scale| log2(e)
     int negate;           // scale < 0
+    int g_shift;          // log2(Hq / Hkv)
+    uint32_t inv_hkv;     // ceil(2^31 / Hkv): units (below 2^31 / 1024) are divided by a product
     Partials part;
     AttnSeq seq[MAX_SEQS];
     TileEntry e[NE];

@@ -19,11 +19,11 @@
 // Roles (512 threads, one CTA per SM, looping over its units):
 //   warps 0-3, 4-7  softmax of tile A / B, one row per thread
 //   warp 8          issues the products with K
-//   warp 9          loads Q, K, V by TMA
-//   warp 10         V tiles whose keys some row does not see: a weight of 0 times NaN would
-//                   still be NaN, so values that are not finite are taken out of the tile and
-//                   noted per column with their first key; the rows that see that key get them back
-//                   in their output.  (Tiles of finite values, the rule, are only scanned.)
+//   warp 9          loads Q and K by TMA
+//   warp 10         loads V by TMA; in tiles with keys that some row does not see a weight of 0 times
+//                   NaN would still be NaN, so values that are not finite are taken out of the
+//                   tile and noted per column with their first key; the rows that see that key get
+//                   them back in their output.  (Tiles of finite values, the rule, are only scanned.)
 //   warp 11         issues the products with V
 //   warps 12-15     outputs, while the next unit's scores are made
 // The two kinds of products have a warp each because issuing one blocks until the tensor cores take
@@ -52,16 +52,16 @@ constexpr int AT_PANEL = AT_TILE_BYTES / 2;               // 64 dims of 128 rows
 constexpr uint32_t AT_S = 0, AT_P = 128, AT_O = 256;      // tensor-memory columns: S, P_A, P_B (64 each), O_A, O_B
 
 struct AtShared {
-    uint64_t q_full, q_empty;
+    uint64_t q_full[2], q_empty[2];   // per Q buffer: of tile A, of tile B; single units take them in turn
     // One warp consumes K tiles and another V tiles, and a phase bit tells a waiter only whether the
     // phase it waits for or the one before is the current one: each has stages of its own, so that it
     // has always seen the phase before.
     uint64_t k_full[AT_KS], k_empty[AT_KS], v_full[AT_VS], v_empty[AT_VS], v_raw[AT_VS];
     uint64_t s_full[2], s_free, p_full[2], o_done[2];    // per score tile
     uint64_t o_last[2], o_free[2], stat_full[2];         // per unit
-    uint32_t tmem, abort, preloaded;
+    uint32_t tmem, abort;
     uint32_t poison_unit;                 // unit number + 1 that the notes are of
-    uint32_t done[4];                     // units that each output warp has finished
+    uint16_t done[4];                     // units that each output warp has finished (a CTA has at most 1536 x 1024 / 152)
     float2 stat[2][TILE_ROWS];            // (m, l) of each row at the end of a unit
     uint16_t poison[3][HEAD_DIM];         // first key (from the unit's first partly seen tile) of +inf, -inf, NaN
 };
@@ -90,9 +90,10 @@ FQ_DEV int unit_at(int r) { return r * (int)gridDim.x + (int)(r & 1 ? gridDim.x 
 template <class Args>
 FQ_DEV Unit unit_of(const Args& a, int w) {
     Unit u;
-    const TileEntry& e = a.e[w / a.io.Hkv];
-    const int G = a.io.Hq / a.io.Hkv, tpt = TILE_ROWS / G;
-    u.head = w % a.io.Hkv;
+    const int entry = (int)((uint64_t)(uint32_t)w * a.inv_hkv >> 31);   // w / Hkv
+    const TileEntry& e = a.e[entry];
+    const int tpt = TILE_ROWS >> a.g_shift;
+    u.head = w - entry * a.io.Hkv;
     u.seq = e.info & 127;
     u.single = (e.info & TILE_SINGLE) != 0;
     u.small = (e.info & TILE_SMALL) != 0;
@@ -107,8 +108,8 @@ FQ_DEV Unit unit_of(const Args& a, int w) {
         return n_tok > 0 && last > 0 ? max(0, min(e.j1, (last + TILE_ROWS - 1) / TILE_ROWS) - e.j0) : 0;
     };
     const int ta = max(0, min(tpt, s.q_len - u.tok_a)), tb = max(0, min(tpt, s.q_len - u.tok_b));
-    u.rows_a = ta * G;
-    u.rows_b = tb * G;
+    u.rows_a = ta << a.g_shift;
+    u.rows_b = tb << a.g_shift;
     u.n_a = tiles(u.tok_a, ta);
     u.n_b = tiles(u.tok_b, tb);
     u.nt = max(u.n_a, u.n_b);
@@ -120,16 +121,12 @@ FQ_DEV Unit unit_of(const Args& a, int w) {
     return u;
 }
 
-// By one thread: the unit's query tiles; one K or V tile.
+// By one thread: a query tile, a K or V tile.
 template <class Args>
-FQ_DEV void load_q(const Args& a, const Unit& u, const AttnSeq& sq, uint8_t* q_sm, AtShared* sh) {
-    const int q0 = u.n_a > 0 ? 0 : 1, q1 = u.single || u.n_b == 0 ? 1 : 2;
-    mbar_arrive_expect_tx(&sh->q_full, (uint32_t)((q1 - q0) * AT_TILE_BYTES));
-    for (int x = q0; x < q1; ++x) {
-        const int row = sq.q_row0 + (x ? u.tok_b : u.tok_a);
-        tma_load_4d(q_sm + x * AT_TILE_BYTES, a.map_q, 0, 0, u.head, row, &sh->q_full);
-        tma_load_4d(q_sm + x * AT_TILE_BYTES + AT_PANEL, a.map_q, 64, 0, u.head, row, &sh->q_full);
-    }
+FQ_DEV void load_q(const Args& a, int row, int head, uint8_t* dst, uint64_t* bar) {
+    mbar_arrive_expect_tx(bar, AT_TILE_BYTES);
+    tma_load_4d(dst, a.map_q, 0, 0, head, row, bar);
+    tma_load_4d(dst + AT_PANEL, a.map_q, 64, 0, head, row, bar);
 }
 FQ_DEV void load_kv(const void* map, uint8_t* dst, int row, int head, uint64_t* bar) {
     mbar_arrive_expect_tx(bar, AT_TILE_BYTES);
@@ -143,10 +140,10 @@ FQ_DEV void give_up(AtShared* sh) {
 }
 FQ_DEV bool at_wait(uint64_t* bar, uint32_t parity, AtShared* sh) {
     if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
+    const uint32_t t0 = (uint32_t)clock();
     while (!mbar_try_wait(bar, parity)) {
         if (*(volatile uint32_t*)&sh->abort) return false;
-        if (clock64() - t0 > WAIT_BUDGET_CYCLES) {
+        if ((uint32_t)clock() - t0 > (uint32_t)WAIT_BUDGET_CYCLES) {
             give_up(sh);
             return false;
         }
@@ -160,7 +157,7 @@ FQ_DEV bool at_wait_warp(uint64_t* bar, uint32_t parity, AtShared* sh) {
 // The outputs of n units are written.
 FQ_DEV bool units_done(uint32_t n, int lane, AtShared* sh) {
     const long long t0 = clock64();
-    while (!__all_sync(0xFFFFFFFFu, *(volatile uint32_t*)&sh->done[lane & 3] >= n)) {
+    while (!__all_sync(0xFFFFFFFFu, *(volatile uint16_t*)&sh->done[lane & 3] >= n)) {
         const bool late = clock64() - t0 > WAIT_BUDGET_CYCLES;
         if (__any_sync(0xFFFFFFFFu, late || *(volatile uint32_t*)&sh->abort)) {
             if (lane == 0 && late) give_up(sh);
@@ -192,63 +189,175 @@ FQ_DEV void set_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :
 template <int N>
 FQ_DEV void set_regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// ---------------- warp 9: loads (Q and the first K tile of the first unit are on their way)
+// No copy may still be landing when the CTA exits.  A role gave up after a quarter second of waiting;
+// copies that were issued land within microseconds of that.
+FQ_DEV void drain() {
+    const long long t0 = clock64();
+    while (clock64() - t0 < DRAIN_CYCLES) {
+    }
+}
+
+// ---------------- warp 9: K and query tiles, each as soon as its buffer is free.  A unit's first K tiles
+// go ahead of its query tiles, whose buffer may be the one that the unit before still reads.
+// (The query tiles and the first K tile of the first unit are on their way already: their release may
+// come before this warp gets here, so it is not waited for again.)
 template <class Args>
-FQ_DEV void loads(const Args& a, AtShared* sh, uint8_t* q_sm, uint8_t* ring, int units, uint32_t preloaded) {
-    // What was preloaded is not waited for again: its release may come before this warp gets here.
-    uint32_t kn = preloaded, vn = 0, qn = preloaded, it = 0;   // K and V tiles, Q tiles, units
+FQ_DEV void load_keys(const Args& a, AtShared* sh, uint8_t* q_sm, uint8_t* ring, int units, bool preloaded) {
+    uint32_t n = preloaded, it = 0;     // K tiles, units
+    uint32_t sel = 0, qp = 0, qu = 0;   // buffer of the next single unit; phase bits of q_empty; buffers used
     bool ok = true;
     for (int w; (w = unit_at(it)) < units && ok; ++it) {
         const Unit u = unit_of(a, w);
         const AttnSeq& sq = a.seq[u.seq];
         if (u.nt == 0) continue;
-        const bool pre = it == 0;
-        if (!pre) {
-            if (!(ok = at_wait_warp(&sh->q_empty, (qn & 1) ^ 1, sh))) break;
-            ++qn;
-            if (elect_one()) load_q(a, u, sq, q_sm, sh);
-            __syncwarp();
-        }
+        const bool pre = preloaded && it == 0;
         const int vw = Args::VIEWS == 1 ? 0 : sq.view;
         const int row0 = sq.k_row0 + u.j0 * TILE_ROWS;
-        auto load_k = [&](int t) {
-            const int s = kn % AT_KS;
-            if (!(ok = at_wait_warp(&sh->k_empty[s], ((kn / AT_KS) & 1) ^ 1, sh))) return;
-            ++kn;
+        for (int t = pre ? 1 : 0; t <= u.nt && ok; ++t) {
+            if (t == min(2, u.nt)) {
+#pragma unroll 1
+                for (int x = 0; x < (u.single ? 1 : 2) && ok; ++x) {
+                    if (u.n(x) == 0) continue;
+                    const uint32_t b = u.single ? sel : x;
+                    if (!pre) {
+                        if (!(ok = at_wait_warp(&sh->q_empty[b], ((qp >> b) & 1) ^ 1, sh))) break;
+                        if (elect_one()) load_q(a, sq.q_row0 + (x ? u.tok_b : u.tok_a), u.head, q_sm + b * AT_TILE_BYTES, &sh->q_full[b]);
+                        __syncwarp();
+                    }
+                    qp ^= 1u << b;
+                    qu |= 1u << b;
+                }
+                if (u.single) sel ^= 1;
+            }
+            if (t == u.nt || !ok) break;
+            const int s = n % AT_KS;
+            if (!(ok = at_wait_warp(&sh->k_empty[s], ((n / AT_KS) & 1) ^ 1, sh))) break;
+            ++n;
             if (elect_one()) load_kv(a.map_k[vw], ring + s * AT_TILE_BYTES, row0 + t * TILE_ROWS, u.head, &sh->k_full[s]);
             __syncwarp();
-        };
-        auto load_v = [&](int t) {
-            const int s = vn % AT_VS;
-            if (!(ok = at_wait_warp(&sh->v_empty[s], ((vn / AT_VS) & 1) ^ 1, sh))) return;
-            ++vn;
-            if (elect_one())
-                load_kv(a.map_v[vw], ring + (AT_KS + s) * AT_TILE_BYTES, row0 + t * TILE_ROWS, u.head,
-                        u.j0 + t >= u.jm ? &sh->v_raw[s] : &sh->v_full[s]);
-            __syncwarp();
-        };
-        // in the order of their use: a pair makes the scores of one tile ahead of the values, a
-        // single unit of two
-        for (int t = pre ? 1 : 0; t < u.step && t < u.nt && ok; ++t) load_k(t);
-        for (int t = 0; t < u.nt && ok; ++t) {
-            if (t + u.step < u.nt) load_k(t + u.step);
-            if (ok) load_v(t);
         }
     }
     // The products' arrivals at these barriers come by themselves: the CTA's shared memory must not
     // be given to another CTA before the last of them.
-    for (uint32_t n = kn > AT_KS ? kn - AT_KS : 0; n < kn && ok; ++n)
-        ok = at_wait_warp(&sh->k_empty[n % AT_KS], (n / AT_KS) & 1, sh);
-    for (uint32_t n = vn > AT_VS ? vn - AT_VS : 0; n < vn && ok; ++n)
-        ok = at_wait_warp(&sh->v_empty[n % AT_VS], (n / AT_VS) & 1, sh);
-    if (qn && ok) ok = at_wait_warp(&sh->q_empty, (qn - 1) & 1, sh);
-    if (!ok) {
-        // No copy may still be landing when the CTA exits.  A role gave up after a quarter second
-        // of waiting; copies that were issued land within microseconds of that.
-        const long long t0 = clock64();
-        while (clock64() - t0 < DRAIN_CYCLES) {
+#pragma unroll 1
+    for (uint32_t i = n > AT_KS ? n - AT_KS : 0; i < n && ok; ++i) ok = at_wait_warp(&sh->k_empty[i % AT_KS], (i / AT_KS) & 1, sh);
+#pragma unroll 1
+    for (uint32_t b = 0; b < 2 && ok; ++b)
+        if (qu >> b & 1) ok = at_wait_warp(&sh->q_empty[b], (qp >> b & 1) ^ 1, sh);
+    if (!ok) drain();
+}
+
+// ---------------- warp 10: V tiles, and the check of those that some row sees in part
+struct PartTile {
+    uint32_t it;                   // its unit
+    int s, tile, k_len, first, jm;   // stage, key tile; keys; keys that every row sees; the unit's first such tile
+};
+
+// Waits for a V tile and takes values that are not finite out of it.
+FQ_DEV bool check_values(AtShared* sh, uint8_t* ring, const PartTile& p, uint32_t& raw_ph, int lane) {
+    if (!at_wait_warp(&sh->v_raw[p.s], (raw_ph >> p.s) & 1, sh)) return false;
+    raw_ph ^= 1u << p.s;
+    uint8_t* tile = ring + (AT_KS + p.s) * AT_TILE_BYTES;
+    // x * 0 is NaN where x is not finite (rows before `from` are seen by every row)
+    const int from = max(0, p.first - p.tile * TILE_ROWS);
+    uint32_t z[4] = {0, 0, 0, 0};
+#pragma unroll 2
+    for (int i = from * 8 + lane; i < TILE_ROWS * 8; i += 32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint4 v = reinterpret_cast<const uint4*>(tile + h * AT_PANEL)[i];
+            z[0] = fma_bf16x2(v.x, 0u, z[0]);
+            z[1] = fma_bf16x2(v.y, 0u, z[1]);
+            z[2] = fma_bf16x2(v.z, 0u, z[2]);
+            z[3] = fma_bf16x2(v.w, 0u, z[3]);
         }
     }
+    bool odd = false;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) odd |= (z[h] & 0x7FFF7FFFu) != 0;
+    if (__any_sync(0xFFFFFFFFu, odd)) {
+        if (*(volatile uint32_t*)&sh->poison_unit != p.it + 1) {
+            if (!units_done(p.it, lane, sh)) return false;   // the notes before are read
+            for (int i = lane; i < 3 * HEAD_DIM; i += 32) sh->poison[0][i] = 0xFFFFu;
+            __syncwarp();
+        }
+        // lane l owns columns 4l .. 4l+3: 8 bytes of every row
+        uint8_t* col = tile + (lane >> 4) * AT_PANEL;
+#pragma unroll 1
+        for (int r = from; r < TILE_ROWS; ++r) {
+            uint16_t* v = reinterpret_cast<uint16_t*>(col + sw128_offset(r, (lane & 15) >> 1) + (lane & 1) * 8);
+            const int key = p.tile * TILE_ROWS + r;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t b = v[c];
+                if ((b & 0x7F80u) != 0x7F80u) continue;
+                v[c] = 0;
+                if (key >= p.k_len) continue;   // seen by no row
+                uint16_t& f = sh->poison[(b & 0x7Fu) ? 2 : (b & 0x8000u) ? 1 : 0][4 * lane + c];
+                const uint16_t k16 = (uint16_t)(key - p.jm * TILE_ROWS);
+                if (k16 < f) f = k16;
+            }
+        }
+        __syncwarp();
+        if (lane == 0) *(volatile uint32_t*)&sh->poison_unit = p.it + 1;
+        __threadfence_block();
+        fence_async_smem();
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->v_full[p.s]);
+    return true;
+}
+
+template <class Args>
+FQ_DEV void load_values(const Args& a, AtShared* sh, uint8_t* ring, int units, int lane) {
+    uint32_t n = 0, raw_ph = 0;   // V tiles; phase bits of v_raw
+    PartTile part[2];             // loaded and not checked yet: at most one per stage
+    static_assert(AT_VS == 2, "two tiles to check at most");
+    int pending = 0, it = -1, t = 0, vw = 0, row0 = 0, seen = 0, k_len = 0;
+    bool more = true, ok = true;
+    Unit u;
+    u.nt = 0;
+#pragma unroll 1
+    while (ok) {
+        while (more && t == u.nt) {   // the next unit
+            const int w = unit_at(++it);
+            more = w < units;
+            if (!more) break;
+            u = unit_of(a, w);
+            const AttnSeq& sq = a.seq[u.seq];
+            vw = Args::VIEWS == 1 ? 0 : sq.view;
+            row0 = sq.k_row0 + u.j0 * TILE_ROWS;
+            k_len = sq.k_len;
+            seen = max(0, min(k_len, u.tok_a + sq.off));
+            t = 0;
+        }
+        const int s = n % AT_VS;
+        const uint32_t parity = ((n / AT_VS) & 1) ^ 1;
+        // checks wait behind a load that can be issued, not behind one that cannot
+        if (pending && !(more && __all_sync(0xFFFFFFFFu, mbar_test_wait(&sh->v_empty[s], parity)))) {
+            ok = check_values(sh, ring, part[0], raw_ph, lane);
+            part[0] = part[1];
+            --pending;
+            continue;
+        }
+        if (!more || !(ok = at_wait_warp(&sh->v_empty[s], parity, sh))) break;
+        const bool whole = u.j0 + t < u.jm;
+        if (elect_one())
+            load_kv(a.map_v[vw], ring + (AT_KS + s) * AT_TILE_BYTES, row0 + t * TILE_ROWS, u.head,
+                    whole ? &sh->v_full[s] : &sh->v_raw[s]);
+        __syncwarp();
+        if (!whole) {
+            const PartTile p{(uint32_t)it, s, u.j0 + t, k_len, seen, u.jm};
+            if (pending) part[1] = p;
+            else part[0] = p;
+            ++pending;
+        }
+        ++t;
+        ++n;
+    }
+#pragma unroll 1
+    for (uint32_t i = n > AT_VS ? n - AT_VS : 0; i < n && ok; ++i) ok = at_wait_warp(&sh->v_empty[i % AT_VS], (i / AT_VS) & 1, sh);
+    if (!ok) drain();
 }
 
 // ---------------- warp 8: S = Q K^T
@@ -256,22 +365,27 @@ template <class Args>
 FQ_DEV void scores(const Args& a, AtShared* sh, uint8_t* q_sm, uint8_t* ring, int units, uint32_t tm) {
     const uint32_t idesc = idesc_bf16_f32(TILE_ROWS, TILE_ROWS, false, a.negate != 0);
     const uint64_t dq0 = sdesc_sw128(smem_u32(q_sm)), dk0 = sdesc_sw128(smem_u32(ring));
-    uint32_t kn = 0, qn = 0, sn = 0, it = 0;   // K tiles, Q tiles, score tiles, units
+    uint32_t kn = 0, qp = 0, sel = 0, sn = 0, it = 0;   // K tiles; phase bits of q_full; buffer of the next single unit; score tiles; units
     bool ok = true;
     for (int w; (w = unit_at(it)) < units && ok; ++it) {
         const Unit u = unit_of(a, w);
         if (u.nt == 0) continue;
-        if (!(ok = at_wait_warp(&sh->q_full, qn++ & 1, sh))) break;
         for (int t = 0; t < u.nt && ok; ++t) {
             const int s = kn % AT_KS;
             if (!(ok = at_wait_warp(&sh->k_full[s], (kn / AT_KS) & 1, sh))) break;
             ++kn;
+#pragma unroll 1
             for (int x = 0; x < 2; ++x) {
                 if (u.single ? x != (t & 1) : t >= u.n(x)) continue;
+                const uint32_t b = u.single ? sel : x;   // the query tile's buffer
+                if (t == 0) {
+                    if (!(ok = at_wait_warp(&sh->q_full[b], (qp >> b) & 1, sh))) break;
+                    qp ^= 1u << b;
+                }
                 // the scores before are in registers
                 if (!(ok = at_wait_warp(&sh->s_free, (sn++ & 1) ^ 1, sh))) break;
                 tc_fence_after();
-                const uint64_t dq = dq0 + (uint32_t)((u.single ? 0 : x) * (AT_TILE_BYTES >> 4));
+                const uint64_t dq = dq0 + b * (uint32_t)(AT_TILE_BYTES >> 4);
                 const uint64_t dk = dk0 + (uint32_t)(s * (AT_TILE_BYTES >> 4));
                 if (elect_one()) {
 #pragma unroll
@@ -280,16 +394,15 @@ FQ_DEV void scores(const Args& a, AtShared* sh, uint8_t* q_sm, uint8_t* ring, in
                         mma_f16(tm + AT_S, dq + off, dk + off, idesc, k > 0);
                     }
                     mma_commit(&sh->s_full[x]);
+                    if (t + 1 == (u.single ? u.nt : u.n(x))) mma_commit(&sh->q_empty[b]);
                 }
                 __syncwarp();
             }
             if (!ok) break;
-            if (elect_one()) {
-                mma_commit(&sh->k_empty[s]);
-                if (t + 1 == u.nt) mma_commit(&sh->q_empty);
-            }
+            if (elect_one()) mma_commit(&sh->k_empty[s]);
             __syncwarp();
         }
+        if (u.single) sel ^= 1;
     }
 }
 
@@ -334,72 +447,10 @@ FQ_DEV void values(const Args& a, AtShared* sh, uint8_t* ring, int units, uint32
     }
 }
 
-// ---------------- warp 10: partly seen V tiles
-template <class Args>
-FQ_DEV void finite_values(const Args& a, AtShared* sh, uint8_t* ring, int units, int lane) {
-    uint32_t vn = 0, it = 0, raw_ph = 0;
-    bool ok = true;
-    for (int w; (w = unit_at(it)) < units && ok; ++it) {
-        const Unit u = unit_of(a, w);
-        const int k_len = a.seq[u.seq].k_len, first = max(0, min(k_len, u.tok_a + a.seq[u.seq].off));
-        for (int t = max(0, u.jm - u.j0); t < u.nt; ++t) {
-            const int s = (vn + t) % AT_VS;
-            if (!(ok = at_wait_warp(&sh->v_raw[s], (raw_ph >> s) & 1, sh))) break;
-            raw_ph ^= 1u << s;
-            uint8_t* tile = ring + (AT_KS + s) * AT_TILE_BYTES;
-            // x * 0 is NaN where x is not finite (rows before `from` are seen by every row)
-            const int from = max(0, first - (u.j0 + t) * TILE_ROWS);
-            uint32_t z[4] = {0, 0, 0, 0};
-            for (int i = from * 8 + lane; i < TILE_ROWS * 8; i += 32) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint4 v = reinterpret_cast<const uint4*>(tile + h * AT_PANEL)[i];
-                    z[0] = fma_bf16x2(v.x, 0u, z[0]);
-                    z[1] = fma_bf16x2(v.y, 0u, z[1]);
-                    z[2] = fma_bf16x2(v.z, 0u, z[2]);
-                    z[3] = fma_bf16x2(v.w, 0u, z[3]);
-                }
-            }
-            bool odd = false;
-#pragma unroll
-            for (int h = 0; h < 4; ++h) odd |= (z[h] & 0x7FFF7FFFu) != 0;
-            if (__any_sync(0xFFFFFFFFu, odd)) {
-                if (*(volatile uint32_t*)&sh->poison_unit != it + 1) {
-                    if (!(ok = units_done(it, lane, sh))) break;   // the notes before are read
-                    for (int i = lane; i < 3 * HEAD_DIM; i += 32) sh->poison[0][i] = 0xFFFFu;
-                    __syncwarp();
-                }
-                // lane l owns columns 4l .. 4l+3: 8 bytes of every row
-                uint8_t* col = tile + (lane >> 4) * AT_PANEL;
-                for (int r = from; r < TILE_ROWS; ++r) {
-                    uint16_t* p = reinterpret_cast<uint16_t*>(col + sw128_offset(r, (lane & 15) >> 1) + (lane & 1) * 8);
-                    const int key = (u.j0 + t) * TILE_ROWS + r;
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t b = p[c];
-                        if ((b & 0x7F80u) != 0x7F80u) continue;
-                        p[c] = 0;
-                        if (key >= k_len) continue;   // seen by no row
-                        uint16_t& f = sh->poison[(b & 0x7Fu) ? 2 : (b & 0x8000u) ? 1 : 0][4 * lane + c];
-                        const uint16_t k16 = (uint16_t)(key - u.jm * TILE_ROWS);
-                        if (k16 < f) f = k16;
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) *(volatile uint32_t*)&sh->poison_unit = it + 1;
-                __threadfence_block();
-                fence_async_smem();
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->v_full[s]);
-        }
-        vn += u.nt;
-    }
-}
-
 // ---------------- warps 0-3 (x = 0), 4-7 (x = 1): softmax, thread = row
 template <class Args>
 FQ_DEV void softmax(const Args& a, AtShared* sh, int units, uint32_t tm, int x, int row, int lane) {
-    const int g_shift = 31 - __clz(a.io.Hq / a.io.Hkv);
+    const int g_shift = a.g_shift;
     const uint32_t lane_base = (uint32_t)(row >> 5) << 21;      // 32 lanes per warp, lane in bits 16..
     const uint32_t tS = tm + AT_S + lane_base, tP = tm + AT_P + 64 * x + lane_base, tO = tm + AT_O + 128 * x + lane_base;
     const float c = a.c;
@@ -501,7 +552,7 @@ FQ_DEV void softmax(const Args& a, AtShared* sh, int units, uint32_t tm, int x, 
 // ---------------- warps 12-15: outputs, thread = row
 template <class Args>
 FQ_DEV void outputs(const Args& a, AtShared* sh, int units, uint32_t tm, int row, int lane) {
-    const int g_shift = 31 - __clz(a.io.Hq / a.io.Hkv);
+    const int g_shift = a.g_shift;
     const uint32_t lane_base = (uint32_t)(row >> 5) << 21;
     const bool out_f32 = a.io.out_f32 != 0;
     const bool wide_out = ((reinterpret_cast<uintptr_t>(a.io.out) | (uintptr_t)(a.io.out_stride * (out_f32 ? 4 : 2))) & 31) == 0;
@@ -553,7 +604,7 @@ FQ_DEV void outputs(const Args& a, AtShared* sh, int units, uint32_t tm, int row
             const uint32_t t0 = tm + AT_O + lane_base + 128 * x;
             // (16 dims at a time in a short loop: its instructions are fetched anew for every unit)
 #pragma unroll 1
-            for (int h = 0; h < 8; ++h) {
+            for (int h = __any_sync(0xFFFFFFFFu, valid) ? 0 : 8; h < 8; ++h) {
                 uint32_t y[16];
                 __syncwarp();
                 if (have) {
@@ -598,6 +649,7 @@ FQ_DEV void outputs(const Args& a, AtShared* sh, int units, uint32_t tm, int row
             if (valid && *(volatile uint32_t*)&sh->poison_unit == it + 1) {   // values that are not finite
                 const int seen = limit - u.jm * TILE_ROWS;                     // noted keys below this are the row's
                 dst = u.slot ? part : out;
+#pragma unroll 1
                 for (int d = 0; d < HEAD_DIM; ++d) {
                     const float add = (sh->poison[0][d] < seen ? INFINITY : 0.f) + (sh->poison[1][d] < seen ? -INFINITY : 0.f) +
                                       (sh->poison[2][d] < seen ? NAN : 0.f);
@@ -612,7 +664,7 @@ FQ_DEV void outputs(const Args& a, AtShared* sh, int units, uint32_t tm, int row
         if (!ok) break;
         __syncwarp();
         __threadfence_block();
-        if (lane == 0) *(volatile uint32_t*)&sh->done[row >> 5] = it + 1;
+        if (lane == 0) *(volatile uint16_t*)&sh->done[row >> 5] = (uint16_t)(it + 1);
     }
 }
 
@@ -625,11 +677,14 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int units = a.n_entries * a.io.Hkv;
 
+    bool preloaded = false;   // (warp 9)
     pdl_trigger();   // the kernel behind this one in the call may start beside it
     if (warp == 9) {
         if (lane == 0) {
-            mbar_init(&sh->q_full, 1);
-            mbar_init(&sh->q_empty, 1);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&sh->q_full[i], 1);
+                mbar_init(&sh->q_empty[i], 1);
+            }
             for (int s = 0; s < AT_KS; ++s) {
                 mbar_init(&sh->k_full[s], 1);
                 mbar_init(&sh->k_empty[s], 1);
@@ -662,10 +717,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
         const int vw = Args::VIEWS == 1 ? 0 : sq.view;
         const bool pre = u.nt > 0 && sh->abort == 0;
         if (pre && elect_one()) {
-            load_q(a, u, sq, q_sm, sh);
+            if (u.n_a > 0) load_q(a, sq.q_row0 + u.tok_a, u.head, q_sm, &sh->q_full[0]);
+            if (!u.single && u.n_b > 0) load_q(a, sq.q_row0 + u.tok_b, u.head, q_sm + AT_TILE_BYTES, &sh->q_full[1]);
             load_kv(a.map_k[vw], ring, sq.k_row0 + u.j0 * TILE_ROWS, u.head, &sh->k_full[0]);
         }
-        if (lane == 0) sh->preloaded = pre;
+        preloaded = pre;
         __syncwarp();
     } else if (warp == 8) {
         tmem_alloc(&sh->tmem, 512);
@@ -682,8 +738,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
         set_regs_down<AT_REGS_ISSUE>();
         if (run) {
             if (warp == 8) scores(a, sh, q_sm, ring, units, tm);
-            else if (warp == 9) loads(a, sh, q_sm, ring, units, sh->preloaded);
-            else if (warp == 10) finite_values(a, sh, ring, units, lane);
+            else if (warp == 9) load_keys(a, sh, q_sm, ring, units, preloaded);
+            else if (warp == 10) load_values(a, sh, ring, units, lane);
             else values(a, sh, ring, units, tm);
         }
     } else {
