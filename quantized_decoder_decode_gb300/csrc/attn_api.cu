@@ -83,11 +83,15 @@ KvRows rows_of(const fq_kv_view& v) {
 constexpr float T_PAIR = 1.45f, T_SINGLE = 0.85f, T_UNIT = 2.5f, T_PARTIAL = 0.5f, T_JOIN = 3.f,
                 T_JOIN_MB = 0.4f, T_READ_MB = 0.16f;
 constexpr int MIN_SPLIT = 4;   // key tiles of a split unit, at least
+constexpr int64_t ROWS_CHUNK = 128;   // keys per chunk of attn_rows.cu, at least
 
 struct Plan {
     std::vector<TileEntry> tiles;     // longest first
+    std::vector<RowGroup> groups;
+    std::vector<int> group_seq;       // their sequences
     std::vector<JoinEntry> join;
     int64_t a_slots = 0, b_slots = 0;   // partial blocks of 128 and of 8 rows
+    int items = 0;                      // chunks of the groups
 
     size_t a_bytes(uint32_t Hkv) const { return (size_t)a_slots * Hkv * TILE_ROWS * HEAD_DIM * 4; }
     size_t b_bytes(uint32_t Hkv) const { return (size_t)b_slots * Hkv * SMALL_ROWS * HEAD_DIM * 4; }
@@ -213,13 +217,60 @@ void emit(Plan& p, std::vector<Unit>& units, bool partial) {
     std::stable_sort(p.tiles.begin(), p.tiles.end(), [&](const TileEntry& a, const TileEntry& b) { return cost(a) > cost(b); });
 }
 
+void add_group(Plan& p, const AttnSeq& q, int s) {
+    p.groups.push_back(RowGroup{q.q_row0, q.q_len, q.k_row0, q.k_len, q.off, 0, 0, -1});
+    p.group_seq.push_back(s);
+}
+
+// Chunks the keys of the groups: the shortest chunks whose CTAs still run all at once.
+void plan_groups(Plan& p, uint32_t Hkv, bool partial) {
+    auto ctas = [&](int64_t per) {
+        int64_t n = 0;
+        for (auto& g : p.groups) n += std::max(1, ceil_div(g.k_len, per));
+        return n * Hkv;
+    };
+    int64_t keys = 0, longest = 0;
+    for (auto& g : p.groups) {
+        keys += g.k_len;
+        longest = std::max<int64_t>(longest, g.k_len);
+    }
+    int64_t per = std::max(ROWS_CHUNK, (keys * Hkv + ROWS_CTAS - 1) / ROWS_CTAS / 64 * 64);
+    while (per < longest && ctas(per) > ROWS_CTAS) per += std::max<int64_t>(64, per / 32 / 64 * 64);
+    for (auto& g : p.groups) {
+        const int splits = std::max(1, ceil_div(g.k_len, per));
+        g.chunk = std::max(64, ceil_div(ceil_div(g.k_len, splits), 64) * 64);
+        const int n = std::max(1, ceil_div(g.k_len, g.chunk));
+        g.item0 = p.items;
+        p.items += n;
+        if (partial || n > 1) {
+            g.slot0 = (int)p.b_slots;
+            p.b_slots += n;
+        }
+    }
+}
+int chunks(const Plan& p, size_t g) { return (g + 1 < p.groups.size() ? p.groups[g + 1].item0 : p.items) - p.groups[g].item0; }
+
 void plan_prompt(Plan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G, uint32_t Hkv) {
     const int tpt = TILE_ROWS / (int)G;
+    // Few rows go to attn_rows.cu, but for short sequences beside others that need tiles: a unit more
+    // costs less than a launch more.
+    bool tiled = false;
+    for (uint32_t s = 0; s < n_seq; ++s) tiled |= (int64_t)seq[s].q_len * G > SMALL_ROWS;
     std::vector<Unit> units;
     float kv_mb = 0.f;
     for (uint32_t s = 0; s < n_seq; ++s) {
-        add_units(units, seq[s], (int)s, (int)G, false);
-        if (seq[s].q_len) kv_mb += (float)seq[s].k_len * Hkv * (HEAD_DIM * 4e-6f);
+        if (seq[s].q_len == 0) continue;
+        if ((int64_t)seq[s].q_len * G > SMALL_ROWS || (tiled && seq[s].k_len <= 1024)) {
+            add_units(units, seq[s], (int)s, (int)G, false);
+            kv_mb += (float)seq[s].k_len * Hkv * (HEAD_DIM * 4e-6f);
+        } else {
+            add_group(p, seq[s], (int)s);
+        }
+    }
+    plan_groups(p, Hkv, false);
+    for (size_t g = 0; g < p.groups.size(); ++g) {
+        const RowGroup& r = p.groups[g];
+        if (r.slot0 >= 0) p.join.push_back(JoinEntry{r.q_row0, r.n_tok, r.k_len, r.off, 0, 0, 0, 0, r.slot0, chunks(p, g), 0, 0, 0});
     }
     choose(units, seq, (int)G, (int)Hkv, false, kv_mb);
     emit(p, units, false);
@@ -243,53 +294,54 @@ void plan_prompt(Plan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G, uint32
     }
 }
 
-// Sequences 0 .. n_seq - 1: the tails, n_seq: all query rows over the prefix.
+// Sequences 0 .. n_seq - 1: the tails (row groups), n_seq: all query rows over the prefix (tiles, or a
+// row group when they are few).
 void plan_shared(Plan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G, uint32_t Hkv) {
     const int tpt = TILE_ROWS / (int)G;
     const AttnSeq& all = seq[n_seq];
+    const bool tiled = all.k_len && n_seq * G > (uint32_t)SMALL_ROWS, rows = all.k_len && !tiled;
     std::vector<Unit> units;
-    float kv_mb = (float)all.k_len * Hkv * (HEAD_DIM * 4e-6f);
-    bool tails = false, empty = false;
-    if (all.k_len) add_units(units, all, (int)n_seq, (int)G, false);
-    for (uint32_t s = 0; s < n_seq; ++s) {
-        if (seq[s].k_len) add_units(units, seq[s], (int)s, (int)G, false);
-        kv_mb += (float)seq[s].k_len * Hkv * (HEAD_DIM * 4e-6f);
-        tails |= seq[s].k_len > 0;
-        empty |= seq[s].k_len == 0;
-    }
+    if (tiled) add_units(units, all, (int)n_seq, (int)G, false);
+    if (rows) add_group(p, all, (int)n_seq);
+    bool tails = false;
+    for (uint32_t s = 0; s < n_seq; ++s)
+        if (seq[s].k_len) {
+            add_group(p, seq[s], (int)s);
+            tails = true;
+        }
     const bool partial = all.k_len && tails;   // both: joined
-    choose(units, seq, (int)G, (int)Hkv, partial, kv_mb);
+    choose(units, seq, (int)G, (int)Hkv, partial, (float)all.k_len * Hkv * (HEAD_DIM * 4e-6f));
     emit(p, units, partial);
+    plan_groups(p, Hkv, partial);
     // where the partial results of each sequence are
     std::vector<JoinEntry> e(n_seq);
     for (uint32_t s = 0; s < n_seq; ++s)
         e[s] = JoinEntry{(int)s, 1, (int)std::min<int64_t>((int64_t)all.k_len + seq[s].k_len, SEES_ALL), SEES_ALL,
                          0, 0, 0, 0, 0, 0, 0, 0, 0};
-    bool any = !all.k_len && empty;   // sequences without a key: zeros from the join
-    for (const Unit& u : units) {
-        if (u.slot < 0) continue;
-        any = true;
-        if (u.seq < (int)n_seq) {
-            e[u.seq].c0 = u.slot;
-            e[u.seq].nC = u.splits;
+    for (const Unit& u : units)
+        for (int i = 0; u.slot >= 0 && i < u.n_tok; ++i) {
+            JoinEntry& j = e[u.tok0 + i];
+            j.a0 = u.slot + i / tpt;
+            j.nA = u.splits;
+            j.a_step = u.single ? 1 : 2;
+            j.a_row = i % tpt * (int)G;
+        }
+    for (size_t g = 0; g < p.groups.size(); ++g) {
+        const RowGroup& r = p.groups[g];
+        if (r.slot0 < 0) continue;
+        if (p.group_seq[g] < (int)n_seq) {
+            e[p.group_seq[g]].c0 = r.slot0;
+            e[p.group_seq[g]].nC = chunks(p, g);
             continue;
         }
-        for (int i = 0; i < u.n_tok; ++i) {
-            JoinEntry& j = e[u.tok0 + i];
-            if (u.small) {
-                j.b0 = u.slot;
-                j.nB = u.splits;
-                j.b_row = i * (int)G;
-            } else {
-                j.a0 = u.slot + i / tpt;
-                j.nA = u.splits;
-                j.a_step = u.single ? 1 : 2;
-                j.a_row = i % tpt * (int)G;
-            }
+        for (uint32_t i = 0; i < n_seq; ++i) {
+            e[i].b0 = r.slot0;
+            e[i].nB = chunks(p, g);
+            e[i].b_row = (int)(i * G);
         }
     }
-    if (!any) return;
-    for (const JoinEntry& j : e)   // (the units finished the others themselves)
+    // (units and groups finish the others themselves; the join writes the zeros of those without a key)
+    for (const JoinEntry& j : e)
         if (j.nA || j.nB || j.nC || j.k_len == 0) p.join.push_back(j);
 }
 
@@ -362,9 +414,44 @@ fq_status run_tiles(const Plan& p, const AttnIo& io, const Partials& part, const
                     const ViewUse* views, int n_views, cudaStream_t s) {
     if (p.tiles.empty()) return FQ_OK;
     const size_t n = p.tiles.size();
+    // maps for the views that the units read
+    AttnSeq own[MAX_SEQS];
+    ViewUse used[MAX_SEQS];
+    if (n_views > 1) {
+        std::copy(seq, seq + n_seq, own);
+        bool read[MAX_SEQS] = {};
+        for (const TileEntry& e : p.tiles) read[e.info & 127] = true;
+        n_views = 0;
+        for (int i = 0; i < n_seq; ++i)
+            if (read[i]) {
+                used[n_views] = views[seq[i].view];
+                own[i].view = n_views++;
+            }
+        seq = own;
+        views = used;
+    }
     auto run = n_views == 1 ? (n <= TileArgs1S::ENTRIES ? run_tiles_t<TileArgs1S> : run_tiles_t<TileArgs1>)
                             : (n <= TileArgsNS::ENTRIES && n_views <= TileArgsNS::VIEWS ? run_tiles_t<TileArgsNS> : run_tiles_t<TileArgsN>);
     return run(p, io, part, seq, n_seq, q_rows, views, n_views, s);
+}
+
+// The row groups; rows[i]: the rows of view i.
+fq_status run_groups(const Plan& p, const AttnIo& io, const Partials& part, const AttnSeq* seq, const ViewUse* views,
+                     cudaStream_t s) {
+    if (p.groups.empty()) return FQ_OK;
+    RowsArgs a;
+    a.io = io;
+    a.part = part;
+    a.n_items = p.items;
+    a.c = std::copysign(std::max(std::fabs(io.scale) * 1.4426950408889634f, FLT_MIN), io.scale);
+    for (size_t g = 0; g < p.groups.size(); ++g) {
+        a.g[g] = p.groups[g];
+        a.kv[g] = views[seq[p.group_seq[g]].view].rows;
+        for (int i = 0; i < chunks(p, g); ++i) a.group[p.groups[g].item0 + i] = (uint8_t)g;
+    }
+    launch_attn_rows(a, !p.tiles.empty(), s);
+    CK(cudaGetLastError());
+    return FQ_OK;
 }
 
 template <class Args>
@@ -536,6 +623,7 @@ fq_status fq_attn_prompt(const void* q, uint64_t q_stride, const fq_kv_view* vie
         const Partials part = p.at(workspace, Hkv);
         cudaStream_t s = (cudaStream_t)stream;
         TRY(run_tiles(p, io, part, seq, (int)n_seq, (int)q_rows, use, (int)n_views, s));
+        TRY(run_groups(p, io, part, seq, use, s));
         return run_join(p, io, part, s);
     } catch (const std::bad_alloc&) {
         return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
@@ -604,7 +692,8 @@ fq_status fq_attn_shared(const void* q, uint64_t q_stride, uint32_t n_seq, const
                         p.bytes(Hkv), io));
         const Partials part = p.at(workspace, Hkv);
         cudaStream_t s = (cudaStream_t)stream;
-        TRY(run_tiles(p, io, part, seq, (int)n_seq + 1, (int)n_seq, use, n_views, s));
+        TRY(run_tiles(p, io, part, seq, (int)n_seq + 1, (int)n_seq, use, 1, s));
+        TRY(run_groups(p, io, part, seq, use, s));
         return run_join(p, io, part, s);
     } catch (const std::bad_alloc&) {
         return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");

@@ -1,5 +1,5 @@
 // Work lists of the prompt and shared-prompt attention kernels, made on the host
-// (attn_api.cu) and passed by value to attn_tiles.cu and attn_join.cu.
+// (attn_api.cu) and passed by value to attn_tiles.cu, attn_rows.cu and attn_join.cu.
 //
 // "Packed rows": a kv head's query rows are (token, head of its group) with the head running
 // fastest, so G heads x tokens fill the 128 rows of a matrix product.
@@ -11,7 +11,7 @@ namespace fq {
 
 constexpr int ATTN_SMS = 152;         // SMs that the work lists are made for
 constexpr int TILE_ROWS = 128;        // packed rows of a query tile = keys of a key tile
-constexpr int SMALL_ROWS = 8;         // packed rows of the small partial results
+constexpr int SMALL_ROWS = 8;         // packed rows of a row group, of the small partial results
 constexpr int32_t SEES_ALL = 1 << 30; // AttnSeq::off of rows that see every key
 constexpr int MAX_SEQS = MAX_SEQ + 1; // the sequences of a call, or tails and a prefix
 
@@ -31,6 +31,15 @@ struct TileEntry {
 };
 constexpr uint32_t TILE_SINGLE = 1u << 7, TILE_SMALL = 1u << 8;   // SMALL: partial results of 8 rows
 constexpr int TILE_SLOT_SHIFT = 9;
+
+// A row group of attn_rows.cu: up to SMALL_ROWS packed rows over keys [0, k_len) in chunks, one CTA per
+// chunk and kv head.
+struct RowGroup {
+    int32_t q_row0, n_tok, k_row0, k_len, off;
+    int32_t item0;        // first work item (chunk) of the group
+    int32_t chunk;        // keys per item, a multiple of 64
+    int32_t slot0;        // first partial block, or -1: one item that writes finished outputs
+};
 
 // Rows whose output is joined from partial results: nA blocks of 128 rows from slot a0 (a0 +
 // a_step, ..; row of token t: a_row + t * G), nB and nC blocks of 8 rows from slots b0 and c0
@@ -74,6 +83,22 @@ void launch_tiles(const Args& a, cudaStream_t s);
 cudaError_t attn_tiles_prepare();     // per device, before the first launch
 cudaError_t attn_wait_record(uint32_t* host, cudaStream_t s);
 
+constexpr int MAX_GROUPS = MAX_SEQS;
+constexpr int ROWS_CTAS_SM = 3;                     // CTAs of attn_rows.cu per SM (156 registers x 128)
+constexpr int ROWS_CTAS = ROWS_CTAS_SM * ATTN_SMS;  // ..  that run at once
+constexpr int MAX_ITEMS = ROWS_CTAS + MAX_GROUPS;   // (a group is one item at least)
+struct RowsArgs {
+    AttnIo io;
+    int n_items;
+    float c;              // scale log2(e)
+    Partials part;
+    uint8_t group[MAX_ITEMS];   // of an item
+    RowGroup g[MAX_GROUPS];
+    KvRows kv[MAX_GROUPS];
+};
+// beside: it may run beside launch_tiles of the same call, launched just before
+void launch_attn_rows(const RowsArgs& a, bool beside, cudaStream_t s);
+
 template <int NE>
 struct JoinArgs {
     static constexpr int ENTRIES = NE;
@@ -85,7 +110,7 @@ struct JoinArgs {
 using JoinArgsS = JoinArgs<64>;
 using JoinArgsL = JoinArgs<512>;
 static_assert(sizeof(JoinArgsL) <= 32764, "kernel parameters");
-// behind launch_tiles (or another join) of the same call
+// behind launch_tiles, launch_attn_rows or another join of the same call
 template <class Args>
 void launch_attn_join(const Args& a, cudaStream_t s);
 
