@@ -88,7 +88,6 @@ constexpr int64_t ROWS_CHUNK = 128;   // keys per chunk of attn_rows.cu, at leas
 struct Plan {
     std::vector<TileEntry> tiles;     // longest first
     std::vector<RowGroup> groups;
-    std::vector<int> group_seq;       // their sequences
     std::vector<JoinEntry> join;
     int64_t a_slots = 0, b_slots = 0;   // partial blocks of 128 and of 8 rows
     int items = 0;                      // chunks of the groups
@@ -218,8 +217,7 @@ void emit(Plan& p, std::vector<Unit>& units, bool partial) {
 }
 
 void add_group(Plan& p, const AttnSeq& q, int s) {
-    p.groups.push_back(RowGroup{q.q_row0, q.q_len, q.k_row0, q.k_len, q.off, 0, 0, -1});
-    p.group_seq.push_back(s);
+    p.groups.push_back(RowGroup{q.q_row0, q.q_len, q.k_row0, q.k_len, q.off, s, 0, 0, -1});
 }
 
 // Chunks the keys of the groups: the shortest chunks whose CTAs still run all at once.
@@ -239,6 +237,12 @@ void plan_groups(Plan& p, uint32_t Hkv, bool partial) {
     for (auto& g : p.groups) {
         const int splits = std::max(1, ceil_div(g.k_len, per));
         g.chunk = std::max(64, ceil_div(ceil_div(g.k_len, splits), 64) * 64);
+    }
+    // longest chunks first
+    std::stable_sort(p.groups.begin(), p.groups.end(), [](const RowGroup& a, const RowGroup& b) {
+        return std::min(a.chunk, a.k_len) > std::min(b.chunk, b.k_len);
+    });
+    for (auto& g : p.groups) {
         const int n = std::max(1, ceil_div(g.k_len, g.chunk));
         g.item0 = p.items;
         p.items += n;
@@ -329,9 +333,9 @@ void plan_shared(Plan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G, uint32
     for (size_t g = 0; g < p.groups.size(); ++g) {
         const RowGroup& r = p.groups[g];
         if (r.slot0 < 0) continue;
-        if (p.group_seq[g] < (int)n_seq) {
-            e[p.group_seq[g]].c0 = r.slot0;
-            e[p.group_seq[g]].nC = chunks(p, g);
+        if (p.groups[g].seq < (int)n_seq) {
+            e[p.groups[g].seq].c0 = r.slot0;
+            e[p.groups[g].seq].nC = chunks(p, g);
             continue;
         }
         for (uint32_t i = 0; i < n_seq; ++i) {
@@ -355,6 +359,7 @@ fq_status prepare_device() {
     std::lock_guard<std::mutex> lk(mu);
     if (dev < 64 && done[dev]) return FQ_OK;
     CK(attn_tiles_prepare());
+    CK(attn_rows_prepare());
     if (dev < 64) done[dev] = true;
     return FQ_OK;
 }
@@ -439,6 +444,7 @@ fq_status run_tiles(const Plan& p, const AttnIo& io, const Partials& part, const
 fq_status run_groups(const Plan& p, const AttnIo& io, const Partials& part, const AttnSeq* seq, const ViewUse* views,
                      cudaStream_t s) {
     if (p.groups.empty()) return FQ_OK;
+    TRY(prepare_device());
     RowsArgs a;
     a.io = io;
     a.part = part;
@@ -446,7 +452,7 @@ fq_status run_groups(const Plan& p, const AttnIo& io, const Partials& part, cons
     a.c = std::copysign(std::max(std::fabs(io.scale) * 1.4426950408889634f, FLT_MIN), io.scale);
     for (size_t g = 0; g < p.groups.size(); ++g) {
         a.g[g] = p.groups[g];
-        a.kv[g] = views[seq[p.group_seq[g]].view].rows;
+        a.kv[g] = views[seq[p.groups[g].seq].view].rows;
         for (int i = 0; i < chunks(p, g); ++i) a.group[p.groups[g].item0 + i] = (uint8_t)g;
     }
     launch_attn_rows(a, !p.tiles.empty(), s);

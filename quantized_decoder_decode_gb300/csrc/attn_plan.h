@@ -36,6 +36,7 @@ constexpr int TILE_SLOT_SHIFT = 9;
 // chunk and kv head.
 struct RowGroup {
     int32_t q_row0, n_tok, k_row0, k_len, off;
+    int32_t seq;          // (for the host)
     int32_t item0;        // first work item (chunk) of the group
     int32_t chunk;        // keys per item, a multiple of 64
     int32_t slot0;        // first partial block, or -1: one item that writes finished outputs
@@ -96,6 +97,7 @@ struct RowsArgs {
     RowGroup g[MAX_GROUPS];
     KvRows kv[MAX_GROUPS];
 };
+cudaError_t attn_rows_prepare();      // per device, before the first launch
 // beside: it may run beside launch_tiles of the same call, launched just before
 void launch_attn_rows(const RowsArgs& a, bool beside, cudaStream_t s);
 

@@ -91,7 +91,10 @@ __global__ void __launch_bounds__(AR_THREADS, ROWS_CTAS_SM) attn_rows_kernel(con
         }
     };
     int k0 = c0 + 16 * warp;
-    if (k0 < c1) load_k(k0);
+    if (k0 < c1) {
+        load_k(k0);
+        load_v(k0);
+    }
     uint4 q[4];   // packed row r: dims 32i + 8c ..
     {
         const uint16_t* p = a.io.q + (int64_t)(g.q_row0 + r / G) * a.io.q_stride + (int64_t)(head * G + r % G) * HEAD_DIM + 8 * c;
@@ -106,14 +109,14 @@ __global__ void __launch_bounds__(AR_THREADS, ROWS_CTAS_SM) attn_rows_kernel(con
     for (int t = 0; t < 8; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     for (; k0 < c1; k0 += 16 * AR_WARPS) {
-        load_v(k0);
+        const bool more = k0 + 16 * AR_WARPS < c1;   // K and V of the next block come while this one is worked on
         float s[4] = {0.f, 0.f, 0.f, 0.f};   // (key r, rows 2c, 2c + 1), (key 8 + r, ..)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             mma16816(s, kr[0][i].x, kr[1][i].x, kr[0][i].y, kr[1][i].y, q[i].x, q[i].y);
             mma16816(s, kr[0][i].z, kr[1][i].z, kr[0][i].w, kr[1][i].w, q[i].z, q[i].w);
         }
-        if (k0 + 16 * AR_WARPS < c1) load_k(k0 + 16 * AR_WARPS);
+        if (more) load_k(k0 + 16 * AR_WARPS);
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[e] = k0 + 8 * (e >> 1) + r < limit[e & 1] ? s[e] * a.c : -INFINITY;
         float f[2];
@@ -175,6 +178,7 @@ __global__ void __launch_bounds__(AR_THREADS, ROWS_CTAS_SM) attn_rows_kernel(con
                          __byte_perm(w[2][0][t >> 1], w[3][0][t >> 1], sel), __byte_perm(w[2][1][t >> 1], w[3][1][t >> 1], sel), p0, p1);
             }
         }
+        if (more) load_v(k0 + 16 * AR_WARPS);
         if (odd) {
             for (int k = 0; k < 16 && k0 + k < c1; ++k) {
                 const uint16_t* p = vb + (int64_t)(k0 + k) * rs + 8 * r;
@@ -244,6 +248,14 @@ __global__ void __launch_bounds__(AR_THREADS, ROWS_CTAS_SM) attn_rows_kernel(con
 }
 
 }  // namespace
+
+// What is in flight from memory (12 warps x 8 KB per SM) is held in the L1 cache, which is what shared
+// memory leaves of 256 KB: behind attn_tiles.cu, with its 227 KB, a block of keys took 3.2 us
+// instead of 1.9 (64 tails behind a shared prefix 45 -> 39 us) until the split was asked for.
+cudaError_t attn_rows_prepare() {
+    constexpr int SHARED_PERCENT = 25;   // 57 KB: three CTAs
+    return cudaFuncSetAttribute(attn_rows_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, SHARED_PERCENT);
+}
 
 void launch_attn_rows(const RowsArgs& a, bool beside, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
