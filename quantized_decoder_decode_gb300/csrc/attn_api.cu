@@ -467,10 +467,11 @@ fq_status run_join_t(const Plan& p, const AttnIo& io, const Partials& part, cuda
     a.part = part;
     for (size_t e0 = 0; e0 < p.join.size(); e0 += Args::ENTRIES) {
         a.n_entries = (int)std::min<size_t>(Args::ENTRIES, p.join.size() - e0);
-        a.max_tok = 0;
+        a.max_tok = a.max_parts = 0;
         for (int i = 0; i < a.n_entries; ++i) {
             a.e[i] = p.join[e0 + i];
             a.max_tok = std::max(a.max_tok, a.e[i].n_tok);
+            a.max_parts = std::max(a.max_parts, a.e[i].nA + a.e[i].nB + a.e[i].nC);
         }
         // (a second launch waits for the first, which waits for the partial results)
         launch_attn_join(a, s);

@@ -14,7 +14,7 @@ namespace {
 
 constexpr int AJ_WARPS = 8;
 
-template <class Args>
+template <class Args, int BATCH>
 __global__ void __launch_bounds__(AJ_WARPS * 32) attn_join_kernel(const __grid_constant__ Args a) {
     const int lane = threadIdx.x & 31;
     const JoinEntry e = a.e[blockIdx.x];
@@ -48,7 +48,6 @@ __global__ void __launch_bounds__(AJ_WARPS * 32) attn_join_kernel(const __grid_c
     // summed so far follows the maximum.
     float M = -INFINITY, L = 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int BATCH = 8;
     for (int i0 = 0; i0 < n; i0 += BATCH) {
         float4 v[BATCH];
         float2 ml[BATCH];
@@ -109,7 +108,7 @@ void launch_attn_join(const Args& a, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, attn_join_kernel<Args>, a);
+    cudaLaunchKernelEx(&cfg, a.max_parts <= 4 ? attn_join_kernel<Args, 4> : attn_join_kernel<Args, 8>, a);
 }
 template void launch_attn_join<JoinArgsS>(const JoinArgsS&, cudaStream_t);
 template void launch_attn_join<JoinArgsL>(const JoinArgsL&, cudaStream_t);

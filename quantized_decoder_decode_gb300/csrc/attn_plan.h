@@ -105,7 +105,7 @@ template <int NE>
 struct JoinArgs {
     static constexpr int ENTRIES = NE;
     AttnIo io;
-    int n_entries, max_tok;
+    int n_entries, max_tok, max_parts;   // tokens and partial results of an entry, at most
     Partials part;
     JoinEntry e[NE];
 };
