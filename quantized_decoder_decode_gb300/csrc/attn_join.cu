@@ -6,7 +6,7 @@
 // the kernel before) and is short.
 
 #include "attn_plan.h"
-#include "common.cuh"
+#include "attn.cuh"
 
 namespace fq {
 

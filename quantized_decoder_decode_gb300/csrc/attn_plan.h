@@ -1,4 +1,4 @@
-// Work lists of the prompt and shared-prompt attention kernels, made on the host
+// Arguments of the prompt and shared-prompt attention operators' kernels, and their work lists, made on the host
 // (attn_api.cu) and passed by value to attn_tiles.cu, attn_rows.cu and attn_join.cu.
 //
 // "Packed rows": a kv head's query rows are (token, head of its group) with the head running
@@ -8,6 +8,40 @@
 #include "kernels.h"
 
 namespace fq {
+
+struct KvRows {                   // element d of row r of kv head h: [r * row_stride + h * head_stride + d]
+    uint16_t *k = nullptr, *v = nullptr;
+    int64_t row_stride = 0, head_stride = 0;
+};
+
+// QK-norm + rope of packed rows, q -> q_out, k and v -> cache rows (qk_rows.cu)
+struct QkRowsArgs {
+    const float* qkv;             // [rows][(Hq + 2 Hkv) * 128]
+    int64_t qkv_stride;
+    const float *q_norm, *k_norm; // [128]
+    const float2* rope;           // [positions][64] (cos, sin)
+    float eps;
+    int Hq, Hkv, n_seq, rows;
+    uint16_t* q_out;              // bf16 [rows][Hq * 128]
+    int64_t q_stride;
+    int32_t row0[MAX_SEQ], pos0[MAX_SEQ], kv_row0[MAX_SEQ];   // per sequence: first row, position, cache row
+    KvRows kv[MAX_SEQ];
+};
+void launch_qk_rows(const QkRowsArgs& a, cudaStream_t s);
+
+struct AttnIo {
+    const uint16_t* q;            // bf16 [rows][Hq][128]
+    int64_t q_stride;
+    void* out;                    // bf16 or f32 [rows][Hq][128]
+    int64_t out_stride;
+    int out_f32;
+    int Hq, Hkv;
+    float scale;
+};
+// tensor map over bf16 values of rank 3 or 4 (strides[0] is not read), 128-byte swizzle, zero
+// fill outside
+bool encode_bf16_tiles(void* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
+                       const uint32_t* box);
 
 constexpr int ATTN_SMS = 152;         // SMs that the work lists are made for
 constexpr int TILE_ROWS = 128;        // packed rows of a query tile = keys of a key tile

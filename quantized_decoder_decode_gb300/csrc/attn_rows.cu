@@ -20,7 +20,7 @@
 // see them.
 
 #include "attn_plan.h"
-#include "common.cuh"
+#include "attn.cuh"
 
 namespace fq {
 

@@ -34,8 +34,8 @@
 // of tensor work and about 2 x 1100 cycles of softmax on four schedulers; what is left is the
 // time from a score tile's last product to the first of its registers and back.
 
+#include "attn.cuh"
 #include "attn_plan.h"
-#include "common.cuh"
 #include "tc.cuh"
 
 namespace fq {

@@ -70,42 +70,6 @@ FQ_DEV float bf2f(unsigned short h) { return __uint_as_float((uint32_t)h << 16);
 FQ_DEV float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 FQ_DEV float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// two floats rounded to a bf16 pair (lo in the low half)
-FQ_DEV uint32_t bf16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-// largest of three (NaN only where all are)
-FQ_DEV float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-// two f32 operations in one instruction
-FQ_DEV uint64_t pair(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-FQ_DEV void unpair(uint64_t p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
-FQ_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-FQ_DEV uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-// 2^x, relative error about 2^-22, results below the normal range flushed to zero
-FQ_DEV float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // Four int8 codes of one 32-bit word to exact floats: bias each byte to unsigned, place it
 // in the low mantissa bits of 2^23 (byte permute: selector nibble 0 picks source byte k of
 // u, nibbles 1-2 pick zero bytes and nibble 3 the 0x4B exponent byte of the constant),

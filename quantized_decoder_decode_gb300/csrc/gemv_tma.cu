@@ -15,11 +15,13 @@
 // kernel), so the first STAGES chunks are already landing while the previous kernel of
 // the step finishes; only the consumers wait for the activations.
 
+#include <atomic>
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
 #include <algorithm>
 
+#include "attn_plan.h"
 #include "common.cuh"
 #include "kernels.h"
 #include "quant.cuh"
@@ -324,7 +326,7 @@ bool launch_t(const GemvArgs& a, cudaStream_t s, bool pdl) {
     return true;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::atomic<PFN_cuTensorMapEncodeTiled_v12000> g_encode{nullptr};   // (first calls may come from several threads)
 
 bool encode(void* map, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t rows, uint64_t row_bytes,
             uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_NONE) {
@@ -332,20 +334,20 @@ bool encode(void* map, CUtensorMapDataType dt, const void* base, uint64_t inner,
     cuuint64_t strides[1] = {row_bytes};
     cuuint32_t box[2] = {box_inner, box_rows};
     cuuint32_t es[2] = {1, 1};
-    CUresult r = g_encode(reinterpret_cast<CUtensorMap*>(map), dt, 2, const_cast<void*>(base), dims, strides, box, es,
+    CUresult r = g_encode.load()(reinterpret_cast<CUtensorMap*>(map), dt, 2, const_cast<void*>(base), dims, strides, box, es,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
 
 bool load_encoder() {
-    if (g_encode) return true;
+    if (g_encode.load()) return true;
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult qr;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &qr) != cudaSuccess ||
         qr != cudaDriverEntryPointSuccess || !fn)
         return false;
-    g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    g_encode.store(reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn));
     return true;
 }
 
@@ -421,7 +423,7 @@ bool encode_bf16_tiles(void* map, const void* base, int rank, const uint64_t* di
         b[i] = box[i];
         if (i) st[i - 1] = strides_bytes[i];
     }
-    return g_encode(reinterpret_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
+    return g_encode.load()(reinterpret_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
                     const_cast<void*>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

@@ -121,11 +121,6 @@ bool make_tma_maps(const QMat& W, TmaMaps* out);
 // tensor map over f16 rows [rows][K], box 64 halves x box_rows, 128-byte swizzle
 bool encode_f16_rows_sw128(void* map, const void* base, uint64_t K, uint64_t rows, uint32_t box_rows);
 
-// tensor map over bf16 values of rank 3 or 4 (strides[0] is not read), 128-byte swizzle, zero
-// fill outside
-bool encode_bf16_tiles(void* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
-                       const uint32_t* box);
-
 // tcgen05 GEMM for lockstep batches of TC_MIN_BATCH..32 rows over Q8_0 weights: a prep
 // kernel (RMSNorm + f16 hi/lo split into xh, 64 x K halves) and the GEMM
 constexpr int TC_MIN_BATCH = 8;
@@ -255,36 +250,6 @@ void launch_moe_route(const float* logits, int E, int k, int n, int norm_topk, M
 void launch_moe_combine(float* x, const float* y, const MoeRoute* route, int n, int k, int H, cudaStream_t s,
                         bool pdl);
 
-// ---- prompt and shared-prompt attention (bf16 rows of head_dim 128)
-struct KvRows {                   // element d of row r of kv head h: [r * row_stride + h * head_stride + d]
-    uint16_t *k = nullptr, *v = nullptr;
-    int64_t row_stride = 0, head_stride = 0;
-};
-
-// QK-norm + rope of packed rows, q -> q_out, k and v -> cache rows (qk_rows.cu)
-struct QkRowsArgs {
-    const float* qkv;             // [rows][(Hq + 2 Hkv) * 128]
-    int64_t qkv_stride;
-    const float *q_norm, *k_norm; // [128]
-    const float2* rope;           // [positions][64] (cos, sin)
-    float eps;
-    int Hq, Hkv, n_seq, rows;
-    uint16_t* q_out;              // bf16 [rows][Hq * 128]
-    int64_t q_stride;
-    int32_t row0[MAX_SEQ], pos0[MAX_SEQ], kv_row0[MAX_SEQ];   // per sequence: first row, position, cache row
-    KvRows kv[MAX_SEQ];
-};
-void launch_qk_rows(const QkRowsArgs& a, cudaStream_t s);
-
-struct AttnIo {
-    const uint16_t* q;            // bf16 [rows][Hq][128]
-    int64_t q_stride;
-    void* out;                    // bf16 or f32 [rows][Hq][128]
-    int64_t out_stride;
-    int out_f32;
-    int Hq, Hkv;
-    float scale;
-};
 // Load-time helpers
 // Source row r lands in destination row (r / group) * group_stride + (r % group) * step + off
 // (fusing q/k/v, interleaving gate/up rows, stacking experts).

@@ -10,8 +10,8 @@
 // four heads of one row, so that four 512-byte reads are in flight per warp before the first
 // reduction, and one read of the row's cos and sin serves its four heads.
 
-#include "common.cuh"
-#include "kernels.h"
+#include "attn.cuh"
+#include "attn_plan.h"
 
 namespace fq {
 
