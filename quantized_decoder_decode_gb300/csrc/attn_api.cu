@@ -79,7 +79,9 @@ KvRows rows_of(const fq_kv_view& v) {
 // Times of attn_tiles.cu in microseconds (measured at head_dim 128 on one GB300) that the choices
 // below weigh: a key tile of a pair of query tiles and of a single one, a unit's own cost (what of
 // its loads, joins and outputs nothing hides), what partial results cost more, and
-// joining them (a launch, the reads); and reading K and V rows from memory.
+// joining them (a launch, the reads); and reading K and V rows from memory.  (The choices are not
+// sensitive to them: T_UNIT of 1.7 or 3.5, T_SINGLE of .78 or .92, T_JOIN of 5 give the same times;
+// T_JOIN_MB of .2 splits too often: 64 sequences behind a shared prefix 38.5 -> 40.7 us.)
 constexpr float T_PAIR = 1.45f, T_SINGLE = 0.85f, T_UNIT = 2.5f, T_PARTIAL = 0.5f, T_JOIN = 3.f,
                 T_JOIN_MB = 0.4f, T_READ_MB = 0.16f;
 constexpr int MIN_SPLIT = 4;   // key tiles of a split unit, at least
@@ -166,9 +168,12 @@ float estimate(const std::vector<Unit>& units, int cap, int G, int Hkv, bool par
 }
 
 // Pairs of query tiles share their K and V tiles, single ones give shorter units, and units may be
-// split along the keys.  Where there are few units per SM an estimate chooses (2048 tokens, 16 / 8
-// heads: single tiles 21 us, pairs 27, split pairs 33).  kv_mb: keys and values read from memory,
-// which bounds what splitting can give.
+// split along the keys.  Where there are few units per SM an estimate chooses:
+//   2048 tokens, 16 / 8 heads            single tiles 23.8 us, pairs 32.6
+//   333 tokens behind 7000, 32 / 4       pairs in three parts 45.2, single tiles in parts 48.3, whole
+//                                        single tiles 54.3, whole pairs 91.3
+//   10 prompts of 1 to 1187, 32 / 8      pairs 50.4, single tiles 50.8 (many units: pairs)
+// kv_mb: keys and values read from memory, which bounds what splitting can give.
 void choose(std::vector<Unit>& units, const AttnSeq* seq, int G, int Hkv, bool partial, float kv_mb) {
     if (units.empty()) return;
     int longest = 1;
@@ -220,7 +225,8 @@ void add_group(Plan& p, const AttnSeq& q, int s) {
     p.groups.push_back(RowGroup{q.q_row0, q.q_len, q.k_row0, q.k_len, q.off, s, 0, 0, -1});
 }
 
-// Chunks the keys of the groups: the shortest chunks whose CTAs still run all at once.
+// Chunks the keys of the groups: the shortest chunks whose CTAs still run all at once, the longest chunks
+// first (behind tiles, CTAs start as SMs become free).
 void plan_groups(Plan& p, uint32_t Hkv, bool partial) {
     auto ctas = [&](int64_t per) {
         int64_t n = 0;
@@ -256,8 +262,9 @@ int chunks(const Plan& p, size_t g) { return (g + 1 < p.groups.size() ? p.groups
 
 void plan_prompt(Plan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G, uint32_t Hkv) {
     const int tpt = TILE_ROWS / (int)G;
-    // Few rows go to attn_rows.cu, but for short sequences beside others that need tiles: a unit more
-    // costs less than a launch more.
+    // Few rows go to attn_rows.cu (16 tokens over 512 to 4097 keys: 30.8 us, as units of tiles 37.1), but
+    // for short sequences beside others that need tiles, where a unit more costs less than a launch more
+    // (one token beside nine prompts: 50.5 us, with a launch of its own 51.2).
     bool tiled = false;
     for (uint32_t s = 0; s < n_seq; ++s) tiled |= (int64_t)seq[s].q_len * G > SMALL_ROWS;
     std::vector<Unit> units;
@@ -546,6 +553,7 @@ fq_status fq_qk_norm_rope(const float* qkv, uint64_t qkv_stride, uint32_t n_seq,
                 return fail(FQ_ERR_INVALID_ARGUMENT, "sequences %u and %u write the same rows", t, s);
     }
     if (rows == 0) return FQ_OK;
+    if (rows * (Hq + 2 * Hkv) >= 1ull << 32) return fail(FQ_ERR_INVALID_ARGUMENT, "2^32 heads of rows or more");
     if (!qkv || !q_norm || !k_norm || !rope || !q_out) return fail(FQ_ERR_INVALID_ARGUMENT, "null argument");
     if (!aligned16(qkv) || !aligned16(q_norm) || !aligned16(k_norm) || !aligned16(rope) || !aligned16(q_out))
         return fail(FQ_ERR_INVALID_ARGUMENT, "qkv, gains, rope and q_out must be 16-byte aligned");

@@ -30,9 +30,15 @@
 // it: what a warp waits for between its products then costs the other kind nothing.
 // Every wait is bounded; one that gives up records it, and all roles leave.
 //
-// What bounds it (one prompt of 8192 tokens, 32 / 8 heads): a pair of 128 x 128 tiles is 2048 cycles
-// of tensor work and about 2 x 1100 cycles of softmax on four schedulers; what is left is the
-// time from a score tile's last product to the first of its registers and back.
+// What bounds it.  One prompt of 8192 tokens, 32 / 8 heads, 367 us: a pair of 128 x 128 tiles is 2048
+// cycles of tensor work (the pipes are busy 70% of the time) and about 2 x 1100 cycles of softmax on
+// four schedulers (issuing 42%); what is left is the time from a score tile's last product to the
+// first of its registers and back, and the masked tiles.  2048 tokens, 16 / 8 heads, 23 us: 2.5 us until the
+// first scores, 12 us of tiles (0.76 us each), 2 us for the last values, 1.7 us of outputs; tensor pipes 38%.
+// Taken out again: the softmax warps as output warps (2048 tokens 24.7 -> 26.0 us), one
+// loading warp for K and V in the order of their use (packed prompts 50 -> 54), three lanes of one warp
+// that load Q, K and V each on their own (4 us more for 2048 tokens: a lane's turn comes too late),
+// outputs transposed between lanes for longer stores (packed prompts 71 us).
 
 #include "attn.cuh"
 #include "attn_plan.h"

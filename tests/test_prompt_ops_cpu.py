@@ -149,3 +149,18 @@ def test_rows_counts():
 
 def test_layer_view_refusals():
     refused(lambda: fq.fq_kv_layer_view(None, 0), fq.INVALID_ARGUMENT)
+
+
+def test_rows_beyond_a_device():
+    n = 1 << 23   # x 512 heads
+    refused(rows, fq.INVALID_ARGUMENT, hq=256, hkv=128, lens=(n,), pos0=(0,), kv_row0=(0,),
+            views=view(rows=n, head_stride=n * 128), rope_rows=n)
+
+
+def test_steps_of_operators_refusals():
+    """What is refused before the model is looked at (the rest needs caches, hence a GPU)."""
+    refused(lambda: fq.fq_forward_step_packed(0, [P], [1], [1]), fq.INVALID_ARGUMENT)
+    refused(lambda: fq.fq_forward_step_packed(0, [P, P], [1, 2], [2]), fq.INVALID_ARGUMENT)
+    refused(lambda: fq.fq_forward_step_packed(0, [P], [1, 2], [1]), fq.INVALID_ARGUMENT)
+    refused(lambda: fq.fq_decode_step_shared(0, 0, [P], [1]), fq.INVALID_ARGUMENT)
+    refused(lambda: fq.fq_decode_step_shared(0, 0, [P], [1, 2]), fq.INVALID_ARGUMENT)
