@@ -27,14 +27,18 @@
 //   warp 11         issues the products with V
 //   warps 12-15     outputs, while the next unit's scores are made
 // The two kinds of products have a warp each because issuing one blocks until the tensor cores take
-// it: what a warp waits for between its products then costs the other kind nothing.
+// it: what a warp waits for between its products then costs the other kind nothing.  In a pair, P V of a
+// score tile is issued behind the scores of the tile after the next: those are what a softmax warpgroup
+// and the one S buffer wait for next, and beside P V they would take twice as long (8192 tokens 369
+// -> 349 us, 333 tokens behind 7000 45.2 -> 43.1 us; in single units 2048 tokens would lose 0.5 us).
 // Every wait is bounded; one that gives up records it, and all roles leave.
 //
-// What bounds it.  One prompt of 8192 tokens, 32 / 8 heads, 367 us: a pair of 128 x 128 tiles is 2048
-// cycles of tensor work (the pipes are busy 70% of the time) and about 2 x 1100 cycles of softmax on
-// four schedulers (issuing 42%); what is left is the time from a score tile's last product to the
-// first of its registers and back, and the masked tiles.  2048 tokens, 16 / 8 heads, 23 us: 2.5 us until the
-// first scores, 12 us of tiles (0.76 us each), 2 us for the last values, 1.7 us of outputs; tensor pipes 38%.
+// What bounds it.  One prompt of 8192 tokens, 32 / 8 heads, 349 us (the products alone 283): a pair of
+// 128 x 128 tiles is 2048 cycles of tensor work and takes 2800, as the S buffer goes round: 610 cycles
+// for the product, 270 until the warpgroup sees it, 180 to load it, 300 until the next product begins,
+// twice.  The softmax of a tile (1060 cycles of arithmetic, 600 of waits and stores) fits in that.  2048
+// tokens, 16 / 8 heads, 23.5 us: 2.5 us until the first scores, 12 us of tiles (0.76 us each), 2 us for the
+// last values, 1.7 us of outputs.
 // Taken out again: the softmax warps as output warps (2048 tokens 24.7 -> 26.0 us), one
 // loading warp for K and V in the order of their use (packed prompts 50 -> 54), three lanes of one warp
 // that load Q, K and V each on their own (4 us more for 2048 tokens: a lane's turn comes too late),
@@ -67,6 +71,7 @@ struct AtShared {
     uint64_t o_last[2], o_free[2], stat_full[2];         // per unit
     uint32_t tmem, abort;
     uint32_t poison_unit;                 // unit number + 1 that the notes are of
+    uint32_t scores_issued;               // score tiles whose products are issued
     uint16_t done[4];                     // units that each output warp has finished (a CTA has at most 1536 x 1024 / 152)
     float2 stat[2][TILE_ROWS];            // (m, l) of each row at the end of a unit
     uint16_t poison[3][HEAD_DIM];         // first key (from the unit's first partly seen tile) of +inf, -inf, NaN
@@ -171,6 +176,17 @@ FQ_DEV bool units_done(uint32_t n, int lane, AtShared* sh) {
         }
     }
     return true;
+}
+// The products of n score tiles are issued.
+FQ_DEV bool scores_ahead(uint32_t n, AtShared* sh) {
+    const uint32_t t0 = (uint32_t)clock();
+    bool ok = true;
+    while (ok && *(volatile uint32_t*)&sh->scores_issued < n) {
+        const bool late = (uint32_t)clock() - t0 > (uint32_t)WAIT_BUDGET_CYCLES;
+        if (late) give_up(sh);
+        ok = !late && !*(volatile uint32_t*)&sh->abort;
+    }
+    return __all_sync(0xFFFFFFFFu, ok);
 }
 constexpr long long DRAIN_CYCLES = 1 << 20;   // half a millisecond
 
@@ -400,6 +416,7 @@ FQ_DEV void scores(const Args& a, AtShared* sh, uint8_t* q_sm, uint8_t* ring, in
                         mma_f16(tm + AT_S, dq + off, dk + off, idesc, k > 0);
                     }
                     mma_commit(&sh->s_full[x]);
+                    *(volatile uint32_t*)&sh->scores_issued = sn;
                     if (t + 1 == (u.single ? u.nt : u.n(x))) mma_commit(&sh->q_empty[b]);
                 }
                 __syncwarp();
@@ -418,13 +435,16 @@ FQ_DEV void values(const Args& a, AtShared* sh, uint8_t* ring, int units, uint32
     const uint32_t idesc = idesc_bf16_f32(TILE_ROWS, HEAD_DIM, true, false);
     const uint64_t dv0 = sdesc_sw128_mn(smem_u32(ring + AT_KS * AT_TILE_BYTES), AT_PANEL);
     uint32_t vn = 0, pc = 0, oc = 0, it = 0;   // V tiles; phase bits of p_full and o_free; units
+    uint32_t n = 0, n_unit = 0;                // score tiles so far; up to the unit's end
     bool ok = true;
     for (int w; (w = unit_at(it)) < units && ok; ++it) {
         const Unit u = unit_of(a, w);
+        n_unit += u.single ? u.nt : u.n_a + u.n_b;
         for (int t = 0; t < u.nt && ok; ++t) {
             const int s = vn % AT_VS;
             if (!(ok = at_wait_warp(&sh->v_full[s], (vn / AT_VS) & 1, sh))) break;
             ++vn;
+#pragma unroll 1
             for (int x = 0; x < 2; ++x) {
                 if (u.single ? x != (t & 1) : t >= u.n(x)) continue;
                 const bool first = t < u.step, last = u.single ? t + 2 >= u.nt : t + 1 == u.n(x);
@@ -432,8 +452,11 @@ FQ_DEV void values(const Args& a, AtShared* sh, uint8_t* ring, int units, uint32
                     if (!(ok = at_wait_warp(&sh->o_free[x], ((oc >> x) & 1) ^ 1, sh))) break;
                     oc ^= 1u << x;
                 }
+                ++n;
+                if (!u.single && !(ok = scores_ahead(min(n + 2, n_unit), sh))) break;
                 if (!(ok = at_wait_warp(&sh->p_full[x], (pc >> x) & 1, sh))) break;
                 pc ^= 1u << x;
+
                 tc_fence_after();
                 const uint64_t dv = dv0 + (uint32_t)(s * (AT_TILE_BYTES >> 4));
                 if (elect_one()) {
@@ -485,50 +508,35 @@ FQ_DEV void softmax(const Args& a, AtShared* sh, int units, uint32_t tm, int x, 
 #pragma unroll
                 for (int k = 0; k < TILE_ROWS; ++k) s[k] = k < left ? s[k] : -INFINITY;
             }
-            // One pass over the scores: weights against the reference m, while the maximum is
-            // taken for the check of m; the rare tile whose maximum is too far above goes
-            // through twice.  A unit's first tile takes its maximum first.
-            if (i == 0) {
-                float mx[4];
+            float mx[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mx[k] = fmaxf(s[k], s[4 + k]);
+            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(s[k], s[4 + k]);
 #pragma unroll
-                for (int k = 8; k < TILE_ROWS; k += 2) mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], s[k], s[k + 1]);
-                m = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+            for (int k = 8; k < TILE_ROWS; k += 2) mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], s[k], s[k + 1]);
+            const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+            // (a row without a key so far has m = -inf and moves at its first one)
+            const bool move = (top - m) * c > 8.f;
+            const float f = move ? ex2((m - top) * c) : 1.f;
+            if (move) m = top;
+            const float mc = m == -INFINITY ? 0.f : m * c;
+            const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
+            uint64_t ls[2] = {0, 0};   // two pairs of partial sums
+            uint32_t p[TILE_ROWS / 2];
+#pragma unroll
+            for (int k = 0; k < TILE_ROWS / 2; ++k) {
+                float p0, p1;
+                unpair(fma2(pair(s[2 * k], s[2 * k + 1]), c2, mc2), p0, p1);
+                p0 = ex2(p0);
+                p1 = ex2(p1);
+                ls[k & 1] = add2(ls[k & 1], pair(p0, p1));
+                p[k] = bf16x2(p0, p1);
             }
-            if (sc > 0) {   // P V of the tile before has read P and written O
+            // P V of the tile before has read P and written O: it ran beside the exponentials
+            if (sc > 0) {
                 if (!(ok = at_wait_warp(&sh->o_done[x], (sc - 1) & 1, sh))) break;
                 tc_fence_after();
             }
-            uint64_t ls[2];
-            for (;;) {
-                const float mc = m == -INFINITY ? 0.f : m * c;
-                const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
-                float mx[2] = {-INFINITY, -INFINITY};
-                ls[0] = ls[1] = 0;   // two pairs of partial sums
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float s0 = s[32 * h + 2 * k], s1 = s[32 * h + 2 * k + 1];
-                        float p0, p1;
-                        unpair(fma2(pair(s0, s1), c2, mc2), p0, p1);
-                        p0 = ex2(p0);
-                        p1 = ex2(p1);
-                        mx[k & 1] = max3(mx[k & 1], s0, s1);
-                        ls[k & 1] = add2(ls[k & 1], pair(p0, p1));
-                        p[k] = bf16x2(p0, p1);
-                    }
-                    tmem_st16(tP + 16 * h, p);
-                }
-                // (a row without a key so far has m = -inf and moves at its first one)
-                const float top = fmaxf(mx[0], mx[1]);
-                const bool move = (top - m) * c > 8.f;
-                if (!__any_sync(0xFFFFFFFFu, move)) break;
-                const float f = move ? ex2((m - top) * c) : 1.f;
-                if (move) m = top;
-                l *= f;   // (i > 0: a first tile has m = top)
+            if (i > 0 && __any_sync(0xFFFFFFFFu, move)) {
 #pragma unroll 1
                 for (int h = 0; h < 8; ++h) {
                     uint32_t o[16];
@@ -539,13 +547,15 @@ FQ_DEV void softmax(const Args& a, AtShared* sh, int units, uint32_t tm, int x, 
                     tmem_st16(tO + 16 * h, o);
                 }
             }
+#pragma unroll
+            for (int h = 0; h < 4; ++h) tmem_st16(tP + 16 * h, p + 16 * h);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->p_full[x]);
             float l0, l1;
             unpair(add2(ls[0], ls[1]), l0, l1);
-            l += l0 + l1;
+            l = fmaf(l, f, l0 + l1);
             ++sc;
         }
         if (!ok || !(ok = units_done(it, lane, sh))) break;   // the statistics before are read
@@ -711,6 +721,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
             }
             for (int i = 0; i < 4; ++i) sh->done[i] = 0;
             sh->poison_unit = 0;
+            sh->scores_issued = 0;
             // the 128-byte swizzle wants 1024-byte aligned tiles
             sh->abort = (smem_u32(smem) & 1023) ? 1 : 0;
             if (sh->abort) atomicAdd(&g_attn_waits, 1u);
