@@ -237,3 +237,62 @@ def test_shared_step_contract(pair_factory):
     call(prefix, [a, b], [1, 2])
     torch.cuda.synchronize()
     assert fq.fq_kv_len(a) == 1 and fq.fq_kv_len(b) == 2
+
+
+def test_one_token_each_equals_the_batch_step(pair_factory):
+    """64 sequences with one token each: what fq_decode_step_batch computes, up to rounding."""
+    p = pair_factory(workload(SMALL_G4, "q8_0", "bf16", seed=45), max_positions=512, with_oracle=False)
+    ctx = [(7 * i * i) % 200 for i in range(64)]
+    a, b = [[p.new_seq(capacity=c + 1, ctx=c, seq=i, oracle_cache=False)[0] for i, c in enumerate(ctx)] for _ in range(2)]
+    toks = tokens_of(SMALL_G4, 45, 0, 64)
+    got = packed(p, a, [[t] for t in toks])
+    ref = torch.empty(64, SMALL_G4.vocab_size, device=DEV)
+    fq.fq_decode_step_batch(p.model, b, toks, ref.data_ptr(), stream())
+    torch.cuda.synchronize()
+    assert_logits_close(got, ref.cpu().numpy(), "logits")
+    for i, (x, y, c) in enumerate(zip(a, b, ctx)):
+        for L in range(SMALL_G4.num_layers):
+            for u, v in zip(p.read_kv(x, L, c, 1), p.read_kv(y, L, c, 1)):
+                assert_rows(u, v, L, f"sequence {i} layer {L}")
+
+
+def test_steps_at_once_on_two_streams(pair_factory):
+    """A workspace belongs to a stream: two threads with a stream each, the prefix shared, get what
+    one after the other gets."""
+    import threading
+    p = pair_factory(workload(SMALL, "q8_0", "bf16", seed=46), max_positions=512, with_oracle=False)
+    prompts = [tokens_of(SMALL, 46, i, 90 + 31 * i) for i in range(2)]
+    prefix, alone, _ = shared_seqs(p, 6, 100, 0)
+    kvs = [shared_seqs(p, 6, 100, 0)[1] for _ in range(2)]
+    ref_p = []
+    for q in prompts:
+        kv, _ = p.new_seq(capacity=200, ctx=0, seq=0, oracle_cache=False)
+        ref_p.append(packed(p, [kv], [q]))
+    toks = tokens_of(SMALL, 46, 9, 6)
+    ref_s = shared_step(p, prefix, alone, toks)
+    streams = [torch.cuda.Stream(DEV) for _ in range(2)]
+    outs = [[] for _ in range(2)]
+    caches = [[p.new_seq(capacity=200, ctx=0, seq=0, oracle_cache=False)[0] for _ in range(3)] for _ in range(2)]
+    torch.cuda.synchronize()
+
+    def work(i):
+        s = streams[i].cuda_stream
+        with torch.cuda.stream(streams[i]):
+            for kv in caches[i]:
+                o = torch.empty(1, SMALL.vocab_size, device=DEV)
+                fq.fq_forward_step_packed(p.model, [kv], prompts[i], [len(prompts[i])], o.data_ptr(), s)
+                outs[i].append(o)
+            o = torch.empty(6, SMALL.vocab_size, device=DEV)
+            fq.fq_decode_step_shared(p.model, prefix, kvs[i], toks, o.data_ptr(), s)
+            outs[i].append(o)
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    torch.cuda.synchronize()
+    fq.fq_check_device(p.model, stream())
+    for i in range(2):
+        for o in outs[i][:3]:
+            assert np.array_equal(o.cpu().numpy(), ref_p[i])
+        assert np.array_equal(outs[i][3].cpu().numpy(), ref_s)
