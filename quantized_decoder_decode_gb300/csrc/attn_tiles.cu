@@ -41,7 +41,7 @@
 // last values, 1.7 us of outputs.
 // Taken out again: the softmax warps as output warps (2048 tokens 24.7 -> 26.0 us), one
 // loading warp for K and V in the order of their use (packed prompts 50 -> 54), three lanes of one warp
-// that load Q, K and V each on their own (4 us more for 2048 tokens: a lane's turn comes too late),
+// that load Q, K and V each on their own (2 us more for 2048 tokens: a lane's turn comes too late),
 // outputs transposed between lanes for longer stores (packed prompts 50 -> 71 us) or with the next dims read
 // from tensor memory ahead of the stores (55), K tiles released by the softmax warps (8192 tokens 366 -> 373 us).
 
