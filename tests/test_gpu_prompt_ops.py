@@ -89,6 +89,28 @@ def test_prompt(hq, hkv, q_len, k_len, layout, out_dtype):
     assert_within(got, ref, bound, out_dtype == "bf16", f"{hq}/{hkv} {q_len} {k_len}")
 
 
+@pytest.mark.parametrize("hq,hkv", HEADS)
+@pytest.mark.parametrize("own_views", [False, True])
+def test_prompt_few_rows_beside_long_ones(hq, hkv, own_views):
+    """Sequences of a few rows next to one that is split along its keys: short ones take part in its
+    kernel (and are split too), long ones run beside it; one view for all, or a view each."""
+    g = gen(91 + hq + own_views)
+    q_len, k_len = [60, 1, 2, 0, 1, 1], [4000, 1000, 700, 5, 3000, 0]
+    q = normal(g, sum(q_len), hq, D)
+    if own_views:
+        stores = [(layer(g, max(K, 1), hkv, pad=150), layer(g, max(K, 1), hkv, pad=150)) for K in k_len]
+        views = [view_of(k[0], v[0], max(K, 1) + 150, k[2], k[3]) for (k, v), K in zip(stores, k_len)]
+        kv = lambda s, h: tuple(t[1][h, :k_len[s]] for t in stores[s])  # noqa: E731
+    else:
+        k, v = layer(g, sum(k_len), hkv, pad=150), layer(g, sum(k_len), hkv, pad=150)
+        views = view_of(k[0], v[0], sum(k_len) + 150, k[2], k[3])
+        kv = lambda s, h: tuple(t[1][h, sum(k_len[:s]):sum(k_len[:s + 1])] for t in (k, v))  # noqa: E731
+    ref, bound = reference_prompt(q, kv, q_len, k_len, hq, hkv)
+    for out_dtype in ("bf16", "f32"):
+        got = run_prompt(q, views, q_len, k_len, hq, hkv, out_dtype=out_dtype)
+        assert_within(got, ref, bound, out_dtype == "bf16", f"{hq}/{hkv} {out_dtype}")
+
+
 def test_prompt_views_rows_and_strides():
     """A view per sequence (one of them used twice, at overlapping rows), row offsets, row strides of q and
     out; what lies between the rows of out and behind them stays."""
