@@ -1,4 +1,4 @@
-// Joins the partial results that attn_tiles.cu leaves where keys are split or come from two places:
+// Joins the partial results of attn_tiles.cu and attn_rows.cu where keys are split or come from two places:
 //   out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,   M = max_i m_i.
 // A kv head's G rows of a token are joined by G warps: a lane takes one row and four dims (one
 // 16-byte load per partial result, eight in flight), so that a warp reads G x 32 bytes at a time

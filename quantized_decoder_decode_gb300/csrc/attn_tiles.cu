@@ -1,5 +1,5 @@
 // Attention of query tiles on the 5th-generation tensor cores (tcgen05, sm_103a): prompts, chunks
-// of prompts and single tokens behind cached rows, the shared prefix of a decode batch.
+// of prompts behind cached rows, the shared prefix of a decode batch (few rows: attn_rows.cu).
 //
 // One pass over the keys per query tile of 128 packed rows (token, head of the kv head's group):
 //   S = Q K^T (f32, tensor memory),  p = 2^(c S - c m),  O += bf16(p) V,  l += p,
