@@ -425,6 +425,16 @@ fq_status fq_check_device(const fq_model* m, void* stream);
  * served by the bulk-copy GEMV (K % 256 != 0). */
 fq_status fq_debug_wait_timeout(const fq_model* m, void* stream);
 
+/* The same for the attention operators' tile kernel: fq_attn_prompt of one sequence (bf16 output, dense
+ * rows, scale 1 / sqrt(128), keys never split, so no workspace) whose waits may take wait_cycles
+ * clock cycles (0: the usual quarter second, which is also the most).  starve = 1 or 2: the loader of K
+ * or of V leaves out the second tile of each CTA's first unit, so that the waits for it run out;
+ * the kernel lets its other copies land, records the failure and returns.  starve = 0: the plain call.
+ * fq_attn_check reports the failure; the next calls run normally. */
+fq_status fq_debug_attn_wait_timeout(const void* q, const fq_kv_view* view, uint32_t q_len, uint32_t k_len,
+                                     uint32_t num_attention_heads, uint32_t num_key_value_heads, void* out, uint32_t starve,
+                                     uint32_t wait_cycles, void* stream);
+
 const char* fq_last_error(void);
 const char* fq_status_str(fq_status s);
 

@@ -380,14 +380,16 @@ fq_status encode_rows(void* map_k, void* map_v, const KvRows& r, uint64_t rows, 
     return FQ_OK;
 }
 
+constexpr AttnWaits WAITS{1u << 29, 0};   // a quarter second: far beyond any wait that ends
+
 struct ViewUse {
     KvRows rows;
     uint64_t used = 0;   // rows it is read up to
 };
 
 template <class Args>
-fq_status run_tiles_t(const Plan& p, const AttnIo& io, const Partials& part, const AttnSeq* seq, int n_seq, int q_rows,
-                      const ViewUse* views, int n_views, cudaStream_t s) {
+fq_status run_tiles_t(const Plan& p, const AttnIo& io, const AttnWaits& waits, const Partials& part, const AttnSeq* seq,
+                      int n_seq, int q_rows, const ViewUse* views, int n_views, cudaStream_t s) {
     TRY(prepare_device());
     Args* a = new (std::nothrow) Args;
     if (!a) return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
@@ -398,6 +400,7 @@ fq_status run_tiles_t(const Plan& p, const AttnIo& io, const Partials& part, con
         a->g_shift = 0;
         while (io.Hkv << a->g_shift < io.Hq) ++a->g_shift;
         a->inv_hkv = (uint32_t)(((1ull << 31) + io.Hkv - 1) / io.Hkv);
+        a->waits = waits;
         a->part = part;
         std::copy(seq, seq + n_seq, a->seq);
         const uint64_t G = io.Hq / io.Hkv;
@@ -422,8 +425,8 @@ fq_status run_tiles_t(const Plan& p, const AttnIo& io, const Partials& part, con
     return st;
 }
 
-fq_status run_tiles(const Plan& p, const AttnIo& io, const Partials& part, const AttnSeq* seq, int n_seq, int q_rows,
-                    const ViewUse* views, int n_views, cudaStream_t s) {
+fq_status run_tiles(const Plan& p, const AttnIo& io, const AttnWaits& waits, const Partials& part, const AttnSeq* seq,
+                    int n_seq, int q_rows, const ViewUse* views, int n_views, cudaStream_t s) {
     if (p.tiles.empty()) return FQ_OK;
     const size_t n = p.tiles.size();
     // maps for the views that the units read
@@ -444,7 +447,7 @@ fq_status run_tiles(const Plan& p, const AttnIo& io, const Partials& part, const
     }
     auto run = n_views == 1 ? (n <= TileArgs1S::ENTRIES ? run_tiles_t<TileArgs1S> : run_tiles_t<TileArgs1>)
                             : (n <= TileArgsNS::ENTRIES && n_views <= TileArgsNS::VIEWS ? run_tiles_t<TileArgsNS> : run_tiles_t<TileArgsN>);
-    return run(p, io, part, seq, n_seq, q_rows, views, n_views, s);
+    return run(p, io, waits, part, seq, n_seq, q_rows, views, n_views, s);
 }
 
 // The row groups; rows[i]: the rows of view i.
@@ -637,7 +640,7 @@ fq_status fq_attn_prompt(const void* q, uint64_t q_stride, const fq_kv_view* vie
         if (q_rows == 0) return FQ_OK;
         const Partials part = p.at(workspace, Hkv);
         cudaStream_t s = (cudaStream_t)stream;
-        TRY(run_tiles(p, io, part, seq, (int)n_seq, (int)q_rows, use, (int)n_views, s));
+        TRY(run_tiles(p, io, WAITS, part, seq, (int)n_seq, (int)q_rows, use, (int)n_views, s));
         TRY(run_groups(p, io, part, seq, use, s));
         return run_join(p, io, part, s);
     } catch (const std::bad_alloc&) {
@@ -707,9 +710,36 @@ fq_status fq_attn_shared(const void* q, uint64_t q_stride, uint32_t n_seq, const
                         p.bytes(Hkv), io));
         const Partials part = p.at(workspace, Hkv);
         cudaStream_t s = (cudaStream_t)stream;
-        TRY(run_tiles(p, io, part, seq, (int)n_seq + 1, (int)n_seq, use, 1, s));
+        TRY(run_tiles(p, io, WAITS, part, seq, (int)n_seq + 1, (int)n_seq, use, 1, s));
         TRY(run_groups(p, io, part, seq, use, s));
         return run_join(p, io, part, s);
+    } catch (const std::bad_alloc&) {
+        return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
+    }
+}
+
+fq_status fq_debug_attn_wait_timeout(const void* q, const fq_kv_view* view, uint32_t q_len, uint32_t k_len,
+                                     uint32_t num_attention_heads, uint32_t num_key_value_heads, void* out, uint32_t starve,
+                                     uint32_t wait_cycles, void* stream) {
+    const uint32_t Hq = num_attention_heads, Hkv = num_key_value_heads;
+    TRY(check_heads(Hq, Hkv));
+    if (!view) return fail(FQ_ERR_INVALID_ARGUMENT, "null argument");
+    if (starve > 2) return fail(FQ_ERR_INVALID_ARGUMENT, "starve %u (0, 1 or 2)", starve);
+    if (wait_cycles > WAITS.limit) return fail(FQ_ERR_INVALID_ARGUMENT, "more than %u cycles", WAITS.limit);
+    if (q_len == 0) return fail(FQ_ERR_INVALID_SEQUENCE_LENGTH, "no query rows");
+    AttnSeq seq[1];
+    ViewUse use[1];
+    uint64_t q_rows = 0;
+    TRY(prompt_sequences(1, &q_len, nullptr, &k_len, view, 1, Hkv, seq, use, &q_rows));
+    AttnIo io;
+    TRY(attn_common(q, 0, Hq, Hkv, 1.f / std::sqrt((float)HEAD_DIM), out, 0, FQ_BF16, q_rows, nullptr, 0, 0, io));
+    try {
+        Plan p;
+        std::vector<Unit> units;   // whole: nothing to join
+        add_units(units, seq[0], 0, (int)(Hq / Hkv), false);
+        emit(p, units, false);
+        const AttnWaits waits{wait_cycles ? wait_cycles : WAITS.limit, (int)starve};
+        return run_tiles(p, io, waits, Partials(), seq, 1, (int)q_rows, use, 1, (cudaStream_t)stream);
     } catch (const std::bad_alloc&) {
         return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
     }

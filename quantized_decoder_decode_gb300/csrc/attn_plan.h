@@ -91,6 +91,13 @@ struct Partials {
     float2 *a_ml = nullptr, *b_ml = nullptr;
 };
 
+// Bounded waits of attn_tiles.cu.  starve (failure tests): the loader of K (1) or V (2) leaves out the second
+// tile of each CTA's first unit, so that what waits for it runs out.
+struct AttnWaits {
+    uint32_t limit;       // cycles
+    int starve;
+};
+
 template <int NV, int NE>
 struct TileArgs {
     static constexpr int VIEWS = NV, ENTRIES = NE;
@@ -102,6 +109,7 @@ struct TileArgs {
     int negate;           // scale < 0
     int g_shift;          // log2(Hq / Hkv)
     uint32_t inv_hkv;     // ceil(2^31 / Hkv): units (below 2^31 / 1024) are divided by a product
+    AttnWaits waits;
     Partials part;
     AttnSeq seq[MAX_SEQS];
     TileEntry e[NE];

@@ -70,7 +70,8 @@ struct AtShared {
     uint64_t k_full[AT_KS], k_empty[AT_KS], v_full[AT_VS], v_empty[AT_VS], v_raw[AT_VS];
     uint64_t s_full[2], s_free, p_full[2], o_done[2];    // per score tile
     uint64_t o_last[2], o_free[2], stat_full[2];         // per unit
-    uint32_t tmem, abort;
+    uint32_t tmem;
+    uint32_t limit;                       // cycles that a wait may take; 0: one gave up, all roles leave
     uint32_t poison_unit;                 // unit number + 1 that the notes are of
     uint32_t scores_issued;               // score tiles whose products are issued
     uint16_t done[4];                     // units that each output warp has finished (a CTA has at most 1536 x 1024 / 152)
@@ -147,16 +148,17 @@ FQ_DEV void load_kv(const void* map, uint8_t* dst, int row, int head, uint64_t* 
 }
 
 FQ_DEV void give_up(AtShared* sh) {
-    *(volatile uint32_t*)&sh->abort = 1;
+    *(volatile uint32_t*)&sh->limit = 0;
     atomicAdd(&g_attn_waits, 1u);
 }
+FQ_DEV uint32_t wait_limit(const AtShared* sh) { return *(const volatile uint32_t*)&sh->limit; }
 FQ_DEV bool at_wait(uint64_t* bar, uint32_t parity, AtShared* sh) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint32_t t0 = (uint32_t)clock();
     while (!mbar_try_wait(bar, parity)) {
-        if (*(volatile uint32_t*)&sh->abort) return false;
-        if ((uint32_t)clock() - t0 > (uint32_t)WAIT_BUDGET_CYCLES) {
-            give_up(sh);
+        const uint32_t limit = wait_limit(sh);
+        if ((uint32_t)clock() - t0 > limit) {
+            if (limit) give_up(sh);
             return false;
         }
     }
@@ -168,11 +170,11 @@ FQ_DEV bool at_wait_warp(uint64_t* bar, uint32_t parity, AtShared* sh) {
 }
 // The outputs of n units are written.
 FQ_DEV bool units_done(uint32_t n, int lane, AtShared* sh) {
-    const long long t0 = clock64();
+    const uint32_t t0 = (uint32_t)clock();
     while (!__all_sync(0xFFFFFFFFu, *(volatile uint16_t*)&sh->done[lane & 3] >= n)) {
-        const bool late = clock64() - t0 > WAIT_BUDGET_CYCLES;
-        if (__any_sync(0xFFFFFFFFu, late || *(volatile uint32_t*)&sh->abort)) {
-            if (lane == 0 && late) give_up(sh);
+        const uint32_t limit = wait_limit(sh);
+        if (__any_sync(0xFFFFFFFFu, (uint32_t)clock() - t0 > limit)) {
+            if (lane == 0 && limit) give_up(sh);
             return false;
         }
     }
@@ -183,9 +185,9 @@ FQ_DEV bool scores_ahead(uint32_t n, AtShared* sh) {
     const uint32_t t0 = (uint32_t)clock();
     bool ok = true;
     while (ok && *(volatile uint32_t*)&sh->scores_issued < n) {
-        const bool late = (uint32_t)clock() - t0 > (uint32_t)WAIT_BUDGET_CYCLES;
-        if (late) give_up(sh);
-        ok = !late && !*(volatile uint32_t*)&sh->abort;
+        const uint32_t limit = wait_limit(sh);
+        ok = (uint32_t)clock() - t0 <= limit;
+        if (!ok && limit) give_up(sh);
     }
     return __all_sync(0xFFFFFFFFu, ok);
 }
@@ -256,7 +258,8 @@ FQ_DEV void load_keys(const Args& a, AtShared* sh, uint8_t* q_sm, uint8_t* ring,
             const int s = n % AT_KS;
             if (!(ok = at_wait_warp(&sh->k_empty[s], ((n / AT_KS) & 1) ^ 1, sh))) break;
             ++n;
-            if (elect_one()) load_kv(a.map_k[vw], ring + s * AT_TILE_BYTES, row0 + t * TILE_ROWS, u.head, &sh->k_full[s]);
+            if (elect_one() && !(a.waits.starve == 1 && it == 0 && t == 1))
+                load_kv(a.map_k[vw], ring + s * AT_TILE_BYTES, row0 + t * TILE_ROWS, u.head, &sh->k_full[s]);
             __syncwarp();
         }
     }
@@ -365,7 +368,7 @@ FQ_DEV void load_values(const Args& a, AtShared* sh, uint8_t* ring, int units, i
         }
         if (!more || !(ok = at_wait_warp(&sh->v_empty[s], parity, sh))) break;
         const bool whole = u.j0 + t < u.jm;
-        if (elect_one())
+        if (elect_one() && !(a.waits.starve == 2 && it == 0 && t == 1))
             load_kv(a.map_v[vw], ring + (AT_KS + s) * AT_TILE_BYTES, row0 + t * TILE_ROWS, u.head,
                     whole ? &sh->v_full[s] : &sh->v_raw[s]);
         __syncwarp();
@@ -724,8 +727,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
             sh->poison_unit = 0;
             sh->scores_issued = 0;
             // the 128-byte swizzle wants 1024-byte aligned tiles
-            sh->abort = (smem_u32(smem) & 1023) ? 1 : 0;
-            if (sh->abort) atomicAdd(&g_attn_waits, 1u);
+            sh->limit = (smem_u32(smem) & 1023) ? 0 : a.waits.limit;
+            if (sh->limit == 0) atomicAdd(&g_attn_waits, 1u);
             mbar_fence_init();
         }
         __syncwarp();
@@ -733,7 +736,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
         const Unit u = unit_of(a, blockIdx.x);
         const AttnSeq& sq = a.seq[u.seq];
         const int vw = Args::VIEWS == 1 ? 0 : sq.view;
-        const bool pre = u.nt > 0 && sh->abort == 0;
+        const bool pre = u.nt > 0 && sh->limit != 0;
         if (pre && elect_one()) {
             if (u.n_a > 0) load_q(a, sq.q_row0 + u.tok_a, u.head, q_sm, &sh->q_full[0]);
             if (!u.single && u.n_b > 0) load_q(a, sq.q_row0 + u.tok_b, u.head, q_sm + AT_TILE_BYTES, &sh->q_full[1]);
@@ -748,7 +751,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = sh->tmem;
-    const bool run = *(volatile uint32_t*)&sh->abort == 0;   // (not with a misaligned base)
+    const bool run = wait_limit(sh) != 0;   // (not with a misaligned base)
     if (warp < 8) {
         set_regs_up<AT_REGS_SOFTMAX>();
         if (run) softmax(a, sh, units, tm, warp >> 2, tid & 127, lane);

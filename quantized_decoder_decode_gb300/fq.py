@@ -114,6 +114,7 @@ def lib():
                                    ctypes.c_size_t, vp],
                 "fq_attn_shared_workspace": [u32, u32, vp, u32, u32, vp],
                 "fq_attn_check": [vp],
+                "fq_debug_attn_wait_timeout": [vp, vp, u32, u32, u32, u32, vp, u32, u32, vp],
             }
             for name, args in sig.items():
                 fn = getattr(L, name)
@@ -140,7 +141,8 @@ EXPORTED = ("fq_desc_init", "fq_load_weights", "fq_model_free", "fq_kv_init", "f
             "fq_decode_step_batch", "fq_decode_step_all_logits", "fq_forward_step", "fq_decode_greedy", "fq_decode_step_trace", "fq_dequant_rows", "fq_quantize_q8_0", "fq_layer_step_trace",
             "fq_gemv", "fq_step_kernels", "fq_check_device", "fq_debug_wait_timeout", "fq_set_option", "fq_step_path", "fq_layer_step_noalloc", "fq_last_error",
             "fq_status_str", "fq_kv_layer_view", "fq_qk_norm_rope", "fq_attn_prompt", "fq_attn_prompt_workspace",
-            "fq_attn_shared", "fq_attn_shared_workspace", "fq_attn_check", "fq_forward_step_packed", "fq_decode_step_shared")
+            "fq_attn_shared", "fq_attn_shared_workspace", "fq_attn_check", "fq_forward_step_packed", "fq_decode_step_shared",
+            "fq_debug_attn_wait_timeout")
 
 
 def _check(status: int, where: str) -> None:
@@ -481,3 +483,12 @@ def fq_attn_shared(q_ptr: int, prefix, prefix_len: int, tails, tail_len, num_att
 
 def fq_attn_check(stream: int = 0) -> None:
     _check(lib().fq_attn_check(stream), "fq_attn_check")
+
+
+def fq_debug_attn_wait_timeout(q_ptr: int, view, q_len: int, k_len: int, num_attention_heads: int,
+                               num_key_value_heads: int, out_ptr: int, starve: int, wait_cycles: int = 0,
+                               stream: int = 0) -> None:
+    """Test hook: the prompt attention's tile kernel with a loader that leaves out a tile of K (1) or V (2)."""
+    _check(lib().fq_debug_attn_wait_timeout(q_ptr, ctypes.byref(view), q_len, k_len, num_attention_heads,
+                                            num_key_value_heads, out_ptr, starve, wait_cycles, stream),
+           "fq_debug_attn_wait_timeout")

@@ -1,0 +1,74 @@
+"""The failure path of the attention operators' bounded waits, made to run out on purpose without any
+fault: a tile kernel whose loader leaves out one tile of K or V and whose waits may take half a
+millisecond.  Every role has to give up and leave, the failure is reported once, and the calls behind it
+are right."""
+import math
+
+import pytest
+import torch
+
+from quantized_decoder_decode_gb300 import fq
+from tests.prompt_ops_util import D, DEV, assert_within, attend, causal, gen, normal
+
+pytestmark = pytest.mark.gpu
+
+HALF_MS = 1 << 20   # cycles
+
+
+def stream():
+    return torch.cuda.current_stream(DEV).cuda_stream
+
+
+class Case:
+    """Prompt attention of one sequence, its reference, and the call with and without a tile left out."""
+
+    def __init__(self, hq, hkv, L, K, seed=3):
+        g = gen(seed)
+        self.hq, self.hkv, self.L, self.K = hq, hkv, L, K
+        self.q, self.k, self.v = normal(g, L, hq, D), normal(g, hkv, K, D), normal(g, hkv, K, D)
+        self.view = fq.fq_kv_view(self.k.data_ptr(), self.v.data_ptr(), K, D, K * D)
+        self.out = torch.empty_like(self.q)
+
+    def starved(self, starve, cycles=HALF_MS):
+        fq.fq_debug_attn_wait_timeout(self.q.data_ptr(), self.view, self.L, self.K, self.hq, self.hkv, self.out.data_ptr(),
+                                      starve, cycles, stream())
+
+    def run(self):
+        need = fq.fq_attn_prompt_workspace([self.L], [self.K], self.hq, self.hkv)
+        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=DEV)
+        self.out.fill_(float("nan"))
+        fq.fq_attn_prompt(self.q.data_ptr(), self.view, [self.L], [self.K], self.hq, self.hkv, 1 / math.sqrt(D),
+                          self.out.data_ptr(), ws.data_ptr(), ws.numel(), stream())
+
+    def check(self):
+        for h in range(self.hq):
+            k, v = self.k[h // (self.hq // self.hkv)], self.v[h // (self.hq // self.hkv)]
+            ref, bound = attend(self.q[:, h], k, v, causal(self.L, self.K), 1 / math.sqrt(D))
+            assert_within(self.out[:, h], ref, bound, True, f"head {h}")
+
+
+def reported(call):
+    with pytest.raises(fq.FqError) as e:
+        call()
+    assert e.value.status == fq.DEVICE_TIMEOUT
+
+
+# pairs of query tiles, single tiles; tiles that every row sees and tiles that some rows see in part; one
+# unit per CTA and several
+@pytest.mark.parametrize("starve", [1, 2])
+@pytest.mark.parametrize("hq,hkv,L,K", [(4, 2, 100, 600), (4, 4, 50, 300), (8, 1, 16, 1500), (4, 2, 700, 700), (32, 8, 1500, 2000)])
+def test_left_out_tile_is_reported_and_later_calls_are_right(starve, hq, hkv, L, K):
+    c = Case(hq, hkv, L, K)
+    c.starved(0)
+    fq.fq_attn_check(stream())
+    c.check()
+    c.starved(starve)
+    reported(lambda: fq.fq_attn_check(stream()))
+    fq.fq_attn_check(stream())   # once
+    c.run()
+    fq.fq_attn_check(stream())
+    c.check()
+    c.starved(starve)            # the call right behind it on the stream is right too
+    c.run()
+    reported(lambda: fq.fq_attn_check(stream()))
+    c.check()
