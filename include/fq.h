@@ -311,9 +311,11 @@ fq_status fq_attn_shared_workspace(uint32_t n_seq, uint32_t prefix_len, const ui
                                    uint32_t num_attention_heads, uint32_t num_key_value_heads, size_t* bytes);
 
 /* Synchronise `stream` and report bounded device waits of the two attentions that gave up on the
- * current device since the last check (DEVICE_TIMEOUT: the outputs of the calls since then are
- * invalid); clears the record.  fq_check_device reads (and clears) the same record next to its
- * model's own. */
+ * current device since this host thread's last check (a thread's first: since the last check of
+ * any).  DEVICE_TIMEOUT: the outputs of the calls since then, of whichever thread and stream, may be
+ * invalid.  No check hides a failure from another thread.  The attention inside
+ * fq_forward_step_packed and fq_decode_step_shared is recorded with its model (fq_check_device) and
+ * not here. */
 fq_status fq_attn_check(void* stream);
 
 /* ---- inspection (tests and tools; not the hot path) ---- */
@@ -413,7 +415,7 @@ fq_status fq_step_kernels(const fq_model* m, void* stream, uint32_t* kernels);
  * CTA gave up (the kernel returned early; results of that step are invalid).  Clears the
  * record and, on a timeout, zeroes the arrival counters and tickets of every workspace of
  * the model (on each workspace's own stream), so that later steps start from a clean state.
- * Waits of the attention operators (fq_attn_check) are reported and cleared too. */
+ * (Calls of the attention operators outside a step: fq_attn_check.) */
 fq_status fq_check_device(const fq_model* m, void* stream);
 
 /* Test hook for the failure path of the bounded device waits (no counterpart on the pages).
@@ -430,8 +432,9 @@ fq_status fq_debug_wait_timeout(const fq_model* m, void* stream);
  * clock cycles (0: the usual quarter second, which is also the most).  starve = 1 or 2: the loader of K
  * or of V leaves out the second tile of each CTA's first unit, so that the waits for it run out;
  * the kernel lets its other copies land, records the failure and returns.  starve = 0: the plain call.
- * fq_attn_check reports the failure; the next calls run normally. */
-fq_status fq_debug_attn_wait_timeout(const void* q, const fq_kv_view* view, uint32_t q_len, uint32_t k_len,
+ * The failure is recorded with the model, as in its steps (fq_check_device), or, with m NULL, as one of
+ * the operators' own (fq_attn_check); the next calls run normally. */
+fq_status fq_debug_attn_wait_timeout(const fq_model* m, const void* q, const fq_kv_view* view, uint32_t q_len, uint32_t k_len,
                                      uint32_t num_attention_heads, uint32_t num_key_value_heads, void* out, uint32_t starve,
                                      uint32_t wait_cycles, void* stream);
 

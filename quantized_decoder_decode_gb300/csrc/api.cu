@@ -627,6 +627,14 @@ fq_status rows_attn_bytes(const fq_model* m, const RowsPass& r, size_t* bytes) {
                     : fq_attn_prompt_workspace(r.n_seq, r.len, r.k_len, Hq, Hkv, bytes);
 }
 
+// The attention's waits in a step go to the model's error word.
+AttnWaits attn_waits(const fq_model* m) {
+    AttnWaits w;
+    w.record = m->err;
+    w.code = 512;
+    return w;
+}
+
 // Embedding and every layer of one pass; the residual rows end up in w->rows.x.  Each projection
 // goes over all rows before the next one, so that its weights come from L2 after the first chunk.
 fq_status enqueue_rows(const fq_model* m, Workspace* w, const RowsPass& r, cudaStream_t s) {
@@ -647,6 +655,7 @@ fq_status enqueue_rows(const fq_model* m, Workspace* w, const RowsPass& r, cudaS
         launch_embed(m->tok_embd, w->st, n, b.x + o * H, s, false);
     });
     const float scale = 1.f / sqrtf((float)HEAD_DIM);
+    const AttnWaits waits = attn_waits(m);
     for (uint32_t L = 0; L < p.num_layers; ++L) {
         const LayerW& lw = m->layers[L];
         chunks([&](size_t o, int n) {
@@ -661,12 +670,12 @@ fq_status enqueue_rows(const fq_model* m, Workspace* w, const RowsPass& r, cudaS
                             p.rms_norm_eps, reinterpret_cast<const float*>(m->rope), (uint32_t)m->max_pos, b.q, 0, s));
         if (r.prefix) {
             TRY(fq_kv_layer_view(r.prefix, L, &shared));
-            TRY(fq_attn_shared(b.q, 0, r.n_seq, &shared, r.prefix->len, views, r.k_len, Hq, Hkv, scale, b.attn, 0, FQ_F32,
-                               b.attn_ws, b.attn_cap, s));
+            TRY(attn_shared(waits, b.q, 0, r.n_seq, &shared, r.prefix->len, views, r.k_len, Hq, Hkv, scale, b.attn, 0, FQ_F32,
+                            b.attn_ws, b.attn_cap, s));
         } else {
             const uint32_t zero[MAX_SEQ] = {};
-            TRY(fq_attn_prompt(b.q, 0, views, r.n_seq, r.n_seq, r.len, zero, r.k_len, Hq, Hkv, scale, b.attn, 0, FQ_F32,
-                               b.attn_ws, b.attn_cap, s));
+            TRY(attn_prompt(waits, b.q, 0, views, r.n_seq, r.n_seq, r.len, zero, r.k_len, Hq, Hkv, scale, b.attn, 0, FQ_F32,
+                            b.attn_ws, b.attn_cap, s));
         }
         chunks([&](size_t o, int n) {
             GemvArgs g = dense_args(lw.o, n, b.attn + o * D, D, b.x + o * H, H, EPI_ADD);
@@ -1478,8 +1487,6 @@ fq_status fq_check_device(const fq_model* m, void* stream) {
     uint32_t host = 0;
     CK(cudaMemcpyAsync(&host, m->err, sizeof host, cudaMemcpyDeviceToHost, s));
     CK(cudaStreamSynchronize(s));
-    uint32_t waits = 0;   // of the packed and shared-prefix steps' attention
-    CK(attn_wait_record(&waits, s));
     if (host) {
         // A CTA that gave up left its arrival counters and tickets half counted; every
         // workspace of the model is re-armed on its own stream (after the work queued there)
@@ -1490,7 +1497,6 @@ fq_status fq_check_device(const fq_model* m, void* stream) {
         CK(cudaMemsetAsync(m->err, 0, sizeof(uint32_t), s));
         return fail(FQ_ERR_DEVICE_TIMEOUT, "a bounded device wait gave up (code %u)", host);
     }
-    if (waits) return fail(FQ_ERR_DEVICE_TIMEOUT, "%u bounded waits of the attention operators gave up", waits);
     return FQ_OK;
 }
 
@@ -1507,6 +1513,17 @@ fq_status fq_debug_wait_timeout(const fq_model* m, void* stream) {
     if (!launch_gemv_tma(g, s, false)) return fail(FQ_ERR_UNSUPPORTED, "bulk-copy GEMV not applicable");
     CK(cudaGetLastError());
     return FQ_OK;
+}
+
+fq_status fq_debug_attn_wait_timeout(const fq_model* m, const void* q, const fq_kv_view* view, uint32_t q_len, uint32_t k_len,
+                                     uint32_t num_attention_heads, uint32_t num_key_value_heads, void* out, uint32_t starve,
+                                     uint32_t wait_cycles, void* stream) {
+    AttnWaits w = m ? attn_waits(m) : AttnWaits();
+    if (starve > 2) return fail(FQ_ERR_INVALID_ARGUMENT, "starve %u (0, 1 or 2)", starve);
+    if (wait_cycles > w.limit) return fail(FQ_ERR_INVALID_ARGUMENT, "more than %u cycles", w.limit);
+    w.starve = (int)starve;
+    if (wait_cycles) w.limit = wait_cycles;
+    return attn_prompt_whole(w, q, view, q_len, k_len, num_attention_heads, num_key_value_heads, out, stream);
 }
 
 fq_status fq_quantize_q8_0(const float* x, uint64_t n, void* blocks, void* stream) {

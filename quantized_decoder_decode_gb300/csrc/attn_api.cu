@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <cmath>
 #include <mutex>
@@ -358,16 +359,39 @@ void plan_shared(Plan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G, uint32
 
 // ---------------------------------------------------------------- launches
 
-fq_status prepare_device() {
-    static std::mutex mu;
-    static bool done[64] = {};
+// The record of give-ups of one device that belongs to no model.  It only ever counts up, so that no check can
+// take one away from another thread: every thread compares it with what it was at its own last check, and
+// starts from the last value that any check has read.
+struct Device {
+    std::mutex mu;
+    uint32_t* word = nullptr;          // (set once the kernels are prepared)
+    std::atomic<uint32_t> read{0};
+};
+constexpr int MAX_DEVICES = 64;
+Device g_devices[MAX_DEVICES];
+struct Seen {
+    bool any = false;
+    uint32_t count = 0;
+};
+thread_local Seen t_seen[MAX_DEVICES];
+
+fq_status prepare_device(Device** out, Seen** seen) {
     int dev = 0;
     CK(cudaGetDevice(&dev));
-    std::lock_guard<std::mutex> lk(mu);
-    if (dev < 64 && done[dev]) return FQ_OK;
-    CK(attn_tiles_prepare());
-    CK(attn_rows_prepare());
-    if (dev < 64) done[dev] = true;
+    if (dev >= MAX_DEVICES) return fail(FQ_ERR_UNSUPPORTED, "device %d of %d at most", dev, MAX_DEVICES);
+    Device& d = g_devices[dev];
+    Seen& s = t_seen[dev];
+    if (!s.any) s = Seen{true, d.read.load()};
+    std::lock_guard<std::mutex> lk(d.mu);
+    if (!d.word) {
+        uint32_t* w = nullptr;
+        CK(attn_tiles_prepare());
+        CK(attn_rows_prepare());
+        CK(attn_wait_word(&w));
+        d.word = w;
+    }
+    *out = &d;
+    *seen = &s;
     return FQ_OK;
 }
 
@@ -380,8 +404,6 @@ fq_status encode_rows(void* map_k, void* map_v, const KvRows& r, uint64_t rows, 
     return FQ_OK;
 }
 
-constexpr AttnWaits WAITS{1u << 29, 0};   // a quarter second: far beyond any wait that ends
-
 struct ViewUse {
     KvRows rows;
     uint64_t used = 0;   // rows it is read up to
@@ -390,7 +412,9 @@ struct ViewUse {
 template <class Args>
 fq_status run_tiles_t(const Plan& p, const AttnIo& io, const AttnWaits& waits, const Partials& part, const AttnSeq* seq,
                       int n_seq, int q_rows, const ViewUse* views, int n_views, cudaStream_t s) {
-    TRY(prepare_device());
+    Device* dev;
+    Seen* seen;
+    TRY(prepare_device(&dev, &seen));
     Args* a = new (std::nothrow) Args;
     if (!a) return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
     auto run = [&]() -> fq_status {
@@ -401,6 +425,7 @@ fq_status run_tiles_t(const Plan& p, const AttnIo& io, const AttnWaits& waits, c
         while (io.Hkv << a->g_shift < io.Hq) ++a->g_shift;
         a->inv_hkv = (uint32_t)(((1ull << 31) + io.Hkv - 1) / io.Hkv);
         a->waits = waits;
+        if (!waits.record) a->waits.record = dev->word;
         a->part = part;
         std::copy(seq, seq + n_seq, a->seq);
         const uint64_t G = io.Hq / io.Hkv;
@@ -454,7 +479,9 @@ fq_status run_tiles(const Plan& p, const AttnIo& io, const AttnWaits& waits, con
 fq_status run_groups(const Plan& p, const AttnIo& io, const Partials& part, const AttnSeq* seq, const ViewUse* views,
                      cudaStream_t s) {
     if (p.groups.empty()) return FQ_OK;
-    TRY(prepare_device());
+    Device* dev;
+    Seen* seen;
+    TRY(prepare_device(&dev, &seen));
     RowsArgs a;
     a.io = io;
     a.part = part;
@@ -520,7 +547,139 @@ fq_status attn_common(const void* q, uint64_t q_stride, uint32_t Hq, uint32_t Hk
     return FQ_OK;
 }
 
+// Row ranges of the sequences of a prompt call; views may be null (lengths only).
+fq_status prompt_sequences(uint32_t n_seq, const uint32_t* q_len, const uint32_t* kv_row0, const uint32_t* k_len,
+                                  const fq_kv_view* views, uint32_t n_views, uint32_t Hkv, AttnSeq* seq, ViewUse* use,
+                                  uint64_t* q_rows) {
+    uint64_t qr = 0, kr = 0;
+    for (uint32_t s = 0; s < n_seq; ++s) {
+        if (q_len[s] > MAX_ROWS || k_len[s] > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 rows");
+        uint64_t r0 = 0;
+        const uint32_t w = n_views == 1 ? 0 : s;
+        if (views) {
+            r0 = kv_row0 ? kv_row0[s] : n_views == 1 ? kr : 0;
+            TRY(check_view(views[w], Hkv, r0, k_len[s], "sequence", s));
+            use[w].rows = rows_of(views[w]);
+            if (k_len[s]) use[w].used = std::max(use[w].used, r0 + k_len[s]);
+        }
+        seq[s] = AttnSeq{(int32_t)qr, (int32_t)q_len[s], (int32_t)r0, (int32_t)k_len[s],
+                         (int32_t)k_len[s] - (int32_t)q_len[s] + 1, (int32_t)w};
+        qr += q_len[s];
+        kr += k_len[s];
+        if (qr > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 query rows");
+    }
+    *q_rows = qr;
+    return FQ_OK;
+}
+
+// The sequences of a shared call: the tails, then all query rows over the prefix.
+fq_status shared_sequences(uint32_t n_seq, uint32_t prefix_len, const uint32_t* tail_len, AttnSeq* seq) {
+    if (prefix_len > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 rows");
+    int32_t view = 1;
+    for (uint32_t s = 0; s < n_seq; ++s) {
+        if (tail_len[s] > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 rows");
+        seq[s] = AttnSeq{(int32_t)s, 1, 0, (int32_t)tail_len[s], SEES_ALL, tail_len[s] ? view++ : 0};
+    }
+    seq[n_seq] = AttnSeq{0, (int32_t)n_seq, 0, (int32_t)prefix_len, SEES_ALL, 0};
+    return FQ_OK;
+}
+
 }  // namespace
+
+namespace fq {
+
+fq_status attn_prompt(const AttnWaits& waits, const void* q, uint64_t q_stride, const fq_kv_view* views, uint32_t n_views,
+                      uint32_t n_seq, const uint32_t* q_len, const uint32_t* kv_row0, const uint32_t* k_len, uint32_t Hq,
+                      uint32_t Hkv, float scale, void* out, uint64_t out_stride, fq_dtype out_dtype, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+    TRY(check_heads(Hq, Hkv));
+    TRY(check_count(n_seq));
+    if (!q_len || !k_len || !views) return fail(FQ_ERR_INVALID_ARGUMENT, "null argument");
+    if (n_views != 1 && n_views != n_seq) return fail(FQ_ERR_INVALID_ARGUMENT, "%u views for %u sequences", n_views, n_seq);
+    AttnSeq seq[MAX_SEQ];
+    ViewUse use[MAX_SEQ];
+    uint64_t q_rows = 0;
+    TRY(prompt_sequences(n_seq, q_len, kv_row0, k_len, views, n_views, Hkv, seq, use, &q_rows));
+    try {
+        Plan p;
+        plan_prompt(p, n_seq, seq, Hq / Hkv, Hkv);
+        AttnIo io;
+        TRY(attn_common(q, q_stride, Hq, Hkv, scale, out, out_stride, out_dtype, q_rows, workspace, workspace_bytes,
+                        p.bytes(Hkv), io));
+        if (q_rows == 0) return FQ_OK;
+        const Partials part = p.at(workspace, Hkv);
+        cudaStream_t s = (cudaStream_t)stream;
+        TRY(run_tiles(p, io, waits, part, seq, (int)n_seq, (int)q_rows, use, (int)n_views, s));
+        TRY(run_groups(p, io, part, seq, use, s));
+        return run_join(p, io, part, s);
+    } catch (const std::bad_alloc&) {
+        return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
+    }
+}
+
+fq_status attn_shared(const AttnWaits& waits, const void* q, uint64_t q_stride, uint32_t n_seq, const fq_kv_view* prefix,
+                      uint32_t prefix_len, const fq_kv_view* tails, const uint32_t* tail_len, uint32_t Hq, uint32_t Hkv,
+                      float scale, void* out, uint64_t out_stride, fq_dtype out_dtype, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+    TRY(check_heads(Hq, Hkv));
+    TRY(check_count(n_seq));
+    if (!tail_len) return fail(FQ_ERR_INVALID_ARGUMENT, "null argument");
+    ViewUse use[MAX_SEQS];
+    int n_views = 1;   // the prefix is view 0
+    if (prefix_len) {
+        if (!prefix) return fail(FQ_ERR_INVALID_ARGUMENT, "null prefix");
+        TRY(check_view(*prefix, Hkv, 0, prefix_len, "prefix", 0));
+        use[0].rows = rows_of(*prefix);
+        use[0].used = prefix_len;
+    }
+    for (uint32_t s = 0; s < n_seq; ++s) {
+        if (!tail_len[s]) continue;
+        if (!tails) return fail(FQ_ERR_INVALID_ARGUMENT, "null tails");
+        TRY(check_view(tails[s], Hkv, 0, tail_len[s], "tail", s));
+        use[n_views].rows = rows_of(tails[s]);
+        use[n_views++].used = tail_len[s];
+    }
+    AttnSeq seq[MAX_SEQS];
+    TRY(shared_sequences(n_seq, prefix_len, tail_len, seq));
+    try {
+        Plan p;
+        plan_shared(p, n_seq, seq, Hq / Hkv, Hkv);
+        AttnIo io;
+        TRY(attn_common(q, q_stride, Hq, Hkv, scale, out, out_stride, out_dtype, n_seq, workspace, workspace_bytes,
+                        p.bytes(Hkv), io));
+        const Partials part = p.at(workspace, Hkv);
+        cudaStream_t s = (cudaStream_t)stream;
+        TRY(run_tiles(p, io, waits, part, seq, (int)n_seq + 1, (int)n_seq, use, 1, s));
+        TRY(run_groups(p, io, part, seq, use, s));
+        return run_join(p, io, part, s);
+    } catch (const std::bad_alloc&) {
+        return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
+    }
+}
+
+fq_status attn_prompt_whole(const AttnWaits& waits, const void* q, const fq_kv_view* view, uint32_t q_len, uint32_t k_len,
+                            uint32_t Hq, uint32_t Hkv, void* out, void* stream) {
+    TRY(check_heads(Hq, Hkv));
+    if (!view) return fail(FQ_ERR_INVALID_ARGUMENT, "null argument");
+    if (q_len == 0) return fail(FQ_ERR_INVALID_SEQUENCE_LENGTH, "no query rows");
+    AttnSeq seq[1];
+    ViewUse use[1];
+    uint64_t q_rows = 0;
+    TRY(prompt_sequences(1, &q_len, nullptr, &k_len, view, 1, Hkv, seq, use, &q_rows));
+    AttnIo io;
+    TRY(attn_common(q, 0, Hq, Hkv, 1.f / std::sqrt((float)HEAD_DIM), out, 0, FQ_BF16, q_rows, nullptr, 0, 0, io));
+    try {
+        Plan p;
+        std::vector<Unit> units;
+        add_units(units, seq[0], 0, (int)(Hq / Hkv), false);
+        emit(p, units, false);
+        return run_tiles(p, io, waits, Partials(), seq, 1, (int)q_rows, use, 1, (cudaStream_t)stream);
+    } catch (const std::bad_alloc&) {
+        return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
+    }
+}
+
+}  // namespace fq
 
 extern "C" {
 
@@ -575,31 +734,6 @@ fq_status fq_qk_norm_rope(const float* qkv, uint64_t qkv_stride, uint32_t n_seq,
     return FQ_OK;
 }
 
-// Row ranges of the sequences of a prompt call; views may be null (lengths only).
-static fq_status prompt_sequences(uint32_t n_seq, const uint32_t* q_len, const uint32_t* kv_row0, const uint32_t* k_len,
-                                  const fq_kv_view* views, uint32_t n_views, uint32_t Hkv, AttnSeq* seq, ViewUse* use,
-                                  uint64_t* q_rows) {
-    uint64_t qr = 0, kr = 0;
-    for (uint32_t s = 0; s < n_seq; ++s) {
-        if (q_len[s] > MAX_ROWS || k_len[s] > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 rows");
-        uint64_t r0 = 0;
-        const uint32_t w = n_views == 1 ? 0 : s;
-        if (views) {
-            r0 = kv_row0 ? kv_row0[s] : n_views == 1 ? kr : 0;
-            TRY(check_view(views[w], Hkv, r0, k_len[s], "sequence", s));
-            use[w].rows = rows_of(views[w]);
-            if (k_len[s]) use[w].used = std::max(use[w].used, r0 + k_len[s]);
-        }
-        seq[s] = AttnSeq{(int32_t)qr, (int32_t)q_len[s], (int32_t)r0, (int32_t)k_len[s],
-                         (int32_t)k_len[s] - (int32_t)q_len[s] + 1, (int32_t)w};
-        qr += q_len[s];
-        kr += k_len[s];
-        if (qr > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 query rows");
-    }
-    *q_rows = qr;
-    return FQ_OK;
-}
-
 fq_status fq_attn_prompt_workspace(uint32_t n_seq, const uint32_t* q_len, const uint32_t* k_len,
                                    uint32_t num_attention_heads, uint32_t num_key_value_heads, size_t* bytes) {
     TRY(check_heads(num_attention_heads, num_key_value_heads));
@@ -615,48 +749,6 @@ fq_status fq_attn_prompt_workspace(uint32_t n_seq, const uint32_t* q_len, const 
     } catch (const std::bad_alloc&) {
         return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
     }
-    return FQ_OK;
-}
-
-fq_status fq_attn_prompt(const void* q, uint64_t q_stride, const fq_kv_view* views, uint32_t n_views, uint32_t n_seq,
-                         const uint32_t* q_len, const uint32_t* kv_row0, const uint32_t* k_len,
-                         uint32_t num_attention_heads, uint32_t num_key_value_heads, float scale, void* out,
-                         uint64_t out_stride, fq_dtype out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
-    const uint32_t Hq = num_attention_heads, Hkv = num_key_value_heads;
-    TRY(check_heads(Hq, Hkv));
-    TRY(check_count(n_seq));
-    if (!q_len || !k_len || !views) return fail(FQ_ERR_INVALID_ARGUMENT, "null argument");
-    if (n_views != 1 && n_views != n_seq) return fail(FQ_ERR_INVALID_ARGUMENT, "%u views for %u sequences", n_views, n_seq);
-    AttnSeq seq[MAX_SEQ];
-    ViewUse use[MAX_SEQ];
-    uint64_t q_rows = 0;
-    TRY(prompt_sequences(n_seq, q_len, kv_row0, k_len, views, n_views, Hkv, seq, use, &q_rows));
-    try {
-        Plan p;
-        plan_prompt(p, n_seq, seq, Hq / Hkv, Hkv);
-        AttnIo io;
-        TRY(attn_common(q, q_stride, Hq, Hkv, scale, out, out_stride, out_dtype, q_rows, workspace, workspace_bytes,
-                        p.bytes(Hkv), io));
-        if (q_rows == 0) return FQ_OK;
-        const Partials part = p.at(workspace, Hkv);
-        cudaStream_t s = (cudaStream_t)stream;
-        TRY(run_tiles(p, io, WAITS, part, seq, (int)n_seq, (int)q_rows, use, (int)n_views, s));
-        TRY(run_groups(p, io, part, seq, use, s));
-        return run_join(p, io, part, s);
-    } catch (const std::bad_alloc&) {
-        return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
-    }
-}
-
-// The sequences of a shared call: the tails, then all query rows over the prefix.
-static fq_status shared_sequences(uint32_t n_seq, uint32_t prefix_len, const uint32_t* tail_len, AttnSeq* seq) {
-    if (prefix_len > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 rows");
-    int32_t view = 1;
-    for (uint32_t s = 0; s < n_seq; ++s) {
-        if (tail_len[s] > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 rows");
-        seq[s] = AttnSeq{(int32_t)s, 1, 0, (int32_t)tail_len[s], SEES_ALL, tail_len[s] ? view++ : 0};
-    }
-    seq[n_seq] = AttnSeq{0, (int32_t)n_seq, 0, (int32_t)prefix_len, SEES_ALL, 0};
     return FQ_OK;
 }
 
@@ -677,78 +769,35 @@ fq_status fq_attn_shared_workspace(uint32_t n_seq, uint32_t prefix_len, const ui
     return FQ_OK;
 }
 
+fq_status fq_attn_prompt(const void* q, uint64_t q_stride, const fq_kv_view* views, uint32_t n_views, uint32_t n_seq,
+                         const uint32_t* q_len, const uint32_t* kv_row0, const uint32_t* k_len,
+                         uint32_t num_attention_heads, uint32_t num_key_value_heads, float scale, void* out,
+                         uint64_t out_stride, fq_dtype out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    return attn_prompt(AttnWaits(), q, q_stride, views, n_views, n_seq, q_len, kv_row0, k_len, num_attention_heads,
+                       num_key_value_heads, scale, out, out_stride, out_dtype, workspace, workspace_bytes, stream);
+}
+
 fq_status fq_attn_shared(const void* q, uint64_t q_stride, uint32_t n_seq, const fq_kv_view* prefix,
                          uint32_t prefix_len, const fq_kv_view* tails, const uint32_t* tail_len,
                          uint32_t num_attention_heads, uint32_t num_key_value_heads, float scale, void* out,
                          uint64_t out_stride, fq_dtype out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
-    const uint32_t Hq = num_attention_heads, Hkv = num_key_value_heads;
-    TRY(check_heads(Hq, Hkv));
-    TRY(check_count(n_seq));
-    if (!tail_len) return fail(FQ_ERR_INVALID_ARGUMENT, "null argument");
-    ViewUse use[MAX_SEQS];
-    int n_views = 1;   // the prefix is view 0
-    if (prefix_len) {
-        if (!prefix) return fail(FQ_ERR_INVALID_ARGUMENT, "null prefix");
-        TRY(check_view(*prefix, Hkv, 0, prefix_len, "prefix", 0));
-        use[0].rows = rows_of(*prefix);
-        use[0].used = prefix_len;
-    }
-    for (uint32_t s = 0; s < n_seq; ++s) {
-        if (!tail_len[s]) continue;
-        if (!tails) return fail(FQ_ERR_INVALID_ARGUMENT, "null tails");
-        TRY(check_view(tails[s], Hkv, 0, tail_len[s], "tail", s));
-        use[n_views].rows = rows_of(tails[s]);
-        use[n_views++].used = tail_len[s];
-    }
-    AttnSeq seq[MAX_SEQS];
-    TRY(shared_sequences(n_seq, prefix_len, tail_len, seq));
-    try {
-        Plan p;
-        plan_shared(p, n_seq, seq, Hq / Hkv, Hkv);
-        AttnIo io;
-        TRY(attn_common(q, q_stride, Hq, Hkv, scale, out, out_stride, out_dtype, n_seq, workspace, workspace_bytes,
-                        p.bytes(Hkv), io));
-        const Partials part = p.at(workspace, Hkv);
-        cudaStream_t s = (cudaStream_t)stream;
-        TRY(run_tiles(p, io, WAITS, part, seq, (int)n_seq + 1, (int)n_seq, use, 1, s));
-        TRY(run_groups(p, io, part, seq, use, s));
-        return run_join(p, io, part, s);
-    } catch (const std::bad_alloc&) {
-        return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
-    }
-}
-
-fq_status fq_debug_attn_wait_timeout(const void* q, const fq_kv_view* view, uint32_t q_len, uint32_t k_len,
-                                     uint32_t num_attention_heads, uint32_t num_key_value_heads, void* out, uint32_t starve,
-                                     uint32_t wait_cycles, void* stream) {
-    const uint32_t Hq = num_attention_heads, Hkv = num_key_value_heads;
-    TRY(check_heads(Hq, Hkv));
-    if (!view) return fail(FQ_ERR_INVALID_ARGUMENT, "null argument");
-    if (starve > 2) return fail(FQ_ERR_INVALID_ARGUMENT, "starve %u (0, 1 or 2)", starve);
-    if (wait_cycles > WAITS.limit) return fail(FQ_ERR_INVALID_ARGUMENT, "more than %u cycles", WAITS.limit);
-    if (q_len == 0) return fail(FQ_ERR_INVALID_SEQUENCE_LENGTH, "no query rows");
-    AttnSeq seq[1];
-    ViewUse use[1];
-    uint64_t q_rows = 0;
-    TRY(prompt_sequences(1, &q_len, nullptr, &k_len, view, 1, Hkv, seq, use, &q_rows));
-    AttnIo io;
-    TRY(attn_common(q, 0, Hq, Hkv, 1.f / std::sqrt((float)HEAD_DIM), out, 0, FQ_BF16, q_rows, nullptr, 0, 0, io));
-    try {
-        Plan p;
-        std::vector<Unit> units;   // whole: nothing to join
-        add_units(units, seq[0], 0, (int)(Hq / Hkv), false);
-        emit(p, units, false);
-        const AttnWaits waits{wait_cycles ? wait_cycles : WAITS.limit, (int)starve};
-        return run_tiles(p, io, waits, Partials(), seq, 1, (int)q_rows, use, 1, (cudaStream_t)stream);
-    } catch (const std::bad_alloc&) {
-        return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
-    }
+    return attn_shared(AttnWaits(), q, q_stride, n_seq, prefix, prefix_len, tails, tail_len, num_attention_heads,
+                       num_key_value_heads, scale, out, out_stride, out_dtype, workspace, workspace_bytes, stream);
 }
 
 fq_status fq_attn_check(void* stream) {
+    Device* dev;
+    Seen* seen;
+    TRY(prepare_device(&dev, &seen));
+    cudaStream_t s = (cudaStream_t)stream;
     uint32_t n = 0;
-    CK(attn_wait_record(&n, (cudaStream_t)stream));
-    if (n) return fail(FQ_ERR_DEVICE_TIMEOUT, "a bounded device wait of an attention operator gave up (%u waits)", n);
+    CK(cudaMemcpyAsync(&n, dev->word, sizeof n, cudaMemcpyDeviceToHost, s));
+    CK(cudaStreamSynchronize(s));
+    const uint32_t before = seen->count;
+    seen->count = n;
+    dev->read.store(n);
+    if (n != before)
+        return fail(FQ_ERR_DEVICE_TIMEOUT, "a bounded device wait of an attention operator gave up (in %u thread blocks)", n - before);
     return FQ_OK;
 }
 

@@ -5,6 +5,7 @@
 // fastest, so G heads x tokens fill the 128 rows of a matrix product.
 #pragma once
 
+#include "fq.h"
 #include "kernels.h"
 
 namespace fq {
@@ -91,11 +92,13 @@ struct Partials {
     float2 *a_ml = nullptr, *b_ml = nullptr;
 };
 
-// Bounded waits of attn_tiles.cu.  starve (failure tests): the loader of K (1) or V (2) leaves out the second
-// tile of each CTA's first unit, so that what waits for it runs out.
+// Bounded waits of attn_tiles.cu: how long one may take, and where a CTA of which one gave up records it.
 struct AttnWaits {
-    uint32_t limit;       // cycles
-    int starve;
+    uint32_t* record = nullptr;   // device word (null: the current device's own)
+    uint32_t code = 0;            // bits set in it; 0: one is added
+    uint32_t limit = 1u << 29;    // cycles: a quarter second, far beyond any wait that ends
+    int starve = 0;               // failure tests: the loader of K (1) or V (2) leaves out the second tile of
+                                  // each CTA's first unit, so that what waits for it runs out
 };
 
 template <int NV, int NE>
@@ -124,7 +127,7 @@ static_assert(sizeof(TileArgs1) <= 32764 && sizeof(TileArgsN) <= 32764, "kernel 
 template <class Args>
 void launch_tiles(const Args& a, cudaStream_t s);
 cudaError_t attn_tiles_prepare();     // per device, before the first launch
-cudaError_t attn_wait_record(uint32_t* host, cudaStream_t s);
+cudaError_t attn_wait_word(uint32_t** word);   // the current device's own record (a count, never cleared)
 
 constexpr int MAX_GROUPS = MAX_SEQS;
 constexpr int ROWS_CTAS_SM = 3;                     // CTAs of attn_rows.cu per SM (156 registers x 128)
@@ -157,5 +160,18 @@ static_assert(sizeof(JoinArgsL) <= 32764, "kernel parameters");
 // behind launch_tiles, launch_attn_rows or another join of the same call
 template <class Args>
 void launch_attn_join(const Args& a, cudaStream_t s);
+
+// The entry points fq_attn_prompt and fq_attn_shared with the record of their waits, and fq_attn_prompt of one
+// sequence with whole units (no workspace).
+fq_status attn_prompt(const AttnWaits& waits, const void* q, uint64_t q_stride, const fq_kv_view* views, uint32_t n_views,
+                      uint32_t n_seq, const uint32_t* q_len, const uint32_t* kv_row0, const uint32_t* k_len, uint32_t Hq,
+                      uint32_t Hkv, float scale, void* out, uint64_t out_stride, fq_dtype out_dtype, void* workspace,
+                      size_t workspace_bytes, void* stream);
+fq_status attn_shared(const AttnWaits& waits, const void* q, uint64_t q_stride, uint32_t n_seq, const fq_kv_view* prefix,
+                      uint32_t prefix_len, const fq_kv_view* tails, const uint32_t* tail_len, uint32_t Hq, uint32_t Hkv,
+                      float scale, void* out, uint64_t out_stride, fq_dtype out_dtype, void* workspace,
+                      size_t workspace_bytes, void* stream);
+fq_status attn_prompt_whole(const AttnWaits& waits, const void* q, const fq_kv_view* view, uint32_t q_len, uint32_t k_len,
+                            uint32_t Hq, uint32_t Hkv, void* out, void* stream);
 
 }  // namespace fq

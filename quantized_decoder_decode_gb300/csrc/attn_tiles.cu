@@ -82,7 +82,7 @@ constexpr int AT_SMEM = (2 + AT_KS + AT_VS) * AT_TILE_BYTES + 3072;
 static_assert(sizeof(AtShared) <= 3072, "shared memory");
 static_assert(AT_SMEM <= 232448, "shared memory");
 
-__device__ uint32_t g_attn_waits;   // waits that gave up, since the last check
+__device__ uint32_t g_attn_waits;   // CTAs that gave up, of calls that name no other record
 
 // One unit as every role sees it.
 struct Unit {
@@ -147,9 +147,8 @@ FQ_DEV void load_kv(const void* map, uint8_t* dst, int row, int head, uint64_t* 
     tma_load_3d(dst + AT_PANEL, map, 64, row, head, bar);
 }
 
-FQ_DEV void give_up(AtShared* sh) {
+FQ_DEV void give_up(AtShared* sh) {   // (recorded when all roles have left)
     *(volatile uint32_t*)&sh->limit = 0;
-    atomicAdd(&g_attn_waits, 1u);
 }
 FQ_DEV uint32_t wait_limit(const AtShared* sh) { return *(const volatile uint32_t*)&sh->limit; }
 FQ_DEV bool at_wait(uint64_t* bar, uint32_t parity, AtShared* sh) {
@@ -728,7 +727,6 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
             sh->scores_issued = 0;
             // the 128-byte swizzle wants 1024-byte aligned tiles
             sh->limit = (smem_u32(smem) & 1023) ? 0 : a.waits.limit;
-            if (sh->limit == 0) atomicAdd(&g_attn_waits, 1u);
             mbar_fence_init();
         }
         __syncwarp();
@@ -771,6 +769,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
     __syncthreads();
     tc_fence_after();
     if (warp == 8) tmem_dealloc(tm, 512);
+    if (tid == 0 && wait_limit(sh) == 0) {
+        if (a.waits.code) atomicOr(a.waits.record, a.waits.code);
+        else atomicAdd(a.waits.record, 1u);
+    }
 }
 
 template <class Args>
@@ -802,14 +804,6 @@ template void launch_tiles<TileArgs1>(const TileArgs1&, cudaStream_t);
 template void launch_tiles<TileArgsNS>(const TileArgsNS&, cudaStream_t);
 template void launch_tiles<TileArgsN>(const TileArgsN&, cudaStream_t);
 
-// Waits that gave up on the current device, read (and cleared) after the work queued on s.
-cudaError_t attn_wait_record(uint32_t* host, cudaStream_t s) {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(host, g_attn_waits, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e != cudaSuccess || *host == 0) return e;
-    const uint32_t zero = 0;
-    e = cudaMemcpyToSymbolAsync(g_attn_waits, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s);
-    return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
-}
+cudaError_t attn_wait_word(uint32_t** word) { return cudaGetSymbolAddress((void**)word, g_attn_waits); }
 
 }  // namespace fq

@@ -114,7 +114,7 @@ def lib():
                                    ctypes.c_size_t, vp],
                 "fq_attn_shared_workspace": [u32, u32, vp, u32, u32, vp],
                 "fq_attn_check": [vp],
-                "fq_debug_attn_wait_timeout": [vp, vp, u32, u32, u32, u32, vp, u32, u32, vp],
+                "fq_debug_attn_wait_timeout": [vp, vp, vp, u32, u32, u32, u32, vp, u32, u32, vp],
             }
             for name, args in sig.items():
                 fn = getattr(L, name)
@@ -487,8 +487,8 @@ def fq_attn_check(stream: int = 0) -> None:
 
 def fq_debug_attn_wait_timeout(q_ptr: int, view, q_len: int, k_len: int, num_attention_heads: int,
                                num_key_value_heads: int, out_ptr: int, starve: int, wait_cycles: int = 0,
-                               stream: int = 0) -> None:
+                               stream: int = 0, model: int = 0) -> None:
     """Test hook: the prompt attention's tile kernel with a loader that leaves out a tile of K (1) or V (2)."""
-    _check(lib().fq_debug_attn_wait_timeout(q_ptr, ctypes.byref(view), q_len, k_len, num_attention_heads,
+    _check(lib().fq_debug_attn_wait_timeout(model or None, q_ptr, ctypes.byref(view), q_len, k_len, num_attention_heads,
                                             num_key_value_heads, out_ptr, starve, wait_cycles, stream),
            "fq_debug_attn_wait_timeout")
