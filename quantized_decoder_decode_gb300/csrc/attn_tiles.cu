@@ -151,12 +151,20 @@ FQ_DEV void give_up(AtShared* sh) {   // (recorded when all roles have left)
     *(volatile uint32_t*)&sh->limit = 0;
 }
 FQ_DEV uint32_t wait_limit(const AtShared* sh) { return *(const volatile uint32_t*)&sh->limit; }
+// LONG: a wait for the end of a unit of other roles, which takes as long as the unit has keys.  What is
+// bounded then is the time without a new score tile.
+template <bool LONG = false>
 FQ_DEV bool at_wait(uint64_t* bar, uint32_t parity, AtShared* sh) {
     if (mbar_try_wait(bar, parity)) return true;
-    const uint32_t t0 = (uint32_t)clock();
+    uint32_t t0 = (uint32_t)clock(), issued = 0xFFFFFFFFu;
     while (!mbar_try_wait(bar, parity)) {
         const uint32_t limit = wait_limit(sh);
         if ((uint32_t)clock() - t0 > limit) {
+            if (LONG && limit && *(volatile uint32_t*)&sh->scores_issued != issued) {
+                issued = *(volatile uint32_t*)&sh->scores_issued;
+                t0 = (uint32_t)clock();
+                continue;
+            }
             if (limit) give_up(sh);
             return false;
         }
@@ -164,8 +172,9 @@ FQ_DEV bool at_wait(uint64_t* bar, uint32_t parity, AtShared* sh) {
     return true;
 }
 // The same by a whole warp, with one answer for all lanes.
+template <bool LONG = false>
 FQ_DEV bool at_wait_warp(uint64_t* bar, uint32_t parity, AtShared* sh) {
-    return __all_sync(0xFFFFFFFFu, at_wait(bar, parity, sh));
+    return __all_sync(0xFFFFFFFFu, at_wait<LONG>(bar, parity, sh));
 }
 // The outputs of n units are written.
 FQ_DEV bool units_done(uint32_t n, int lane, AtShared* sh) {
@@ -498,7 +507,7 @@ FQ_DEV void softmax(const Args& a, AtShared* sh, int units, uint32_t tm, int x, 
                    (u.j0 + (u.single ? x : 0)) * TILE_ROWS;
         float m = -INFINITY, l = 0.f;
         for (int i = 0; i < n; ++i, left -= u.step * TILE_ROWS) {
-            if (!(ok = at_wait_warp(&sh->s_full[x], sc & 1, sh))) break;
+            if (!(ok = at_wait_warp<true>(&sh->s_full[x], sc & 1, sh))) break;   // (its tile in the units before may have been empty)
             tc_fence_after();
             float s[TILE_ROWS];
 #pragma unroll
@@ -589,7 +598,7 @@ FQ_DEV void outputs(const Args& a, AtShared* sh, int units, uint32_t tm, int row
             const bool have = u.n(x) > 0, two = u.single && u.n_b > 0;
             for (int y = x; y <= (two ? 1 : x); ++y) {
                 if (!have) break;
-                if (!(ok = at_wait_warp(&sh->stat_full[y], (uc >> y) & 1, sh) && at_wait_warp(&sh->o_last[y], (uc >> y) & 1, sh))) break;
+                if (!(ok = at_wait_warp<true>(&sh->stat_full[y], (uc >> y) & 1, sh) && at_wait_warp(&sh->o_last[y], (uc >> y) & 1, sh))) break;
                 uc ^= 1u << y;
                 const float2 st = sh->stat[y][row];
                 if (y == x) {

@@ -131,3 +131,13 @@ def test_every_thread_is_told_of_a_failure():
     t.start()
     t.join()
     assert late == [fq.OK]
+
+
+@pytest.mark.parametrize("hq,hkv,L,K", [(4, 2, 60, 1 << 16), (4, 4, 200, 50000)])
+def test_units_longer_than_the_limit_of_a_wait(hq, hkv, L, K):
+    """What a wait's limit bounds is the time without progress, not the length of a unit: units of 300 us and
+    more whose outputs wait for their end under a limit of 65 us."""
+    c = Case(hq, hkv, L, K)
+    c.starved(0, 1 << 17)
+    fq.fq_attn_check(stream())
+    c.check()
