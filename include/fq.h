@@ -284,7 +284,9 @@ fq_status fq_qk_norm_rope(const float* qkv, uint64_t qkv_stride, uint32_t n_seq,
  * Only the keys a row sees have an influence on it, whatever values the others hold (NaN and
  * infinities included).  out: device [rows][Hq][128] bf16 or f32 (out_dtype), row stride
  * out_stride elements (0 = Hq * 128).  Scores and sums are f32; the softmax weights are rounded to
- * bf16 for the product with V (up to 2^-8 of each weight), for f32 outputs too.
+ * bf16 for the product with V (up to 2^-8 of each weight), for f32 outputs too.  Values of V of up to
+ * 2^127 give finite outputs; weights below 2^-80 of a row's largest, and products with V below 2^-80,
+ * may count as zero.
  * workspace: device, 32-byte aligned, at least the bytes fq_attn_prompt_workspace gives for the
  * same lengths and heads (may be 0); its contents do not matter.
  * Errors: INVALID_SEQUENCE_LENGTH (n_seq = 0), KV_CACHE_OVERFLOW (keys beyond the view),

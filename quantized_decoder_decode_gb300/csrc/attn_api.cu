@@ -524,8 +524,8 @@ fq_status run_join(const Plan& p, const AttnIo& io, const Partials& part, cudaSt
 
 // the checks that both attentions share, and the common part of their arguments
 fq_status attn_common(const void* q, uint64_t q_stride, uint32_t Hq, uint32_t Hkv, float scale, void* out,
-                      uint64_t out_stride, fq_dtype out_dtype, uint64_t q_rows, void* ws, size_t ws_bytes, size_t need,
-                      AttnIo& io) {
+                      uint64_t out_stride, fq_dtype out_dtype, uint64_t q_rows, uint64_t max_keys, void* ws, size_t ws_bytes,
+                      size_t need, AttnIo& io) {
     if (out_dtype != FQ_BF16 && out_dtype != FQ_F32) return fail(FQ_ERR_UNSUPPORTED, "out dtype must be BF16 or F32");
     if (!std::isfinite(scale)) return fail(FQ_ERR_INVALID_ARGUMENT, "scale is not finite");
     if (q_rows > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 query rows");
@@ -544,6 +544,11 @@ fq_status attn_common(const void* q, uint64_t q_stride, uint32_t Hq, uint32_t Hk
     io.Hq = (int)Hq;
     io.Hkv = (int)Hkv;
     io.scale = scale;
+    io.lift = 9.f;   // 2^8 above the reference maximum, and a bit for roundings
+    while (max_keys > 1) {
+        io.lift += 1.f;
+        max_keys = (max_keys + 1) / 2;
+    }
     return FQ_OK;
 }
 
@@ -604,8 +609,8 @@ fq_status attn_prompt(const AttnWaits& waits, const void* q, uint64_t q_stride, 
         Plan p;
         plan_prompt(p, n_seq, seq, Hq / Hkv, Hkv);
         AttnIo io;
-        TRY(attn_common(q, q_stride, Hq, Hkv, scale, out, out_stride, out_dtype, q_rows, workspace, workspace_bytes,
-                        p.bytes(Hkv), io));
+        TRY(attn_common(q, q_stride, Hq, Hkv, scale, out, out_stride, out_dtype, q_rows, *std::max_element(k_len, k_len + n_seq),
+                        workspace, workspace_bytes, p.bytes(Hkv), io));
         if (q_rows == 0) return FQ_OK;
         const Partials part = p.at(workspace, Hkv);
         cudaStream_t s = (cudaStream_t)stream;
@@ -645,7 +650,8 @@ fq_status attn_shared(const AttnWaits& waits, const void* q, uint64_t q_stride, 
         Plan p;
         plan_shared(p, n_seq, seq, Hq / Hkv, Hkv);
         AttnIo io;
-        TRY(attn_common(q, q_stride, Hq, Hkv, scale, out, out_stride, out_dtype, n_seq, workspace, workspace_bytes,
+        TRY(attn_common(q, q_stride, Hq, Hkv, scale, out, out_stride, out_dtype, n_seq,
+                        (uint64_t)prefix_len + *std::max_element(tail_len, tail_len + n_seq), workspace, workspace_bytes,
                         p.bytes(Hkv), io));
         const Partials part = p.at(workspace, Hkv);
         cudaStream_t s = (cudaStream_t)stream;
@@ -667,7 +673,7 @@ fq_status attn_prompt_whole(const AttnWaits& waits, const void* q, const fq_kv_v
     uint64_t q_rows = 0;
     TRY(prompt_sequences(1, &q_len, nullptr, &k_len, view, 1, Hkv, seq, use, &q_rows));
     AttnIo io;
-    TRY(attn_common(q, 0, Hq, Hkv, 1.f / std::sqrt((float)HEAD_DIM), out, 0, FQ_BF16, q_rows, nullptr, 0, 0, io));
+    TRY(attn_common(q, 0, Hq, Hkv, 1.f / std::sqrt((float)HEAD_DIM), out, 0, FQ_BF16, q_rows, k_len, nullptr, 0, 0, io));
     try {
         Plan p;
         std::vector<Unit> units;

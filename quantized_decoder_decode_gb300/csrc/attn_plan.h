@@ -38,6 +38,8 @@ struct AttnIo {
     int out_f32;
     int Hq, Hkv;
     float scale;
+    float lift;                   // softmax weights are held as 2^-lift of the usual ones: their sum over a row's keys
+                                  // stays below 1, and sums of weight x value below the largest value
 };
 // tensor map over bf16 values of rank 3 or 4 (strides[0] is not read), 128-byte swizzle, zero
 // fill outside

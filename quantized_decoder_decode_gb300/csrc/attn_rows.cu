@@ -14,7 +14,8 @@
 //     bytes again and a thread ends up with 8 neighbouring dims of two rows.
 // A CTA of four warps takes a chunk of the keys of one (row group, kv head); the warps take
 // blocks of 16 keys in turn with a running reference maximum (moved only when the maximum has
-// grown by more than 2^8) and are joined in shared memory.
+// grown by more than 2^8; weights 2^-lift of the usual ones, as in attn_tiles.cu) and are joined in shared
+// memory.
 // Measured: 16 single tokens over 512 to 4097 rows (152 MB, 32 / 8 heads) 26 us, 5.8 TB/s; a block of 64
 // keys of a CTA takes 1.9 us, of which its reads wait for memory all but 0.3.  The start of a CTA (its
 // arguments, the first reads) is 2.5 us, the join in it 0.7 us.  CTAs of two warps, six per SM, balance better but
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(AR_THREADS, ROWS_CTAS_SM) attn_rows_kernel(con
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const float mm = m[e] == -INFINITY ? 0.f : m[e];
+            const float mm = m[e] == -INFINITY ? 0.f : m[e] + a.io.lift;
             s[e] = ex2(s[e] - mm);
             s[2 + e] = ex2(s[2 + e] - mm);
             l[e] += s[e] + s[2 + e];

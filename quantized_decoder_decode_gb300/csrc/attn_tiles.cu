@@ -2,10 +2,13 @@
 // of prompts behind cached rows, the shared prefix of a decode batch (few rows: attn_rows.cu).
 //
 // One pass over the keys per query tile of 128 packed rows (token, head of the kv head's group):
-//   S = Q K^T (f32, tensor memory),  p = 2^(c S - c m),  O += bf16(p) V,  l += p,
+//   S = Q K^T (f32, tensor memory),  p = 2^(c S - c m - lift),  O += bf16(p) V,  l += p,
 // c = scale log2(e), m a reference maximum per row.  m follows the running maximum only when that
-// has grown by more than 2^8 = 256 (then O and l of the warp's rows are rescaled); until then
-// p <= 256, which bf16 and the f32 sums carry at the same relative precision.
+// has grown by more than 2^8 = 256 (conditional rescaling, a published method: then O and l of the
+// warp's rows are rescaled); until then p <= 2^(8 - lift), which bf16 and the f32 sums carry at the
+// same relative precision.  lift = 9 + log2(keys): the weights of a row add up to less than 1, so that O, which is
+// divided by l only at the end, stays below the largest |V| and does not overflow where the output is finite.
+// What it costs is at the other end: weights below 2^(lift - 126) of the row's largest are zero.
 //
 // A work unit is a pair of query tiles over the same keys, or (few rows, short prompts) one tile
 // whose key tiles alternate between the two softmax warpgroups and whose halves are joined at the
@@ -530,7 +533,7 @@ FQ_DEV void softmax(const Args& a, AtShared* sh, int units, uint32_t tm, int x, 
             const bool move = (top - m) * c > 8.f;
             const float f = move ? ex2((m - top) * c) : 1.f;
             if (move) m = top;
-            const float mc = m == -INFINITY ? 0.f : m * c;
+            const float mc = m == -INFINITY ? 0.f : fmaf(m, c, a.io.lift);
             const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
             uint64_t ls[2] = {0, 0};   // two pairs of partial sums
             uint32_t p[TILE_ROWS / 2];
