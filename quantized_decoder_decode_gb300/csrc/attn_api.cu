@@ -404,6 +404,12 @@ fq_status encode_rows(void* map_k, void* map_v, const KvRows& r, uint64_t rows, 
     return FQ_OK;
 }
 
+// scale log2(e).  For a scale of 0 the smallest number: scores that are finite weigh the same, and a masked one
+// (-inf) still weighs nothing.
+float score_factor(float scale) {
+    return std::copysign(std::max(std::fabs(scale) * 1.4426950408889634f, FLT_TRUE_MIN), scale);
+}
+
 struct ViewUse {
     KvRows rows;
     uint64_t used = 0;   // rows it is read up to
@@ -419,7 +425,7 @@ fq_status run_tiles_t(const Plan& p, const AttnIo& io, const AttnWaits& waits, c
     if (!a) return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
     auto run = [&]() -> fq_status {
         a->io = io;
-        a->c = std::max(std::fabs(io.scale) * 1.4426950408889634f, FLT_MIN);   // (a scale of 0: equal weights)
+        a->c = std::fabs(score_factor(io.scale));
         a->negate = io.scale < 0.f;
         a->g_shift = 0;
         while (io.Hkv << a->g_shift < io.Hq) ++a->g_shift;
@@ -486,7 +492,7 @@ fq_status run_groups(const Plan& p, const AttnIo& io, const Partials& part, cons
     a.io = io;
     a.part = part;
     a.n_items = p.items;
-    a.c = std::copysign(std::max(std::fabs(io.scale) * 1.4426950408889634f, FLT_MIN), io.scale);
+    a.c = score_factor(io.scale);
     for (size_t g = 0; g < p.groups.size(); ++g) {
         a.g[g] = p.groups[g];
         a.kv[g] = views[seq[p.groups[g].seq].view].rows;

@@ -55,3 +55,16 @@ def test_the_largest_value_everywhere(L, K):
     v = torch.full_like(k, top)
     got = run_prompt(q, view_of(k, v, K, D, K * D), [L], [K], hq, hkv)
     assert bool((got.float() == top).all())
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-39, -1e-39, 2e-38])
+@pytest.mark.parametrize("L,K", [(300, 300), (3, 500), (30, 9000)])
+def test_tiny_scales_of_large_scores(scale, L, K):
+    """Scores of up to 1e38 with scales from 0 to the smallest normal numbers: every scale counts as it is."""
+    g, hq, hkv = gen(63), 4, 2
+    q = (normal(g, L, hq, D, dtype=torch.float32).clamp(-3, 3) * 1.5e18).to(torch.bfloat16)
+    k = (normal(g, hkv, K, D, dtype=torch.float32).clamp(-3, 3) * 1.5e18).to(torch.bfloat16)
+    v = normal(g, hkv, K, D)
+    got = run_prompt(q, view_of(k, v, K, D, K * D), [L], [K], hq, hkv, scale=scale)
+    ref, bound = reference_prompt(q, lambda s, h: (k[h], v[h]), [L], [K], hq, hkv, scale)
+    assert_within(got, ref, bound, True)
