@@ -5,7 +5,9 @@ the CUDA library.  Loading fails loudly when ``libfq.so`` has not been built.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 import os
 import threading
 
@@ -380,14 +382,25 @@ _U32Array = {}   # array types by length
 
 def u32_array(values):
     """A host array of lengths or rows as the calls below take it; a program that calls again
-    with the same lengths keeps it."""
+    with the same lengths keeps it.  Raises ValueError for what is no whole number of 32 bits."""
     if isinstance(values, ctypes.Array) and values._type_ is ctypes.c_uint32:
         return values
     n = len(values)
     t = _U32Array.get(n)
     if t is None:
         t = _U32Array[n] = ctypes.c_uint32 * n
-    return t(*[int(v) for v in values])
+    try:   # (a ctypes array would wrap around)
+        return t.from_buffer(array.array("I", values))
+    except (OverflowError, TypeError) as e:
+        raise ValueError(f"lengths and rows are whole numbers below 2^32: {e}") from None
+
+
+def _u32(name: str, v) -> int:
+    """A length for a 32-bit argument, which ctypes would wrap around."""
+    i = operator.index(v)
+    if not 0 <= i < 1 << 32:
+        raise ValueError(f"{name} {i} does not fit 32 bits")
+    return i
 
 
 def kv_view_array(views):
@@ -426,7 +439,7 @@ def fq_qk_norm_rope(qkv_ptr: int, lens, pos0, views, kv_row0, num_attention_head
     _same_length(len(n), "pos0", p)
     _same_length(len(n), "kv_row0", r)
     st = L.fq_qk_norm_rope(qkv_ptr, qkv_stride, len(n), n, p, w, n_w, r, num_attention_heads, num_key_value_heads,
-                           q_norm_ptr, k_norm_ptr, eps, rope_ptr, rope_rows, q_out_ptr, q_stride, stream)
+                           q_norm_ptr, k_norm_ptr, eps, rope_ptr, _u32("rope_rows", rope_rows), q_out_ptr, q_stride, stream)
     if st:
         _check(st, "fq_qk_norm_rope")
 
@@ -459,8 +472,8 @@ def fq_attn_prompt(q_ptr: int, views, q_len, k_len, num_attention_heads: int, nu
 
 def fq_attn_shared_workspace(prefix_len: int, tail_len, num_attention_heads: int, num_key_value_heads: int) -> int:
     a, out = u32_array(tail_len), ctypes.c_size_t(0)
-    _check(lib().fq_attn_shared_workspace(len(a), prefix_len, a, num_attention_heads, num_key_value_heads,
-                                          ctypes.byref(out)), "fq_attn_shared_workspace")
+    _check(lib().fq_attn_shared_workspace(len(a), _u32("prefix_len", prefix_len), a, num_attention_heads,
+                                          num_key_value_heads, ctypes.byref(out)), "fq_attn_shared_workspace")
     return int(out.value)
 
 
@@ -475,8 +488,8 @@ def fq_attn_shared(q_ptr: int, prefix, prefix_len: int, tails, tail_len, num_att
         t = kv_view_array(tails)
         _same_length(len(a), "tails", t)
     p = None if prefix is None else ctypes.byref(prefix)
-    st = L.fq_attn_shared(q_ptr, q_stride, len(a), p, prefix_len, t, a, num_attention_heads, num_key_value_heads,
-                          scale, out_ptr, out_stride, DTYPES[out_dtype], ws_ptr, ws_bytes, stream)
+    st = L.fq_attn_shared(q_ptr, q_stride, len(a), p, _u32("prefix_len", prefix_len), t, a, num_attention_heads,
+                          num_key_value_heads, scale, out_ptr, out_stride, DTYPES[out_dtype], ws_ptr, ws_bytes, stream)
     if st:
         _check(st, "fq_attn_shared")
 
