@@ -266,8 +266,9 @@ fq_status fq_kv_layer_view(const fq_kv* kv, uint32_t layer, fq_kv_view* out);
  * the sequence's view, all rounded to the nearest bf16.  views: n_views = 1 (all sequences) or
  * n_seq entries.  Rows of the views and of q_out outside the call's stay as they were.
  * Errors: INVALID_SEQUENCE_LENGTH (n_seq = 0, pos0 + len > rope_rows), KV_CACHE_OVERFLOW
- * (kv_row0 + len > rows), INVALID_ARGUMENT (null, alignment, strides, n_seq > 64, two sequences
- * writing the same rows), UNSUPPORTED (group). */
+ * (kv_row0 + len > rows), INVALID_ARGUMENT (null, alignment, strides, n_seq > 64, K or V rows that
+ * would be written twice, by one sequence or by two, through one view or through views that overlap),
+ * UNSUPPORTED (group). */
 fq_status fq_qk_norm_rope(const float* qkv, uint64_t qkv_stride, uint32_t n_seq, const uint32_t* len,
                           const uint32_t* pos0, const fq_kv_view* views, uint32_t n_views, const uint32_t* kv_row0,
                           uint32_t num_attention_heads, uint32_t num_key_value_heads, const float* q_norm,

@@ -8,6 +8,7 @@
 #include <atomic>
 #include <cfloat>
 #include <cmath>
+#include <cstdlib>
 #include <mutex>
 #include <new>
 #include <vector>
@@ -48,6 +49,85 @@ fq_status check_view(const fq_kv_view& v, uint32_t Hkv, uint64_t row0, uint64_t 
         return fail(FQ_ERR_INVALID_ARGUMENT, "%s %u: strides (%llu, %llu) (multiples of 8 elements, at least %d)", what, s,
                     (unsigned long long)v.row_stride, (unsigned long long)v.head_stride, HEAD_DIM);
     if (row0 + n > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "%s %u: more than 2^30 rows", what, s);
+    if ((double)(row0 + n) * (double)v.row_stride + (double)Hkv * (double)v.head_stride > 0x1p47)
+        return fail(FQ_ERR_INVALID_ARGUMENT, "%s %u: rows beyond 2^47 elements", what, s);
+    return FQ_OK;
+}
+
+// The K or V rows that one sequence writes: element d of row r and head h is at lo + r * rs + h * hs + d.
+struct Span {
+    int64_t lo, hi, rs, hs, n;   // in elements; hi: behind the last
+    uint32_t seq;
+};
+Span span_of(const void* p, const fq_kv_view& v, uint32_t row0, uint32_t n, uint32_t Hkv, uint32_t s) {
+    const int64_t lo = (int64_t)(reinterpret_cast<uintptr_t>(p) / 2) + (int64_t)row0 * (int64_t)v.row_stride;
+    return Span{lo, lo + (n - 1) * (int64_t)v.row_stride + (Hkv - 1) * (int64_t)v.head_stride + HEAD_DIM, (int64_t)v.row_stride,
+                (int64_t)v.head_stride, n, s};
+}
+
+// Is there a row difference d in [-(n2 - 1), n1 - 1] with |c + d * rs| < HEAD_DIM?  (rs >= HEAD_DIM: one of the two
+// that bring it to both sides of zero)
+bool rows_near(int64_t c, int64_t rs, int64_t n1, int64_t n2, bool not_zero) {
+    const int64_t below = c > 0 ? -((c + rs - 1) / rs) : -c / rs;
+    for (int64_t d = below; d <= below + 1; ++d)
+        if (d > -n2 && d < n1 && !(not_zero && d == 0) && std::llabs(c + d * rs) < HEAD_DIM) return true;
+    return false;
+}
+// Do two of the spans' rows share elements (self: two different rows or heads of one span)?
+bool rows_meet(const Span& a, const Span& b, int64_t Hkv, bool self) {
+    if (a.hi <= b.lo || b.hi <= a.lo) return false;
+    const int64_t c = a.lo - b.lo;
+    if (a.rs == b.rs && a.hs == b.hs) {
+        // rows of one layout: heads far apart (a cache layer), or all heads of a row before the next row
+        if (std::max(std::llabs(c - (b.n - 1) * a.rs), std::llabs(c + (a.n - 1) * a.rs)) <= a.hs - HEAD_DIM ||
+            (c % a.rs == 0 && a.rs >= Hkv * a.hs))
+            return rows_near(c, a.rs, a.n, b.n, self);
+        for (int64_t dh = 1 - Hkv; dh < Hkv; ++dh)
+            if (rows_near(c + dh * a.hs, a.rs, a.n, b.n, self && dh == 0)) return true;
+        return false;
+    }
+    for (int64_t h = 0; h < Hkv; ++h)
+        for (int64_t g = 0; g < Hkv; ++g)
+            for (int64_t r = 0; r < a.n; ++r)
+                if (rows_near(c + h * a.hs - g * b.hs + r * a.rs, b.rs, 1, b.n, false)) return true;
+    return false;
+}
+
+// Rows that are written twice in one call would race.
+fq_status check_apart(uint32_t n_seq, const uint32_t* len, const fq_kv_view* views, uint32_t n_views, const uint32_t* row0,
+                      uint32_t Hkv) {
+    auto refuse = [](uint32_t a, uint32_t b) {
+        return fail(FQ_ERR_INVALID_ARGUMENT, "sequences %u and %u write the same rows", std::min(a, b), std::max(a, b));
+    };
+    if (n_views == 1) {   // where all rows of the view are apart, only row ranges count
+        struct Range {
+            uint64_t r0, r1;
+            uint32_t seq;
+        } r[MAX_SEQ];
+        int n = 0;
+        for (uint32_t i = 0; i < n_seq; ++i)
+            if (len[i]) r[n++] = Range{row0[i], (uint64_t)row0[i] + len[i], i};
+        std::sort(r, r + n, [](const Range& a, const Range& b) { return a.r0 < b.r0; });
+        for (int i = 0; i + 1 < n; ++i)
+            if (r[i].r1 > r[i + 1].r0) return refuse(r[i].seq, r[i + 1].seq);
+        const uint32_t first = (uint32_t)r[0].r0, rows = (uint32_t)(r[n - 1].r1 - r[0].r0);
+        const Span k = span_of(views->k, *views, first, rows, Hkv, 0), v = span_of(views->v, *views, first, rows, Hkv, 0);
+        if (!rows_meet(k, k, Hkv, true) && !rows_meet(k, v, Hkv, false)) return FQ_OK;
+    }
+    Span s[2 * MAX_SEQ];
+    int n = 0;
+    for (uint32_t i = 0; i < n_seq; ++i) {
+        if (len[i] == 0) continue;
+        const fq_kv_view& v = views[n_views == 1 ? 0 : i];
+        s[n++] = span_of(v.k, v, row0[i], len[i], Hkv, i);
+        s[n++] = span_of(v.v, v, row0[i], len[i], Hkv, i);
+        if (rows_meet(s[n - 1], s[n - 1], Hkv, true))
+            return fail(FQ_ERR_INVALID_ARGUMENT, "sequence %u: rows or heads of its view overlap", i);
+    }
+    std::sort(s, s + n, [](const Span& a, const Span& b) { return a.lo < b.lo; });
+    for (int i = 0; i < n; ++i)
+        for (int j = i + 1; j < n && s[j].lo < s[i].hi; ++j)
+            if (rows_meet(s[i], s[j], Hkv, false)) return refuse(s[i].seq, s[j].seq);
     return FQ_OK;
 }
 
@@ -721,16 +801,13 @@ fq_status fq_qk_norm_rope(const float* qkv, uint64_t qkv_stride, uint32_t n_seq,
         TRY(check_view(v, Hkv, kv_row0[s], len[s], "view", s));
         rows += len[s];
         if (rows > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 rows");
-        for (uint32_t t = 0; t < s && len[s]; ++t)   // two sequences that write the same rows race
-            if (len[t] && (a.kv[t].k == a.kv[s].k || a.kv[t].v == a.kv[s].v) &&
-                kv_row0[t] < (uint64_t)kv_row0[s] + len[s] && kv_row0[s] < (uint64_t)kv_row0[t] + len[t])
-                return fail(FQ_ERR_INVALID_ARGUMENT, "sequences %u and %u write the same rows", t, s);
     }
     if (rows == 0) return FQ_OK;
     if (rows * (Hq + 2 * Hkv) >= 1ull << 32) return fail(FQ_ERR_INVALID_ARGUMENT, "2^32 heads of rows or more");
     if (!qkv || !q_norm || !k_norm || !rope || !q_out) return fail(FQ_ERR_INVALID_ARGUMENT, "null argument");
     if (!aligned16(qkv) || !aligned16(q_norm) || !aligned16(k_norm) || !aligned16(rope) || !aligned16(q_out))
         return fail(FQ_ERR_INVALID_ARGUMENT, "qkv, gains, rope and q_out must be 16-byte aligned");
+    TRY(check_apart(n_seq, len, views, n_views, kv_row0, Hkv));
     a.qkv = qkv;
     a.q_norm = q_norm;
     a.k_norm = k_norm;

@@ -1,17 +1,24 @@
 """Host side of the prompt and shared-prompt attention operators, without a GPU: what is refused before
-anything is launched.  Addresses are made up."""
+anything is launched, and (with launches that are only written down) what is not.  Addresses are made up."""
+import random
+
 import pytest
 
-from quantized_decoder_decode_gb300 import build as fqbuild
 from quantized_decoder_decode_gb300 import fq
+from tests import attn_host_util
 
 P = 0x10000   # a 16-byte aligned address that is never read
 
 
 @pytest.fixture(scope="module", autouse=True)
-def lib():
-    fqbuild.build()
-    return fq.lib()
+def host(tmp_path_factory):
+    return attn_host_util.build(tmp_path_factory.mktemp("attn_host"))
+
+
+@pytest.fixture
+def launches(host):
+    with attn_host_util.recorded(host) as f:
+        yield f
 
 
 def view(k=P, v=P, rows=64, row_stride=128, head_stride=64 * 128):
@@ -65,3 +72,89 @@ def test_lengths_as_they_come():
     for values in ([], [0], [1, 2 ** 32 - 1], (3, 4), np.array([5, 6]), np.array([7], dtype=np.uint32)):
         a = fq.u32_array(values)
         assert list(a) == [int(v) for v in values] and fq.u32_array(a) is a
+
+
+# ---- rows that one fq_qk_norm_rope call would write twice
+
+B = 1 << 30   # bytes between made-up buffers
+
+
+def elements(views, kv_row0, lens, hkv):
+    """Every eighth element that the call writes, K and V of every sequence, as a list of addresses / 2."""
+    out = []
+    for s, n in enumerate(lens):
+        v = views[s] if isinstance(views, list) else views
+        for base in (v.k, v.v):
+            out += [base // 2 + (kv_row0[s] + r) * v.row_stride + h * v.head_stride + d
+                    for r in range(n) for h in range(hkv) for d in range(0, 128, 8)]
+    return out
+
+
+def written_twice(views, kv_row0, lens, hkv):
+    e = elements(views, kv_row0, lens, hkv)
+    return len(set(e)) < len(e)
+
+
+def is_refused(launches, views, kv_row0, lens, hkv):
+    try:
+        fq.fq_qk_norm_rope(P, lens, [0] * len(lens), views, kv_row0, 2 * hkv, hkv, P, P, 1e-6, P, 64, P)
+    except fq.FqError as e:
+        assert e.status == fq.INVALID_ARGUMENT and ("same rows" in str(e) or "overlap" in str(e)), e
+        assert launches() == []
+        return True
+    assert launches() == [[3, sum(lens)]]
+    return False
+
+
+def cache(k, cap=64):
+    """A cache layer, [kv head][row][128], V at some distance from K."""
+    return fq.fq_kv_view(k, k + B, cap, 128, cap * 128)
+
+
+A = cache(P)
+SHIFTED = fq.fq_kv_view(P + 16 * 256, P + B + 16 * 256, 48, 128, 64 * 128)   # rows 16 .. of the same layer
+BETWEEN = fq.fq_kv_view(P + 256, P + 2 * B, 9, 256, 64 * 128)                # every second row of the layer's K, from 1
+SIDE = fq.fq_kv_view(P, P + 2 * 256, 64, 4 * 128, 128)                       # K | V of two heads side by side in a row
+
+
+@pytest.mark.parametrize("views,row0,lens,hkv,bad", [
+    (A, [0, 4], [4, 4], 2, False), (A, [4, 0], [4, 5], 2, True), (A, [0, 0, 9], [0, 4, 1], 2, False),
+    ([A, SHIFTED], [0, 0], [16, 4], 2, False), ([A, SHIFTED], [0, 0], [17, 4], 2, True),
+    ([A, SHIFTED], [20, 3], [2, 1], 2, False), ([A, SHIFTED], [20, 5], [2, 1], 2, True),
+    (SIDE, [0, 7], [7, 3], 2, False), ([SIDE, SIDE], [0, 7], [7, 3], 2, False), (SIDE, [0], [5], 3, True),
+    (fq.fq_kv_view(P, P, 64, 128, 64 * 128), [0], [1], 2, True),         # K and V in one place
+    (fq.fq_kv_view(P, P + B, 64, 128, 128), [0], [2], 2, True),          # head 1 of row 0 is row 1 of head 0
+    (fq.fq_kv_view(P, P + B, 64, 128, 128), [0], [1], 2, False),
+    (fq.fq_kv_view(P, P + B, 64, 256, 136), [0], [1], 2, False), (fq.fq_kv_view(P, P + B, 64, 256, 136), [0], [2], 2, True),
+    ([A, cache(P + B)], [0, 0], [4, 4], 2, True),                        # V of one, K of the other
+    ([A, cache(P + 2 * B)], [0, 0], [4, 4], 2, False),
+    ([A, BETWEEN], [0, 0], [1, 4], 2, False), ([A, BETWEEN], [2, 0], [1, 4], 2, False), ([A, BETWEEN], [3, 0], [1, 4], 2, True)])
+def test_rows_written_twice_are_refused(launches, views, row0, lens, hkv, bad):
+    assert written_twice(views, row0, lens, hkv) == bad
+    assert is_refused(launches, views, row0, lens, hkv) == bad
+
+
+def test_rows_written_twice_in_random_layouts(launches):
+    rng, seen = random.Random(5), [0, 0]
+    for _ in range(4000):
+        hkv, n = rng.choice((1, 2, 3, 4)), rng.randint(1, 4)
+        rs, hs = rng.choice(((128, 12 * 128), (hkv * 128, 128), (2 * hkv * 128, 128), (136, 2000), (hkv * 136, 136), (256, 136)))
+
+        def make():
+            k = P + 16 * rng.choice((0, 1, 16, 32, 33, 16 * hkv, 16 * 12, rng.randint(0, 900), rng.randint(0, 9000)))
+            wider = 8 if n < 3 and rng.random() < .3 else 0
+            return fq.fq_kv_view(k, k + rng.choice((0, B, B, B, 256 * hkv)), 12, rs + wider, hs)
+        views = make() if rng.random() < .4 else [make() for _ in range(n)]
+        lens, row0 = [rng.choice((0, 1, 2, 5)) for _ in range(n)], [rng.randint(0, 7) for _ in range(n)]
+        if sum(lens):
+            bad = written_twice(views, row0, lens, hkv)
+            seen[bad] += 1
+            assert is_refused(launches, views, row0, lens, hkv) == bad, (views, row0, lens, hkv)
+    assert min(seen) > 600, seen
+
+
+def test_rows_beyond_any_memory(launches):
+    v = fq.fq_kv_view(P, P + B, 1 << 30, 1 << 36, 128)
+    refused(lambda: fq.fq_qk_norm_rope(P, [1], [0], v, [1 << 20], 4, 2, P, P, 1e-6, P, 64, P), fq.INVALID_ARGUMENT)
+    refused(lambda: fq.fq_attn_prompt(P, v, [1], [1], 4, 2, .1, P, P, 1 << 30, kv_row0=[1 << 20]), fq.INVALID_ARGUMENT)
+    assert launches() == []
