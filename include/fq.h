@@ -217,7 +217,7 @@ fq_status fq_decode_greedy(const fq_model* m, fq_kv* const* caches, uint32_t n, 
  * what it costs in fq_forward_step's passes of 32 rows.  Equal, up to rounding, to one
  * fq_forward_step per sequence.  Errors (state unchanged): INVALID_SEQUENCE_LENGTH (n = 0,
  * len[s] = 0), KV_CACHE_OVERFLOW, MISMATCHED_KV_CACHES, INVALID_ARGUMENT, UNSUPPORTED (f32 or q8_0
- * caches).  After a CUDA error the cache lengths cover the passes enqueued. */
+ * caches; a stream that is being captured, since a replay would append the same tokens at the same rows).  After a CUDA error the cache lengths cover the passes enqueued. */
 fq_status fq_forward_step_packed(const fq_model* m, fq_kv* const* caches, uint32_t n, const int32_t* tokens,
                                  const uint32_t* len, float* logits, void* stream);
 
@@ -230,7 +230,7 @@ fq_status fq_forward_step_packed(const fq_model* m, fq_kv* const* caches, uint32
  * prefix.  P must stay what it was when caches[s] was filled; a cache filled here is of use behind
  * that prefix alone.  Errors (state unchanged): INVALID_SEQUENCE_LENGTH (n = 0, P + len at
  * max_positions), KV_CACHE_OVERFLOW, MISMATCHED_KV_CACHES (also: the prefix among the caches),
- * INVALID_ARGUMENT, UNSUPPORTED (f32 or q8_0 caches). */
+ * INVALID_ARGUMENT, UNSUPPORTED (f32 or q8_0 caches; a stream that is being captured). */
 fq_status fq_decode_step_shared(const fq_model* m, const fq_kv* prefix, fq_kv* const* caches, uint32_t n,
                                 const int32_t* tokens, float* logits, void* stream);
 

@@ -635,6 +635,15 @@ AttnWaits attn_waits(const fq_model* m) {
     return w;
 }
 
+// A captured packed or shared-prefix step would hold this call's tokens, rows and lengths, and buffers that a later
+// step may replace, while the caches advance without it.
+fq_status check_not_captured(cudaStream_t s) {
+    cudaStreamCaptureStatus st;
+    CK(cudaStreamIsCapturing(s, &st));
+    if (st != cudaStreamCaptureStatusNone) return fail(FQ_ERR_UNSUPPORTED, "the stream is being captured");
+    return FQ_OK;
+}
+
 // Embedding and every layer of one pass; the residual rows end up in w->rows.x.  Each projection
 // goes over all rows before the next one, so that its weights come from L2 after the first chunk.
 fq_status enqueue_rows(const fq_model* m, Workspace* w, const RowsPass& r, cudaStream_t s) {
@@ -1255,6 +1264,7 @@ fq_status fq_forward_step_packed(const fq_model* m, fq_kv* const* caches, uint32
     }
     TRY(check_tokens(m, tokens, total));
     cudaStream_t s = (cudaStream_t)stream;
+    TRY(check_not_captured(s));
     Workspace* w;
     TRY(ensure_ws(m, s, (int)std::min(total, PROJ_ROWS), 1, &w));
     // f(pass, its first sequence, the first sequence whose last row is not in it)
@@ -1321,6 +1331,7 @@ fq_status fq_decode_step_shared(const fq_model* m, const fq_kv* prefix, fq_kv* c
     }
     TRY(check_tokens(m, tokens, n));
     cudaStream_t s = (cudaStream_t)stream;
+    TRY(check_not_captured(s));
     Workspace* w;
     TRY(ensure_ws(m, s, (int)std::min(n, PROJ_ROWS), 1, &w));
     size_t bytes;
