@@ -245,8 +245,9 @@ fq_status fq_decode_step_shared(const fq_model* m, const fq_kv* prefix, fq_kv* c
  * different streams need workspaces of their own).  Outputs must not overlap inputs. */
 
 /* K and V rows on the device: element d of row r of kv head h is at k[r * row_stride +
- * h * head_stride + d] (v alike), bf16.  k and v are 16-byte aligned, strides count elements and
- * are multiples of 8 (row_stride at least 128).  `rows` rows per head belong to the view. */
+ * h * head_stride + d] (v alike), bf16.  k and v are 16-byte aligned; strides count elements and
+ * are multiples of 8 from 128 to 2^36 (head_stride is not looked at with one kv head).  `rows` rows per
+ * head belong to the view; what a call uses of it ends within 2^47 elements. */
 typedef struct fq_kv_view {
     void *k, *v;
     uint64_t rows, row_stride, head_stride;

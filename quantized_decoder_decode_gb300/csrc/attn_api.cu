@@ -44,12 +44,12 @@ fq_status check_view(const fq_kv_view& v, uint32_t Hkv, uint64_t row0, uint64_t 
     if (n == 0) return FQ_OK;
     if (!v.k || !v.v) return fail(FQ_ERR_INVALID_ARGUMENT, "%s %u: null k or v", what, s);
     if (!aligned16(v.k) || !aligned16(v.v)) return fail(FQ_ERR_INVALID_ARGUMENT, "%s %u: k or v not 16-byte aligned", what, s);
-    if (v.row_stride % 8 || v.head_stride % 8 || v.row_stride < HEAD_DIM || v.row_stride > MAX_STRIDE ||
-        (Hkv > 1 && v.head_stride < HEAD_DIM) || v.head_stride > MAX_STRIDE)
-        return fail(FQ_ERR_INVALID_ARGUMENT, "%s %u: strides (%llu, %llu) (multiples of 8 elements, at least %d)", what, s,
+    auto bad = [](uint64_t stride) { return stride % 8 || stride < HEAD_DIM || stride > MAX_STRIDE; };
+    if (bad(v.row_stride) || (Hkv > 1 && bad(v.head_stride)))
+        return fail(FQ_ERR_INVALID_ARGUMENT, "%s %u: strides (%llu, %llu) (multiples of 8 elements, %d to 2^36)", what, s,
                     (unsigned long long)v.row_stride, (unsigned long long)v.head_stride, HEAD_DIM);
     if (row0 + n > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "%s %u: more than 2^30 rows", what, s);
-    if ((double)(row0 + n) * (double)v.row_stride + (double)Hkv * (double)v.head_stride > 0x1p47)
+    if ((double)(row0 + n) * (double)v.row_stride + (Hkv - 1.) * (double)v.head_stride > 0x1p47)
         return fail(FQ_ERR_INVALID_ARGUMENT, "%s %u: rows beyond 2^47 elements", what, s);
     return FQ_OK;
 }
@@ -60,9 +60,9 @@ struct Span {
     uint32_t seq;
 };
 Span span_of(const void* p, const fq_kv_view& v, uint32_t row0, uint32_t n, uint32_t Hkv, uint32_t s) {
-    const int64_t lo = (int64_t)(reinterpret_cast<uintptr_t>(p) / 2) + (int64_t)row0 * (int64_t)v.row_stride;
-    return Span{lo, lo + (n - 1) * (int64_t)v.row_stride + (Hkv - 1) * (int64_t)v.head_stride + HEAD_DIM, (int64_t)v.row_stride,
-                (int64_t)v.head_stride, n, s};
+    const int64_t rs = (int64_t)v.row_stride, hs = Hkv > 1 ? (int64_t)v.head_stride : 0;
+    const int64_t lo = (int64_t)(reinterpret_cast<uintptr_t>(p) / 2) + (int64_t)row0 * rs;
+    return Span{lo, lo + (n - 1) * rs + (Hkv - 1) * hs + HEAD_DIM, rs, hs, n, s};
 }
 
 // Is there a row difference d in [-(n2 - 1), n1 - 1] with |c + d * rs| < HEAD_DIM?  (rs >= HEAD_DIM: one of the two

@@ -158,3 +158,13 @@ def test_rows_beyond_any_memory(launches):
     refused(lambda: fq.fq_qk_norm_rope(P, [1], [0], v, [1 << 20], 4, 2, P, P, 1e-6, P, 64, P), fq.INVALID_ARGUMENT)
     refused(lambda: fq.fq_attn_prompt(P, v, [1], [1], 4, 2, .1, P, P, 1 << 30, kv_row0=[1 << 20]), fq.INVALID_ARGUMENT)
     assert launches() == []
+
+
+@pytest.mark.parametrize("head_stride", [0, 3, 1 << 37, 2 ** 64 - 1])
+def test_one_kv_head_has_no_head_stride(launches, head_stride):
+    v, w = fq.fq_kv_view(P, P + B, 64, 128, head_stride), fq.fq_kv_view(P + 2 * B, P + 3 * B, 64, 128, 128)
+    fq.fq_qk_norm_rope(P, [3, 2], [0, 0], [v, w], [0, 0], 4, 1, P, P, 1e-6, P, 64, P)
+    fq.fq_attn_prompt(P, [v, w], [3, 2], [3, 2], 4, 1, .1, P, P, 1 << 30)
+    fq.fq_attn_shared(P, v, 5, [w], [3], 4, 1, .1, P, P, 1 << 30)
+    assert len(launches()) >= 3
+    refused(lambda: fq.fq_attn_prompt(P, v, [3], [3], 4, 2, .1, P, P, 1 << 30), fq.INVALID_ARGUMENT)
