@@ -68,3 +68,17 @@ def test_tiny_scales_of_large_scores(scale, L, K):
     got = run_prompt(q, view_of(k, v, K, D, K * D), [L], [K], hq, hkv, scale=scale)
     ref, bound = reference_prompt(q, lambda s, h: (k[h], v[h]), [L], [K], hq, hkv, scale)
     assert_within(got, ref, bound, True)
+
+
+@pytest.mark.parametrize("bad", [3e38, -3e38])
+@pytest.mark.parametrize("hq,hkv,at,L,K", [(4, 4, 100, 300, 300), (8, 1, 299, 300, 300), (4, 2, 0, 300, 300), (8, 2, 250, 20, 260),
+                                           (8, 2, 255, 3, 256), (8, 2, 5000, 20, 9000), (8, 2, 100, 1, 3000)])
+def test_one_large_value_among_ordinary_ones(bad, hq, hkv, at, L, K):
+    """A finite value near the largest at one key: rows that see the key give what the definition gives, the others
+    what they give without it."""
+    g = gen(64)
+    q, k, v = normal(g, L, hq, D), normal(g, hkv, K, D), normal(g, hkv, K, D)
+    v[:, at, 60:70] = bad
+    got = run_prompt(q, view_of(k, v, K, D, K * D), [L], [K], hq, hkv)
+    ref, bound = reference_prompt(q, lambda s, h: (k[h], v[h]), [L], [K], hq, hkv)
+    assert_within(got, ref, bound, True)
