@@ -261,7 +261,7 @@ fq_status fq_kv_layer_view(const fq_kv* kv, uint32_t layer, fq_kv_view* out);
  * other: sequence s has len[s] rows (0 allowed) at positions pos0[s], pos0[s] + 1, ...  Each row
  * of qkv (device f32, row stride qkv_stride elements, 0 = (Hq + 2 Hkv) * 128, a multiple of 4;
  * 16-byte aligned) holds the heads q | k | v.  Every q and k head is RMS-normalised with its
- * gain (q_norm, k_norm: device f32 [128]; eps) and rotated at its position (half-split pairing
+ * gain (q_norm, k_norm: device f32 [128]; eps; the sum of squares is f32, for values up to 1e18) and rotated at its position (half-split pairing
  * (i, i + 64); rope: device f32 [rope_rows][64][2], cos and sin); q goes to q_out (device bf16
  * [rows][Hq][128], row stride q_stride elements, 0 = Hq * 128), k and v to rows kv_row0[s] + i of
  * the sequence's view, all rounded to the nearest bf16.  views: n_views = 1 (all sequences) or

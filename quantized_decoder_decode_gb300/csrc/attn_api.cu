@@ -254,6 +254,9 @@ float estimate(const std::vector<Unit>& units, int cap, int G, int Hkv, bool par
 //   333 tokens behind 7000, 32 / 4       pairs in three parts 45.2, single tiles in parts 48.3, whole
 //                                        single tiles 54.3, whole pairs 91.3
 //   10 prompts of 1 to 1187, 32 / 8      pairs 50.4, single tiles 50.8 (many units: pairs)
+// From 456 units on (three per SM) pairs are taken whole.  That was measured with units of 1 to 10 key tiles
+// alone; a long sequence beside many short ones loses by it (200 rows behind 30000, 32 / 8: beside 40 prompts of
+// 20 tokens, split, 100 us; beside 60, whole, 315; floor 51).
 // kv_mb: keys and values read from memory, which bounds what splitting can give.
 void choose(std::vector<Unit>& units, const AttnSeq* seq, int G, int Hkv, bool partial, float kv_mb) {
     if (units.empty()) return;
@@ -307,7 +310,9 @@ void add_group(Plan& p, const AttnSeq& q, int s) {
 }
 
 // Chunks the keys of the groups: the shortest chunks whose CTAs still run all at once, the longest chunks
-// first (behind tiles, CTAs start as SMs become free).
+// first (behind tiles, CTAs start as SMs become free).  Chosen at 16 sequences, 32 / 8 heads, 512 to 4096 keys (38 us
+// cold, floor 22; 48: 96, floor 67; 64: 114, floor 89); where the sequences alone fill a wave the longest is hardly
+// split any more (55 over 500 keys and one over 30000: 268 us, floor 35; 63 and one: 513).
 void plan_groups(Plan& p, uint32_t Hkv, bool partial) {
     auto ctas = [&](int64_t per) {
         int64_t n = 0;
@@ -345,7 +350,8 @@ void plan_prompt(Plan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G, uint32
     const int tpt = TILE_ROWS / (int)G;
     // Few rows go to attn_rows.cu (16 tokens over 512 to 4097 keys: 30.8 us, as units of tiles 37.1), but
     // for short sequences beside others that need tiles, where a unit more costs less than a launch more
-    // (one token beside nine prompts: 50.5 us, with a launch of its own 51.2).
+    // (one token beside nine prompts: 50.5 us, with a launch of its own 51.2; the limit of 1024 keys is not
+    // measured).
     bool tiled = false;
     for (uint32_t s = 0; s < n_seq; ++s) tiled |= (int64_t)seq[s].q_len * G > SMALL_ROWS;
     std::vector<Unit> units;

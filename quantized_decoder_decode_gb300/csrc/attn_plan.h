@@ -132,7 +132,7 @@ cudaError_t attn_tiles_prepare();     // per device, before the first launch
 cudaError_t attn_wait_word(uint32_t** word);   // the current device's own record (a count, never cleared)
 
 constexpr int MAX_GROUPS = MAX_SEQS;
-constexpr int ROWS_CTAS_SM = 3;                     // CTAs of attn_rows.cu per SM (156 registers x 128)
+constexpr int ROWS_CTAS_SM = 3;                     // CTAs of attn_rows.cu per SM (158 registers x 128)
 constexpr int ROWS_CTAS = ROWS_CTAS_SM * ATTN_SMS;  // ..  that run at once
 constexpr int MAX_ITEMS = ROWS_CTAS + MAX_GROUPS;   // (a group is one item at least)
 struct RowsArgs {

@@ -40,8 +40,9 @@
 // 128 x 128 tiles is 2048 cycles of tensor work and takes 2800, as the S buffer goes round: 610 cycles
 // for the product, 270 until the warpgroup sees it, 180 to load it, 300 until the next product begins,
 // twice.  The softmax of a tile (1060 cycles of arithmetic, 600 of waits and stores) fits in that.  2048
-// tokens, 16 / 8 heads, 23.5 us: 2.5 us until the first scores, 12 us of tiles (0.76 us each), 2 us for the
-// last values, 1.7 us of outputs.
+// tokens, 16 / 8 heads, 23.5 us: 2.5 us until the first scores, 12 us of the 16 tiles of the longest unit (0.76 us
+// each), 2 us for the last values, 1.7 us of outputs: 18.2; the other 5 (the start and end of the grid, and what
+// two short units on one SM take more than a long one) are not told apart.
 // Taken out again: the softmax warps as output warps (2048 tokens 24.7 -> 26.0 us), one
 // loading warp for K and V in the order of their use (packed prompts 50 -> 54), three lanes of one warp
 // that load Q, K and V each on their own (2 us more for 2048 tokens: a lane's turn comes too late),
