@@ -268,7 +268,8 @@ fq_status fq_kv_layer_view(const fq_kv* kv, uint32_t layer, fq_kv_view* out);
  * n_seq entries.  Rows of the views and of q_out outside the call's stay as they were.
  * Errors: INVALID_SEQUENCE_LENGTH (n_seq = 0, pos0 + len > rope_rows), KV_CACHE_OVERFLOW
  * (kv_row0 + len > rows), INVALID_ARGUMENT (null, alignment, strides, n_seq > 64, K or V rows that
- * would be written twice, by one sequence or by two, through one view or through views that overlap),
+ * would be written twice, by one sequence or by two, through one view or through views that overlap;
+ * views of different strides whose rows lie in between one another may be taken for such),
  * UNSUPPORTED (group). */
 fq_status fq_qk_norm_rope(const float* qkv, uint64_t qkv_stride, uint32_t n_seq, const uint32_t* len,
                           const uint32_t* pos0, const fq_kv_view* views, uint32_t n_views, const uint32_t* kv_row0,

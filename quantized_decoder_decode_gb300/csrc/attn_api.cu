@@ -73,8 +73,10 @@ bool rows_near(int64_t c, int64_t rs, int64_t n1, int64_t n2, bool not_zero) {
         if (d > -n2 && d < n1 && !(not_zero && d == 0) && std::llabs(c + d * rs) < HEAD_DIM) return true;
     return false;
 }
-// Do two of the spans' rows share elements (self: two different rows or heads of one span)?
-bool rows_meet(const Span& a, const Span& b, int64_t Hkv, bool self) {
+// Do two of the spans' rows share elements (self: two different rows or heads of one span)?  `steps` is what the
+// call's check may still take, some 10 ms in all; beyond that the
+// answer is yes.
+bool rows_meet(const Span& a, const Span& b, int64_t Hkv, bool self, int64_t& steps) {
     if (a.hi <= b.lo || b.hi <= a.lo) return false;
     const int64_t c = a.lo - b.lo;
     if (a.rs == b.rs && a.hs == b.hs) {
@@ -82,14 +84,24 @@ bool rows_meet(const Span& a, const Span& b, int64_t Hkv, bool self) {
         if (std::max(std::llabs(c - (b.n - 1) * a.rs), std::llabs(c + (a.n - 1) * a.rs)) <= a.hs - HEAD_DIM ||
             (c % a.rs == 0 && a.rs >= Hkv * a.hs))
             return rows_near(c, a.rs, a.n, b.n, self);
+        if ((steps -= 2 * Hkv) < 0) return true;
         for (int64_t dh = 1 - Hkv; dh < Hkv; ++dh)
             if (rows_near(c + dh * a.hs, a.rs, a.n, b.n, self && dh == 0)) return true;
         return false;
     }
+    // other strides: head by head where their extents overlap, row by row
+    const int64_t la = (a.n - 1) * a.rs + HEAD_DIM, lb = (b.n - 1) * b.rs + HEAD_DIM;
     for (int64_t h = 0; h < Hkv; ++h)
-        for (int64_t g = 0; g < Hkv; ++g)
+        for (int64_t g = 0; g < Hkv; ++g) {
+            const int64_t d = c + h * a.hs - g * b.hs;
+            if (d + la <= 0 || d >= lb) {
+                if (--steps < 0) return true;
+                continue;
+            }
+            if ((steps -= a.n) < 0) return true;
             for (int64_t r = 0; r < a.n; ++r)
-                if (rows_near(c + h * a.hs - g * b.hs + r * a.rs, b.rs, 1, b.n, false)) return true;
+                if (rows_near(d + r * a.rs, b.rs, 1, b.n, false)) return true;
+        }
     return false;
 }
 
@@ -99,6 +111,7 @@ fq_status check_apart(uint32_t n_seq, const uint32_t* len, const fq_kv_view* vie
     auto refuse = [](uint32_t a, uint32_t b) {
         return fail(FQ_ERR_INVALID_ARGUMENT, "sequences %u and %u write the same rows", std::min(a, b), std::max(a, b));
     };
+    int64_t steps = 1 << 20;
     if (n_views == 1) {   // where all rows of the view are apart, only row ranges count
         struct Range {
             uint64_t r0, r1;
@@ -112,7 +125,7 @@ fq_status check_apart(uint32_t n_seq, const uint32_t* len, const fq_kv_view* vie
             if (r[i].r1 > r[i + 1].r0) return refuse(r[i].seq, r[i + 1].seq);
         const uint32_t first = (uint32_t)r[0].r0, rows = (uint32_t)(r[n - 1].r1 - r[0].r0);
         const Span k = span_of(views->k, *views, first, rows, Hkv, 0), v = span_of(views->v, *views, first, rows, Hkv, 0);
-        if (!rows_meet(k, k, Hkv, true) && !rows_meet(k, v, Hkv, false)) return FQ_OK;
+        if (!rows_meet(k, k, Hkv, true, steps) && !rows_meet(k, v, Hkv, false, steps)) return FQ_OK;
     }
     Span s[2 * MAX_SEQ];
     int n = 0;
@@ -121,13 +134,13 @@ fq_status check_apart(uint32_t n_seq, const uint32_t* len, const fq_kv_view* vie
         const fq_kv_view& v = views[n_views == 1 ? 0 : i];
         s[n++] = span_of(v.k, v, row0[i], len[i], Hkv, i);
         s[n++] = span_of(v.v, v, row0[i], len[i], Hkv, i);
-        if (rows_meet(s[n - 1], s[n - 1], Hkv, true))
+        if (rows_meet(s[n - 1], s[n - 1], Hkv, true, steps))
             return fail(FQ_ERR_INVALID_ARGUMENT, "sequence %u: rows or heads of its view overlap", i);
     }
     std::sort(s, s + n, [](const Span& a, const Span& b) { return a.lo < b.lo; });
     for (int i = 0; i < n; ++i)
         for (int j = i + 1; j < n && s[j].lo < s[i].hi; ++j)
-            if (rows_meet(s[i], s[j], Hkv, false)) return refuse(s[i].seq, s[j].seq);
+            if (rows_meet(s[i], s[j], Hkv, false, steps)) return refuse(s[i].seq, s[j].seq);
     return FQ_OK;
 }
 

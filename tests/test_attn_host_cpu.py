@@ -97,7 +97,7 @@ def written_twice(views, kv_row0, lens, hkv):
 
 def is_refused(launches, views, kv_row0, lens, hkv):
     try:
-        fq.fq_qk_norm_rope(P, lens, [0] * len(lens), views, kv_row0, 2 * hkv, hkv, P, P, 1e-6, P, 64, P)
+        fq.fq_qk_norm_rope(P, lens, [0] * len(lens), views, kv_row0, 2 * hkv, hkv, P, P, 1e-6, P, 1 << 20, P)
     except fq.FqError as e:
         assert e.status == fq.INVALID_ARGUMENT and ("same rows" in str(e) or "overlap" in str(e)), e
         assert launches() == []
@@ -151,6 +151,15 @@ def test_rows_written_twice_in_random_layouts(launches):
             seen[bad] += 1
             assert is_refused(launches, views, row0, lens, hkv) == bad, (views, row0, lens, hkv)
     assert min(seen) > 600, seen
+
+
+def test_long_interleaved_rows_of_other_strides_are_refused_at_once(launches):
+    """Two views of other strides whose rows lie between each other: found apart row by row where that is quick,
+    refused where it is not."""
+    for hkv, n, bad in ((2, 500, False), (64, 100000, True)):
+        a = fq.fq_kv_view(P, P + B * 4096, n, 512, 512 * n)
+        b = fq.fq_kv_view(P + 512, P + 2 * B * 4096, n, 1024, 512 * n)
+        assert is_refused(launches, [a, b], [0, 0], [n // 4, n // 4], hkv) == bad
 
 
 def test_rows_beyond_any_memory(launches):
