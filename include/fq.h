@@ -315,12 +315,70 @@ fq_status fq_attn_shared(const void* q, uint64_t q_stride, uint32_t n_seq, const
 fq_status fq_attn_shared_workspace(uint32_t n_seq, uint32_t prefix_len, const uint32_t* tail_len,
                                    uint32_t num_attention_heads, uint32_t num_key_value_heads, size_t* bytes);
 
+/* ---- windows, pages, and caches made shorter ----
+ *
+ * What a program needs that serves contexts longer than it wants to keep whole: attention that looks at a window
+ * of the last keys and at the first few (which trained models lean on whatever they hold), a cache whose rows lie in
+ * pages, and a cache of which only the keys that queries have looked at stay.  The conventions of the operators
+ * above hold: head_dim 128, bf16 rows, groups of 1, 2, 4 or 8, up to 64 sequences a call, nothing allocated but (once per device and process) by
+ * the first call's preparation of the kernels, calls may be captured, and outputs do not overlap inputs. */
+
+/* fq_attn_prompt in which query row i of a sequence, whose own key is e - 1, e = i + 1 + k_len - q_len, sees the
+ * keys j < e with j >= e - window or j < sinks: its last `window` keys (its own among them) and the first
+ * `sinks` of the sequence.  window = 0: all keys up to its own.
+ *   out[i] = sum_j softmax_j(scale * q[i].k[j]) v[j],   lse[i] = log sum_j exp(scale * q[i].k[j])
+ * over the keys that row i sees; a row that sees none gives zeros and -infinity.  lse: device f32 [rows][Hq], 4-byte
+ * aligned, or NULL.  Keys that no row of a call sees are not read, but for the rest of a tile of 128 keys that one
+ * sees into.  Everything else as in fq_attn_prompt, workspace and errors included. */
+fq_status fq_attn_window(const void* q, uint64_t q_stride, const fq_kv_view* views, uint32_t n_views, uint32_t n_seq,
+                         const uint32_t* q_len, const uint32_t* kv_row0, const uint32_t* k_len,
+                         uint32_t num_attention_heads, uint32_t num_key_value_heads, uint32_t window, uint32_t sinks,
+                         float scale, void* out, uint64_t out_stride, fq_dtype out_dtype, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream);
+fq_status fq_attn_window_workspace(uint32_t n_seq, const uint32_t* q_len, const uint32_t* k_len,
+                                   uint32_t num_attention_heads, uint32_t num_key_value_heads, uint32_t window,
+                                   uint32_t sinks, size_t* bytes);
+
+/* A pool of pages of K and V rows on the device: element d of row r of kv head h of page p is at
+ * k[p * page_stride + r * row_stride + h * head_stride + d] (v alike), bf16.  page_rows is 16, 32, 64, 128 or
+ * 256; k and v are 16-byte aligned; strides count elements and are multiples of 8 from 128 to 2^36 (head_stride is not
+ * looked at with one kv head, page_stride with one page), n_pages is below 2^31, and the pool ends within 2^47 elements.
+ *
+ * A page table (device int32 [n_seq][table_stride]) says where the rows of a sequence are: row r is row
+ * r % page_rows of page table[s * table_stride + r / page_rows].  Sequences may share pages that a call reads.  Only
+ * entries of pages are read that some row of the call sees into (or that it writes), so the others may hold
+ * anything.  An entry that names no page of the pool is recorded (fq_attn_check: INVALID_ARGUMENT) and read as rows of
+ * zeros; nothing is written for it. */
+typedef struct fq_kv_pages {
+    void *k, *v;
+    uint32_t n_pages, page_rows;
+    uint64_t page_stride, row_stride, head_stride;
+} fq_kv_pages;
+
+/* fq_attn_window over pages: sequence s has the k_len[s] rows 0 .. of its pages.  Workspace:
+ * fq_attn_window_workspace.  Errors: also INVALID_ARGUMENT (null table, a table_stride that does not hold the rows of a
+ * sequence, page_rows, strides). */
+fq_status fq_attn_paged(const void* q, uint64_t q_stride, const fq_kv_pages* pages, const int32_t* page_table,
+                        uint64_t table_stride, uint32_t n_seq, const uint32_t* q_len, const uint32_t* k_len,
+                        uint32_t num_attention_heads, uint32_t num_key_value_heads, uint32_t window, uint32_t sinks,
+                        float scale, void* out, uint64_t out_stride, fq_dtype out_dtype, float* lse, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* fq_qk_norm_rope into pages: k and v of row i of sequence s go to row kv_row0[s] + i of its pages.  A page that
+ * a call writes into belongs to one sequence: rows that two sequences write through a shared page end up as
+ * either's.  Errors: as there, and those of fq_attn_paged's table (KV_CACHE_OVERFLOW: rows beyond the table). */
+fq_status fq_qk_norm_rope_paged(const float* qkv, uint64_t qkv_stride, uint32_t n_seq, const uint32_t* len,
+                                const uint32_t* pos0, const fq_kv_pages* pages, const int32_t* page_table,
+                                uint64_t table_stride, const uint32_t* kv_row0, uint32_t num_attention_heads,
+                                uint32_t num_key_value_heads, const float* q_norm, const float* k_norm, float eps,
+                                const float* rope, uint32_t rope_rows, void* q_out, uint64_t q_stride, void* stream);
+
 /* Synchronise `stream` and report bounded device waits of the two attentions that gave up on the
  * current device since this host thread's last check (a thread's first: since the last check of
  * any).  DEVICE_TIMEOUT: the outputs of the calls since then, of whichever thread and stream, may be
  * invalid.  No check hides a failure from another thread.  The attention inside
  * fq_forward_step_packed and fq_decode_step_shared is recorded with its model (fq_check_device) and
- * not here. */
+ * not here.  INVALID_ARGUMENT: a paged call since then met a page table entry outside its pool. */
 fq_status fq_attn_check(void* stream);
 
 /* ---- inspection (tests and tools; not the hot path) ---- */

@@ -43,6 +43,9 @@ FQ_DEV float ex2(float x) {
     return y;
 }
 
+// log(sum e^x) of a row from its reference maximum m (base 2) and the sum l of weights held 2^-lift lower
+FQ_DEV float log_sum(float m, float l, float lift) { return (m + (log2f(l) + lift)) * 0.6931471805599453f; }
+
 // mbar_try_wait without suspending.
 FQ_DEV bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
     uint32_t ok;

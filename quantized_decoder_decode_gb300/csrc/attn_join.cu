@@ -92,6 +92,8 @@ __global__ void __launch_bounds__(AJ_WARPS * 32) attn_join_kernel(const __grid_c
         y.z *= inv;
         y.w *= inv;
     }
+    if (a.io.lse && d == 0)
+        a.io.lse[(int64_t)(e.q_row0 + t) * Hq + kh * G + gh] = min(e.k_len, t + e.off) > 0 ? log_sum(M, L, a.io.lift) : -INFINITY;
     const int64_t at = (int64_t)(e.q_row0 + t) * a.io.out_stride + (int64_t)(kh * G + gh) * HEAD_DIM + d;
     if (a.io.out_f32) *reinterpret_cast<float4*>((float*)a.io.out + at) = y;
     else *reinterpret_cast<uint2*>((uint16_t*)a.io.out + at) = make_uint2(bf16x2(y.x, y.y), bf16x2(y.z, y.w));

@@ -15,8 +15,19 @@ struct KvRows {                   // element d of row r of kv head h: [r * row_s
     int64_t row_stride = 0, head_stride = 0;
 };
 
+// K and V rows in pages: element d of row r of kv head h of page p is at [p * page_stride + r * row_stride +
+// h * head_stride + d].  Row r of sequence s is row r % page_rows of page table[s * table_stride + r / page_rows].
+struct KvPages {
+    uint16_t *k = nullptr, *v = nullptr;
+    int64_t page_stride = 0, row_stride = 0, head_stride = 0;
+    const int32_t* table = nullptr;
+    int64_t table_stride = 0;
+    int32_t n_pages = 0, shift = 0;        // rows of a page: 2^shift, 16 to 256
+    uint32_t* bad = nullptr;               // counts CTAs that met a table entry outside [0, n_pages): no row is read or written for it
+};
+
 // QK-norm + rope of packed rows, q -> q_out, k and v -> cache rows (qk_rows.cu)
-struct QkRowsArgs {
+struct QkRowsBase {
     const float* qkv;             // [rows][(Hq + 2 Hkv) * 128]
     int64_t qkv_stride;
     const float *q_norm, *k_norm; // [128]
@@ -26,9 +37,17 @@ struct QkRowsArgs {
     uint16_t* q_out;              // bf16 [rows][Hq * 128]
     int64_t q_stride;
     int32_t row0[MAX_SEQ], pos0[MAX_SEQ], kv_row0[MAX_SEQ];   // per sequence: first row, position, cache row
+};
+struct QkRowsArgs : QkRowsBase {
+    static constexpr bool PAGED = false;
     KvRows kv[MAX_SEQ];
 };
+struct QkPagedArgs : QkRowsBase {
+    static constexpr bool PAGED = true;
+    KvPages pages;
+};
 void launch_qk_rows(const QkRowsArgs& a, cudaStream_t s);
+void launch_qk_paged(const QkPagedArgs& a, cudaStream_t s);
 
 struct AttnIo {
     const uint16_t* q;            // bf16 [rows][Hq][128]
@@ -38,6 +57,7 @@ struct AttnIo {
     int out_f32;
     int Hq, Hkv;
     float scale;
+    float* lse = nullptr;         // f32 [rows][Hq]: log of the row's sum of exponentials, or null
     float lift;                   // softmax weights are held as 2^-lift of the usual ones: their sum over a row's keys
                                   // stays below 1, and sums of weight x value below the largest value
 };
@@ -58,6 +78,52 @@ struct AttnSeq {
     int32_t q_row0, q_len, k_row0, k_len, off, view;
 };
 
+// What a row sees of the keys up to its own: the last `window` of them, and the first `sinks` of the sequence.
+struct AttnMask {
+    int32_t window = 1 << 30, sinks = 0;   // (no sequence has more than 2^30 keys)
+};
+
+// The key tiles that token rows [tok, tok + n_tok) of a sequence look at: [0, sinks) and [first, ..), n in all.
+// They are counted through: tile number v is key tile at(v).
+struct KeyTiles {
+    int32_t sinks = 0, first = 0, n = 0;
+    FQ_HD int32_t at(int32_t v) const { return v < sinks ? v : v - sinks + first; }
+    // tiles up to the one with the last of `keys` keys (which the window of the first row reaches)
+    FQ_HD int32_t up_to(int32_t keys) const {
+        const int32_t end = (keys + TILE_ROWS - 1) / TILE_ROWS;
+        return keys <= 0 ? 0 : sinks + (end > first ? end - first : 0);
+    }
+};
+FQ_HD inline KeyTiles key_tiles(const AttnMask& m, int32_t k_len, int32_t off, int32_t tok, int32_t n_tok) {
+    KeyTiles t;
+    const int32_t end = tok + n_tok - 1 + off, last = end < k_len ? end : k_len;   // keys below `last` are seen by some row
+    if (n_tok <= 0 || last <= 0) return t;
+    const int32_t lo = tok + off - m.window;
+    t.first = lo > 0 ? lo / TILE_ROWS : 0;
+    const int32_t s = m.sinks < last ? m.sinks : last, st = (s + TILE_ROWS - 1) / TILE_ROWS;
+    t.sinks = st < t.first ? st : t.first;
+    t.n = t.up_to(last);
+    return t;
+}
+
+// The same for a row group of attn_rows.cu, in keys: [0, sinks) and from sinks + gap on, n in all; both edges
+// are multiples of 16 keys (a block of that kernel, which no page ends in).
+struct KeySpan {
+    int32_t sinks = 0, gap = 0, n = 0;
+    FQ_HD int32_t at(int32_t v) const { return v < sinks ? v : v + gap; }
+};
+FQ_HD inline KeySpan key_span(const AttnMask& m, int32_t k_len, int32_t off, int32_t n_tok) {
+    KeySpan s;
+    const int32_t end = n_tok - 1 + off, last = end < k_len ? end : k_len;
+    if (n_tok <= 0 || last <= 0) return s;
+    const int32_t lo = off - m.window, first = lo > 0 ? lo & ~15 : 0;
+    const int32_t k = ((m.sinks < last ? m.sinks : last) + 15) & ~15;
+    s.sinks = k < first ? k : first;
+    s.gap = first - s.sinks;
+    s.n = last - s.gap;
+    return s;
+}
+
 // One unit of attn_tiles.cu per kv head: two query tiles (pair) over the same keys, or one tile
 // whose key tiles alternate between the two softmax warpgroups.
 struct TileEntry {
@@ -77,6 +143,7 @@ struct RowGroup {
     int32_t item0;        // first work item (chunk) of the group
     int32_t chunk;        // keys per item, a multiple of 64
     int32_t slot0;        // first partial block, or -1: one item that writes finished outputs
+    int32_t keys;         // that some row looks at (KeySpan::n)
 };
 
 // Rows whose output is joined from partial results: nA blocks of 128 rows from slot a0 (a0 +
@@ -106,6 +173,7 @@ struct AttnWaits {
 template <int NV, int NE>
 struct TileArgs {
     static constexpr int VIEWS = NV, ENTRIES = NE;
+    static constexpr bool WINDOW = false, PAGED = false;
     alignas(64) unsigned long long map_q[16];
     alignas(64) unsigned long long map_k[NV][16], map_v[NV][16];
     AttnIo io;
@@ -126,9 +194,25 @@ using TileArgs1 = TileArgs<1, 1536>;
 using TileArgsNS = TileArgs<17, 192>;
 using TileArgsN = TileArgs<MAX_SEQS, 768>;
 static_assert(sizeof(TileArgs1) <= 32764 && sizeof(TileArgsN) <= 32764, "kernel parameters");
+// Windows and sinks over views (kv: the views' rows), or over pages (one map of the whole pool).
+template <int NV, int NE, bool PAGES>
+struct WindowTileArgs : TileArgs<NV, NE> {
+    static constexpr bool WINDOW = true, PAGED = PAGES;
+    AttnMask mask;
+    KvRows kv[PAGES ? 1 : NV];
+    KvPages pages;
+};
+using WindowArgs1S = WindowTileArgs<1, 64, false>;
+using WindowArgs1 = WindowTileArgs<1, 1536, false>;
+using WindowArgsN = WindowTileArgs<MAX_SEQS, 576, false>;
+using PagedArgsS = WindowTileArgs<1, 64, true>;
+using PagedArgsL = WindowTileArgs<1, 1536, true>;
+static_assert(sizeof(WindowArgs1) <= 32764 && sizeof(WindowArgsN) <= 32764 && sizeof(PagedArgsL) <= 32764, "kernel parameters");
 template <class Args>
 void launch_tiles(const Args& a, cudaStream_t s);
 cudaError_t attn_tiles_prepare();     // per device, before the first launch
+cudaError_t attn_window_tiles_prepare();
+cudaError_t attn_page_word(uint32_t** word);   // the current device's count of table entries without a page (never cleared)
 cudaError_t attn_wait_word(uint32_t** word);   // the current device's own record (a count, never cleared)
 
 constexpr int MAX_GROUPS = MAX_SEQS;
@@ -136,6 +220,7 @@ constexpr int ROWS_CTAS_SM = 3;                     // CTAs of attn_rows.cu per 
 constexpr int ROWS_CTAS = ROWS_CTAS_SM * ATTN_SMS;  // ..  that run at once
 constexpr int MAX_ITEMS = ROWS_CTAS + MAX_GROUPS;   // (a group is one item at least)
 struct RowsArgs {
+    static constexpr bool WINDOW = false, PAGED = false;
     AttnIo io;
     int n_items;
     float c;              // scale log2(e)
@@ -144,9 +229,18 @@ struct RowsArgs {
     RowGroup g[MAX_GROUPS];
     KvRows kv[MAX_GROUPS];
 };
+template <bool PAGES>
+struct WindowRowsArgs : RowsArgs {
+    static constexpr bool WINDOW = true, PAGED = PAGES;
+    AttnMask mask;
+    KvPages pages;
+};
 cudaError_t attn_rows_prepare();      // per device, before the first launch
+cudaError_t attn_window_rows_prepare();
 // beside: it may run beside launch_tiles of the same call, launched just before
 void launch_attn_rows(const RowsArgs& a, bool beside, cudaStream_t s);
+void launch_attn_window_rows(const WindowRowsArgs<false>& a, bool beside, cudaStream_t s);
+void launch_attn_window_rows(const WindowRowsArgs<true>& a, bool beside, cudaStream_t s);
 
 template <int NE>
 struct JoinArgs {
@@ -173,6 +267,10 @@ fq_status attn_shared(const AttnWaits& waits, const void* q, uint64_t q_stride, 
                       uint32_t prefix_len, const fq_kv_view* tails, const uint32_t* tail_len, uint32_t Hq, uint32_t Hkv,
                       float scale, void* out, uint64_t out_stride, fq_dtype out_dtype, void* workspace,
                       size_t workspace_bytes, void* stream);
+// The current device's number and the word that counts its give-ups of calls that belong to no model; and the word that counts
+// table entries without a page there (one for all paged calls), for fq_attn_check.
+fq_status attn_device(int* dev, uint32_t** waits);
+void attn_set_page_word(int dev, uint32_t* word);
 fq_status attn_prompt_whole(const AttnWaits& waits, const void* q, const fq_kv_view* view, uint32_t q_len, uint32_t k_len,
                             uint32_t Hq, uint32_t Hkv, void* out, void* stream);
 

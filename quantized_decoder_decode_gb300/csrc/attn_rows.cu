@@ -58,7 +58,11 @@ FQ_DEV float max_over_rows(float v) {   // over the lanes with the same lane % 4
     return fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
 }
 
-__global__ void __launch_bounds__(AR_THREADS, ROWS_CTAS_SM) attn_rows_kernel(const __grid_constant__ RowsArgs a) {
+// (Args::WINDOW, Args::PAGED: a window with sinks, over views or over pages.  The group's keys are then counted through
+// without those that none of its rows sees (KeySpan); a warp's block of 16 keys lies in one page, and the page of the
+// block after the next is looked up ahead.)
+template <class Args>
+__global__ void __launch_bounds__(AR_THREADS, ROWS_CTAS_SM) attn_rows_kernel(const __grid_constant__ Args a) {
     __shared__ float so[AR_WARPS][SMALL_ROWS][AR_OPAD];
     __shared__ float2 sml[AR_WARPS][SMALL_ROWS];
     pdl_trigger();
@@ -69,7 +73,10 @@ __global__ void __launch_bounds__(AR_THREADS, ROWS_CTAS_SM) attn_rows_kernel(con
     const KvRows& kv = a.kv[a.group[item]];
     const int rows = g.n_tok * G;
     const int c0 = (item - g.item0) * g.chunk;
-    const int c1 = max(0, min(min(g.k_len, g.n_tok - 1 + g.off), c0 + g.chunk));
+    KeySpan span;
+    if constexpr (Args::WINDOW) span = key_span(a.mask, g.k_len, g.off, g.n_tok);
+    // the keys' numbers in the chunk: [c0, c1)
+    const int c1 = Args::WINDOW ? min(span.n, c0 + g.chunk) : max(0, min(min(g.k_len, g.n_tok - 1 + g.off), c0 + g.chunk));
     const int first = max(0, min(g.k_len, g.off));   // keys that every row sees
     const int r = lane >> 2, c = lane & 3;
 
@@ -77,25 +84,49 @@ __global__ void __launch_bounds__(AR_THREADS, ROWS_CTAS_SM) attn_rows_kernel(con
     const uint16_t* kb = kv.k + (int64_t)g.k_row0 * rs + (int64_t)head * kv.head_stride + 8 * c;
     const uint16_t* vb = kv.v + (int64_t)g.k_row0 * rs + (int64_t)head * kv.head_stride;
     uint4 kr[2][4], vr[4][2];
+    // Block of 16 keys from number k0: the index of its first row in the view, or the row's offset in the pool (negative: no page)
+    auto page_of = [&](int k0) -> int64_t {
+        if constexpr (Args::PAGED) {
+            if (k0 >= c1) return -1;
+            const int key = span.at(k0);
+            const int32_t id = __ldg(a.pages.table + (int64_t)g.seq * a.pages.table_stride + (key >> a.pages.shift));
+            if ((uint32_t)id < (uint32_t)a.pages.n_pages)
+                return id * a.pages.page_stride + (key & ((1 << a.pages.shift) - 1)) * rs;
+            if (lane == 0) atomicAdd(a.pages.bad, 1u);
+            return -1;
+        }
+        return (int64_t)span.at(k0) * rs;
+    };
+    int64_t at = 0, at_next = 0;   // of the block that is loaded next, of the one after it
     auto load_k = [&](int k0) {   // keys k0 + r, k0 + 8 + r: dims 32i + 8c ..
+        const uint16_t* base = kb;
+        if constexpr (Args::WINDOW) base += at - (int64_t)k0 * rs;
+        const int c1_ = !Args::PAGED || at >= 0 ? c1 : 0;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int key = k0 + 8 * j + r;
-            const uint16_t* p = kb + (int64_t)key * rs;
+            const uint16_t* p = base + (int64_t)key * rs;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) kr[j][i] = key < c1 ? ld_stream16(p + 32 * i) : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < 4; ++i) kr[j][i] = key < c1_ ? ld_stream16(p + 32 * i) : make_uint4(0, 0, 0, 0);
         }
     };
     auto load_v = [&](int k0) {   // keys k0 + 2c, + 1, + 8, + 9: dims 64h + 8r ..
+        const uint16_t* base = vb;
+        if constexpr (Args::WINDOW) base += at - (int64_t)k0 * rs;
+        const int c1_ = !Args::PAGED || at >= 0 ? c1 : 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int key = k0 + 2 * c + (j & 1) + 8 * (j >> 1);
-            const uint16_t* p = vb + (int64_t)key * rs + 8 * r;
+            const uint16_t* p = base + (int64_t)key * rs + 8 * r;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) vr[j][h] = key < c1 ? ld_stream16(p + 64 * h) : make_uint4(0, 0, 0, 0);
+            for (int h = 0; h < 2; ++h) vr[j][h] = key < c1_ ? ld_stream16(p + 64 * h) : make_uint4(0, 0, 0, 0);
         }
     };
     int k0 = c0 + 16 * warp;
+    if constexpr (Args::WINDOW) {
+        at = page_of(k0);
+        at_next = page_of(k0 + 16 * AR_WARPS);
+    }
     if (k0 < c1) {
         load_k(k0);
         load_v(k0);
@@ -108,7 +139,8 @@ __global__ void __launch_bounds__(AR_THREADS, ROWS_CTAS_SM) attn_rows_kernel(con
     }
     int limit[2];   // keys of this chunk's range that rows 2c, 2c + 1 see
 #pragma unroll
-    for (int e = 0; e < 2; ++e) limit[e] = 2 * c + e < rows ? min(c1, max(0, (2 * c + e) / G + g.off)) : 0;
+    for (int e = 0; e < 2; ++e)
+        limit[e] = 2 * c + e < rows ? min(Args::WINDOW ? span.at(c1 - 1) + 1 : c1, max(0, (2 * c + e) / G + g.off)) : 0;
     float o[8][4];   // dims 8r + t (rows 2c, 2c + 1), 64 + 8r + t
 #pragma unroll
     for (int t = 0; t < 8; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
@@ -121,9 +153,20 @@ __global__ void __launch_bounds__(AR_THREADS, ROWS_CTAS_SM) attn_rows_kernel(con
             mma16816(s, kr[0][i].x, kr[1][i].x, kr[0][i].y, kr[1][i].y, q[i].x, q[i].y);
             mma16816(s, kr[0][i].z, kr[1][i].z, kr[0][i].w, kr[1][i].w, q[i].z, q[i].w);
         }
+        [[maybe_unused]] const int64_t at_now = at;
+        if constexpr (Args::WINDOW) {
+            at = at_next;
+            at_next = page_of(k0 + 32 * AR_WARPS);
+        }
         if (more) load_k(k0 + 16 * AR_WARPS);
+        const int key0 = Args::WINDOW ? span.at(k0) : k0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] = k0 + 8 * (e >> 1) + r < limit[e & 1] ? s[e] * a.c : -INFINITY;
+        for (int e = 0; e < 4; ++e) {
+            const int key = key0 + 8 * (e >> 1) + r;
+            bool sees = key < limit[e & 1];
+            if constexpr (Args::WINDOW) sees = sees && (key >= (2 * c + (e & 1)) / G + g.off - a.mask.window || key < a.mask.sinks);
+            s[e] = sees ? s[e] * a.c : -INFINITY;
+        }
         float f[2];
         bool move = false;
 #pragma unroll
@@ -154,7 +197,9 @@ __global__ void __launch_bounds__(AR_THREADS, ROWS_CTAS_SM) attn_rows_kernel(con
         }
         const uint32_t p0 = transpose8(bf16x2(s[0], s[1])), p1 = transpose8(bf16x2(s[2], s[3]));
         bool odd = false;
-        if (k0 + 16 > first) {   // some row does not see all of these keys
+        bool part = key0 + 16 > first;   // some row does not see all of these keys
+        if constexpr (Args::WINDOW) part |= key0 < g.n_tok - 1 + g.off - a.mask.window && key0 + 16 > a.mask.sinks;
+        if (part) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -186,13 +231,16 @@ __global__ void __launch_bounds__(AR_THREADS, ROWS_CTAS_SM) attn_rows_kernel(con
         if (more) load_v(k0 + 16 * AR_WARPS);
         if (odd) {
             for (int k = 0; k < 16 && k0 + k < c1; ++k) {
-                const uint16_t* p = vb + (int64_t)(k0 + k) * rs + 8 * r;
+                const uint16_t* p = vb + (Args::WINDOW ? at_now + k * rs : (int64_t)(k0 + k) * rs) + 8 * r;
 #pragma unroll
                 for (int t = 0; t < 8; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const uint16_t b = p[64 * (e >> 1) + t];
-                        if ((b & 0x7F80u) == 0x7F80u && k0 + k < limit[e & 1]) o[t][e] += bf2f(b);
+                        bool sees = key0 + k < limit[e & 1];
+                        if constexpr (Args::WINDOW)
+                            sees = sees && (key0 + k >= (2 * c + (e & 1)) / G + g.off - a.mask.window || key0 + k < a.mask.sinks);
+                        if ((b & 0x7F80u) == 0x7F80u && sees) o[t][e] += bf2f(b);
                     }
             }
         }
@@ -244,6 +292,10 @@ __global__ void __launch_bounds__(AR_THREADS, ROWS_CTAS_SM) attn_rows_kernel(con
                 y.z *= inv;
                 y.w *= inv;
             }
+            if constexpr (Args::WINDOW)
+                if (a.io.lse && lane == 0)
+                    a.io.lse[(int64_t)(g.q_row0 + tok) * a.io.Hq + head * G + row % G] =
+                        min(g.k_len, tok + g.off) > 0 ? log_sum(M, L, a.io.lift) : -INFINITY;
             const int64_t at = (int64_t)(g.q_row0 + tok) * a.io.out_stride + (int64_t)(head * G + row % G) * HEAD_DIM;
             if (a.io.out_f32) reinterpret_cast<float4*>((float*)a.io.out + at)[lane] = y;
             else reinterpret_cast<uint2*>((uint16_t*)a.io.out + at)[lane] = make_uint2(bf16x2(y.x, y.y), bf16x2(y.z, y.w));
@@ -257,12 +309,19 @@ __global__ void __launch_bounds__(AR_THREADS, ROWS_CTAS_SM) attn_rows_kernel(con
 // What is in flight from memory (12 warps x 8 KB per SM) is held in the L1 cache, which is what shared
 // memory leaves of 256 KB: behind attn_tiles.cu, with its 227 KB, a block of keys took 3.2 us
 // instead of 1.9 (64 tails behind a shared prefix 45 -> 39 us) until the split was asked for.
-cudaError_t attn_rows_prepare() {
+template <class Args>
+static cudaError_t prepare() {
     constexpr int SHARED_PERCENT = 25;   // 57 KB: three CTAs
-    return cudaFuncSetAttribute(attn_rows_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, SHARED_PERCENT);
+    return cudaFuncSetAttribute(attn_rows_kernel<Args>, cudaFuncAttributePreferredSharedMemoryCarveout, SHARED_PERCENT);
+}
+cudaError_t attn_rows_prepare() { return prepare<RowsArgs>(); }
+cudaError_t attn_window_rows_prepare() {
+    const cudaError_t e = prepare<WindowRowsArgs<false>>();
+    return e != cudaSuccess ? e : prepare<WindowRowsArgs<true>>();
 }
 
-void launch_attn_rows(const RowsArgs& a, bool beside, cudaStream_t s) {
+template <class Args>
+static void launch(const Args& a, bool beside, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3((unsigned)((int64_t)a.n_items * a.io.Hkv));
@@ -272,7 +331,10 @@ void launch_attn_rows(const RowsArgs& a, bool beside, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = beside ? 1 : 0;
-    cudaLaunchKernelEx(&cfg, attn_rows_kernel, a);
+    cudaLaunchKernelEx(&cfg, attn_rows_kernel<Args>, a);
 }
+void launch_attn_rows(const RowsArgs& a, bool beside, cudaStream_t s) { launch(a, beside, s); }
+void launch_attn_window_rows(const WindowRowsArgs<false>& a, bool beside, cudaStream_t s) { launch(a, beside, s); }
+void launch_attn_window_rows(const WindowRowsArgs<true>& a, bool beside, cudaStream_t s) { launch(a, beside, s); }
 
 }  // namespace fq

@@ -71,6 +71,12 @@ class fq_kv_view(ctypes.Structure):
                 ("row_stride", ctypes.c_uint64), ("head_stride", ctypes.c_uint64)]
 
 
+class fq_kv_pages(ctypes.Structure):
+    """A pool of pages of K and V rows on the device; strides in elements."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_uint32), ("page_rows", ctypes.c_uint32),
+                ("page_stride", ctypes.c_uint64), ("row_stride", ctypes.c_uint64), ("head_stride", ctypes.c_uint64)]
+
+
 def lib():
     """The loaded ``libfq.so``; raises if it is missing (no fallback path exists)."""
     global _lib
@@ -116,6 +122,13 @@ def lib():
                                    ctypes.c_size_t, vp],
                 "fq_attn_shared_workspace": [u32, u32, vp, u32, u32, vp],
                 "fq_attn_check": [vp],
+                "fq_attn_window": [vp, u64, vp, u32, u32, vp, vp, vp, u32, u32, u32, u32, ctypes.c_float, vp, u64, ctypes.c_int,
+                                   vp, vp, ctypes.c_size_t, vp],
+                "fq_attn_window_workspace": [u32, vp, vp, u32, u32, u32, u32, vp],
+                "fq_attn_paged": [vp, u64, vp, vp, u64, u32, vp, vp, u32, u32, u32, u32, ctypes.c_float, vp, u64, ctypes.c_int,
+                                  vp, vp, ctypes.c_size_t, vp],
+                "fq_qk_norm_rope_paged": [vp, u64, u32, vp, vp, vp, vp, u64, vp, u32, u32, vp, vp, ctypes.c_float, vp, u32, vp,
+                                          u64, vp],
                 "fq_debug_attn_wait_timeout": [vp, vp, vp, u32, u32, u32, u32, vp, u32, u32, vp],
             }
             for name, args in sig.items():
@@ -144,7 +157,8 @@ EXPORTED = ("fq_desc_init", "fq_load_weights", "fq_model_free", "fq_kv_init", "f
             "fq_gemv", "fq_step_kernels", "fq_check_device", "fq_debug_wait_timeout", "fq_set_option", "fq_step_path", "fq_layer_step_noalloc", "fq_last_error",
             "fq_status_str", "fq_kv_layer_view", "fq_qk_norm_rope", "fq_attn_prompt", "fq_attn_prompt_workspace",
             "fq_attn_shared", "fq_attn_shared_workspace", "fq_attn_check", "fq_forward_step_packed", "fq_decode_step_shared",
-            "fq_debug_attn_wait_timeout")
+            "fq_debug_attn_wait_timeout", "fq_attn_window", "fq_attn_window_workspace", "fq_attn_paged",
+            "fq_qk_norm_rope_paged")
 
 
 def _check(status: int, where: str) -> None:
@@ -505,3 +519,64 @@ def fq_debug_attn_wait_timeout(q_ptr: int, view, q_len: int, k_len: int, num_att
     _check(lib().fq_debug_attn_wait_timeout(model or None, q_ptr, ctypes.byref(view), q_len, k_len, num_attention_heads,
                                             num_key_value_heads, out_ptr, starve, wait_cycles, stream),
            "fq_debug_attn_wait_timeout")
+
+
+# ---------------------------------------------------------------- windows, pages, and caches made shorter
+
+def fq_attn_window_workspace(q_len, k_len, num_attention_heads: int, num_key_value_heads: int, window: int, sinks: int) -> int:
+    """Bytes of workspace of fq_attn_window and of fq_attn_paged."""
+    a, b, out = u32_array(q_len), u32_array(k_len), ctypes.c_size_t(0)
+    _same_length(len(a), "k_len", b)
+    _check(lib().fq_attn_window_workspace(len(a), a, b, num_attention_heads, num_key_value_heads, _u32("window", window),
+                                          _u32("sinks", sinks), ctypes.byref(out)), "fq_attn_window_workspace")
+    return int(out.value)
+
+
+def fq_attn_window(q_ptr: int, views, q_len, k_len, num_attention_heads: int, num_key_value_heads: int, window: int, sinks: int,
+                   scale: float, out_ptr: int, ws_ptr: int = 0, ws_bytes: int = 0, stream: int = 0, kv_row0=None,
+                   q_stride: int = 0, out_stride: int = 0, out_dtype: str = "bf16", lse_ptr: int = 0) -> None:
+    """fq_attn_prompt over the last `window` keys (0: all) and the first `sinks`; lse_ptr: log-sums of the rows."""
+    L = _lib or lib()
+    a, b = u32_array(q_len), u32_array(k_len)
+    w, n_w = _views(views)
+    _same_length(len(a), "k_len", b)
+    r = None
+    if kv_row0 is not None:
+        r = u32_array(kv_row0)
+        _same_length(len(a), "kv_row0", r)
+    st = L.fq_attn_window(q_ptr, q_stride, w, n_w, len(a), a, r, b, num_attention_heads, num_key_value_heads,
+                          _u32("window", window), _u32("sinks", sinks), scale, out_ptr, out_stride, DTYPES[out_dtype],
+                          lse_ptr or None, ws_ptr, ws_bytes, stream)
+    if st:
+        _check(st, "fq_attn_window")
+
+
+def fq_attn_paged(q_ptr: int, pages: fq_kv_pages, table_ptr: int, table_stride: int, q_len, k_len, num_attention_heads: int,
+                  num_key_value_heads: int, window: int, sinks: int, scale: float, out_ptr: int, ws_ptr: int = 0,
+                  ws_bytes: int = 0, stream: int = 0, q_stride: int = 0, out_stride: int = 0, out_dtype: str = "bf16",
+                  lse_ptr: int = 0) -> None:
+    """fq_attn_window over rows in pages, found through a device table (int32 [sequences][table_stride])."""
+    L = _lib or lib()
+    a, b = u32_array(q_len), u32_array(k_len)
+    _same_length(len(a), "k_len", b)
+    st = L.fq_attn_paged(q_ptr, q_stride, ctypes.byref(pages), table_ptr, table_stride, len(a), a, b, num_attention_heads,
+                         num_key_value_heads, _u32("window", window), _u32("sinks", sinks), scale, out_ptr, out_stride,
+                         DTYPES[out_dtype], lse_ptr or None, ws_ptr, ws_bytes, stream)
+    if st:
+        _check(st, "fq_attn_paged")
+
+
+def fq_qk_norm_rope_paged(qkv_ptr: int, lens, pos0, pages: fq_kv_pages, table_ptr: int, table_stride: int, kv_row0,
+                          num_attention_heads: int, num_key_value_heads: int, q_norm_ptr: int, k_norm_ptr: int, eps: float,
+                          rope_ptr: int, rope_rows: int, q_out_ptr: int, stream: int = 0, qkv_stride: int = 0,
+                          q_stride: int = 0) -> None:
+    """fq_qk_norm_rope with k and v into rows kv_row0[s] .. of the sequences' pages."""
+    L = _lib or lib()
+    n, p, r = u32_array(lens), u32_array(pos0), u32_array(kv_row0)
+    _same_length(len(n), "pos0", p)
+    _same_length(len(n), "kv_row0", r)
+    st = L.fq_qk_norm_rope_paged(qkv_ptr, qkv_stride, len(n), n, p, ctypes.byref(pages), table_ptr, table_stride, r,
+                                 num_attention_heads, num_key_value_heads, q_norm_ptr, k_norm_ptr, eps, rope_ptr,
+                                 _u32("rope_rows", rope_rows), q_out_ptr, q_stride, stream)
+    if st:
+        _check(st, "fq_qk_norm_rope_paged")
