@@ -373,6 +373,49 @@ fq_status fq_qk_norm_rope_paged(const float* qkv, uint64_t qkv_stride, uint32_t 
                                 uint32_t num_key_value_heads, const float* q_norm, const float* k_norm, float eps,
                                 const float* rope, uint32_t rope_rows, void* q_out, uint64_t q_stride, void* stream);
 
+/* Gathered weights of the rows of a view on the device: that of row r and kv head h is the float at
+ * w[h * head_stride + r].  head_stride covers the rows that a call uses (it is not looked at with one kv head). */
+typedef struct fq_key_weights {
+    float* w;
+    uint64_t head_stride;
+} fq_key_weights;
+
+/* The attention weight that every key receives from the query rows of a call, added to what it has gathered before:
+ *   after[h][j] = before[h][j] + sum over the rows i that see key j and the heads g of kv head h's group of
+ *                 exp(scale * q[i][g].k[j][h] - lse[i][g]),
+ * for the k_len[s] keys of every sequence (rows, views, window, sinks and who sees what as in fq_attn_window; V is not looked
+ * at).  lse: device f32 [rows][Hq], as fq_attn_window gives it for the same rows.  before, after: host arrays of n_views
+ * entries, of the views' rows; before NULL: zeros; before and after may be the same weights, and overlap in no other
+ * way.  Keys that no row sees get before's value.  Products, exponentials and sums are f32 (the sums of many
+ * rows are compensated), and the result does not depend on the order in which thread blocks run.
+ * workspace: as there, fq_attn_key_weights_workspace.  Errors: as fq_attn_window, and INVALID_ARGUMENT (null lse or
+ * weights, a head_stride too short, two sequences of a call that write the same weights; weights of different strides that lie in
+ * between one another are taken for such). */
+fq_status fq_attn_key_weights(const void* q, uint64_t q_stride, const float* lse, const fq_kv_view* views, uint32_t n_views,
+                              uint32_t n_seq, const uint32_t* q_len, const uint32_t* kv_row0, const uint32_t* k_len,
+                              uint32_t num_attention_heads, uint32_t num_key_value_heads, uint32_t window, uint32_t sinks,
+                              float scale, const fq_key_weights* before, const fq_key_weights* after, void* workspace,
+                              size_t workspace_bytes, void* stream);
+fq_status fq_attn_key_weights_workspace(uint32_t n_seq, const uint32_t* q_len, const uint32_t* k_len,
+                                        uint32_t num_attention_heads, uint32_t num_key_value_heads, uint32_t window,
+                                        uint32_t sinks, size_t* bytes);
+
+/* Caches made shorter: of the k_len[s] rows kv_row0[s] .. of sequence s's view (n_from = 1 or n_seq; kv_row0 NULL: with one
+ * view the sequences' rows follow one another, else 0), n[s] = min(keep[s], k_len[s]) stay per kv head: the
+ * first `sinks`, the last `recent`, and of the others those with the largest weights (equal ones: the first; a NaN counts as larger
+ * than any number).  They move, in their order, to rows to_row0[s] .. of views of other storage (n_to, to_row0 alike),
+ * their weights to to_weights (n_to entries, or NULL), and their numbers (from 0 in the sequence) to
+ * kept, device int32: the sequences one after the other, [kv head][n[s]] each.  Rows carry the positions they were
+ * rotated at, so later rows go on at their own positions behind them; the rows of different heads are no longer those of
+ * one token.  weights: n_from entries.  Other rows of `to` stay as they were.
+ * Errors: INVALID_SEQUENCE_LENGTH (n_seq = 0), KV_CACHE_OVERFLOW (rows beyond a view), INVALID_ARGUMENT (null,
+ * alignment, strides, n_seq > 64, more than 1024 heads, sinks + recent > keep where rows go, rows or weights that would be written
+ * twice, a destination among the rows that are read). */
+fq_status fq_kv_evict(const fq_kv_view* from, uint32_t n_from, const fq_key_weights* weights, uint32_t n_seq,
+                      const uint32_t* kv_row0, const uint32_t* k_len, const uint32_t* keep, uint32_t sinks, uint32_t recent,
+                      uint32_t num_key_value_heads, const fq_kv_view* to, uint32_t n_to, const fq_key_weights* to_weights,
+                      const uint32_t* to_row0, int32_t* kept, void* stream);
+
 /* Synchronise `stream` and report bounded device waits of the two attentions that gave up on the
  * current device since this host thread's last check (a thread's first: since the last check of
  * any).  DEVICE_TIMEOUT: the outputs of the calls since then, of whichever thread and stream, may be

@@ -1,10 +1,11 @@
 // Host side of the operators on windows, pages and caches made shorter (fq_attn_window, fq_attn_paged,
-// fq_qk_norm_rope_paged): argument checks, then the launches.  The checks and the work lists
+// fq_qk_norm_rope_paged, fq_attn_key_weights, fq_kv_evict): argument checks, then the launches.  The checks and the work lists
 // are those of attn_host.h.
 
 #include <mutex>
 
 #include "attn_host.h"
+#include "cache_plan.h"
 
 using namespace fq;
 
@@ -26,6 +27,7 @@ fq_status prepare_device(uint32_t** waits, uint32_t** bad) {
         uint32_t* w = nullptr;
         CK(attn_window_tiles_prepare());
         CK(attn_window_rows_prepare());
+        CK(key_weights_prepare());
         CK(attn_page_word(&w));
         attn_set_page_word(dev, w);
         d.bad = w;
@@ -219,6 +221,169 @@ fq_status run_window(Call& c, bool paged, const void* q, uint64_t q_stride, uint
     }
 }
 
+// ---------------------------------------------------------------- gathered weights
+
+constexpr int KW_MAX_RUN = 4096;    // tiles of a unit, at most (no wait for a unit's end comes near its limit)
+constexpr int KW_MIN_BLOCKS = 8;    // query blocks of a unit that is cut, at least
+
+struct KwPlan {
+    std::vector<KwEntry> units;     // longest first
+    std::vector<KwJoin> join;
+    int64_t slots = 0;
+    size_t bytes(uint32_t Hkv) const { return (size_t)slots * Hkv * KW_KEY_TILES * TILE_ROWS * 4; }
+};
+
+// Few query rows (two blocks of 128 packed ones) stay while the keys pass by; of more, the query blocks pass by keys that
+// stay, in units of about a quarter of an SM's share.
+void plan_key_weights(KwPlan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G, uint32_t Hkv, const AttnMask& m) {
+    int64_t key_tiles_all = 0, blocks_all = 0;
+    struct Pair {
+        int seq, j0, j1, b0, b1;
+    };
+    struct Run {
+        int seq, j0, j1, blocks;
+    };
+    std::vector<Pair> pairs;
+    std::vector<Run> runs;
+    auto none = [&](int s, int j0, int j1) {
+        for (; j0 < j1; j0 += KW_MAX_RUN) p.units.push_back(KwEntry{s | KW_NONE, j0, std::min(j1, j0 + KW_MAX_RUN), 0, 0, -1});
+    };
+    for (uint32_t i = 0; i < n_seq; ++i) {
+        const AttnSeq& q = seq[i];
+        if (q.k_len == 0) continue;
+        const int s = (int)i, all = ceil_div(q.k_len, TILE_ROWS), blocks = ceil_div((int64_t)q.q_len * G, TILE_ROWS);
+        const KeyTiles t = key_tiles(m, q.k_len, q.off, 0, q.q_len);
+        if (t.n == 0) {
+            none(s, 0, all);
+            continue;
+        }
+        none(s, t.sinks, t.first);
+        const int ends[2][2] = {{0, t.sinks}, {t.first, all}};
+        for (auto& e : ends) {
+            if (e[0] >= e[1]) continue;
+            if (blocks <= 2) {
+                runs.push_back(Run{s, e[0], e[1], blocks});
+                key_tiles_all += e[1] - e[0];
+                continue;
+            }
+            for (int j = e[0]; j < e[1]; j += KW_KEY_TILES) {
+                const int j1 = std::min(e[1], j + KW_KEY_TILES);
+                // the tokens that see one of these keys
+                const int64_t k0 = (int64_t)j * TILE_ROWS, k1 = std::min<int64_t>(q.k_len, (int64_t)j1 * TILE_ROWS) - 1;
+                const int64_t first = std::max<int64_t>(0, k0 - q.off + 1);
+                const int64_t last = k0 < m.sinks ? q.q_len - 1 : std::min<int64_t>(q.q_len - 1, k1 + m.window - q.off);
+                if (last < first) {
+                    none(s, j, j1);
+                    continue;
+                }
+                const int b0 = (int)(first * G / TILE_ROWS), b1 = (int)((last * G + G - 1) / TILE_ROWS) + 1;
+                pairs.push_back(Pair{s, j, j1, b0, b1});
+                blocks_all += b1 - b0;
+            }
+        }
+    }
+    const int per = (int)std::min<int64_t>(KW_MAX_RUN, std::max<int64_t>(KW_MIN_BLOCKS, blocks_all * Hkv / (4 * ATTN_SMS)));
+    for (const Pair& x : pairs) {
+        const int n = ceil_div(x.b1 - x.b0, per), blocks = x.b1 - x.b0;
+        if (n > 1) p.join.push_back(KwJoin{x.seq, x.j0, x.j1, (int)p.slots, n});
+        for (int i = 0; i < n; ++i)
+            p.units.push_back(KwEntry{x.seq | KW_KEYS, x.j0, x.j1, x.b0 + (int)((int64_t)blocks * i / n),
+                                      x.b0 + (int)((int64_t)blocks * (i + 1) / n), n > 1 ? (int)p.slots++ : -1});
+    }
+    const int run = (int)std::min<int64_t>(KW_MAX_RUN, std::max<int64_t>(2, key_tiles_all * Hkv / (4 * ATTN_SMS)));
+    for (const Run& x : runs) {
+        const int n = ceil_div(x.j1 - x.j0, run), tiles = x.j1 - x.j0;
+        for (int i = 0; i < n; ++i)
+            p.units.push_back(KwEntry{x.seq | KW_ROWS, x.j0 + (int)((int64_t)tiles * i / n), x.j0 + (int)((int64_t)tiles * (i + 1) / n),
+                                      0, x.blocks, -1});
+    }
+    auto cost = [](const KwEntry& e) {
+        return e.info & KW_NONE ? 0 : e.info & KW_ROWS ? (e.j1 - e.j0) * (e.b1 - e.b0) : (e.b1 - e.b0) * (e.j1 - e.j0);
+    };
+    std::stable_sort(p.units.begin(), p.units.end(), [&](const KwEntry& a, const KwEntry& b) { return cost(a) > cost(b); });
+}
+
+// What a call reads and writes of gathered weights: of sequence s and kv head h, the floats at lo + h * stride and behind.
+struct WeightRows {
+    int64_t lo = 0, stride = 0, n = 0;   // in floats; n of each head
+};
+// Do two sequences' weights share floats?  (Other strides: where their extents meet.)
+bool weights_meet(const WeightRows& a, const WeightRows& b, int64_t Hkv) {
+    if (!a.n || !b.n) return false;
+    const int64_t ea = a.lo + (Hkv - 1) * a.stride + a.n, eb = b.lo + (Hkv - 1) * b.stride + b.n;
+    if (ea <= b.lo || eb <= a.lo) return false;
+    if (Hkv == 1 || a.stride != b.stride) return true;
+    const int64_t d = b.lo - a.lo;   // heads h of b and g of a meet where d + (h - g) stride is between -b.n and a.n
+    const int64_t below = d >= 0 ? d / a.stride : -((-d + a.stride - 1) / a.stride);
+    for (int64_t x = below; x <= below + 1; ++x) {
+        const int64_t at = d - x * a.stride;
+        if (x > -Hkv && x < Hkv && at < a.n && at + b.n > 0) return true;
+    }
+    return false;
+}
+fq_status check_weights(const fq_key_weights& w, uint32_t Hkv, uint64_t row0, uint64_t n, const char* what, uint32_t s, WeightRows& r) {
+    if (n == 0) return FQ_OK;
+    if (!w.w || (reinterpret_cast<uintptr_t>(w.w) & 3)) return fail(FQ_ERR_INVALID_ARGUMENT, "%s %u: null or misaligned weights", what, s);
+    if (Hkv > 1 && (w.head_stride < row0 + n || w.head_stride > MAX_STRIDE))
+        return fail(FQ_ERR_INVALID_ARGUMENT, "%s %u: head stride %llu (at least the rows used, %llu, at most 2^36)", what, s,
+                    (unsigned long long)w.head_stride, (unsigned long long)(row0 + n));
+    r.lo = (int64_t)(reinterpret_cast<uintptr_t>(w.w) / 4) + (int64_t)row0;
+    r.stride = Hkv > 1 ? (int64_t)w.head_stride : 0;
+    r.n = (int64_t)n;
+    return FQ_OK;
+}
+fq_status check_weights_apart(const WeightRows* r, uint32_t n_seq, uint32_t Hkv) {
+    for (uint32_t i = 0; i < n_seq; ++i)
+        for (uint32_t j = i + 1; j < n_seq; ++j)
+            if (weights_meet(r[i], r[j], Hkv)) return fail(FQ_ERR_INVALID_ARGUMENT, "sequences %u and %u write the same weights", i, j);
+    return FQ_OK;
+}
+
+template <class Args>
+fq_status run_key_weights_t(const KwPlan& p, const AttnIo& io, const float* lse, const AttnMask& mask, uint32_t* waits, float* part,
+                            const AttnSeq* seq, int n_seq, int q_rows, const ViewUse* views, const KeyWeights* w, int n_views,
+                            cudaStream_t s) {
+    Args* a = new (std::nothrow) Args;
+    if (!a) return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
+    auto run = [&]() -> fq_status {
+        a->lse = lse;
+        a->Hq = io.Hq;
+        a->Hkv = io.Hkv;
+        a->g_shift = 0;
+        while (io.Hkv << a->g_shift < io.Hq) ++a->g_shift;
+        a->c = std::fabs(score_factor(io.scale));
+        a->negate = io.scale < 0.f;
+        a->mask = mask;
+        a->waits.record = waits;
+        a->part = part;
+        std::copy(seq, seq + n_seq, a->seq);
+        const uint64_t G = io.Hq / io.Hkv;
+        const uint64_t dims[4] = {(uint64_t)HEAD_DIM, G, (uint64_t)io.Hkv, (uint64_t)q_rows};
+        const uint64_t strides[4] = {2, HEAD_DIM * 2, G * HEAD_DIM * 2, (uint64_t)io.q_stride * 2};
+        const uint32_t box[4] = {64, (uint32_t)G, 1, (uint32_t)(TILE_ROWS / G)};
+        if (q_rows && !encode_bf16_tiles(a->map_q, io.q, 4, dims, strides, box)) return fail(FQ_ERR_CUDA, "tensor map of q refused");
+        for (int v = 0; v < n_views; ++v) {
+            a->w[v] = w[v];
+            if (!views[v].used) continue;
+            const uint64_t rs = (uint64_t)views[v].rows.row_stride * 2, hs = io.Hkv > 1 ? (uint64_t)views[v].rows.head_stride * 2 : rs;
+            const uint64_t kd[3] = {(uint64_t)HEAD_DIM, views[v].used, (uint64_t)io.Hkv}, ks[3] = {2, rs, hs};
+            const uint32_t kb[3] = {64, (uint32_t)TILE_ROWS, 1};
+            if (!encode_bf16_tiles(a->map_k[v], views[v].rows.k, 3, kd, ks, kb)) return fail(FQ_ERR_CUDA, "tensor map of K refused");
+        }
+        constexpr size_t NE = Args::ENTRIES;
+        for (size_t e0 = 0; e0 < p.units.size(); e0 += NE) {
+            a->n_entries = (int)std::min(NE, p.units.size() - e0);
+            std::copy(p.units.begin() + e0, p.units.begin() + e0 + a->n_entries, a->e);
+            launch_key_weights(*a, s);
+            CK(cudaGetLastError());
+        }
+        return FQ_OK;
+    };
+    const fq_status st = run();
+    delete a;
+    return st;
+}
+
 }  // namespace
 
 extern "C" {
@@ -302,6 +467,177 @@ fq_status fq_qk_norm_rope_paged(const float* qkv, uint64_t qkv_stride, uint32_t 
     uint32_t* waits;
     TRY(prepare_device(&waits, &a.pages.bad));
     launch_qk_paged(a, (cudaStream_t)stream);
+    CK(cudaGetLastError());
+    return FQ_OK;
+}
+
+fq_status fq_attn_key_weights_workspace(uint32_t n_seq, const uint32_t* q_len, const uint32_t* k_len,
+                                        uint32_t num_attention_heads, uint32_t num_key_value_heads, uint32_t window,
+                                        uint32_t sinks, size_t* bytes) {
+    TRY(check_heads(num_attention_heads, num_key_value_heads));
+    TRY(check_count(n_seq));
+    if (!q_len || !k_len || !bytes) return fail(FQ_ERR_INVALID_ARGUMENT, "null argument");
+    AttnSeq seq[MAX_SEQ];
+    uint64_t q_rows;
+    TRY(prompt_sequences(n_seq, q_len, nullptr, k_len, nullptr, 0, num_key_value_heads, seq, nullptr, &q_rows));
+    try {
+        KwPlan p;
+        plan_key_weights(p, n_seq, seq, num_attention_heads / num_key_value_heads, num_key_value_heads, mask_of(window, sinks));
+        *bytes = p.bytes(num_key_value_heads);
+    } catch (const std::bad_alloc&) {
+        return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
+    }
+    return FQ_OK;
+}
+
+fq_status fq_attn_key_weights(const void* q, uint64_t q_stride, const float* lse, const fq_kv_view* views, uint32_t n_views,
+                              uint32_t n_seq, const uint32_t* q_len, const uint32_t* kv_row0, const uint32_t* k_len,
+                              uint32_t num_attention_heads, uint32_t num_key_value_heads, uint32_t window, uint32_t sinks,
+                              float scale, const fq_key_weights* before, const fq_key_weights* after, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+    const uint32_t Hq = num_attention_heads, Hkv = num_key_value_heads;
+    TRY(check_heads(Hq, Hkv));
+    TRY(check_count(n_seq));
+    if (!q_len || !k_len || !views || !after) return fail(FQ_ERR_INVALID_ARGUMENT, "null argument");
+    if (n_views != 1 && n_views != n_seq) return fail(FQ_ERR_INVALID_ARGUMENT, "%u views for %u sequences", n_views, n_seq);
+    AttnSeq seq[MAX_SEQ];
+    ViewUse use[MAX_SEQ];
+    fq_kv_view keys[MAX_SEQ];   // V is not looked at
+    for (uint32_t v = 0; v < n_views; ++v) {
+        keys[v] = views[v];
+        keys[v].v = views[v].k;
+    }
+    uint64_t q_rows = 0;
+    TRY(prompt_sequences(n_seq, q_len, kv_row0, k_len, keys, n_views, Hkv, seq, use, &q_rows));
+    KeyWeights w[MAX_SEQ];
+    WeightRows written[MAX_SEQ], read;
+    for (uint32_t s = 0; s < n_seq; ++s) {
+        const uint32_t v = n_views == 1 ? 0 : s;
+        TRY(check_weights(after[v], Hkv, (uint64_t)seq[s].k_row0, k_len[s], "after", s, written[s]));
+        w[v].after = after[v].w;
+        w[v].after_stride = written[s].stride;
+        if (!before || !k_len[s]) continue;
+        TRY(check_weights(before[v], Hkv, (uint64_t)seq[s].k_row0, k_len[s], "before", s, read));
+        w[v].before = before[v].w;
+        w[v].before_stride = read.stride;
+    }
+    // (strides come from sequences with keys)
+    for (uint32_t s = 0; s < n_seq; ++s)
+        if (written[s].n) w[n_views == 1 ? 0 : s].after_stride = written[s].stride;
+    TRY(check_weights_apart(written, n_seq, Hkv));
+    AttnMask mask = mask_of(window, sinks);
+    try {
+        KwPlan p;
+        plan_key_weights(p, n_seq, seq, Hq / Hkv, Hkv, mask);
+        AttnIo io;
+        // (no output of the rows' shape: q stands in for it)
+        TRY(attn_common(q, q_stride, Hq, Hkv, scale, (void*)q, 0, FQ_BF16, q_rows, 0, workspace, workspace_bytes, p.bytes(Hkv), io));
+        if (q_rows && (!lse || (reinterpret_cast<uintptr_t>(lse) & 3))) return fail(FQ_ERR_INVALID_ARGUMENT, "null or misaligned lse");
+        if (p.units.empty()) return FQ_OK;
+        uint32_t *waits, *bad;
+        TRY(prepare_device(&waits, &bad));
+        cudaStream_t s = (cudaStream_t)stream;
+        auto run = n_views > 1 ? run_key_weights_t<KwArgsN>
+                               : p.units.size() <= KwArgs1S::ENTRIES ? run_key_weights_t<KwArgs1S> : run_key_weights_t<KwArgs1>;
+        TRY(run(p, io, lse, mask, waits, (float*)workspace, seq, (int)n_seq, (int)q_rows, use, w, (int)n_views, s));
+        KwJoinArgs j;
+        j.part = (const float*)workspace;
+        j.Hkv = (int)Hkv;
+        for (uint32_t i = 0; i < n_seq; ++i) {
+            j.seq[i] = seq[i];
+            j.w[i] = w[n_views == 1 ? 0 : i];
+        }
+        for (size_t e0 = 0; e0 < p.join.size(); e0 += KwJoinArgs::ENTRIES) {
+            j.n_entries = (int)std::min<size_t>(KwJoinArgs::ENTRIES, p.join.size() - e0);
+            std::copy(p.join.begin() + e0, p.join.begin() + e0 + j.n_entries, j.e);
+            launch_key_weights_join(j, s);
+            CK(cudaGetLastError());
+        }
+        return FQ_OK;
+    } catch (const std::bad_alloc&) {
+        return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
+    }
+}
+
+fq_status fq_kv_evict(const fq_kv_view* from, uint32_t n_from, const fq_key_weights* weights, uint32_t n_seq,
+                      const uint32_t* kv_row0, const uint32_t* k_len, const uint32_t* keep, uint32_t sinks, uint32_t recent,
+                      uint32_t num_key_value_heads, const fq_kv_view* to, uint32_t n_to, const fq_key_weights* to_weights,
+                      const uint32_t* to_row0, int32_t* kept, void* stream) {
+    const uint32_t Hkv = num_key_value_heads;
+    TRY(check_count(n_seq));
+    if (!Hkv || Hkv > MAX_HEADS) return fail(FQ_ERR_INVALID_ARGUMENT, "%u kv heads (1 to %u)", Hkv, MAX_HEADS);
+    if (!from || !weights || !k_len || !keep || !to) return fail(FQ_ERR_INVALID_ARGUMENT, "null argument");
+    if ((n_from != 1 && n_from != n_seq) || (n_to != 1 && n_to != n_seq))
+        return fail(FQ_ERR_INVALID_ARGUMENT, "%u and %u views for %u sequences", n_from, n_to, n_seq);
+    EvictArgs a;
+    a.n_seq = (int)n_seq;
+    a.Hkv = (int)Hkv;
+    a.sinks = (int32_t)std::min<uint64_t>(sinks, MAX_ROWS);
+    a.recent = (int32_t)std::min<uint64_t>(recent, MAX_ROWS);
+    a.kept = kept;
+    uint64_t r0 = 0, d0 = 0;
+    int64_t total = 0, blocks = 0;
+    uint32_t longest = 0, n[MAX_SEQ], to_rows[MAX_SEQ];
+    WeightRows written[MAX_SEQ], read;
+    Span reads[2 * MAX_SEQ];
+    int n_reads = 0;
+    for (uint32_t s = 0; s < n_seq; ++s) {
+        if (k_len[s] > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 rows");
+        n[s] = std::min(k_len[s], keep[s]);
+        if (n[s] < k_len[s] && (uint64_t)sinks + recent > keep[s])
+            return fail(FQ_ERR_INVALID_ARGUMENT, "sequence %u: %u rows do not hold %u first and %u recent ones", s, keep[s], sinks, recent);
+        const uint32_t v = n_from == 1 ? 0 : s, t = n_to == 1 ? 0 : s;
+        const uint64_t row = kv_row0 ? kv_row0[s] : n_from == 1 ? r0 : 0, at = to_row0 ? to_row0[s] : n_to == 1 ? d0 : 0;
+        TRY(check_view(from[v], Hkv, row, k_len[s], "sequence", s));
+        TRY(check_view(to[t], Hkv, at, n[s], "destination", s));
+        TRY(check_weights(weights[v], Hkv, row, k_len[s], "sequence", s, read));
+        EvictSeq& e = a.s[s];
+        e = EvictSeq{};
+        e.len = (int32_t)k_len[s];
+        e.n = (int32_t)n[s];
+        e.kept0 = total;
+        e.block0 = (int32_t)blocks;
+        to_rows[s] = (uint32_t)at;
+        if (n[s]) {
+            if (to_weights) TRY(check_weights(to_weights[t], Hkv, at, n[s], "destination", s, written[s]));
+            auto rows_at = [&](const fq_kv_view& g, uint64_t r) {
+                KvRows x = rows_of(g);
+                x.k += r * g.row_stride;
+                x.v += r * g.row_stride;
+                if (Hkv == 1) x.head_stride = 0;
+                return x;
+            };
+            e.w = weights[v].w + row;
+            e.w_stride = read.stride;
+            e.w_to = to_weights ? to_weights[t].w + at : nullptr;
+            e.w_to_stride = written[s].stride;
+            e.from = rows_at(from[v], row);
+            e.to = rows_at(to[t], at);
+            reads[n_reads++] = span_of(from[v].k, from[v], (uint32_t)row, k_len[s], Hkv, s);
+            reads[n_reads++] = span_of(from[v].v, from[v], (uint32_t)row, k_len[s], Hkv, s);
+        }
+        longest = std::max(longest, n[s] < k_len[s] ? k_len[s] : 0);
+        total += (int64_t)n[s] * Hkv;
+        blocks += (int64_t)ceil_div(n[s], EVICT_ROWS) * Hkv;
+        if (blocks > 0x7FFFFFFF) return fail(FQ_ERR_INVALID_ARGUMENT, "2^36 rows of heads or more stay");
+        r0 += k_len[s];
+        d0 += n[s];
+    }
+    if (total == 0) return FQ_OK;
+    if (!kept || (reinterpret_cast<uintptr_t>(kept) & 3)) return fail(FQ_ERR_INVALID_ARGUMENT, "null or misaligned kept");
+    TRY(check_apart(n_seq, n, to, n_to, to_rows, Hkv));
+    TRY(check_weights_apart(written, n_seq, Hkv));
+    // a row that is written while another block still has to read it
+    int64_t steps = 1 << 20;
+    for (uint32_t s = 0; s < n_seq; ++s) {
+        if (!n[s]) continue;
+        const fq_kv_view& t = to[n_to == 1 ? 0 : s];
+        const Span k = span_of(t.k, t, to_rows[s], n[s], Hkv, s), v = span_of(t.v, t, to_rows[s], n[s], Hkv, s);
+        for (int i = 0; i < n_reads; ++i)
+            if (rows_meet(reads[i], k, Hkv, false, steps) || rows_meet(reads[i], v, Hkv, false, steps))
+                return fail(FQ_ERR_INVALID_ARGUMENT, "sequence %u moves to rows that sequence %u is read from", s, reads[i].seq);
+    }
+    launch_evict(a, (int)longest, (int)blocks, (cudaStream_t)stream);
     CK(cudaGetLastError());
     return FQ_OK;
 }

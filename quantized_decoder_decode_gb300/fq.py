@@ -77,6 +77,11 @@ class fq_kv_pages(ctypes.Structure):
                 ("page_stride", ctypes.c_uint64), ("row_stride", ctypes.c_uint64), ("head_stride", ctypes.c_uint64)]
 
 
+class fq_key_weights(ctypes.Structure):
+    """Gathered weights of a view's rows on the device: address, head stride in floats."""
+    _fields_ = [("w", ctypes.c_void_p), ("head_stride", ctypes.c_uint64)]
+
+
 def lib():
     """The loaded ``libfq.so``; raises if it is missing (no fallback path exists)."""
     global _lib
@@ -129,6 +134,10 @@ def lib():
                                   vp, vp, ctypes.c_size_t, vp],
                 "fq_qk_norm_rope_paged": [vp, u64, u32, vp, vp, vp, vp, u64, vp, u32, u32, vp, vp, ctypes.c_float, vp, u32, vp,
                                           u64, vp],
+                "fq_attn_key_weights": [vp, u64, vp, vp, u32, u32, vp, vp, vp, u32, u32, u32, u32, ctypes.c_float, vp, vp, vp,
+                                        ctypes.c_size_t, vp],
+                "fq_attn_key_weights_workspace": [u32, vp, vp, u32, u32, u32, u32, vp],
+                "fq_kv_evict": [vp, u32, vp, u32, vp, vp, vp, u32, u32, u32, vp, u32, vp, vp, vp, vp],
                 "fq_debug_attn_wait_timeout": [vp, vp, vp, u32, u32, u32, u32, vp, u32, u32, vp],
             }
             for name, args in sig.items():
@@ -158,7 +167,7 @@ EXPORTED = ("fq_desc_init", "fq_load_weights", "fq_model_free", "fq_kv_init", "f
             "fq_status_str", "fq_kv_layer_view", "fq_qk_norm_rope", "fq_attn_prompt", "fq_attn_prompt_workspace",
             "fq_attn_shared", "fq_attn_shared_workspace", "fq_attn_check", "fq_forward_step_packed", "fq_decode_step_shared",
             "fq_debug_attn_wait_timeout", "fq_attn_window", "fq_attn_window_workspace", "fq_attn_paged",
-            "fq_qk_norm_rope_paged")
+            "fq_qk_norm_rope_paged", "fq_attn_key_weights", "fq_attn_key_weights_workspace", "fq_kv_evict")
 
 
 def _check(status: int, where: str) -> None:
@@ -580,3 +589,71 @@ def fq_qk_norm_rope_paged(qkv_ptr: int, lens, pos0, pages: fq_kv_pages, table_pt
                                  _u32("rope_rows", rope_rows), q_out_ptr, q_stride, stream)
     if st:
         _check(st, "fq_qk_norm_rope_paged")
+
+
+def key_weights_array(weights):
+    """A sequence of gathered weights as a host array of ``fq_key_weights``."""
+    if isinstance(weights, ctypes.Array) and weights._type_ is fq_key_weights:
+        return weights
+    return (fq_key_weights * len(weights))(*weights)
+
+
+def _weights(name: str, weights, n: int):
+    """The argument for the weights of n views."""
+    if type(weights) is fq_key_weights:
+        if n != 1:
+            raise ValueError(f"{name}: one entry for {n} views")
+        return ctypes.byref(weights)
+    a = key_weights_array(weights)
+    if len(a) != n:
+        raise ValueError(f"{name} has {len(a)} entries for {n} views")
+    return a
+
+
+def fq_attn_key_weights_workspace(q_len, k_len, num_attention_heads: int, num_key_value_heads: int, window: int, sinks: int) -> int:
+    a, b, out = u32_array(q_len), u32_array(k_len), ctypes.c_size_t(0)
+    _same_length(len(a), "k_len", b)
+    _check(lib().fq_attn_key_weights_workspace(len(a), a, b, num_attention_heads, num_key_value_heads, _u32("window", window),
+                                               _u32("sinks", sinks), ctypes.byref(out)), "fq_attn_key_weights_workspace")
+    return int(out.value)
+
+
+def fq_attn_key_weights(q_ptr: int, lse_ptr: int, views, q_len, k_len, num_attention_heads: int, num_key_value_heads: int,
+                        window: int, sinks: int, scale: float, before, after, ws_ptr: int = 0, ws_bytes: int = 0,
+                        stream: int = 0, kv_row0=None, q_stride: int = 0) -> None:
+    """after = before (fq_key_weights, one per view, or None) + the weight that every key receives from the query rows."""
+    L = _lib or lib()
+    a, b = u32_array(q_len), u32_array(k_len)
+    w, n_w = _views(views)
+    _same_length(len(a), "k_len", b)
+    r = None
+    if kv_row0 is not None:
+        r = u32_array(kv_row0)
+        _same_length(len(a), "kv_row0", r)
+    st = L.fq_attn_key_weights(q_ptr, q_stride, lse_ptr, w, n_w, len(a), a, r, b, num_attention_heads, num_key_value_heads,
+                               _u32("window", window), _u32("sinks", sinks), scale,
+                               None if before is None else _weights("before", before, n_w), _weights("after", after, n_w), ws_ptr,
+                               ws_bytes, stream)
+    if st:
+        _check(st, "fq_attn_key_weights")
+
+
+def fq_kv_evict(views, weights, kv_row0, k_len, keep, sinks: int, recent: int, num_key_value_heads: int, to_views, to_weights,
+                to_row0, kept_ptr: int, stream: int = 0) -> None:
+    """The rows with the largest gathered weights (and the first and most recent ones) to other rows; their numbers to kept."""
+    L = _lib or lib()
+    a, b = u32_array(k_len), u32_array(keep)
+    _same_length(len(a), "keep", b)
+    w, n_w = _views(views)
+    t, n_t = _views(to_views)
+    rows = []
+    for name, r in (("kv_row0", kv_row0), ("to_row0", to_row0)):
+        if r is not None:
+            r = u32_array(r)
+            _same_length(len(a), name, r)
+        rows.append(r)
+    st = L.fq_kv_evict(w, n_w, _weights("weights", weights, n_w), len(a), rows[0], a, b, _u32("sinks", sinks),
+                       _u32("recent", recent), num_key_value_heads, t, n_t,
+                       None if to_weights is None else _weights("to_weights", to_weights, n_t), rows[1], kept_ptr, stream)
+    if st:
+        _check(st, "fq_kv_evict")
