@@ -233,7 +233,7 @@ struct KwPlan {
     size_t bytes(uint32_t Hkv) const { return (size_t)slots * Hkv * KW_KEY_TILES * TILE_ROWS * 4; }
 };
 
-// Few query rows (two blocks of 128 packed ones) stay while the keys pass by; of more, the query blocks pass by keys that
+// Few query rows (two blocks of 96 packed ones) stay while the keys pass by; of more, the query blocks pass by keys that
 // stay, in units of about a quarter of an SM's share.
 void plan_key_weights(KwPlan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G, uint32_t Hkv, const AttnMask& m) {
     int64_t key_tiles_all = 0, blocks_all = 0;
@@ -251,7 +251,7 @@ void plan_key_weights(KwPlan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G,
     for (uint32_t i = 0; i < n_seq; ++i) {
         const AttnSeq& q = seq[i];
         if (q.k_len == 0) continue;
-        const int s = (int)i, all = ceil_div(q.k_len, TILE_ROWS), blocks = ceil_div((int64_t)q.q_len * G, TILE_ROWS);
+        const int s = (int)i, all = ceil_div(q.k_len, TILE_ROWS), blocks = ceil_div((int64_t)q.q_len * G, KW_BLOCK);
         const KeyTiles t = key_tiles(m, q.k_len, q.off, 0, q.q_len);
         if (t.n == 0) {
             none(s, 0, all);
@@ -276,7 +276,7 @@ void plan_key_weights(KwPlan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G,
                     none(s, j, j1);
                     continue;
                 }
-                const int b0 = (int)(first * G / TILE_ROWS), b1 = (int)((last * G + G - 1) / TILE_ROWS) + 1;
+                const int b0 = (int)(first * G / KW_BLOCK), b1 = (int)((last * G + G - 1) / KW_BLOCK) + 1;
                 pairs.push_back(Pair{s, j, j1, b0, b1});
                 blocks_all += b1 - b0;
             }
@@ -351,8 +351,7 @@ fq_status run_key_weights_t(const KwPlan& p, const AttnIo& io, const float* lse,
         a->Hkv = io.Hkv;
         a->g_shift = 0;
         while (io.Hkv << a->g_shift < io.Hq) ++a->g_shift;
-        a->c = std::fabs(score_factor(io.scale));
-        a->negate = io.scale < 0.f;
+        a->c = score_factor(io.scale);
         a->mask = mask;
         a->waits.record = waits;
         a->part = part;
@@ -360,7 +359,7 @@ fq_status run_key_weights_t(const KwPlan& p, const AttnIo& io, const float* lse,
         const uint64_t G = io.Hq / io.Hkv;
         const uint64_t dims[4] = {(uint64_t)HEAD_DIM, G, (uint64_t)io.Hkv, (uint64_t)q_rows};
         const uint64_t strides[4] = {2, HEAD_DIM * 2, G * HEAD_DIM * 2, (uint64_t)io.q_stride * 2};
-        const uint32_t box[4] = {64, (uint32_t)G, 1, (uint32_t)(TILE_ROWS / G)};
+        const uint32_t box[4] = {64, (uint32_t)G, 1, (uint32_t)(KW_BLOCK / G)};
         if (q_rows && !encode_bf16_tiles(a->map_q, io.q, 4, dims, strides, box)) return fail(FQ_ERR_CUDA, "tensor map of q refused");
         for (int v = 0; v < n_views; ++v) {
             a->w[v] = w[v];

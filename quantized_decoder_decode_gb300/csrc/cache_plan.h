@@ -13,7 +13,8 @@ struct KeyWeights {
     int64_t before_stride = 0, after_stride = 0;
 };
 
-// A unit of key_weights.cu per kv head.  Query blocks are 128 packed rows of the sequence.
+// A unit of key_weights.cu per kv head.  Query blocks are 96 packed rows of the sequence (whole tokens of every group).
+constexpr int KW_BLOCK = 96;
 struct KwEntry {
     int32_t info;         // sequence | kind
     int32_t j0, j1;       // key tiles
@@ -37,8 +38,7 @@ struct KwArgs {
     alignas(64) unsigned long long map_k[NV][16];
     const float* lse;     // [rows][Hq]
     int Hq, Hkv, g_shift, n_entries;
-    float c;              // |scale| log2(e)
-    int negate;           // scale < 0
+    float c;              // scale log2(e)
     AttnMask mask;
     AttnWaits waits;
     float* part;          // [slot][kv head][256]

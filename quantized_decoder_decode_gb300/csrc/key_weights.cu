@@ -9,15 +9,18 @@
 // as one tile does.
 //
 // A unit holds what is few and lets the rest pass by through a ring of 32 KB tiles (TMA):
-//   KW_KEYS  two key tiles stay (one for each of the two warpgroups), query blocks of 128 packed rows pass by;
+//   KW_KEYS  two key tiles stay (one for each of two pairs of warpgroups), query blocks of 128 packed rows pass by;
 //   KW_ROWS  up to two query blocks stay (single tokens, a few observed rows), key tiles pass by, to the two
 //            warpgroups in turn: K is read once, which is what bounds it.
 // What stays has two sets of buffers, so that the next unit's comes while this one is worked on.  Long ranges of query
 // blocks are cut into units of their own, whose partial sums (4 bytes a key) a second kernel adds up in order.
 //
-// Tensor memory: two S buffers of 128 columns for each warpgroup.  Shared memory: 2 x 2 tiles that stay, 3 that pass by.
-// Roles (320 threads, one CTA per SM, looping over its units): warps 0-3 and 4-7 exponentials and sums, a key per thread; warp
-// 8 loads; warp 9 issues the products.  Every wait is bounded; one that gives up records it, and all roles leave.
+// Tensor memory: an S buffer of 128 columns for each of four warpgroups.  Shared memory: 2 x 2 tiles that stay, 3 that pass by.
+// Roles (608 threads, one CTA per SM, looping over its units): warps 0-15 exponentials and sums, a key per thread; warp 16 loads;
+// warp 17 issues the products; warp 18 brings the rows' log-sums.  Four warpgroups, because the exponentials of a tile take the special-function units as
+// long as its product takes the tensor cores (512 cycles each): two warpgroups with two buffers each kept either busy 31 % of the
+// time (8192 tokens 384 us), four that share tiles by their columns 39 % (297 us).  Every wait is bounded; one that gives up
+// records it, and all roles leave.
 
 #include <cstddef>
 
@@ -29,23 +32,40 @@ namespace fq {
 
 namespace {
 
-constexpr int KW_THREADS = 320;
+constexpr int KW_THREADS = 608;
 constexpr int KW_RING = 3;
 constexpr int KW_TILE_BYTES = TILE_ROWS * HEAD_DIM * 2;   // 32 KB
-constexpr int KW_PANEL = KW_TILE_BYTES / 2;               // 64 dims of 128 rows
+constexpr int KW_PANEL = KW_TILE_BYTES / 2;               // 64 dims of 128 keys
+constexpr int KW_Q_PANEL = KW_BLOCK * 128;                // 64 dims of a query block
+constexpr uint32_t KW_S = 0, KW_K = 4 * KW_BLOCK;         // tensor-memory columns: four S buffers, two key tiles (64 each)
+static_assert(KW_K + 128 <= 512, "tensor memory");
 
+// Warpgroup x + 2 y (x, y = 0, 1).  Where keys stay, x is its key tile and the query blocks go to y = 0 and 1 in turn; where query blocks
+// stay, the key tiles go to warpgroups 0, 1, 2, 3 in turn.
 struct KwShared {
     uint64_t st_full[2], st_empty[2];              // per set of tiles that stay
     uint64_t ring_full[KW_RING], ring_empty[KW_RING];
-    uint64_t s_full[2][2], s_free[2][2];           // per warpgroup and S buffer
-    uint64_t neg_full[2][2];                       // per warpgroup and buffer of statistics
+    uint64_t s_full[4], s_free[4];                 // per warpgroup: its S buffer
+    uint64_t neg_full[2][2], neg_empty[2][2];      // per y, two buffers in turn
+    uint64_t half_full[2];                         // per x: the sums of y = 1 are in its S buffer
+    uint64_t k_go[2], k_ready[2];                  // per x: its key tile may move to tensor memory; is there
     uint32_t tmem;
     uint32_t limit;                                // cycles that a wait may take; 0: one gave up, all roles leave
-    alignas(16) float neg[2][2][TILE_ROWS];        // (read 16 bytes at a time) -lse log2(e) of a query block's rows: per warpgroup, two in turn
+    alignas(16) float neg[2][2][KW_BLOCK];         // (read 16 bytes at a time) -lse log2(e) of a query block's rows
 };
 constexpr int KW_SMEM = (4 + KW_RING) * KW_TILE_BYTES + 3072;
 static_assert(sizeof(KwShared) <= 3072 && KW_SMEM <= 232448, "shared memory");
 static_assert(offsetof(KwShared, neg) % 16 == 0, "16-byte reads");
+
+// one column of tensor memory, a value per lane
+FQ_DEV void tmem_st1(uint32_t taddr, float x) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(x)) : "memory");
+}
+FQ_DEV float tmem_ld1(uint32_t taddr) {
+    uint32_t x;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;" : "=r"(x) : "r"(taddr) : "memory");
+    return __uint_as_float(x);
+}
 
 FQ_DEV uint32_t wait_limit(const KwShared* sh) { return *(const volatile uint32_t*)&sh->limit; }
 FQ_DEV bool kw_wait(uint64_t* bar, uint32_t parity, KwShared* sh) {
@@ -103,19 +123,19 @@ FQ_DEV void kw_load_k(const Args& a, const KwUnit& u, int j, uint8_t* dst, uint6
 }
 template <class Args>
 FQ_DEV void kw_load_q(const Args& a, const KwUnit& u, int b, uint8_t* dst, uint64_t* bar) {
-    const int row = a.seq[u.seq].q_row0 + (b * TILE_ROWS >> a.g_shift);
+    const int row = a.seq[u.seq].q_row0 + (b * KW_BLOCK >> a.g_shift);
     tma_load_4d(dst, a.map_q, 0, 0, u.head, row, bar);
-    tma_load_4d(dst + KW_PANEL, a.map_q, 64, 0, u.head, row, bar);
+    tma_load_4d(dst + KW_Q_PANEL, a.map_q, 64, 0, u.head, row, bar);
 }
 
 // Columns of a product with query block b: packed rows, in steps of 32 where the block stays.
 template <class Args>
 FQ_DEV int kw_columns(const Args& a, const KwUnit& u, int b) {
-    if (u.kind == KW_KEYS) return TILE_ROWS;
-    return min(TILE_ROWS, ((a.seq[u.seq].q_len << a.g_shift) - b * TILE_ROWS + 31) & ~31);
+    if (u.kind == KW_KEYS) return KW_BLOCK;
+    return min(KW_BLOCK, ((a.seq[u.seq].q_len << a.g_shift) - b * KW_BLOCK + 31) & ~31);
 }
 
-// ---------------- warp 8
+// ---------------- warp 16
 template <class Args>
 FQ_DEV void kw_load(const Args& a, KwShared* sh, uint8_t* stay, uint8_t* ring, int units) {
     uint32_t n = 0, un = 0;   // tiles that pass by; units with tiles
@@ -127,7 +147,7 @@ FQ_DEV void kw_load(const Args& a, KwShared* sh, uint8_t* stay, uint8_t* ring, i
         if (!(ok = kw_wait_warp(&sh->st_empty[set], ((un >> 1) & 1) ^ 1, sh))) break;
         ++un;
         if (elect_one()) {
-            mbar_arrive_expect_tx(&sh->st_full[set], u.stay * KW_TILE_BYTES);
+            mbar_arrive_expect_tx(&sh->st_full[set], u.stay * (u.kind == KW_ROWS ? 2 * KW_Q_PANEL : KW_TILE_BYTES));
             for (int x = 0; x < u.stay; ++x) {
                 uint8_t* dst = stay + (2 * set + x) * KW_TILE_BYTES;
                 if (u.kind == KW_ROWS) kw_load_q(a, u, u.b0 + x, dst, &sh->st_full[set]);
@@ -139,7 +159,7 @@ FQ_DEV void kw_load(const Args& a, KwShared* sh, uint8_t* stay, uint8_t* ring, i
             const int s = n % KW_RING;
             if (!(ok = kw_wait_warp(&sh->ring_empty[s], ((n / KW_RING) & 1) ^ 1, sh))) break;
             if (elect_one()) {
-                mbar_arrive_expect_tx(&sh->ring_full[s], KW_TILE_BYTES);
+                mbar_arrive_expect_tx(&sh->ring_full[s], u.kind == KW_ROWS ? KW_TILE_BYTES : 2 * KW_Q_PANEL);
                 if (u.kind == KW_ROWS) kw_load_k(a, u, u.j0 + i, ring + s * KW_TILE_BYTES, &sh->ring_full[s]);
                 else kw_load_q(a, u, u.b0 + i, ring + s * KW_TILE_BYTES, &sh->ring_full[s]);
             }
@@ -154,51 +174,116 @@ FQ_DEV void kw_load(const Args& a, KwShared* sh, uint8_t* stay, uint8_t* ring, i
     if (!ok) kw_drain();
 }
 
-// ---------------- warp 9
+// ---------------- warp 17, one thread of it.  A product takes the tensor cores 384 cycles, and this loop has no more for it: its waits are
+// tests of one thread, its addresses are counted on, and what depends on the kind of unit is decided outside it.
+template <bool ROWS>
+FQ_DEV bool kw_unit_products(KwShared* sh, const KwUnit& u, uint64_t d_stay, uint64_t d_ring, uint32_t tm, const uint32_t (&idesc)[2],
+                             uint32_t& slot, uint32_t& slot_ph, uint32_t& free_ph, int set) {
+    uint64_t dr = d_ring + (uint32_t)(slot * (KW_TILE_BYTES >> 4));
+#pragma unroll 1
+    for (int i = 0; i < u.pass; ++i) {
+        if (!kw_wait(&sh->ring_full[slot], slot_ph, sh)) return false;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            if (x >= u.stay) break;
+            const int wg = ROWS ? i & 3 : x + 2 * (i & 1);
+            if (!kw_wait(&sh->s_free[wg], (free_ph >> wg & 1) ^ 1, sh)) return false;
+            free_ph ^= 1u << wg;
+            tc_fence_after();
+            const uint32_t d = tm + KW_S + KW_BLOCK * wg;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t q_off = (k >> 2) * (KW_Q_PANEL >> 4) + (k & 3) * 2, k_off = (k >> 2) * (KW_PANEL >> 4) + (k & 3) * 2;
+                if (ROWS) mma_f16(d, dr + k_off, d_stay + (uint32_t)(x * (KW_TILE_BYTES >> 4)) + q_off, idesc[x], k > 0);
+                else mma_f16_ta(d, tm + KW_K + 64 * x + 8 * k, dr + q_off, idesc[0], k > 0);
+            }
+            mma_commit(&sh->s_full[wg]);
+        }
+        mma_commit(&sh->ring_empty[slot]);
+        dr += KW_TILE_BYTES >> 4;
+        if (++slot == KW_RING) {
+            slot = 0;
+            slot_ph ^= 1;
+            dr = d_ring;
+        }
+    }
+    if (ROWS) mma_commit(&sh->st_empty[set]);
+    return true;
+}
+
 template <class Args>
 FQ_DEV void kw_products(const Args& a, KwShared* sh, uint8_t* stay, uint8_t* ring, int units, uint32_t tm) {
     const uint64_t d_stay = sdesc_sw128(smem_u32(stay)), d_ring = sdesc_sw128(smem_u32(ring));
-    uint32_t n = 0, un = 0, tiles[2] = {0, 0};   // tiles that passed; units; score tiles of a warpgroup
-    bool ok = true;
-    for (int it = 0, w; (w = kw_unit_at(it)) < units && ok; ++it) {
+    uint32_t un = 0, free_ph = 0, ready_ph = 0, slot = 0, slot_ph = 0;   // units; phase bits of s_free and of k_ready; the ring's next tile
+    for (int it = 0, w; (w = kw_unit_at(it)) < units; ++it) {
         const KwUnit u = kw_unit(a, w);
         if (!u.pass) continue;
         const int set = un & 1;
-        if (!(ok = kw_wait_warp(&sh->st_full[set], (un >> 1) & 1, sh))) break;
+        if (!kw_wait(&sh->st_full[set], (un >> 1) & 1, sh)) break;
         ++un;
-        for (int i = 0; i < u.pass && ok; ++i, ++n) {
-            const int s = n % KW_RING;
-            if (!(ok = kw_wait_warp(&sh->ring_full[s], (n / KW_RING) & 1, sh))) break;
-#pragma unroll 1
-            for (int x = 0; x < u.stay; ++x) {
-                const int g = u.kind == KW_ROWS ? i & 1 : x;   // the warpgroup
-                const uint32_t t = g ? tiles[1]++ : tiles[0]++;
-                if (!(ok = kw_wait_warp(&sh->s_free[g][t & 1], ((t >> 1) & 1) ^ 1, sh))) break;
-                tc_fence_after();
-                const uint64_t dx = d_stay + (uint32_t)((2 * set + x) * (KW_TILE_BYTES >> 4)), dr = d_ring + (uint32_t)(s * (KW_TILE_BYTES >> 4));
-                const uint64_t dk = u.kind == KW_ROWS ? dr : dx, dq = u.kind == KW_ROWS ? dx : dr;
-                const uint32_t idesc = idesc_bf16_f32(TILE_ROWS, kw_columns(a, u, u.b0 + x), false, a.negate != 0);
-                if (elect_one()) {
+        const uint32_t idesc[2] = {idesc_bf16_f32(TILE_ROWS, kw_columns(a, u, u.b0), false, false),
+                                   u.stay > 1 ? idesc_bf16_f32(TILE_ROWS, kw_columns(a, u, u.b0 + 1), false, false) : 0u};
+        const uint64_t d_set = d_stay + (uint32_t)(2 * set * (KW_TILE_BYTES >> 4));
+        if (u.kind == KW_ROWS) {
+            if (!kw_unit_products<true>(sh, u, d_set, d_ring, tm, idesc, slot, slot_ph, free_ph, set)) break;
+            continue;
+        }
+        // the key tiles become operands in tensor memory
+        for (int x = 0; x < u.stay; ++x) mbar_arrive(&sh->k_go[x]);
+        bool ok = true;
+        for (int x = 0; x < u.stay && ok; ++x) {
+            ok = kw_wait(&sh->k_ready[x], ready_ph >> x & 1, sh);
+            ready_ph ^= 1u << x;
+        }
+        if (!ok) break;
+        tc_fence_after();
+        mbar_arrive(&sh->st_empty[set]);
+        if (!kw_unit_products<false>(sh, u, d_set, d_ring, tm, idesc, slot, slot_ph, free_ph, set)) break;
+    }
+}
+
+// ---------------- warp 18: -lse log2(e) of the rows of query blocks, for y = 0 and 1 in turn where keys stay, for both where
+// query blocks do.  A block's values are on their way while the one before is put down.
+template <class Args>
+FQ_DEV void kw_statistics(const Args& a, KwShared* sh, int units, int lane) {
+    constexpr float LOG2E = 1.4426950408889634f;
+    const int shift = a.g_shift, G = 1 << shift;
+    uint32_t blk[2] = {0, 0};
+    bool ok = true;
+    for (int it = 0, w; (w = kw_unit_at(it)) < units && ok; ++it) {
+        const KwUnit u = kw_unit(a, w);
+        if (u.kind == KW_NONE) continue;
+        const AttnSeq& sq = a.seq[u.seq];
+        const int n = u.b1 - u.b0;
+        auto fetch = [&](int b, float (&v)[4]) {   // rows 4 lane .. (beyond the sequence: a weight of 0)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t off = (k >> 2) * (KW_PANEL >> 4) + (k & 3) * 2;
-                        mma_f16(tm + 256 * g + 128 * (t & 1), dk + off, dq + off, idesc, k > 0);
-                    }
-                    mma_commit(&sh->s_full[g][t & 1]);
-                }
+            for (int k = 0; k < 4; ++k) {
+                const int p = b * KW_BLOCK + 4 * lane + k, tok = p >> shift;
+                v[k] = 4 * lane < KW_BLOCK && tok < sq.q_len ? __ldg(a.lse + (int64_t)(sq.q_row0 + tok) * a.Hq + (u.head << shift) + (p & (G - 1))) : INFINITY;
+            }
+        };
+        float v[4];
+        fetch(u.b0, v);
+        for (int i = 0; i < n && ok; ++i) {
+            float now[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) now[k] = -LOG2E * v[k];
+            if (i + 1 < n) fetch(u.b0 + i + 1, v);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                if (u.kind != KW_ROWS && y != (i & 1)) continue;
+                const int s = blk[y] & 1;
+                if (!(ok = kw_wait_warp(&sh->neg_empty[y][s], ((blk[y] >> 1) & 1) ^ 1, sh))) break;
+                ++blk[y];
+                if (4 * lane < KW_BLOCK) *reinterpret_cast<float4*>(&sh->neg[y][s][4 * lane]) = make_float4(now[0], now[1], now[2], now[3]);
                 __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->neg_full[y][s]);
             }
-            if (!ok) break;
-            if (elect_one()) {
-                mma_commit(&sh->ring_empty[s]);
-                if (i + 1 == u.pass) mma_commit(&sh->st_empty[set]);
-            }
-            __syncwarp();
         }
     }
 }
 
-// ---------------- warps 0-3 (g = 0), 4-7 (g = 1)
+// ---------------- warps 0-15
 // A number with the rounding errors of its additions beside it (compensated summation).
 struct Total {
     float sum = 0.f, err = 0.f;
@@ -209,51 +294,48 @@ struct Total {
     }
 };
 
-// (in order with the loads around them: the compiler would fetch a whole tile's at once, and spill)
-FQ_DEV void lds_pairs(const float* p, uint64_t& a, uint64_t& b) {
-    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(smem_u32(p)));
-}
-// tcgen05.wait::ld for 32 registers: what uses them comes behind it
-FQ_DEV void tmem_wait_ld32(uint32_t* r) {
+// tcgen05.wait::ld, for 16 registers: what uses them comes behind it
+FQ_DEV void tmem_wait_ld16(uint32_t* r) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
-                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
-                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29])
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                  :
                  : "memory");
-    asm volatile("" : "+r"(r[30]), "+r"(r[31]));
 }
 
-// The sum of 2^(c s + neg) over the columns [lo, hi) of a score tile's row (PART: they are not all).
+// The sum of 2^(c s + neg) over `columns` columns (a multiple of 32) of a score tile's row; of those, [lo, hi) count (PART: not all
+// do).  16 columns are on their way from tensor memory while the 16 before are worked on.  s_free (if any) is told when
+// the scores are read.
 template <bool PART>
 FQ_DEV float kw_row(uint32_t tS, uint64_t* s_free, const float* neg, uint64_t c2, int columns, int lo, int hi, int lane) {
     uint64_t acc[4] = {0, 0, 0, 0};
-    uint32_t s[2][32];
-    tmem_ld32(tS, s[0]);
+    uint32_t x[2][16];
+    tmem_ld16(tS, x[0]);
+#pragma unroll 1
+    for (int h = 0; h < columns; h += 32) {
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-        if (32 * h < columns) {
-            tmem_wait_ld32(s[h & 1]);
-            if (32 * (h + 1) < columns) {
-                if (h < 3) tmem_ld32(tS + 32 * (h + 1), s[(h + 1) & 1]);
-            } else {   // the next scores may come
+        for (int b = 0; b < 2; ++b) {
+            const int at = h + 16 * b;
+            ulonglong2 m[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m[k] = *reinterpret_cast<const ulonglong2*>(neg + at + 4 * k);
+            tmem_wait_ld16(x[b]);
+            if (b == 0 || h + 32 < columns) {
+                tmem_ld16(tS + at + 16, x[b ^ 1]);
+            } else if (s_free) {   // the next scores may come
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_free);
             }
-            const uint32_t* x = s[h & 1];
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-                uint64_t m0, m1;
+            for (int k = 0; k < 16; k += 4) {
                 float p[4];
-                lds_pairs(neg + 32 * h + k, m0, m1);
-                unpair(fma2(pair(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), c2, m0), p[0], p[1]);
-                unpair(fma2(pair(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])), c2, m1), p[2], p[3]);
+                unpair(fma2(pair(__uint_as_float(x[b][k]), __uint_as_float(x[b][k + 1])), c2, m[k >> 2].x), p[0], p[1]);
+                unpair(fma2(pair(__uint_as_float(x[b][k + 2]), __uint_as_float(x[b][k + 3])), c2, m[k >> 2].y), p[2], p[3]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     p[e] = ex2(p[e]);
-                    if (PART) p[e] = 32 * h + k + e >= lo && 32 * h + k + e < hi ? p[e] : 0.f;
+                    if (PART) p[e] = at + k + e >= lo && at + k + e < hi ? p[e] : 0.f;
                 }
                 acc[(k >> 1) & 3] = add2(acc[(k >> 1) & 3], pair(p[0], p[1]));
                 acc[((k >> 1) & 3) + 1] = add2(acc[((k >> 1) & 3) + 1], pair(p[2], p[3]));
@@ -265,13 +347,27 @@ FQ_DEV float kw_row(uint32_t tS, uint64_t* s_free, const float* neg, uint64_t c2
     return a0 + a1;
 }
 
+// The packed rows of a sequence that see a key: [lo, hi), relative to query block b's first and kept near it.
+struct KwRange {
+    int lo, hi;
+};
+FQ_DEV KwRange kw_range(const AttnMask& m, const AttnSeq& sq, int key, int b, int shift) {
+    constexpr int64_t FAR = 1 << 30;
+    const int64_t p0 = (int64_t)b * KW_BLOCK;
+    int64_t end = sq.q_len;
+    if (key >= m.sinks) end = min(end, (int64_t)key + m.window - sq.off + 1);
+    if (key >= sq.k_len) end = 0;
+    const int64_t lo = (max((int64_t)0, (int64_t)key - sq.off + 1) << shift) - p0, hi = (max((int64_t)0, end) << shift) - p0;
+    return KwRange{(int)max(-FAR, min(FAR, lo)), (int)max(-FAR, min(FAR, hi))};
+}
+
 template <class Args>
-FQ_DEV void kw_sum(const Args& a, KwShared* sh, int units, uint32_t tm, int g, int row, int lane) {
-    constexpr float LOG2E = 1.4426950408889634f;
-    const int shift = a.g_shift, G = 1 << shift;
-    const uint32_t tS = tm + 256 * g + ((uint32_t)(row >> 5) << 21);
+FQ_DEV void kw_sum(const Args& a, KwShared* sh, const uint8_t* stay, int units, uint32_t tm, int wg, int row, int lane) {
+    const int x = wg & 1, y = wg >> 1, shift = a.g_shift;
+    const uint32_t lanes = (uint32_t)(row >> 5) << 21, tS = tm + KW_S + KW_BLOCK * wg + lanes;
     const uint64_t c2 = pair(a.c, a.c);
-    uint32_t tile = 0, blk = 0;   // score tiles; buffers of statistics filled
+    uint32_t tile = 0, blk = 0, halves = 0;   // score tiles; query blocks of this y; units whose halves were added
+    uint32_t un = 0, moved = 0;               // units with tiles; key tiles moved
     bool ok = true;
     for (int it = 0, w; (w = kw_unit_at(it)) < units && ok; ++it) {
         const KwUnit u = kw_unit(a, w);
@@ -284,69 +380,103 @@ FQ_DEV void kw_sum(const Args& a, KwShared* sh, int units, uint32_t tm, int g, i
             kw.after[u.head * kw.after_stride + r] = sum;
         };
         if (u.kind == KW_NONE) {
-            for (int64_t key = (int64_t)u.j0 * TILE_ROWS + TILE_ROWS * g + row; key < min((int64_t)sq.k_len, (int64_t)u.j1 * TILE_ROWS); key += 2 * TILE_ROWS)
+            for (int64_t key = (int64_t)u.j0 * TILE_ROWS + TILE_ROWS * wg + row; key < min((int64_t)sq.k_len, (int64_t)u.j1 * TILE_ROWS); key += 4 * TILE_ROWS)
                 finish((int)key, 0.f);
             continue;
         }
-        const bool rows_stay = u.kind == KW_ROWS;
-        if (!rows_stay && g >= u.stay) continue;
-        // -lse log2(e) of this thread's column of query block b (beyond the sequence: a weight of 0)
-        auto statistic = [&](int b) {
-            const int p = b * TILE_ROWS + row, tok = p >> shift;
-            return tok < sq.q_len ? -LOG2E * __ldg(a.lse + (int64_t)(sq.q_row0 + tok) * a.Hq + (u.head << shift) + (p & (G - 1))) : -INFINITY;
-        };
-        // The next buffer of statistics.  What it held two buffers ago is no longer read: every warp has come to the one
-        // between, and comes there only when it is through with it.
-        auto bring = [&](float x, bool write) {
-            const int b = blk & 1;
-            if (write) sh->neg[g][b][row] = x;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->neg_full[g][b]);
-            ok = kw_wait_warp(&sh->neg_full[g][b], (blk >> 1) & 1, sh);
+        // the statistics of the next query block of this y
+        auto bring = [&]() {
+            ok = kw_wait_warp(&sh->neg_full[y][blk & 1], (blk >> 1) & 1, sh);
             ++blk;
         };
-        float next = statistic(u.b0);
-        const uint32_t blk0 = blk & 1;
-        if (rows_stay) {
-            const float x1 = u.stay > 1 ? statistic(u.b0 + 1) : 0.f;
-            bring(next, true);
-            if (ok) bring(x1, true);
-        }
-        Total total;
-        for (int i = rows_stay ? g : 0; i < u.pass && ok; i += rows_stay ? 2 : 1) {
-            const int key = (u.j0 + (rows_stay ? i : g)) * TILE_ROWS + row;
-            float both = 0.f;
-            for (int x = 0; x < (rows_stay ? u.stay : 1); ++x) {
-                const int b = u.b0 + (rows_stay ? x : i);
-                const float* neg = sh->neg[g][rows_stay ? blk0 ^ x : blk & 1];
-                if (!rows_stay) {
-                    bring(next, true);
-                    if (!ok) break;
-                    if (i + 1 < u.pass) next = statistic(b + 1);
-                }
-                const int columns = kw_columns(a, u, b), buf = tile & 1;
-                // packed rows of the block that see the key: those of tokens [first, end)
-                const int t0 = b * TILE_ROWS >> shift;
-                const int64_t first = (int64_t)key - sq.off + 1 - t0;
-                int64_t end = sq.q_len - t0;
-                if (key >= a.mask.sinks) end = min(end, (int64_t)key + a.mask.window - sq.off + 1 - t0);
-                const int lo = (int)max((int64_t)0, min((int64_t)TILE_ROWS, first)) << shift;
-                const int hi = key < sq.k_len ? (int)max((int64_t)0, min((int64_t)TILE_ROWS, end)) << shift : 0;
-                if (!(ok = kw_wait_warp(&sh->s_full[g][buf], (tile >> 1) & 1, sh))) break;
-                ++tile;
-                tc_fence_after();
-                both += __any_sync(0xFFFFFFFFu, lo > 0 || hi < columns)
-                            ? kw_row<true>(tS + 128 * buf, &sh->s_free[g][buf], neg, c2, columns, lo, hi, lane)
-                            : kw_row<false>(tS + 128 * buf, &sh->s_free[g][buf], neg, c2, columns, lo, hi, lane);
+        auto leave = [&](int s) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->neg_empty[y][s]);
+        };
+        auto score_tile = [&](int s, int columns, int lo, int hi, uint64_t* s_free) -> float {
+            if (!(ok = kw_wait_warp(&sh->s_full[wg], tile & 1, sh))) return 0.f;
+            ++tile;
+            tc_fence_after();
+            const float* neg = sh->neg[y][s];
+            return __any_sync(0xFFFFFFFFu, lo > 0 || hi < columns) ? kw_row<true>(tS, s_free, neg, c2, columns, lo, hi, lane)
+                                                                 : kw_row<false>(tS, s_free, neg, c2, columns, lo, hi, lane);
+        };
+        if (u.kind == KW_ROWS) {
+            ++un;
+            const uint32_t first = blk & 1;
+            for (int z = 0; z < u.stay && ok; ++z) bring();
+            for (int i = wg; i < u.pass && ok; i += 4) {
+                const int key = (u.j0 + i) * TILE_ROWS + row;
+                const KwRange r = kw_range(a.mask, sq, key, u.b0, shift);
+                float sum = 0.f;
+                for (int z = 0; z < u.stay && ok; ++z)
+                    sum += score_tile(first ^ z, kw_columns(a, u, u.b0 + z), r.lo - KW_BLOCK * z, r.hi - KW_BLOCK * z, &sh->s_free[wg]);
+                if (ok) finish(key, sum);
             }
             if (!ok) break;
-            if (rows_stay) finish(key, both);
-            else total.add(both);
+            for (int z = 0; z < u.stay; ++z) leave(first ^ z);
+            continue;
+        }
+        const int key = (u.j0 + x) * TILE_ROWS + row;
+        const bool idle = x >= u.stay;
+        const int set = un & 1, set_ph = un >> 1 & 1;
+        ++un;
+        if (y == 0 && !idle) {
+            // The key tile to tensor memory, a row per thread.  (What held this place has been multiplied: this warpgroup had
+            // all sums of the unit before.)
+            if (!(ok = kw_wait_warp(&sh->k_go[x], moved++ & 1, sh) && kw_wait_warp(&sh->st_full[set], set_ph, sh))) break;
+            const uint8_t* k_sm = stay + (2 * set + x) * KW_TILE_BYTES;
+#pragma unroll 1
+            for (int h = 0; h < 4; ++h) {   // 32 dims
+                uint32_t v[16];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 t = *reinterpret_cast<const uint4*>(k_sm + (h >> 1) * KW_PANEL + sw128_offset(row, 4 * (h & 1) + j));
+                    v[4 * j] = t.x;
+                    v[4 * j + 1] = t.y;
+                    v[4 * j + 2] = t.z;
+                    v[4 * j + 3] = t.w;
+                }
+                tmem_st16(tm + KW_K + 64 * x + 16 * h + lanes, v);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->k_ready[x]);
+        }
+        KwRange r = kw_range(a.mask, sq, key, u.b0 + y, shift);
+        Total total;
+        for (int b = u.b0 + y; b < u.b1 && ok; b += 2, r.lo -= 2 * KW_BLOCK, r.hi -= 2 * KW_BLOCK) {
+            const int s = blk & 1;
+            bring();
+            if (!ok) break;
+            // (the last S buffer of y = 1 takes its sums first)
+            if (!idle) total.add(score_tile(s, KW_BLOCK, r.lo, r.hi, y && b + 2 >= u.b1 ? nullptr : &sh->s_free[wg]));
+            leave(s);
         }
         if (!ok) break;
-        if (rows_stay) bring(0.f, false);   // (both buffers were in use: the next one waits for all warps)
-        else if (u.slot < 0) finish((u.j0 + g) * TILE_ROWS + row, total.sum);
-        else a.part[((int64_t)u.slot * a.Hkv + u.head) * (KW_KEY_TILES * TILE_ROWS) + g * TILE_ROWS + row] = total.sum;
+        if (idle) continue;
+        if (u.b0 + 1 < u.b1) {   // both have sums
+            if (y) {
+                tmem_st1(tS, total.sum);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->half_full[x]);
+                continue;
+            }
+            if (!(ok = kw_wait_warp(&sh->half_full[x], halves++ & 1, sh))) break;
+            tc_fence_after();
+            float other = tmem_ld1(tm + KW_S + KW_BLOCK * (x + 2) + lanes);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->s_free[x + 2]);
+            total.add(other);
+        } else if (y) {
+            continue;
+        }
+        if (u.slot < 0) finish(key, total.sum);
+        else a.part[((int64_t)u.slot * a.Hkv + u.head) * (KW_KEY_TILES * TILE_ROWS) + x * TILE_ROWS + row] = total.sum;
     }
 }
 
@@ -359,15 +489,19 @@ __global__ void __launch_bounds__(KW_THREADS, 1) key_weights_kernel(const __grid
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int units = a.n_entries * a.Hkv;
     pdl_trigger();
-    if (warp == 8) {
+    if (warp == 16) {
         if (lane == 0) {
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&sh->st_full[i], 1);
                 mbar_init(&sh->st_empty[i], 1);
+                mbar_init(&sh->half_full[i], 4);
+                mbar_init(&sh->k_go[i], 1);
+                mbar_init(&sh->k_ready[i], 4);
                 for (int b = 0; b < 2; ++b) {
-                    mbar_init(&sh->s_full[i][b], 1);
-                    mbar_init(&sh->s_free[i][b], 4);
-                    mbar_init(&sh->neg_full[i][b], 4);
+                    mbar_init(&sh->neg_full[i][b], 1);
+                    mbar_init(&sh->neg_empty[i][b], 8);
+                    mbar_init(&sh->s_full[2 * i + b], 1);
+                    mbar_init(&sh->s_free[2 * i + b], 4);
                 }
             }
             for (int s = 0; s < KW_RING; ++s) {
@@ -379,7 +513,7 @@ __global__ void __launch_bounds__(KW_THREADS, 1) key_weights_kernel(const __grid
             mbar_fence_init();
         }
         __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         tmem_alloc(&sh->tmem, 512);
         tmem_relinquish();
     }
@@ -387,14 +521,16 @@ __global__ void __launch_bounds__(KW_THREADS, 1) key_weights_kernel(const __grid
     tc_fence_after();
     const uint32_t tm = sh->tmem;
     if (wait_limit(sh) != 0) {   // (not with a misaligned base)
-        if (warp < 8) kw_sum(a, sh, units, tm, warp >> 2, tid & 127, lane);
-        else if (warp == 8) kw_load(a, sh, stay, ring, units);
-        else kw_products(a, sh, stay, ring, units, tm);
+        if (warp < 16) kw_sum(a, sh, stay, units, tm, warp >> 2, tid & 127, lane);
+        else if (warp == 16) kw_load(a, sh, stay, ring, units);
+        else if (warp == 18) kw_statistics(a, sh, units, lane);
+        else if (elect_one()) kw_products(a, sh, stay, ring, units, tm);
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 9) tmem_dealloc(tm, 512);
+    if (warp == 17) tmem_dealloc(tm, 512);
     if (tid == 0 && wait_limit(sh) == 0) atomicAdd(a.waits.record, 1u);
 }
 
