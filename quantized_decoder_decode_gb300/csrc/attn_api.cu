@@ -27,7 +27,7 @@ void plan_shared(Plan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G, uint32
             tails = true;
         }
     const bool partial = all.k_len && tails;   // both: joined
-    choose(units, seq, (int)G, (int)Hkv, partial, (float)all.k_len * Hkv * (HEAD_DIM * 4e-6f));
+    choose(p.even, units, seq, (int)G, (int)Hkv, partial, (float)all.k_len * Hkv * (HEAD_DIM * 4e-6f));
     emit(p, units, partial);
     plan_groups(p, Hkv, partial);
     // where the partial results of each sequence are

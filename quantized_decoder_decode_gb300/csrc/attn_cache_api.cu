@@ -203,6 +203,7 @@ fq_status run_window(Call& c, bool paged, const void* q, uint64_t q_stride, uint
                      size_t workspace_bytes, void* stream) {
     try {
         Plan p;
+        p.even = true;
         plan_prompt(p, (uint32_t)c.n_seq, c.seq, Hq / Hkv, Hkv, c.mask);
         TRY(attn_common(q, q_stride, Hq, Hkv, scale, out, out_stride, out_dtype, q_rows, *std::max_element(k_len, k_len + c.n_seq),
                         workspace, workspace_bytes, p.bytes(Hkv), c.io));
@@ -418,6 +419,7 @@ fq_status fq_attn_window_workspace(uint32_t n_seq, const uint32_t* q_len, const 
     TRY(prompt_sequences(n_seq, q_len, nullptr, k_len, nullptr, 0, num_key_value_heads, seq, nullptr, &q_rows));
     try {
         Plan p;
+        p.even = true;
         plan_prompt(p, n_seq, seq, num_attention_heads / num_key_value_heads, num_key_value_heads, mask_of(window, sinks));
         *bytes = p.bytes(num_key_value_heads);
     } catch (const std::bad_alloc&) {
@@ -536,9 +538,12 @@ fq_status fq_attn_key_weights(const void* q, uint64_t q_stride, const float* lse
         uint32_t *waits, *bad;
         TRY(prepare_device(&waits, &bad));
         cudaStream_t s = (cudaStream_t)stream;
+        const size_t n_units = p.units.size();
         auto run = n_views > 1 ? run_key_weights_t<KwArgsN>
-                               : p.units.size() <= KwArgs1S::ENTRIES ? run_key_weights_t<KwArgs1S> : run_key_weights_t<KwArgs1>;
+                               : n_units <= KwArgs1S::ENTRIES ? run_key_weights_t<KwArgs1S>
+                                                              : n_units <= KwArgs1M::ENTRIES ? run_key_weights_t<KwArgs1M> : run_key_weights_t<KwArgs1>;
         TRY(run(p, io, lse, mask, waits, (float*)workspace, seq, (int)n_seq, (int)q_rows, use, w, (int)n_views, s));
+        if (p.join.empty()) return FQ_OK;
         KwJoinArgs j;
         j.part = (const float*)workspace;
         j.Hkv = (int)Hkv;

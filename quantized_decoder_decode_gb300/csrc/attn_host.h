@@ -184,6 +184,7 @@ struct Plan {
     std::vector<JoinEntry> join;
     int64_t a_slots = 0, b_slots = 0;   // partial blocks of 128 and of 8 rows
     int items = 0;                      // chunks of the groups
+    bool even = false;                  // long sequences beside many short ones are cut as well (see choose and plan_groups)
 
     size_t a_bytes(uint32_t Hkv) const { return (size_t)a_slots * Hkv * TILE_ROWS * HEAD_DIM * 4; }
     size_t b_bytes(uint32_t Hkv) const { return (size_t)b_slots * Hkv * SMALL_ROWS * HEAD_DIM * 4; }
@@ -268,7 +269,8 @@ float estimate(const std::vector<Unit>& units, int cap, int G, int Hkv, bool par
 // alone; a long sequence beside many short ones loses by it (200 rows behind 30000, 32 / 8: beside 40 prompts of
 // 20 tokens, split, 100 us; beside 60, whole, 315; floor 51).
 // kv_mb: keys and values read from memory, which bounds what splitting can give.
-void choose(std::vector<Unit>& units, const AttnSeq* seq, int G, int Hkv, bool partial, float kv_mb, const AttnMask& m = AttnMask()) {
+//   ... which is why `even` cuts units that are longer than twice an SM's share into pieces of that share.
+void choose(bool even, std::vector<Unit>& units, const AttnSeq* seq, int G, int Hkv, bool partial, float kv_mb, const AttnMask& m = AttnMask()) {
     if (units.empty()) return;
     int longest = 1;
     for (const Unit& u : units) longest = std::max(longest, u.nt);
@@ -293,6 +295,11 @@ void choose(std::vector<Unit>& units, const AttnSeq* seq, int G, int Hkv, bool p
                 }
             }
         if (singles) units.swap(other);
+    } else if (even) {
+        int64_t all = 0;
+        for (const Unit& u : units) all += (int64_t)u.nt * Hkv;
+        const int share = (int)std::max<int64_t>(MIN_SPLIT, all / ATTN_SMS);
+        if (longest > 2 * share) cap = share;
     }
     for (Unit& u : units) u.splits = std::max(1, ceil_div(u.nt, cap));
 }
@@ -336,6 +343,9 @@ void plan_groups(Plan& p, uint32_t Hkv, bool partial) {
     }
     int64_t per = std::max(ROWS_CHUNK, (keys * Hkv + ROWS_CTAS - 1) / ROWS_CTAS / 64 * 64);
     while (per < longest && ctas(per) > ROWS_CTAS) per += std::max<int64_t>(64, per / 32 / 64 * 64);
+    // one wave of very uneven chunks: a second wave of short ones costs less (rounded up, the chunks are at most MAX_ITEMS)
+    const int64_t share = std::max(ROWS_CHUNK, (keys * Hkv + ROWS_CTAS - 1) / ROWS_CTAS + 63) / 64 * 64;
+    if (p.even && per > 2 * share) per = share;
     for (auto& g : p.groups) {
         const int splits = std::max(1, ceil_div(g.keys, per));
         g.chunk = std::max(64, ceil_div(ceil_div(g.keys, splits), 64) * 64);
@@ -380,7 +390,7 @@ void plan_prompt(Plan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G, uint32
         const RowGroup& r = p.groups[g];
         if (r.slot0 >= 0) p.join.push_back(JoinEntry{r.q_row0, r.n_tok, r.k_len, r.off, 0, 0, 0, 0, r.slot0, chunks(p, g), 0, 0, 0});
     }
-    choose(units, seq, (int)G, (int)Hkv, false, kv_mb, m);
+    choose(p.even, units, seq, (int)G, (int)Hkv, false, kv_mb, m);
     emit(p, units, false);
     for (const Unit& u : units) {
         if (u.slot < 0) continue;

@@ -301,7 +301,9 @@ __global__ void __launch_bounds__(AR_THREADS, ROWS_CTAS_SM) attn_rows_kernel(con
             else reinterpret_cast<uint2*>((uint16_t*)a.io.out + at)[lane] = make_uint2(bf16x2(y.x, y.y), bf16x2(y.z, y.w));
         }
     }
-    pdl_wait();   // this grid ends after the one it may run beside, so what waits for it waits for both
+    // This grid ends after the one it may run beside, so that what waits for it waits for both.  One CTA sees to that: the others
+    // make room for those that have not started.
+    if (blockIdx.x == gridDim.x - 1) pdl_wait();
 }
 
 }  // namespace

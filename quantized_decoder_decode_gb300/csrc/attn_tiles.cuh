@@ -248,36 +248,54 @@ FQ_DEV void set_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :
 template <int N>
 FQ_DEV void set_regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// The page table's entries of the unit's tile number t, one per lane.  Pages that no row sees into (their entries are not
-// read: a program may have given them away), and entries that name no page, get the page behind the last, which
-// reads as zeros.
+// The page table's entries of a unit's tiles, 32 at a time (one per lane) and the next 32 on their way: a tile waits for its
+// entries only at a unit's start.  Small pages cost copies, two for each page of a tile: 333 tokens behind 1000, 16 / 8 heads, 16.8
+// us from a view, 18.2 from pages of 128 rows, 19.6 of 32, 22.7 of 16 (a lane for each copy: no faster).  Pages that no row sees into (their entries are not read: a program may have given them away), and entries
+// that name no page, get the page behind the last, which reads as zeros.
 template <class Args>
-FQ_DEV int tile_pages(const Args& a, const Unit& u, int t, int lane) {
-    const KvPages& p = a.pages;
-    const int per = p.shift < 7 ? TILE_ROWS >> p.shift : 1;   // pages of a tile
-    const int i = (u.kt.at(u.j0 + t) * TILE_ROWS >> p.shift) + lane, k0 = i << p.shift;   // page of the sequence, its first key
-    if (t >= u.nt || lane >= per || k0 >= u.end || (k0 + (1 << p.shift) <= u.lo0 && k0 >= a.mask.sinks)) return p.n_pages;
-    const int32_t id = __ldg(p.table + (int64_t)u.seq * p.table_stride + i);
-    if ((uint32_t)id < (uint32_t)p.n_pages) return id;
-    atomicAdd(p.bad, 1u);
-    return p.n_pages;
-}
-// A K or V tile from its pages, by a warp.
-FQ_DEV void load_pages(const void* map, const KvPages& p, uint8_t* dst, int j, int ids, int head, uint64_t* bar, bool issue) {
-    const bool lead = elect_one() && issue;
-    if (lead) mbar_arrive_expect_tx(bar, AT_TILE_BYTES);
-    __syncwarp();
-    const int rows = min(TILE_ROWS, 1 << p.shift), row = p.shift > 7 ? j * TILE_ROWS & ((1 << p.shift) - 1) : 0;
-#pragma unroll 1
-    for (int b = 0; b * rows < TILE_ROWS; ++b) {
-        const int id = __shfl_sync(0xFFFFFFFFu, ids, b);
-        if (lead) {
-            tma_load_4d(dst + b * rows * 128, map, 0, row, head, id, bar);
-            tma_load_4d(dst + AT_PANEL + b * rows * 128, map, 64, row, head, id, bar);
-        }
+struct PageIds {
+    int ids, next, base;   // pages number base + lane, base + 32 + lane of the unit
+    static FQ_DEV int fetch(const Args& a, const Unit& u, int n) {
+        const KvPages& p = a.pages;
+        const int lp = p.shift < 7 ? 7 - p.shift : 0;   // log2 of a tile's pages
+        const int t = n >> lp;
+        if (t >= u.nt) return p.n_pages;
+        const int i = (u.kt.at(u.j0 + t) * TILE_ROWS >> p.shift) + (n & ((1 << lp) - 1)), k0 = i << p.shift;   // page of the sequence, its first key
+        if (k0 >= u.end || (k0 + (1 << p.shift) <= u.lo0 && k0 >= a.mask.sinks)) return p.n_pages;
+        const int32_t id = __ldg(p.table + (int64_t)u.seq * p.table_stride + i);
+        if ((uint32_t)id < (uint32_t)p.n_pages) return id;
+        atomicAdd(p.bad, 1u);
+        return p.n_pages;
     }
-    __syncwarp();
-}
+    FQ_DEV void start(const Args& a, const Unit& u, int lane) {
+        base = 0;
+        ids = fetch(a, u, lane);
+        next = fetch(a, u, 32 + lane);
+    }
+    // Tile number t of the unit (not before those of earlier calls) from its pages, by a warp.
+    FQ_DEV void load(const Args& a, const Unit& u, const void* map, uint8_t* dst, int t, uint64_t* bar, bool issue, int lane) {
+        const KvPages& p = a.pages;
+        const bool lead = elect_one() && issue;
+        if (lead) mbar_arrive_expect_tx(bar, AT_TILE_BYTES);
+        __syncwarp();
+        const int lp = p.shift < 7 ? 7 - p.shift : 0, first = t << lp;
+        if (first >= base + 32) {
+            ids = next;
+            base += 32;
+            next = fetch(a, u, base + 32 + lane);
+        }
+        const int rows = TILE_ROWS >> lp, row = p.shift > 7 ? u.kt.at(u.j0 + t) * TILE_ROWS & ((1 << p.shift) - 1) : 0;
+#pragma unroll 1
+        for (int b = 0; b < 1 << lp; ++b) {
+            const int id = __shfl_sync(0xFFFFFFFFu, ids, first - base + b);
+            if (lead) {
+                tma_load_4d(dst + b * rows * 128, map, 0, row, u.head, id, bar);
+                tma_load_4d(dst + AT_PANEL + b * rows * 128, map, 64, row, u.head, id, bar);
+            }
+        }
+        __syncwarp();
+    }
+};
 
 // No copy may still be landing when the CTA exits.  A role gave up after a quarter second of waiting;
 // copies that were issued land within microseconds of that.
@@ -303,8 +321,8 @@ FQ_DEV void load_keys(const Args& a, AtShared* sh, uint8_t* q_sm, uint8_t* ring,
         const bool pre = preloaded && it == 0;
         const int vw = Args::VIEWS == 1 ? 0 : sq.view;
         const int row0 = sq.k_row0 + u.j0 * TILE_ROWS;
-        int ids = 0;   // pages of the tile to come
-        if constexpr (Args::PAGED) ids = tile_pages(a, u, pre ? 1 : 0, lane);
+        [[maybe_unused]] PageIds<Args> pages;
+        if constexpr (Args::PAGED) pages.start(a, u, lane);
         for (int t = pre ? 1 : 0; t <= u.nt && ok; ++t) {
             if (t == min(2, u.nt)) {
 #pragma unroll 1
@@ -326,10 +344,7 @@ FQ_DEV void load_keys(const Args& a, AtShared* sh, uint8_t* q_sm, uint8_t* ring,
             if (!(ok = at_wait_warp(&sh->k_empty[s], ((n / AT_KS) & 1) ^ 1, sh))) break;
             ++n;
             if constexpr (Args::PAGED) {
-                const int now = ids;
-                ids = tile_pages(a, u, t + 1, lane);
-                load_pages(a.map_k[0], a.pages, ring + s * AT_TILE_BYTES, u.kt.at(u.j0 + t), now, u.head, &sh->k_full[s],
-                           !(a.waits.starve == 1 && it == 0 && t == 1));
+                pages.load(a, u, a.map_k[0], ring + s * AT_TILE_BYTES, t, &sh->k_full[s], !(a.waits.starve == 1 && it == 0 && t == 1), lane);
                 continue;
             }
             const int row = Args::WINDOW ? sq.k_row0 + u.kt.at(u.j0 + t) * TILE_ROWS : row0 + t * TILE_ROWS;
@@ -417,7 +432,8 @@ FQ_DEV void load_values(const Args& a, AtShared* sh, uint8_t* ring, int units, i
     uint32_t n = 0, raw_ph = 0;   // V tiles; phase bits of v_raw
     PartTile part[2];             // loaded and not checked yet: at most one per stage
     static_assert(AT_VS == 2, "two tiles to check at most");
-    int pending = 0, it = -1, t = 0, vw = 0, row0 = 0, seen = 0, k_len = 0, ids = 0;
+    int pending = 0, it = -1, t = 0, vw = 0, row0 = 0, seen = 0, k_len = 0;
+    [[maybe_unused]] PageIds<Args> pages;
     bool more = true, ok = true;
     Unit u;
     u.nt = 0;
@@ -434,7 +450,7 @@ FQ_DEV void load_values(const Args& a, AtShared* sh, uint8_t* ring, int units, i
             k_len = sq.k_len;
             seen = max(0, min(k_len, u.tok_a + sq.off));
             t = 0;
-            if constexpr (Args::PAGED) ids = tile_pages(a, u, 0, lane);
+            if constexpr (Args::PAGED) pages.start(a, u, lane);
         }
         const int s = n % AT_VS;
         const uint32_t parity = ((n / AT_VS) & 1) ^ 1;
@@ -454,10 +470,7 @@ FQ_DEV void load_values(const Args& a, AtShared* sh, uint8_t* ring, int units, i
         }
         uint64_t* full = whole ? &sh->v_full[s] : &sh->v_raw[s];
         if constexpr (Args::PAGED) {
-            const int now = ids;
-            ids = tile_pages(a, u, t + 1, lane);
-            load_pages(a.map_v[0], a.pages, ring + (AT_KS + s) * AT_TILE_BYTES, j, now, u.head, full,
-                       !(a.waits.starve == 2 && it == 0 && t == 1));
+            pages.load(a, u, a.map_v[0], ring + (AT_KS + s) * AT_TILE_BYTES, t, full, !(a.waits.starve == 2 && it == 0 && t == 1), lane);
         } else {
             if (elect_one() && !(a.waits.starve == 2 && it == 0 && t == 1))
                 load_kv(a.map_v[vw], ring + (AT_KS + s) * AT_TILE_BYTES, Args::WINDOW ? row0 + (j - u.j0) * TILE_ROWS : row0 + t * TILE_ROWS,
@@ -906,7 +919,12 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
         }
         __syncwarp();
         if constexpr (Args::PAGED)
-            if (pre) load_pages(a.map_k[0], a.pages, ring, u.kt.at(u.j0), tile_pages(a, u, 0, lane), u.head, &sh->k_full[0], true);
+            if (pre) {
+                PageIds<Args> pages;
+                pages.base = 0;
+                pages.ids = PageIds<Args>::fetch(a, u, lane);
+                pages.load(a, u, a.map_k[0], ring, 0, &sh->k_full[0], true, lane);
+            }
         preloaded = pre;
         __syncwarp();
     } else if (warp == 8) {

@@ -47,6 +47,7 @@ struct KwArgs {
     KwEntry e[NE];
 };
 using KwArgs1S = KwArgs<1, 64>;
+using KwArgs1M = KwArgs<1, 256>;
 using KwArgs1 = KwArgs<1, 1152>;
 using KwArgsN = KwArgs<MAX_SEQ, 768>;
 static_assert(sizeof(KwArgs1) <= 32764 && sizeof(KwArgsN) <= 32764, "kernel parameters");

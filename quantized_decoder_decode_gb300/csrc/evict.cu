@@ -21,7 +21,7 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int EV_THREADS = 512, EV_PER = 8, EV_CHUNK = EV_THREADS * EV_PER;   // rows that a block holds at a time
+constexpr int EV_THREADS = 1024, EV_PER = 8, EV_CHUNK = EV_THREADS * EV_PER;   // rows that a block holds at a time
 constexpr int EV_BINS = 2048, EV_PASSES = 3, EV_CLUSTER = 8;
 constexpr int EV_MOVE_WARPS = 4, EV_MOVE_ROWS = EVICT_ROWS / EV_MOVE_WARPS;   // rows of a warp
 
@@ -39,18 +39,19 @@ FQ_DEV uint32_t block_scan(uint32_t v, uint32_t* sums, uint32_t& total) {
         const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
         if (lane >= o) x += y;
     }
+    static_assert(EV_THREADS / 32 == 32, "a lane per warp");
     __syncthreads();
     if (lane == 31) sums[warp] = x;
     __syncthreads();
-    uint32_t before = 0;
-    total = 0;
+    uint32_t w = sums[lane];
 #pragma unroll
-    for (int i = 0; i < EV_THREADS / 32; ++i) {
-        const uint32_t s = sums[i];
-        if (i < warp) before += s;
-        total += s;
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, w, o);
+        if (lane >= o) w += y;
     }
-    return before + x - v;
+    total = __shfl_sync(0xFFFFFFFFu, w, 31);
+    const uint32_t before = __shfl_sync(0xFFFFFFFFu, w, (warp + 31) & 31);
+    return (warp ? before : 0) + x - v;
 }
 
 __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const __grid_constant__ EvictArgs a) {
@@ -90,6 +91,10 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const __grid_c
             key[i] = r >= lo && r < hi && r < r1 ? order_key(__ldg(w + r)) : 0u;
         }
     };
+    auto meet = [&]() {
+        if (C > 1) cluster.sync();
+        else __syncthreads();
+    };
     uint32_t top = 0;   // the digits found so far
     int shift = 32;
 #pragma unroll 1
@@ -106,27 +111,25 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const __grid_c
                     atomicAdd(&hist[p][key[i] >> shift & ((1u << bits) - 1)], 1u);
             }
         }
-        cluster.sync();
-        // bins from the top: thread t has the four below EV_BINS - 4 t
-        const int b0 = EV_BINS - 4 - 4 * tid;
-        uint32_t n[4] = {0, 0, 0, 0};
+        meet();
+        // bins from the top: thread t has the two below EV_BINS - 2 t
+        static_assert(EV_BINS == 2 * EV_THREADS, "two bins per thread");
+        const int b0 = EV_BINS - 2 - 2 * tid;
+        uint2 n = make_uint2(0, 0);
+        if (C == 1) n = *reinterpret_cast<const uint2*>(&hist[p][b0]);
+        else
 #pragma unroll 1
-        for (int c = 0; c < C; ++c) {
-            const uint4 h = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(&hist[p][0], c) + b0);
-            n[3] += h.x;
-            n[2] += h.y;
-            n[1] += h.z;
-            n[0] += h.w;
-        }
-        uint32_t total;
-        uint32_t over = block_scan(n[0] + n[1] + n[2] + n[3], sums, total);   // in the bins above these
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (over < want && want <= over + n[i]) {
-                found[0] = (uint32_t)(b0 + 3 - i);
-                found[1] = want - over;
+            for (int c = 0; c < C; ++c) {
+                const uint2 h = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&hist[p][0], c) + b0);
+                n.x += h.x;
+                n.y += h.y;
             }
-            over += n[i];
+        uint32_t total;
+        const uint32_t over = block_scan(n.x + n.y, sums, total);   // in the bins above these
+        if (over < want && want <= over + n.x + n.y) {
+            const bool upper = want <= over + n.y;
+            found[0] = (uint32_t)(b0 + upper);
+            found[1] = want - over - (upper ? 0 : n.y);
         }
         __syncthreads();
         if (want) {
@@ -147,20 +150,26 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const __grid_c
             else if (any && key[i] == top) equal |= 1u << i;
         }
     };
-    uint32_t n_sure = 0, n_equal = 0;
-#pragma unroll 1
-    for (int64_t base = r0; base < r1; base += EV_CHUNK) {
-        uint32_t sure, equal, total;
+    uint32_t sure = 0, equal = 0, before = 0, total = 0;   // of a chunk
+    auto count = [&](int64_t base) {
         classes(base, sure, equal);
-        block_scan((uint32_t)__popc(sure) << 16 | (uint32_t)__popc(equal), sums, total);
-        n_sure += total >> 16;
-        n_equal += total & 0xFFFFu;
+        before = block_scan((uint32_t)__popc(sure) << 16 | (uint32_t)__popc(equal), sums, total);
+    };
+    const bool once = r1 - r0 <= EV_CHUNK;   // one chunk is counted once
+    if (C > 1) {
+        uint32_t n_sure = 0, n_equal = 0;
+#pragma unroll 1
+        for (int64_t base = r0; base < r1; base += EV_CHUNK) {
+            count(base);
+            n_sure += total >> 16;
+            n_equal += total & 0xFFFFu;
+        }
+        if (tid == 0) {
+            counts[0] = n_sure;
+            counts[1] = n_equal;
+        }
+        cluster.sync();
     }
-    if (tid == 0) {
-        counts[0] = n_sure;
-        counts[1] = n_equal;
-    }
-    cluster.sync();
     uint32_t equal_before = 0, place = 0;
 #pragma unroll 1
     for (int c = 0; c < rank; ++c) {
@@ -171,9 +180,7 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const __grid_c
     place += min(equal_before, want);
 #pragma unroll 1
     for (int64_t base = r0; base < r1; base += EV_CHUNK) {
-        uint32_t sure, equal, total;
-        classes(base, sure, equal);
-        const uint32_t before = block_scan((uint32_t)__popc(sure) << 16 | (uint32_t)__popc(equal), sums, total);
+        if (C == 1 || !once) count(base);
         uint32_t eq = equal_before + (before & 0xFFFFu);
         uint32_t at = place + (before >> 16) + (min(eq, want) - min(equal_before, want));
 #pragma unroll
@@ -185,7 +192,7 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const __grid_c
         place += (total >> 16) + (min(equal_before + (total & 0xFFFFu), want) - min(equal_before, want));
         equal_before += total & 0xFFFFu;
     }
-    cluster.sync();   // the others have read this block's counts
+    if (C > 1) cluster.sync();   // the others have read this block's counts
 }
 
 __global__ void __launch_bounds__(EV_MOVE_WARPS * 32) evict_move_kernel(const __grid_constant__ EvictArgs a) {

@@ -551,10 +551,15 @@ __global__ void __launch_bounds__(KW_KEY_TILES* TILE_ROWS) key_weights_join_kern
 
 }  // namespace
 
+template <class Args>
+static cudaError_t prepare() {
+    return cudaFuncSetAttribute(key_weights_kernel<Args>, cudaFuncAttributeMaxDynamicSharedMemorySize, KW_SMEM);
+}
 cudaError_t key_weights_prepare() {
-    cudaError_t e = cudaFuncSetAttribute(key_weights_kernel<KwArgs1S>, cudaFuncAttributeMaxDynamicSharedMemorySize, KW_SMEM);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(key_weights_kernel<KwArgs1>, cudaFuncAttributeMaxDynamicSharedMemorySize, KW_SMEM);
-    return e != cudaSuccess ? e : cudaFuncSetAttribute(key_weights_kernel<KwArgsN>, cudaFuncAttributeMaxDynamicSharedMemorySize, KW_SMEM);
+    cudaError_t e = prepare<KwArgs1S>();
+    if (e == cudaSuccess) e = prepare<KwArgs1M>();
+    if (e == cudaSuccess) e = prepare<KwArgs1>();
+    return e != cudaSuccess ? e : prepare<KwArgsN>();
 }
 
 template <class Args>
@@ -564,6 +569,7 @@ void launch_key_weights(const Args& a, cudaStream_t s) {
     key_weights_kernel<Args><<<grid, KW_THREADS, KW_SMEM, s>>>(a);
 }
 template void launch_key_weights<KwArgs1S>(const KwArgs1S&, cudaStream_t);
+template void launch_key_weights<KwArgs1M>(const KwArgs1M&, cudaStream_t);
 template void launch_key_weights<KwArgs1>(const KwArgs1&, cudaStream_t);
 template void launch_key_weights<KwArgsN>(const KwArgsN&, cudaStream_t);
 
