@@ -56,10 +56,10 @@ fq_status check_pages(const fq_kv_pages* pages, const int32_t* table, uint64_t t
     uint64_t most = 0;
     for (uint32_t s = 0; s < n_seq; ++s) {
         most = std::max(most, rows[s]);
-        if (rows[s] > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 rows");
         if ((rows[s] + g.page_rows - 1) / g.page_rows > table_stride)
             return fail(FQ_ERR_KV_CACHE_OVERFLOW, "sequence %u: %llu rows need more than the table's %llu pages of %u", s,
                         (unsigned long long)rows[s], (unsigned long long)table_stride, g.page_rows);
+        if (rows[s] > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 rows");
     }
     p.n_pages = (int32_t)g.n_pages;
     p.table = table;
