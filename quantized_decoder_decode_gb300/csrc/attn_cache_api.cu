@@ -225,7 +225,7 @@ fq_status run_window(Call& c, bool paged, const void* q, uint64_t q_stride, uint
 // ---------------------------------------------------------------- gathered weights
 
 constexpr int KW_MAX_RUN = 4096;    // tiles of a unit, at most (no wait for a unit's end comes near its limit)
-constexpr int KW_MIN_BLOCKS = 8;    // query blocks of a unit that is cut, at least
+constexpr int KW_MIN_BLOCKS = 6;    // query blocks of a unit that is cut, at least (2048 tokens, 16 / 8 heads 20.1 us; 4: 22.0, 8: 21.6)
 
 struct KwPlan {
     std::vector<KwEntry> units;     // longest first
@@ -234,15 +234,17 @@ struct KwPlan {
     size_t bytes(uint32_t Hkv) const { return (size_t)slots * Hkv * KW_KEY_TILES * TILE_ROWS * 4; }
 };
 
-// Few query rows (two blocks of 96 packed ones) stay while the keys pass by; of more, the query blocks pass by keys that
-// stay, in units of about a quarter of an SM's share.
+// Up to 96 packed query rows (a block) stay while the keys pass by; of more, the query blocks pass by keys that stay.  20 tokens
+// over 16000 keys, 32 / 8 heads (80 rows): 12.9 us, 15.9 with keys that stay; 48 tokens (192 rows): 20.5 and 17.5.
+// Units of half an SM's share of the key tiles (16 single tokens over 512 to 4097 keys 12.7 us; a quarter 14.1, an eighth 16.4),
+// or of a third of its share of the query blocks (one prompt of 8192: 235 us; a half 249, a quarter 238, an eighth 244).
 void plan_key_weights(KwPlan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G, uint32_t Hkv, const AttnMask& m) {
     int64_t key_tiles_all = 0, blocks_all = 0;
     struct Pair {
         int seq, j0, j1, b0, b1;
     };
     struct Run {
-        int seq, j0, j1, blocks;
+        int seq, j0, j1;
     };
     std::vector<Pair> pairs;
     std::vector<Run> runs;
@@ -262,8 +264,8 @@ void plan_key_weights(KwPlan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G,
         const int ends[2][2] = {{0, t.sinks}, {t.first, all}};
         for (auto& e : ends) {
             if (e[0] >= e[1]) continue;
-            if (blocks <= 2) {
-                runs.push_back(Run{s, e[0], e[1], blocks});
+            if (blocks <= 1) {
+                runs.push_back(Run{s, e[0], e[1]});
                 key_tiles_all += e[1] - e[0];
                 continue;
             }
@@ -283,7 +285,7 @@ void plan_key_weights(KwPlan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G,
             }
         }
     }
-    const int per = (int)std::min<int64_t>(KW_MAX_RUN, std::max<int64_t>(KW_MIN_BLOCKS, blocks_all * Hkv / (4 * ATTN_SMS)));
+    const int per = (int)std::min<int64_t>(KW_MAX_RUN, std::max<int64_t>(KW_MIN_BLOCKS, blocks_all * Hkv / (3 * ATTN_SMS)));
     for (const Pair& x : pairs) {
         const int n = ceil_div(x.b1 - x.b0, per), blocks = x.b1 - x.b0;
         if (n > 1) p.join.push_back(KwJoin{x.seq, x.j0, x.j1, (int)p.slots, n});
@@ -291,15 +293,15 @@ void plan_key_weights(KwPlan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G,
             p.units.push_back(KwEntry{x.seq | KW_KEYS, x.j0, x.j1, x.b0 + (int)((int64_t)blocks * i / n),
                                       x.b0 + (int)((int64_t)blocks * (i + 1) / n), n > 1 ? (int)p.slots++ : -1});
     }
-    const int run = (int)std::min<int64_t>(KW_MAX_RUN, std::max<int64_t>(2, key_tiles_all * Hkv / (4 * ATTN_SMS)));
+    const int run = (int)std::min<int64_t>(KW_MAX_RUN, std::max<int64_t>(2, key_tiles_all * Hkv / (2 * ATTN_SMS)));
     for (const Run& x : runs) {
         const int n = ceil_div(x.j1 - x.j0, run), tiles = x.j1 - x.j0;
         for (int i = 0; i < n; ++i)
             p.units.push_back(KwEntry{x.seq | KW_ROWS, x.j0 + (int)((int64_t)tiles * i / n), x.j0 + (int)((int64_t)tiles * (i + 1) / n),
-                                      0, x.blocks, -1});
+                                      0, 1, -1});
     }
     auto cost = [](const KwEntry& e) {
-        return e.info & KW_NONE ? 0 : e.info & KW_ROWS ? (e.j1 - e.j0) * (e.b1 - e.b0) : (e.b1 - e.b0) * (e.j1 - e.j0);
+        return e.info & KW_NONE ? 0 : (e.b1 - e.b0) * (e.j1 - e.j0);
     };
     std::stable_sort(p.units.begin(), p.units.end(), [&](const KwEntry& a, const KwEntry& b) { return cost(a) > cost(b); });
 }

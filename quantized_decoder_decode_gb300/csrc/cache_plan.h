@@ -22,7 +22,7 @@ struct KwEntry {
     int32_t slot;         // partial sums of the unit's 256 keys, or -1: finished
 };
 constexpr int KW_KEYS = 0;           // up to two key tiles stay, query blocks [b0, b1) pass by
-constexpr int KW_ROWS = 1 << 7;      // up to two query blocks stay, key tiles [j0, j1) pass by
+constexpr int KW_ROWS = 1 << 7;      // the only query block stays, key tiles [j0, j1) pass by
 constexpr int KW_NONE = 2 << 7;      // keys that no row sees
 constexpr int KW_KEY_TILES = 2;      // .. that stay
 

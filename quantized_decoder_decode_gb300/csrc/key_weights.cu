@@ -9,8 +9,8 @@
 // as one tile does.
 //
 // A unit holds what is few and lets the rest pass by through a ring of 32 KB tiles (TMA):
-//   KW_KEYS  two key tiles stay (one for each of two pairs of warpgroups), query blocks of 128 packed rows pass by;
-//   KW_ROWS  up to two query blocks stay (single tokens, a few observed rows), key tiles pass by, to the two
+//   KW_KEYS  two key tiles stay (one for each of two pairs of warpgroups), query blocks of 96 packed rows pass by;
+//   KW_ROWS  the rows of a query block stay (single tokens, a few observed ones), key tiles pass by, to the four
 //            warpgroups in turn: K is read once, which is what bounds it.
 // What stays has two sets of buffers, so that the next unit's comes while this one is worked on.  Long ranges of query
 // blocks are cut into units of their own, whose partial sums (4 bytes a key) a second kernel adds up in order.
@@ -128,11 +128,10 @@ FQ_DEV void kw_load_q(const Args& a, const KwUnit& u, int b, uint8_t* dst, uint6
     tma_load_4d(dst + KW_Q_PANEL, a.map_q, 64, 0, u.head, row, bar);
 }
 
-// Columns of a product with query block b: packed rows, in steps of 32 where the block stays.
+// Columns of a product: a query block's rows, or (a block that stays) what there are of them, in steps of 32.
 template <class Args>
-FQ_DEV int kw_columns(const Args& a, const KwUnit& u, int b) {
-    if (u.kind == KW_KEYS) return KW_BLOCK;
-    return min(KW_BLOCK, ((a.seq[u.seq].q_len << a.g_shift) - b * KW_BLOCK + 31) & ~31);
+FQ_DEV int kw_columns(const Args& a, const KwUnit& u) {
+    return u.kind == KW_KEYS ? KW_BLOCK : ((a.seq[u.seq].q_len << a.g_shift) + 31) & ~31;
 }
 
 // ---------------- warp 16
@@ -177,14 +176,14 @@ FQ_DEV void kw_load(const Args& a, KwShared* sh, uint8_t* stay, uint8_t* ring, i
 // ---------------- warp 17, one thread of it.  A product takes the tensor cores 384 cycles, and this loop has no more for it: its waits are
 // tests of one thread, its addresses are counted on, and what depends on the kind of unit is decided outside it.
 template <bool ROWS>
-FQ_DEV bool kw_unit_products(KwShared* sh, const KwUnit& u, uint64_t d_stay, uint64_t d_ring, uint32_t tm, const uint32_t (&idesc)[2],
-                             uint32_t& slot, uint32_t& slot_ph, uint32_t& free_ph, int set) {
+FQ_DEV bool kw_unit_products(KwShared* sh, const KwUnit& u, uint64_t d_stay, uint64_t d_ring, uint32_t tm, uint32_t idesc, uint32_t& slot,
+                             uint32_t& slot_ph, uint32_t& free_ph) {
     uint64_t dr = d_ring + (uint32_t)(slot * (KW_TILE_BYTES >> 4));
 #pragma unroll 1
     for (int i = 0; i < u.pass; ++i) {
         if (!kw_wait(&sh->ring_full[slot], slot_ph, sh)) return false;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < (ROWS ? 1 : 2); ++x) {
             if (x >= u.stay) break;
             const int wg = ROWS ? i & 3 : x + 2 * (i & 1);
             if (!kw_wait(&sh->s_free[wg], (free_ph >> wg & 1) ^ 1, sh)) return false;
@@ -194,8 +193,8 @@ FQ_DEV bool kw_unit_products(KwShared* sh, const KwUnit& u, uint64_t d_stay, uin
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const uint32_t q_off = (k >> 2) * (KW_Q_PANEL >> 4) + (k & 3) * 2, k_off = (k >> 2) * (KW_PANEL >> 4) + (k & 3) * 2;
-                if (ROWS) mma_f16(d, dr + k_off, d_stay + (uint32_t)(x * (KW_TILE_BYTES >> 4)) + q_off, idesc[x], k > 0);
-                else mma_f16_ta(d, tm + KW_K + 64 * x + 8 * k, dr + q_off, idesc[0], k > 0);
+                if (ROWS) mma_f16(d, dr + k_off, d_stay + q_off, idesc, k > 0);
+                else mma_f16_ta(d, tm + KW_K + 64 * x + 8 * k, dr + q_off, idesc, k > 0);
             }
             mma_commit(&sh->s_full[wg]);
         }
@@ -207,7 +206,6 @@ FQ_DEV bool kw_unit_products(KwShared* sh, const KwUnit& u, uint64_t d_stay, uin
             dr = d_ring;
         }
     }
-    if (ROWS) mma_commit(&sh->st_empty[set]);
     return true;
 }
 
@@ -221,11 +219,10 @@ FQ_DEV void kw_products(const Args& a, KwShared* sh, uint8_t* stay, uint8_t* rin
         const int set = un & 1;
         if (!kw_wait(&sh->st_full[set], (un >> 1) & 1, sh)) break;
         ++un;
-        const uint32_t idesc[2] = {idesc_bf16_f32(TILE_ROWS, kw_columns(a, u, u.b0), false, false),
-                                   u.stay > 1 ? idesc_bf16_f32(TILE_ROWS, kw_columns(a, u, u.b0 + 1), false, false) : 0u};
-        const uint64_t d_set = d_stay + (uint32_t)(2 * set * (KW_TILE_BYTES >> 4));
+        const uint32_t idesc = idesc_bf16_f32(TILE_ROWS, kw_columns(a, u), false, false);
         if (u.kind == KW_ROWS) {
-            if (!kw_unit_products<true>(sh, u, d_set, d_ring, tm, idesc, slot, slot_ph, free_ph, set)) break;
+            if (!kw_unit_products<true>(sh, u, d_stay + (uint32_t)(2 * set * (KW_TILE_BYTES >> 4)), d_ring, tm, idesc, slot, slot_ph, free_ph)) break;
+            mma_commit(&sh->st_empty[set]);
             continue;
         }
         // the key tiles become operands in tensor memory
@@ -238,7 +235,7 @@ FQ_DEV void kw_products(const Args& a, KwShared* sh, uint8_t* stay, uint8_t* rin
         if (!ok) break;
         tc_fence_after();
         mbar_arrive(&sh->st_empty[set]);
-        if (!kw_unit_products<false>(sh, u, d_set, d_ring, tm, idesc, slot, slot_ph, free_ph, set)) break;
+        if (!kw_unit_products<false>(sh, u, 0, d_ring, tm, idesc, slot, slot_ph, free_ph)) break;
     }
 }
 
@@ -403,18 +400,16 @@ FQ_DEV void kw_sum(const Args& a, KwShared* sh, const uint8_t* stay, int units, 
         };
         if (u.kind == KW_ROWS) {
             ++un;
-            const uint32_t first = blk & 1;
-            for (int z = 0; z < u.stay && ok; ++z) bring();
+            const int s = blk & 1, columns = kw_columns(a, u);
+            bring();
             for (int i = wg; i < u.pass && ok; i += 4) {
                 const int key = (u.j0 + i) * TILE_ROWS + row;
-                const KwRange r = kw_range(a.mask, sq, key, u.b0, shift);
-                float sum = 0.f;
-                for (int z = 0; z < u.stay && ok; ++z)
-                    sum += score_tile(first ^ z, kw_columns(a, u, u.b0 + z), r.lo - KW_BLOCK * z, r.hi - KW_BLOCK * z, &sh->s_free[wg]);
+                const KwRange r = kw_range(a.mask, sq, key, 0, shift);
+                const float sum = score_tile(s, columns, r.lo, r.hi, &sh->s_free[wg]);
                 if (ok) finish(key, sum);
             }
             if (!ok) break;
-            for (int z = 0; z < u.stay; ++z) leave(first ^ z);
+            leave(s);
             continue;
         }
         const int key = (u.j0 + x) * TILE_ROWS + row;

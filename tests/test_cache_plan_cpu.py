@@ -279,7 +279,7 @@ def check_weights(host, q_len, k_len, hq, hkv, window, sinks, own_views):
         if kind == 0:
             assert j1 - j0 <= 2
         if kind == 1:
-            assert b0 == 0 and 1 <= b1 <= 2
+            assert (b0, b1) == (0, 1)
     assert slots == set(joins)
     for s, (L, K) in enumerate(zip(q_len, k_len)):
         for j in range(-(-K // TILE)):
