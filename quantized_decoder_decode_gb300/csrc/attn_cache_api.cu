@@ -123,7 +123,8 @@ fq_status run_tiles_t(const Plan& p, const Call& c, const AttnSeq* seq, const Vi
             const uint64_t pd[4] = {(uint64_t)HEAD_DIM, 1ull << g.shift, (uint64_t)io.Hkv, (uint64_t)g.n_pages};
             const uint64_t ps[4] = {2, (uint64_t)g.row_stride * 2, (uint64_t)g.head_stride * 2, (uint64_t)g.page_stride * 2};
             const uint32_t pb[4] = {64, (uint32_t)std::min(TILE_ROWS, 1 << g.shift), 1, 1};
-            if (!encode_bf16_tiles(a->map_k[0], g.k, 4, pd, ps, pb) || !encode_bf16_tiles(a->map_v[0], g.v, 4, pd, ps, pb))
+            // (without rows no pool is asked for, and none is read)
+            if (g.k && (!encode_bf16_tiles(a->map_k[0], g.k, 4, pd, ps, pb) || !encode_bf16_tiles(a->map_v[0], g.v, 4, pd, ps, pb)))
                 return fail(FQ_ERR_CUDA, "tensor map of the pages refused");
         } else {
             for (int v = 0; v < n_views; ++v)

@@ -367,3 +367,20 @@ def test_prompt_and_tokens_through_pages():
     for h in range(hkv):
         pk, pv = pool.rows(0, h)
         assert bool((pk == k[h]).all()) and bool((pv == v[h]).all())
+
+
+@pytest.mark.parametrize("q_len", [[1], [3, 1], [300], [300, 1, 40]])
+def test_no_keys_at_all(q_len):
+    """Rows of sequences without keys: zeros and -infinity, through views and through a pool that has no pages."""
+    g, hq, hkv = gen(53), 8, 2
+    k_len = [0] * len(q_len)
+    q = normal(g, sum(q_len), hq, D)
+    k = cache(g, 1, hkv)
+    out, lse = run_window(q, view(k, k), q_len, k_len, hq, hkv, 5, 2)
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+    ws = junk(fq.fq_attn_window_workspace(q_len, k_len, hq, hkv, 0, 0))
+    out.fill_(NAN)
+    fq.fq_attn_paged(q.data_ptr(), fq.fq_kv_pages(0, 0, 0, 16, 0, 0, 0), 0, 0, q_len, k_len, hq, hkv, 0, 0, SCALE, out.data_ptr(),
+                     ws.data_ptr(), ws.numel() * 4, stream())
+    fq.fq_attn_check(stream())
+    assert bool((out == 0).all())
