@@ -226,6 +226,7 @@ fq_status run_window(Call& c, bool paged, const void* q, uint64_t q_stride, uint
 // ---------------------------------------------------------------- gathered weights
 
 constexpr int KW_MAX_RUN = 4096;    // tiles of a unit, at most (no wait for a unit's end comes near its limit)
+constexpr int64_t KW_MAX_UNITS = 1 << 22;   // of a call
 constexpr int KW_MIN_BLOCKS = 6;    // query blocks of a unit that is cut, at least (2048 tokens, 16 / 8 heads 20.1 us; 4: 22.0, 8: 21.6)
 
 struct KwPlan {
@@ -239,7 +240,8 @@ struct KwPlan {
 // over 16000 keys, 32 / 8 heads (80 rows): 12.9 us, 15.9 with keys that stay; 48 tokens (192 rows): 20.5 and 17.5.
 // Units of half an SM's share of the key tiles (16 single tokens over 512 to 4097 keys 12.7 us; a quarter 14.1, an eighth 16.4),
 // or of a third of its share of the query blocks (one prompt of 8192: 235 us; a half 249, a quarter 238, an eighth 244).
-void plan_key_weights(KwPlan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G, uint32_t Hkv, const AttnMask& m) {
+fq_status plan_key_weights(KwPlan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G, uint32_t Hkv, const AttnMask& m) {
+    int64_t n_units = 0;
     int64_t key_tiles_all = 0, blocks_all = 0;
     struct Pair {
         int seq, j0, j1, b0, b1;
@@ -287,6 +289,8 @@ void plan_key_weights(KwPlan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G,
         }
     }
     const int per = (int)std::min<int64_t>(KW_MAX_RUN, std::max<int64_t>(KW_MIN_BLOCKS, blocks_all * Hkv / (3 * ATTN_SMS)));
+    for (const Pair& x : pairs) n_units += ceil_div(x.b1 - x.b0, per);
+    if (n_units > KW_MAX_UNITS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^22 units of work: fewer rows in a call");
     for (const Pair& x : pairs) {
         const int n = ceil_div(x.b1 - x.b0, per), blocks = x.b1 - x.b0;
         if (n > 1) p.join.push_back(KwJoin{x.seq, x.j0, x.j1, (int)p.slots, n});
@@ -305,6 +309,7 @@ void plan_key_weights(KwPlan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G,
         return e.info & KW_NONE ? 0 : (e.b1 - e.b0) * (e.j1 - e.j0);
     };
     std::stable_sort(p.units.begin(), p.units.end(), [&](const KwEntry& a, const KwEntry& b) { return cost(a) > cost(b); });
+    return FQ_OK;
 }
 
 // What a call reads and writes of gathered weights: of sequence s and kv head h, the floats at lo + h * stride and behind.
@@ -337,6 +342,21 @@ fq_status check_weights(const fq_key_weights& w, uint32_t Hkv, uint64_t row0, ui
     return FQ_OK;
 }
 fq_status check_weights_apart(const WeightRows* r, uint32_t n_seq, uint32_t Hkv) {
+    // rows of one array (the rule): apart in one head, and all of them inside a head's stride
+    WeightRows o[MAX_SEQ];
+    int n = 0;
+    bool same = true;
+    for (uint32_t i = 0; i < n_seq; ++i)
+        if (r[i].n) {
+            o[n] = r[i];
+            same = same && o[n].stride == o[0].stride;
+            ++n;
+        }
+    if (n < 2) return FQ_OK;
+    std::sort(o, o + n, [](const WeightRows& a, const WeightRows& b) { return a.lo < b.lo; });
+    bool apart = same && (Hkv == 1 || o[n - 1].lo + o[n - 1].n - o[0].lo <= o[0].stride);
+    for (int i = 0; i + 1 < n; ++i) apart = apart && o[i].lo + o[i].n <= o[i + 1].lo;
+    if (apart) return FQ_OK;
     for (uint32_t i = 0; i < n_seq; ++i)
         for (uint32_t j = i + 1; j < n_seq; ++j)
             if (weights_meet(r[i], r[j], Hkv)) return fail(FQ_ERR_INVALID_ARGUMENT, "sequences %u and %u write the same weights", i, j);
@@ -486,7 +506,7 @@ fq_status fq_attn_key_weights_workspace(uint32_t n_seq, const uint32_t* q_len, c
     TRY(prompt_sequences(n_seq, q_len, nullptr, k_len, nullptr, 0, num_key_value_heads, seq, nullptr, &q_rows));
     try {
         KwPlan p;
-        plan_key_weights(p, n_seq, seq, num_attention_heads / num_key_value_heads, num_key_value_heads, mask_of(window, sinks));
+        TRY(plan_key_weights(p, n_seq, seq, num_attention_heads / num_key_value_heads, num_key_value_heads, mask_of(window, sinks)));
         *bytes = p.bytes(num_key_value_heads);
     } catch (const std::bad_alloc&) {
         return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
@@ -532,7 +552,7 @@ fq_status fq_attn_key_weights(const void* q, uint64_t q_stride, const float* lse
     AttnMask mask = mask_of(window, sinks);
     try {
         KwPlan p;
-        plan_key_weights(p, n_seq, seq, Hq / Hkv, Hkv, mask);
+        TRY(plan_key_weights(p, n_seq, seq, Hq / Hkv, Hkv, mask));
         AttnIo io;
         // (no output of the rows' shape: q stands in for it)
         TRY(attn_common(q, q_stride, Hq, Hkv, scale, (void*)q, 0, FQ_BF16, q_rows, 0, workspace, workspace_bytes, p.bytes(Hkv), io));
@@ -585,9 +605,9 @@ fq_status fq_kv_evict(const fq_kv_view* from, uint32_t n_from, const fq_key_weig
     uint64_t r0 = 0, d0 = 0;
     int64_t total = 0, blocks = 0;
     uint32_t longest = 0, n[MAX_SEQ], to_rows[MAX_SEQ];
-    WeightRows written[MAX_SEQ], read;
-    Span reads[2 * MAX_SEQ];
-    int n_reads = 0;
+    WeightRows written[MAX_SEQ], read[MAX_SEQ];
+    Span reads[2 * MAX_SEQ], writes[2 * MAX_SEQ];
+    int n_reads = 0, n_writes = 0;
     for (uint32_t s = 0; s < n_seq; ++s) {
         if (k_len[s] > MAX_ROWS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^30 rows");
         n[s] = std::min(k_len[s], keep[s]);
@@ -597,7 +617,7 @@ fq_status fq_kv_evict(const fq_kv_view* from, uint32_t n_from, const fq_key_weig
         const uint64_t row = kv_row0 ? kv_row0[s] : n_from == 1 ? r0 : 0, at = to_row0 ? to_row0[s] : n_to == 1 ? d0 : 0;
         TRY(check_view(from[v], Hkv, row, k_len[s], "sequence", s));
         TRY(check_view(to[t], Hkv, at, n[s], "destination", s));
-        TRY(check_weights(weights[v], Hkv, row, k_len[s], "sequence", s, read));
+        TRY(check_weights(weights[v], Hkv, row, k_len[s], "sequence", s, read[s]));
         EvictSeq& e = a.s[s];
         e = EvictSeq{};
         e.len = (int32_t)k_len[s];
@@ -615,7 +635,7 @@ fq_status fq_kv_evict(const fq_kv_view* from, uint32_t n_from, const fq_key_weig
                 return x;
             };
             e.w = weights[v].w + row;
-            e.w_stride = read.stride;
+            e.w_stride = read[s].stride;
             e.w_to = to_weights ? to_weights[t].w + at : nullptr;
             e.w_to_stride = written[s].stride;
             e.from = rows_at(from[v], row);
@@ -634,16 +654,37 @@ fq_status fq_kv_evict(const fq_kv_view* from, uint32_t n_from, const fq_key_weig
     if (!kept || (reinterpret_cast<uintptr_t>(kept) & 3)) return fail(FQ_ERR_INVALID_ARGUMENT, "null or misaligned kept");
     TRY(check_apart(n_seq, n, to, n_to, to_rows, Hkv));
     TRY(check_weights_apart(written, n_seq, Hkv));
-    // a row that is written while another block still has to read it
-    int64_t steps = 1 << 20;
+    // A row (or weight) that is written while another block still has to read it: looked for where what is read and what is
+    // written lie among one another at all.
+    struct Extent {
+        int64_t lo = INT64_MAX, hi = INT64_MIN;
+        void add(int64_t l, int64_t h) {
+            lo = std::min(lo, l);
+            hi = std::max(hi, h);
+        }
+        bool meets(const Extent& e) const { return lo < e.hi && e.lo < hi; }
+    } rows_read, rows_written, weights_read, weights_written;
     for (uint32_t s = 0; s < n_seq; ++s) {
         if (!n[s]) continue;
         const fq_kv_view& t = to[n_to == 1 ? 0 : s];
-        const Span k = span_of(t.k, t, to_rows[s], n[s], Hkv, s), v = span_of(t.v, t, to_rows[s], n[s], Hkv, s);
-        for (int i = 0; i < n_reads; ++i)
-            if (rows_meet(reads[i], k, Hkv, false, steps) || rows_meet(reads[i], v, Hkv, false, steps))
-                return fail(FQ_ERR_INVALID_ARGUMENT, "sequence %u moves to rows that sequence %u is read from", s, reads[i].seq);
+        for (void* p : {t.k, t.v}) writes[n_writes++] = span_of(p, t, to_rows[s], n[s], Hkv, s);
+        for (int i : {1, 2}) {
+            rows_read.add(reads[n_writes - i].lo, reads[n_writes - i].hi);
+            rows_written.add(writes[n_writes - i].lo, writes[n_writes - i].hi);
+        }
+        const WeightRows &r = read[s], &w = written[s];
+        weights_read.add(r.lo, r.lo + (Hkv - 1) * r.stride + r.n);
+        if (w.n) weights_written.add(w.lo, w.lo + (Hkv - 1) * w.stride + w.n);
     }
+    int64_t steps = 1 << 20;
+    for (int j = 0; j < n_writes && rows_read.meets(rows_written); ++j)
+        for (int i = 0; i < n_reads; ++i)
+            if (rows_meet(reads[i], writes[j], Hkv, false, steps))
+                return fail(FQ_ERR_INVALID_ARGUMENT, "sequence %u moves to rows that sequence %u is read from", writes[j].seq, reads[i].seq);
+    for (uint32_t j = 0; j < n_seq && weights_read.meets(weights_written); ++j)
+        for (uint32_t i = 0; i < n_seq; ++i)
+            if (n[i] && weights_meet(read[i], written[j], Hkv))
+                return fail(FQ_ERR_INVALID_ARGUMENT, "weights of sequence %u move to where those of sequence %u are read", j, i);
     launch_evict(a, (int)longest, (int)blocks, (cudaStream_t)stream);
     CK(cudaGetLastError());
     return FQ_OK;

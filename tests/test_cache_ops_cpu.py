@@ -125,6 +125,9 @@ def test_workspaces():
     refused(paged, fq.INVALID_ARGUMENT, stride=1 << 12, ws_bytes=need - 1, **big)
     refused(paged, fq.INVALID_ARGUMENT, stride=1 << 12, ws=P + 16, **big)
     refused(window, fq.INVALID_ARGUMENT, views=view(rows=1 << 16), window=0, ws=0, **big)
+    with pytest.raises(fq.FqError) as e:   # more work than a call is cut into
+        fq.fq_attn_key_weights_workspace((1 << 30,), (1 << 30,), 8, 1, 0, 0)
+    assert e.value.status == fq.INVALID_ARGUMENT
     long = dict(q_len=(4096,), k_len=(4096,), hq=32, hkv=8, views=view(rows=4096))
     refused(weights, fq.INVALID_ARGUMENT, after=fq.fq_key_weights(P, 4096), ws_bytes=64, **long)
     for call in (fq.fq_attn_window_workspace, fq.fq_attn_key_weights_workspace):
@@ -199,9 +202,13 @@ def test_evict_rows_that_would_race():
     two = dict(k_len=(20, 20), keep=(10, 10))
     refused(evict, fq.INVALID_ARGUMENT, to_row0=(0, 9), **two)
     refused(evict, fq.INVALID_ARGUMENT, to=[view(k=FAR, v=FAR + (1 << 30))] * 2, **two)
-    refused(evict, fq.INVALID_ARGUMENT, to_w=w(P, 64), to_row0=(0, 5), **two)
+    refused(evict, fq.INVALID_ARGUMENT, to_w=w(FAR, 64), to_row0=(0, 5), **two)
     refused(evict, fq.INVALID_ARGUMENT, to=[view(k=FAR, v=FAR + (1 << 30)), view(k=FAR + (1 << 31), v=FAR + (1 << 32))],
-            to_w=[w(P, 64), w(P + 36, 64)], **two)
+            to_w=[w(FAR, 64), w(FAR + 36, 64)], **two)
+    far = dict(to=view(k=FAR, v=FAR + (1 << 30)))
+    refused(evict, fq.INVALID_ARGUMENT, to_w=w(P, 64), **far)                                  # weights in place
+    refused(evict, fq.INVALID_ARGUMENT, to_w=w(P + 39 * 4, 64), **far)
+    refused(evict, fq.INVALID_ARGUMENT, to_w=w(P, 64), to_row0=(30,), **far)
     with pytest.raises(ValueError):
         evict(k_len=(1, 2), keep=(1,))
     for bad in (-1, 1 << 32):
