@@ -365,8 +365,8 @@ fq_status fq_attn_paged(const void* q, uint64_t q_stride, const fq_kv_pages* pag
                         size_t workspace_bytes, void* stream);
 
 /* fq_qk_norm_rope into pages: k and v of row i of sequence s go to row kv_row0[s] + i of its pages.  A page that
- * a call writes into belongs to one sequence: rows that two sequences write through a shared page end up as
- * either's.  Errors: as there, and those of fq_attn_paged's table (KV_CACHE_OVERFLOW: rows beyond the table). */
+ * a call writes into belongs to one sequence: rows that are written twice through a shared page end up with
+ * elements of either.  Errors: as there, and those of fq_attn_paged's table (KV_CACHE_OVERFLOW: rows beyond the table). */
 fq_status fq_qk_norm_rope_paged(const float* qkv, uint64_t qkv_stride, uint32_t n_seq, const uint32_t* len,
                                 const uint32_t* pos0, const fq_kv_pages* pages, const int32_t* page_table,
                                 uint64_t table_stride, const uint32_t* kv_row0, uint32_t num_attention_heads,
@@ -390,7 +390,8 @@ typedef struct fq_key_weights {
  * rows are compensated), and the result does not depend on the order in which thread blocks run.
  * workspace: as there, fq_attn_key_weights_workspace.  Errors: as fq_attn_window, and INVALID_ARGUMENT (null lse or
  * weights, a head_stride too short, two sequences of a call that write the same weights; weights of different strides that lie in
- * between one another are taken for such). */
+ * between one another are taken for such; more than 2^22 units of work, each 256 keys by up to 4096 x 96 query rows of a
+ * kv head). */
 fq_status fq_attn_key_weights(const void* q, uint64_t q_stride, const float* lse, const fq_kv_view* views, uint32_t n_views,
                               uint32_t n_seq, const uint32_t* q_len, const uint32_t* kv_row0, const uint32_t* k_len,
                               uint32_t num_attention_heads, uint32_t num_key_value_heads, uint32_t window, uint32_t sinks,

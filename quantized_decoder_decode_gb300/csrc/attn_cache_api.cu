@@ -251,6 +251,7 @@ fq_status plan_key_weights(KwPlan& p, uint32_t n_seq, const AttnSeq* seq, uint32
     };
     std::vector<Pair> pairs;
     std::vector<Run> runs;
+    auto too_many = [] { return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^22 units of work: fewer rows in a call"); };
     auto none = [&](int s, int j0, int j1) {
         for (; j0 < j1; j0 += KW_MAX_RUN) p.units.push_back(KwEntry{s | KW_NONE, j0, std::min(j1, j0 + KW_MAX_RUN), 0, 0, -1});
     };
@@ -272,6 +273,7 @@ fq_status plan_key_weights(KwPlan& p, uint32_t n_seq, const AttnSeq* seq, uint32
                 key_tiles_all += e[1] - e[0];
                 continue;
             }
+            if ((int64_t)pairs.size() + (e[1] - e[0]) / KW_KEY_TILES > KW_MAX_UNITS) return too_many();
             for (int j = e[0]; j < e[1]; j += KW_KEY_TILES) {
                 const int j1 = std::min(e[1], j + KW_KEY_TILES);
                 // the tokens that see one of these keys
@@ -290,7 +292,7 @@ fq_status plan_key_weights(KwPlan& p, uint32_t n_seq, const AttnSeq* seq, uint32
     }
     const int per = (int)std::min<int64_t>(KW_MAX_RUN, std::max<int64_t>(KW_MIN_BLOCKS, blocks_all * Hkv / (3 * ATTN_SMS)));
     for (const Pair& x : pairs) n_units += ceil_div(x.b1 - x.b0, per);
-    if (n_units > KW_MAX_UNITS) return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^22 units of work: fewer rows in a call");
+    if (n_units > KW_MAX_UNITS) return too_many();
     for (const Pair& x : pairs) {
         const int n = ceil_div(x.b1 - x.b0, per), blocks = x.b1 - x.b0;
         if (n > 1) p.join.push_back(KwJoin{x.seq, x.j0, x.j1, (int)p.slots, n});

@@ -5,22 +5,31 @@
 // The scores are taken the other way round than in attention, S = K Q^T with the keys as the rows of the product: a
 // thread then has one key's scores in its own lane of tensor memory and adds their exponentials up by itself.  No
 // maximum is needed, no weight leaves the registers, and no two threads write the same sum (atomics would add
-// in any order).  Sums of a tile of 128 weights go to the key's total by compensated addition: 2^15 rows add up as exactly
+// in any order).  Sums of a tile of 96 weights go to the key's total by compensated addition: 2^15 rows add up as exactly
 // as one tile does.
 //
 // A unit holds what is few and lets the rest pass by through a ring of 32 KB tiles (TMA):
 //   KW_KEYS  two key tiles stay (one for each of two pairs of warpgroups), query blocks of 96 packed rows pass by;
 //   KW_ROWS  the rows of a query block stay (single tokens, a few observed ones), key tiles pass by, to the four
 //            warpgroups in turn: K is read once, which is what bounds it.
-// What stays has two sets of buffers, so that the next unit's comes while this one is worked on.  Long ranges of query
-// blocks are cut into units of their own, whose partial sums (4 bytes a key) a second kernel adds up in order.
+// What stays has two sets of buffers, so that the next unit's comes while this one is worked on; keys that stay move on to
+// tensor memory, as the product's first operand (with both operands in shared memory its reads, those of the statistics and
+// the copies coming in ask for more than its 128 bytes a cycle).  Long ranges of query blocks are cut into units of their
+// own, whose partial sums (4 bytes a key) a second kernel adds up in order.
 //
-// Tensor memory: an S buffer of 128 columns for each of four warpgroups.  Shared memory: 2 x 2 tiles that stay, 3 that pass by.
-// Roles (608 threads, one CTA per SM, looping over its units): warps 0-15 exponentials and sums, a key per thread; warp 16 loads;
-// warp 17 issues the products; warp 18 brings the rows' log-sums.  Four warpgroups, because the exponentials of a tile take the special-function units as
-// long as its product takes the tensor cores (512 cycles each): two warpgroups with two buffers each kept either busy 31 % of the
-// time (8192 tokens 384 us), four that share tiles by their columns 39 % (297 us).  Every wait is bounded; one that gives up
-// records it, and all roles leave.
+// Tensor memory: an S buffer of 96 columns for each of four warpgroups, two key tiles.  Shared memory: 2 x 2 tiles that stay, 3
+// that pass by.  Roles (608 threads, one CTA per SM, looping over its units): warps 0-15 exponentials and sums, a key per thread; warp 16
+// loads; warp 17 issues the products; warp 18 brings the rows' log-sums.  Every wait is bounded; one that gives up records it,
+// and all roles leave.
+//
+// What bounds it.  16 single tokens over 512 to 4097 keys, 32 / 8 heads (79 MB): 12.2 us, memory (floor 11.5).  One prompt of
+// 8192 tokens, 32 / 8 heads: 231 us (products alone 144).  The exponentials of a tile take the special-function units as
+// long as its product takes the tensor cores (384 cycles for 96 columns); each is busy 37 % of a call of 4096 tokens (83 us)
+// and half of the issue slots are taken.  Of a warpgroup's round of about 2900 cycles (four tiles, one for each) 580 pass
+// until its one S buffer is filled again, and tensor memory has no room for a second.  Before: two warpgroups with two S buffers
+// each 384 us, four that share tiles by their columns 297, four with a buffer each and both operands in shared memory 260.  Against the 239 us
+// of whole query blocks in smaller shares of work (now 231), no faster: reads of 24 columns (248; of 32 they spill, 265), S
+// given back before its last columns are worked on (249), a second issuing thread (240).
 
 #include <cstddef>
 
@@ -286,7 +295,7 @@ struct Total {
     float sum = 0.f, err = 0.f;
     FQ_DEV void add(float x) {
         const float y = __fsub_rn(x, err), t = __fadd_rn(sum, y);
-        err = __fsub_rn(__fsub_rn(t, sum), y);
+        err = fabsf(t) < INFINITY ? __fsub_rn(__fsub_rn(t, sum), y) : 0.f;   // an infinite sum stays one
         sum = t;
     }
 };
@@ -373,7 +382,7 @@ FQ_DEV void kw_sum(const Args& a, KwShared* sh, const uint8_t* stay, int units, 
         auto finish = [&](int key, float sum) {
             if (key >= sq.k_len) return;
             const int64_t r = sq.k_row0 + key;
-            if (kw.before) sum += __ldg(kw.before + u.head * kw.before_stride + r);
+            if (kw.before) sum += kw.before[u.head * kw.before_stride + r];   // (maybe where `after` is written)
             kw.after[u.head * kw.after_stride + r] = sum;
         };
         if (u.kind == KW_NONE) {
@@ -538,7 +547,7 @@ __global__ void __launch_bounds__(KW_KEY_TILES* TILE_ROWS) key_weights_join_kern
     const int64_t key = (int64_t)e.j0 * TILE_ROWS + threadIdx.x;
     pdl_wait();   // the partial sums are written
     if (key >= sq.k_len || key >= (int64_t)e.j1 * TILE_ROWS) return;
-    float sum = kw.before ? __ldg(kw.before + head * kw.before_stride + sq.k_row0 + key) : 0.f;
+    float sum = kw.before ? kw.before[head * kw.before_stride + sq.k_row0 + key] : 0.f;
     float part = 0.f;
     for (int i = 0; i < e.n; ++i) part += a.part[((int64_t)(e.slot + i) * a.Hkv + head) * (KW_KEY_TILES * TILE_ROWS) + threadIdx.x];
     kw.after[head * kw.after_stride + sq.k_row0 + key] = sum + part;

@@ -128,6 +128,9 @@ def test_workspaces():
     with pytest.raises(fq.FqError) as e:   # more work than a call is cut into
         fq.fq_attn_key_weights_workspace((1 << 30,), (1 << 30,), 8, 1, 0, 0)
     assert e.value.status == fq.INVALID_ARGUMENT
+    with pytest.raises(fq.FqError) as e:   # (of many sequences: before they are listed)
+        fq.fq_attn_key_weights_workspace((1000,) * 64, (1 << 30,) * 64, 8, 1, 0, 0)
+    assert e.value.status == fq.INVALID_ARGUMENT
     long = dict(q_len=(4096,), k_len=(4096,), hq=32, hkv=8, views=view(rows=4096))
     refused(weights, fq.INVALID_ARGUMENT, after=fq.fq_key_weights(P, 4096), ws_bytes=64, **long)
     for call in (fq.fq_attn_window_workspace, fq.fq_attn_key_weights_workspace):

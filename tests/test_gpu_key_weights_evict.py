@@ -187,6 +187,27 @@ def test_key_weights_rows_that_do_not_see_a_key(bad, L, K, window):
             assert_weights(part[~touched], torch.zeros_like(part[~touched]), r[~touched], b[~touched], f"{s} {h}")
 
 
+@pytest.mark.parametrize("L,K", [(1, 300), (20, 500), (700, 900), (4000, 4000)])
+@pytest.mark.parametrize("low", [-math.inf, -1e6])
+def test_weights_beyond_f32_are_infinite(L, K, low):
+    """A log-sum far below its row's scores: the formula is infinite in f32 for every key that the row sees, and stays so
+    whatever is added behind it; the other head's keys have what they had."""
+    g, hq, hkv = gen(17), 4, 2
+    q, k = normal(g, L, hq, D), normal(g, hkv, K, D)
+    lse = log_sums(q, lambda s, h: k[h], [L], [K], hq, hkv, 0, 0)
+    row = L // 3
+    lse[row, 1] = low
+    w = torch.empty(hkv, K, device=DEV)
+    run(q, lse, view(k), [L], [K], hq, hkv, 0, 0, None, weights(w))
+    seen = visible(L, K, 0, 0)
+    assert bool((w[0, seen[row]] == math.inf).all())
+    ref, bound = gathered(q[:, :2], lse[:, :2], k[0], seen, SCALE)
+    rest = ~seen[row]
+    assert_weights(w[0, rest], torch.zeros_like(w[0, rest]), ref[rest], bound[rest])
+    ref, bound = gathered(q[:, 2:], lse[:, 2:], k[1], seen, SCALE)
+    assert_weights(w[1], torch.zeros_like(w[1]), ref, bound)
+
+
 def plain_evict(w, n, sinks, recent):
     """The rows of one head that stay, by sorting."""
     K = w.shape[0]
