@@ -167,7 +167,7 @@ KvRows rows_of(const fq_kv_view& v) {
 
 // ---------------------------------------------------------------- work lists
 
-// Times of attn_tiles.cu in microseconds (measured at head_dim 128 on one GB300) that the choices
+// Times of attn_tiles.cuh in microseconds (measured at head_dim 128 on one GB300) that the choices
 // below weigh: a key tile of a pair of query tiles and of a single one, a unit's own cost (what of
 // its loads, joins and outputs nothing hides), what partial results cost more, and
 // joining them (a launch, the reads); and reading K and V rows from memory.  (The choices are not

@@ -1,5 +1,5 @@
 // Arguments of the prompt and shared-prompt attention operators' kernels, and their work lists, made on the host
-// (attn_api.cu) and passed by value to attn_tiles.cu, attn_rows.cu and attn_join.cu.
+// (attn_host.h) and passed by value to attn_tiles.cuh, attn_rows.cu and attn_join.cu.
 //
 // "Packed rows": a kv head's query rows are (token, head of its group) with the head running
 // fastest, so G heads x tokens fill the 128 rows of a matrix product.
@@ -124,7 +124,7 @@ FQ_HD inline KeySpan key_span(const AttnMask& m, int32_t k_len, int32_t off, int
     return s;
 }
 
-// One unit of attn_tiles.cu per kv head: two query tiles (pair) over the same keys, or one tile
+// One unit of attn_tiles.cuh per kv head: two query tiles (pair) over the same keys, or one tile
 // whose key tiles alternate between the two softmax warpgroups.
 struct TileEntry {
     int32_t tok0;         // first token (of its sequence)
@@ -161,7 +161,7 @@ struct Partials {
     float2 *a_ml = nullptr, *b_ml = nullptr;
 };
 
-// Bounded waits of attn_tiles.cu: how long one may take, and where a CTA of which one gave up records it.
+// Bounded waits of attn_tiles.cuh: how long one may take, and where a CTA of which one gave up records it.
 struct AttnWaits {
     uint32_t* record = nullptr;   // device word (null: the current device's own)
     uint32_t code = 0;            // bits set in it; 0: one is added

@@ -14,12 +14,16 @@
 //     bytes again and a thread ends up with 8 neighbouring dims of two rows.
 // A CTA of four warps takes a chunk of the keys of one (row group, kv head); the warps take
 // blocks of 16 keys in turn with a running reference maximum (moved only when the maximum has
-// grown by more than 2^8; weights 2^-lift of the usual ones, as in attn_tiles.cu) and are joined in shared
+// grown by more than 2^8; weights 2^-lift of the usual ones, as in attn_tiles.cuh) and are joined in shared
 // memory.
 // Measured: 16 single tokens over 512 to 4097 rows (152 MB, 32 / 8 heads) 26 us, 5.8 TB/s; a block of 64
 // keys of a CTA takes 1.9 us, of which its reads wait for memory all but 0.3.  The start of a CTA (its
 // arguments, the first reads) is 2.5 us, the join in it 0.7 us.  CTAs of two warps, six per SM, balance better but
 // leave twice the partial results: 32.8 us for the call instead of 31.0.
+// With windows and pages (Args::WINDOW): 16 tokens over a window of 2048 (121 MB) 27.3 us, 32 tokens over pages of 16 rows (281 MB) 58 us,
+// of which the join 4.  Taken out again there: K and V through shared memory by copies of 16 bytes (31 and 66 us), of a row (33
+// and 71) or of 4 KB (28.5 and 59); 128-key tiles by TMA for tcgen05 products with the keys as rows (30 and 62 to 72: all SMs' first
+// tiles take 2.5 us to land, and a tile of small pages is 16 copies).
 // Keys beyond the chunk are read as zeros with weight 0.  In blocks where some row does not see a
 // key, V values that are not finite are set to zero for the product and added to the rows that
 // see them.
@@ -302,14 +306,14 @@ __global__ void __launch_bounds__(AR_THREADS, ROWS_CTAS_SM) attn_rows_kernel(con
         }
     }
     // This grid ends after the one it may run beside, so that what waits for it waits for both.  One CTA sees to that: the others
-    // make room for those that have not started.
+    // make room for those that have not started (32 sequences behind a shared prefix 18.8 -> 15.9 us, 64 of them 34.2 -> 33.1).
     if (blockIdx.x == gridDim.x - 1) pdl_wait();
 }
 
 }  // namespace
 
 // What is in flight from memory (12 warps x 8 KB per SM) is held in the L1 cache, which is what shared
-// memory leaves of 256 KB: behind attn_tiles.cu, with its 227 KB, a block of keys took 3.2 us
+// memory leaves of 256 KB: behind attn_tiles.cuh, with its 227 KB, a block of keys took 3.2 us
 // instead of 1.9 (64 tails behind a shared prefix 45 -> 39 us) until the split was asked for.
 template <class Args>
 static cudaError_t prepare() {
