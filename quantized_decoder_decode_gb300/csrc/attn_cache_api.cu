@@ -225,36 +225,41 @@ fq_status run_window(Call& c, bool paged, const void* q, uint64_t q_stride, uint
 
 // ---------------------------------------------------------------- gathered weights
 
-constexpr int KW_MAX_RUN = 4096;    // tiles of a unit, at most (no wait for a unit's end comes near its limit)
-constexpr int64_t KW_MAX_UNITS = 1 << 22;   // of a call
-constexpr int KW_MIN_BLOCKS = 6;    // query blocks of a unit that is cut, at least (2048 tokens, 16 / 8 heads 20.1 us; 4: 22.0, 8: 21.6)
+constexpr int KW_MAX_RUN = 4096;    // blocks of an entry, at most (no wait for a unit's end comes near its limit)
+constexpr size_t KW_MAX_ENTRIES = 1 << 22;   // of a call
+// What a thread block's part of the line is, at least, with keys that stay (512 tokens, 32 / 8 heads 11.1 us; 10: 12.9) and without.
+constexpr int KW_MIN_SHARE = 6, KW_MIN_ROWS_SHARE = 3;
+// What cutting entries costs: the units that begin with a cut, and the launch that joins their sums (100 tokens over 500 keys,
+// 16 / 8 heads: 14 us cut, 7.6 whole).
+constexpr int KW_CUT = 8;
+
+int kw_grid(int64_t line, bool keys) {
+    const int64_t least = keys ? KW_MIN_SHARE : KW_MIN_ROWS_SHARE;
+    return (int)std::min<int64_t>(ATTN_SMS, (line + least - 1) / least);
+}
+int kw_cost(const KwEntry& e) { return kw_start(e.info & (KW_ROWS | KW_NONE)) + e.len; }
+bool kw_keys(const KwEntry& e) { return !(e.info & (KW_ROWS | KW_NONE)); }
 
 struct KwPlan {
-    std::vector<KwEntry> units;     // longest first
-    std::vector<KwJoin> join;
-    int64_t slots = 0;
-    size_t bytes(uint32_t Hkv) const { return (size_t)slots * Hkv * KW_KEY_TILES * TILE_ROWS * 4; }
+    std::vector<KwEntry> e;         // those with the same keys KW_MAX_RUN query blocks apart
+    int64_t line = 0;               // of a kv head
+    bool keys = false;
+    size_t bytes(uint32_t Hkv) const {   // (a launch of a part of the entries has as many thread blocks at most)
+        const int grid = keys ? kw_grid(line * Hkv, true) : 0;
+        return grid > 1 ? (size_t)grid * 2 * KW_KEY_TILES * TILE_ROWS * 4 : 0;
+    }
 };
 
 // Up to 96 packed query rows (a block) stay while the keys pass by; of more, the query blocks pass by keys that stay.  20 tokens
 // over 16000 keys, 32 / 8 heads (80 rows): 12.9 us, 15.9 with keys that stay; 48 tokens (192 rows): 20.5 and 17.5.
-// Units of half an SM's share of the key tiles (16 single tokens over 512 to 4097 keys 12.7 us; a quarter 14.1, an eighth 16.4),
-// or of a third of its share of the query blocks (one prompt of 8192: 235 us; a half 249, a quarter 238, an eighth 244).
-fq_status plan_key_weights(KwPlan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G, uint32_t Hkv, const AttnMask& m) {
-    int64_t n_units = 0;
-    int64_t key_tiles_all = 0, blocks_all = 0;
-    struct Pair {
-        int seq, j0, j1, b0, b1;
-    };
-    struct Run {
-        int seq, j0, j1;
-    };
-    std::vector<Pair> pairs;
-    std::vector<Run> runs;
-    auto too_many = [] { return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^22 units of work: fewer rows in a call"); };
+fq_status plan_key_weights(KwPlan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G, const AttnMask& m) {
     auto none = [&](int s, int j0, int j1) {
-        for (; j0 < j1; j0 += KW_MAX_RUN) p.units.push_back(KwEntry{s | KW_NONE, j0, std::min(j1, j0 + KW_MAX_RUN), 0, 0, -1});
+        for (const int most = KW_MAX_RUN * KW_REST; j0 < j1; j0 += most) {
+            const int end = std::min(j1, j0 + most);
+            p.e.push_back(KwEntry{s | KW_NONE, j0, end, 0, ceil_div(end - j0, KW_REST), 0});
+        }
     };
+    bool sorted = true;
     for (uint32_t i = 0; i < n_seq; ++i) {
         const AttnSeq& q = seq[i];
         if (q.k_len == 0) continue;
@@ -267,13 +272,11 @@ fq_status plan_key_weights(KwPlan& p, uint32_t n_seq, const AttnSeq* seq, uint32
         none(s, t.sinks, t.first);
         const int ends[2][2] = {{0, t.sinks}, {t.first, all}};
         for (auto& e : ends) {
-            if (e[0] >= e[1]) continue;
             if (blocks <= 1) {
-                runs.push_back(Run{s, e[0], e[1]});
-                key_tiles_all += e[1] - e[0];
+                for (int j = e[0]; j < e[1]; j += KW_MAX_RUN)
+                    p.e.push_back(KwEntry{s | KW_ROWS, j, 0, 0, std::min(e[1] - j, KW_MAX_RUN), 0});
                 continue;
             }
-            if ((int64_t)pairs.size() + (e[1] - e[0]) / KW_KEY_TILES > KW_MAX_UNITS) return too_many();
             for (int j = e[0]; j < e[1]; j += KW_KEY_TILES) {
                 const int j1 = std::min(e[1], j + KW_KEY_TILES);
                 // the tokens that see one of these keys
@@ -285,32 +288,21 @@ fq_status plan_key_weights(KwPlan& p, uint32_t n_seq, const AttnSeq* seq, uint32
                     continue;
                 }
                 const int b0 = (int)(first * G / KW_BLOCK), b1 = (int)((last * G + G - 1) / KW_BLOCK) + 1;
-                pairs.push_back(Pair{s, j, j1, b0, b1});
-                blocks_all += b1 - b0;
+                int more = 0;
+                for (int b = b0; b < b1; more = KW_MORE) {
+                    const int end = std::min(b1, (b / KW_MAX_RUN + 1) * KW_MAX_RUN);
+                    p.e.push_back(KwEntry{s | KW_KEYS | more, j, j1, b, end - b, 0});
+                    sorted = sorted && end <= KW_MAX_RUN;
+                    b = end;
+                }
+                p.keys = true;
+                if (p.e.size() > KW_MAX_ENTRIES)
+                    return fail(FQ_ERR_INVALID_ARGUMENT, "more than 2^22 units of work: fewer rows in a call");
             }
         }
     }
-    const int per = (int)std::min<int64_t>(KW_MAX_RUN, std::max<int64_t>(KW_MIN_BLOCKS, blocks_all * Hkv / (3 * ATTN_SMS)));
-    for (const Pair& x : pairs) n_units += ceil_div(x.b1 - x.b0, per);
-    if (n_units > KW_MAX_UNITS) return too_many();
-    for (const Pair& x : pairs) {
-        const int n = ceil_div(x.b1 - x.b0, per), blocks = x.b1 - x.b0;
-        if (n > 1) p.join.push_back(KwJoin{x.seq, x.j0, x.j1, (int)p.slots, n});
-        for (int i = 0; i < n; ++i)
-            p.units.push_back(KwEntry{x.seq | KW_KEYS, x.j0, x.j1, x.b0 + (int)((int64_t)blocks * i / n),
-                                      x.b0 + (int)((int64_t)blocks * (i + 1) / n), n > 1 ? (int)p.slots++ : -1});
-    }
-    const int run = (int)std::min<int64_t>(KW_MAX_RUN, std::max<int64_t>(2, key_tiles_all * Hkv / (2 * ATTN_SMS)));
-    for (const Run& x : runs) {
-        const int n = ceil_div(x.j1 - x.j0, run), tiles = x.j1 - x.j0;
-        for (int i = 0; i < n; ++i)
-            p.units.push_back(KwEntry{x.seq | KW_ROWS, x.j0 + (int)((int64_t)tiles * i / n), x.j0 + (int)((int64_t)tiles * (i + 1) / n),
-                                      0, 1, -1});
-    }
-    auto cost = [](const KwEntry& e) {
-        return e.info & KW_NONE ? 0 : (e.b1 - e.b0) * (e.j1 - e.j0);
-    };
-    std::stable_sort(p.units.begin(), p.units.end(), [&](const KwEntry& a, const KwEntry& b) { return cost(a) > cost(b); });
+    for (const KwEntry& e : p.e) p.line += kw_cost(e);
+    if (!sorted) std::stable_sort(p.e.begin(), p.e.end(), [](const KwEntry& a, const KwEntry& b) { return a.b0 / KW_MAX_RUN < b.b0 / KW_MAX_RUN; });
     return FQ_OK;
 }
 
@@ -396,10 +388,34 @@ fq_status run_key_weights_t(const KwPlan& p, const AttnIo& io, const float* lse,
             if (!encode_bf16_tiles(a->map_k[v], views[v].rows.k, 3, kd, ks, kb)) return fail(FQ_ERR_CUDA, "tensor map of K refused");
         }
         constexpr size_t NE = Args::ENTRIES;
-        for (size_t e0 = 0; e0 < p.units.size(); e0 += NE) {
-            a->n_entries = (int)std::min(NE, p.units.size() - e0);
-            std::copy(p.units.begin() + e0, p.units.begin() + e0 + a->n_entries, a->e);
-            launch_key_weights(*a, s);
+        for (size_t e0 = 0; e0 < p.e.size();) {
+            bool keys = false, cuts = false;
+            int longest = 0;
+            a->total = a->n_entries = 0;
+            for (; (size_t)a->n_entries < NE && e0 < p.e.size() && p.e[e0].b0 / KW_MAX_RUN == p.e[e0 - a->n_entries].b0 / KW_MAX_RUN; ++e0) {
+                KwEntry& e = a->e[a->n_entries++];
+                e = p.e[e0];
+                e.pos = a->total;
+                a->total += kw_cost(e);
+                longest = std::max(longest, kw_cost(e));
+                keys = keys || kw_keys(e);
+                cuts = cuts || (kw_keys(e) && e.len > KW_WHOLE);
+            }
+            const int64_t line = (int64_t)a->total * io.Hkv;
+            int grid = kw_grid(line, keys);
+            a->share = (line + grid - 1) / grid;
+            grid = (int)((line + a->share - 1) / a->share);
+            const bool whole = keys && (int64_t)a->n_entries * io.Hkv <= ATTN_SMS && longest <= a->share + KW_CUT;
+            if (whole) {   // a thread block each
+                for (int i = 0; i < a->n_entries; ++i) a->e[i].pos = i * longest;
+                a->share = longest;
+                a->total = a->n_entries * longest;
+                grid = a->n_entries * io.Hkv;
+            }
+            launch_key_weights(*a, grid, s);
+            CK(cudaGetLastError());
+            if (!cuts || whole || grid == 1) continue;
+            launch_key_weights_join(*a, s);
             CK(cudaGetLastError());
         }
         return FQ_OK;
@@ -508,7 +524,7 @@ fq_status fq_attn_key_weights_workspace(uint32_t n_seq, const uint32_t* q_len, c
     TRY(prompt_sequences(n_seq, q_len, nullptr, k_len, nullptr, 0, num_key_value_heads, seq, nullptr, &q_rows));
     try {
         KwPlan p;
-        TRY(plan_key_weights(p, n_seq, seq, num_attention_heads / num_key_value_heads, num_key_value_heads, mask_of(window, sinks)));
+        TRY(plan_key_weights(p, n_seq, seq, num_attention_heads / num_key_value_heads, mask_of(window, sinks)));
         *bytes = p.bytes(num_key_value_heads);
     } catch (const std::bad_alloc&) {
         return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
@@ -554,35 +570,20 @@ fq_status fq_attn_key_weights(const void* q, uint64_t q_stride, const float* lse
     AttnMask mask = mask_of(window, sinks);
     try {
         KwPlan p;
-        TRY(plan_key_weights(p, n_seq, seq, Hq / Hkv, Hkv, mask));
+        TRY(plan_key_weights(p, n_seq, seq, Hq / Hkv, mask));
         AttnIo io;
         // (no output of the rows' shape: q stands in for it)
         TRY(attn_common(q, q_stride, Hq, Hkv, scale, (void*)q, 0, FQ_BF16, q_rows, 0, workspace, workspace_bytes, p.bytes(Hkv), io));
         if (q_rows && (!lse || (reinterpret_cast<uintptr_t>(lse) & 3))) return fail(FQ_ERR_INVALID_ARGUMENT, "null or misaligned lse");
-        if (p.units.empty()) return FQ_OK;
+        if (p.e.empty()) return FQ_OK;
         uint32_t *waits, *bad;
         TRY(prepare_device(&waits, &bad));
         cudaStream_t s = (cudaStream_t)stream;
-        const size_t n_units = p.units.size();
+        const size_t n = p.e.size();
         auto run = n_views > 1 ? run_key_weights_t<KwArgsN>
-                               : n_units <= KwArgs1S::ENTRIES ? run_key_weights_t<KwArgs1S>
-                                                              : n_units <= KwArgs1M::ENTRIES ? run_key_weights_t<KwArgs1M> : run_key_weights_t<KwArgs1>;
-        TRY(run(p, io, lse, mask, waits, (float*)workspace, seq, (int)n_seq, (int)q_rows, use, w, (int)n_views, s));
-        if (p.join.empty()) return FQ_OK;
-        KwJoinArgs j;
-        j.part = (const float*)workspace;
-        j.Hkv = (int)Hkv;
-        for (uint32_t i = 0; i < n_seq; ++i) {
-            j.seq[i] = seq[i];
-            j.w[i] = w[n_views == 1 ? 0 : i];
-        }
-        for (size_t e0 = 0; e0 < p.join.size(); e0 += KwJoinArgs::ENTRIES) {
-            j.n_entries = (int)std::min<size_t>(KwJoinArgs::ENTRIES, p.join.size() - e0);
-            std::copy(p.join.begin() + e0, p.join.begin() + e0 + j.n_entries, j.e);
-            launch_key_weights_join(j, s);
-            CK(cudaGetLastError());
-        }
-        return FQ_OK;
+                               : n <= KwArgs1S::ENTRIES ? run_key_weights_t<KwArgs1S>
+                                                        : n <= KwArgs1M::ENTRIES ? run_key_weights_t<KwArgs1M> : run_key_weights_t<KwArgs1>;
+        return run(p, io, lse, mask, waits, (float*)workspace, seq, (int)n_seq, (int)q_rows, use, w, (int)n_views, s);
     } catch (const std::bad_alloc&) {
         return fail(FQ_ERR_OUT_OF_MEMORY, "host memory");
     }

@@ -14,22 +14,25 @@
 //            warpgroups in turn: K is read once, which is what bounds it.
 // What stays has two sets of buffers, so that the next unit's comes while this one is worked on; keys that stay move on to
 // tensor memory, as the product's first operand (with both operands in shared memory its reads, those of the statistics and
-// the copies coming in ask for more than its 128 bytes a cycle).  Long ranges of query blocks are cut into units of their
-// own, whose partial sums (4 bytes a key) a second kernel adds up in order.
+// the copies coming in ask for more than its 128 bytes a cycle).  All units of a call are laid in a line that the CTAs share
+// out in equal parts; keys of which several CTAs have a part get their sums from a second kernel, which adds the parts up in order.
 //
 // Tensor memory: an S buffer of 96 columns for each of four warpgroups, two key tiles.  Shared memory: 2 x 2 tiles that stay, 3
 // that pass by.  Roles (608 threads, one CTA per SM, looping over its units): warps 0-15 exponentials and sums, a key per thread; warp 16
 // loads; warp 17 issues the products; warp 18 brings the rows' log-sums.  Every wait is bounded; one that gives up records it,
 // and all roles leave.
 //
-// What bounds it.  16 single tokens over 512 to 4097 keys, 32 / 8 heads (79 MB): 12.2 us, memory (floor 11.5).  One prompt of
-// 8192 tokens, 32 / 8 heads: 231 us (products alone 144).  The exponentials of a tile take the special-function units as
-// long as its product takes the tensor cores (384 cycles for 96 columns); each is busy 37 % of a call of 4096 tokens (83 us)
-// and half of the issue slots are taken.  Of a warpgroup's round of about 2900 cycles (four tiles, one for each) 580 pass
-// until its one S buffer is filled again, and tensor memory has no room for a second.  Before: two warpgroups with two S buffers
-// each 384 us, four that share tiles by their columns 297, four with a buffer each and both operands in shared memory 260.  Against the 239 us
-// of whole query blocks in smaller shares of work (now 231), no faster: reads of 24 columns (248; of 32 they spill, 265), S
-// given back before its last columns are worked on (249), a second issuing thread (240).
+// What bounds it.  16 single tokens over 512 to 4097 keys, 32 / 8 heads (79 MB): 11.1 us, memory (floor 11.5 at the rate of a
+// plain copy).  One prompt, 32 / 8 heads: 2048 tokens 25 us, 4096 65, 8192 220 (products alone 144).  The exponentials of a
+// tile take the special-function units as long as its product takes the tensor cores (384 cycles for 96 columns), and a
+// block of query rows, two tiles, takes 1380 cycles: of a warpgroup's round of 2760 cycles (four tiles, one for each) some 580 pass
+// until its one S buffer is filled again, and tensor memory has no room for a second.  A tile that is masked in part
+// takes half as long again; a warp whose keys all see none of its rows leaves it out, and keys that see all of
+// them beside keys that see none (a window's sinks) take the short way: 8192 tokens with a window of 1000, 137 -> 80 us.
+//
+// Slower, of 8192 tokens: two warpgroups with two S buffers each (384 us), four that share tiles by their columns (297),
+// operands in shared memory (260), S in halves of 48 columns (287: such a product takes the tensor cores as long as one of 96).
+// No faster: reads of 24 columns, of 32 (they spill), S given back before its last columns are worked on, a second issuing thread.
 
 #include <cstddef>
 
@@ -98,30 +101,6 @@ FQ_DEV void kw_drain() {   // copies in flight land within microseconds of a wai
     }
 }
 
-// One unit as every role sees it.
-struct KwUnit {
-    int seq, head, kind, j0, j1, b0, b1, slot;
-    int stay, pass;       // tiles that stay; that pass by
-};
-FQ_DEV int kw_unit_at(int r) { return r * (int)gridDim.x + (int)(r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x); }
-template <class Args>
-FQ_DEV KwUnit kw_unit(const Args& a, int w) {
-    KwUnit u;
-    const int entry = w / a.Hkv;
-    const KwEntry& e = a.e[entry];
-    u.head = w - entry * a.Hkv;
-    u.seq = e.info & 127;
-    u.kind = e.info & (KW_ROWS | KW_NONE);
-    u.j0 = e.j0;
-    u.j1 = e.j1;
-    u.b0 = e.b0;
-    u.b1 = e.b1;
-    u.slot = e.slot;
-    u.stay = u.kind == KW_NONE ? 0 : u.kind == KW_ROWS ? u.b1 - u.b0 : u.j1 - u.j0;
-    u.pass = u.kind == KW_NONE ? 0 : u.kind == KW_ROWS ? u.j1 - u.j0 : u.b1 - u.b0;
-    return u;
-}
-
 // By one thread: key tile j or query block b of a unit's sequence.
 template <class Args>
 FQ_DEV void kw_load_k(const Args& a, const KwUnit& u, int j, uint8_t* dst, uint64_t* bar) {
@@ -145,11 +124,11 @@ FQ_DEV int kw_columns(const Args& a, const KwUnit& u) {
 
 // ---------------- warp 16
 template <class Args>
-FQ_DEV void kw_load(const Args& a, KwShared* sh, uint8_t* stay, uint8_t* ring, int units) {
+FQ_DEV void kw_load(const Args& a, KwShared* sh, uint8_t* stay, uint8_t* ring) {
     uint32_t n = 0, un = 0;   // tiles that pass by; units with tiles
     bool ok = true;
-    for (int it = 0, w; (w = kw_unit_at(it)) < units && ok; ++it) {
-        const KwUnit u = kw_unit(a, w);
+    KwUnit u;
+    for (KwLine l = kw_line(a, blockIdx.x); ok && kw_next(a, l, u);) {
         if (!u.pass) continue;
         const int set = un & 1;
         if (!(ok = kw_wait_warp(&sh->st_empty[set], ((un >> 1) & 1) ^ 1, sh))) break;
@@ -219,11 +198,11 @@ FQ_DEV bool kw_unit_products(KwShared* sh, const KwUnit& u, uint64_t d_stay, uin
 }
 
 template <class Args>
-FQ_DEV void kw_products(const Args& a, KwShared* sh, uint8_t* stay, uint8_t* ring, int units, uint32_t tm) {
+FQ_DEV void kw_products(const Args& a, KwShared* sh, uint8_t* stay, uint8_t* ring, uint32_t tm) {
     const uint64_t d_stay = sdesc_sw128(smem_u32(stay)), d_ring = sdesc_sw128(smem_u32(ring));
     uint32_t un = 0, free_ph = 0, ready_ph = 0, slot = 0, slot_ph = 0;   // units; phase bits of s_free and of k_ready; the ring's next tile
-    for (int it = 0, w; (w = kw_unit_at(it)) < units; ++it) {
-        const KwUnit u = kw_unit(a, w);
+    KwUnit u;
+    for (KwLine l = kw_line(a, blockIdx.x); kw_next(a, l, u);) {
         if (!u.pass) continue;
         const int set = un & 1;
         if (!kw_wait(&sh->st_full[set], (un >> 1) & 1, sh)) break;
@@ -251,13 +230,13 @@ FQ_DEV void kw_products(const Args& a, KwShared* sh, uint8_t* stay, uint8_t* rin
 // ---------------- warp 18: -lse log2(e) of the rows of query blocks, for y = 0 and 1 in turn where keys stay, for both where
 // query blocks do.  A block's values are on their way while the one before is put down.
 template <class Args>
-FQ_DEV void kw_statistics(const Args& a, KwShared* sh, int units, int lane) {
+FQ_DEV void kw_statistics(const Args& a, KwShared* sh, int lane) {
     constexpr float LOG2E = 1.4426950408889634f;
     const int shift = a.g_shift, G = 1 << shift;
     uint32_t blk[2] = {0, 0};
     bool ok = true;
-    for (int it = 0, w; (w = kw_unit_at(it)) < units && ok; ++it) {
-        const KwUnit u = kw_unit(a, w);
+    KwUnit u;
+    for (KwLine l = kw_line(a, blockIdx.x); ok && kw_next(a, l, u);) {
         if (u.kind == KW_NONE) continue;
         const AttnSeq& sq = a.seq[u.seq];
         const int n = u.b1 - u.b0;
@@ -325,6 +304,11 @@ FQ_DEV float kw_row(uint32_t tS, uint64_t* s_free, const float* neg, uint64_t c2
             ulonglong2 m[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) m[k] = *reinterpret_cast<const ulonglong2*>(neg + at + 4 * k);
+            [[maybe_unused]] uint32_t seen = 0;   // a bit per column
+            if (PART) {
+                const int from = max(0, min(16, lo - at)), to = max(0, min(16, hi - at));
+                seen = (1u << to) - 1 >> from << from;
+            }
             tmem_wait_ld16(x[b]);
             if (b == 0 || h + 32 < columns) {
                 tmem_ld16(tS + at + 16, x[b ^ 1]);
@@ -341,7 +325,7 @@ FQ_DEV float kw_row(uint32_t tS, uint64_t* s_free, const float* neg, uint64_t c2
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     p[e] = ex2(p[e]);
-                    if (PART) p[e] = at + k + e >= lo && at + k + e < hi ? p[e] : 0.f;
+                    if (PART) p[e] = seen & 1u << (k + e) ? p[e] : 0.f;
                 }
                 acc[(k >> 1) & 3] = add2(acc[(k >> 1) & 3], pair(p[0], p[1]));
                 acc[((k >> 1) & 3) + 1] = add2(acc[((k >> 1) & 3) + 1], pair(p[2], p[3]));
@@ -367,23 +351,27 @@ FQ_DEV KwRange kw_range(const AttnMask& m, const AttnSeq& sq, int key, int b, in
     return KwRange{(int)max(-FAR, min(FAR, lo)), (int)max(-FAR, min(FAR, hi))};
 }
 
+// what a key had before (maybe where `after` is written)
+FQ_DEV float kw_had(const KeyWeights& w, bool more, int head, int64_t row) {
+    return more ? w.after[head * w.after_stride + row] : w.before ? w.before[head * w.before_stride + row] : 0.f;
+}
+
 template <class Args>
-FQ_DEV void kw_sum(const Args& a, KwShared* sh, const uint8_t* stay, int units, uint32_t tm, int wg, int row, int lane) {
+FQ_DEV void kw_sum(const Args& a, KwShared* sh, const uint8_t* stay, uint32_t tm, int wg, int row, int lane) {
     const int x = wg & 1, y = wg >> 1, shift = a.g_shift;
     const uint32_t lanes = (uint32_t)(row >> 5) << 21, tS = tm + KW_S + KW_BLOCK * wg + lanes;
     const uint64_t c2 = pair(a.c, a.c);
     uint32_t tile = 0, blk = 0, halves = 0;   // score tiles; query blocks of this y; units whose halves were added
     uint32_t un = 0, moved = 0;               // units with tiles; key tiles moved
     bool ok = true;
-    for (int it = 0, w; (w = kw_unit_at(it)) < units && ok; ++it) {
-        const KwUnit u = kw_unit(a, w);
+    KwUnit u;
+    for (KwLine l = kw_line(a, blockIdx.x); ok && kw_next(a, l, u);) {
         const AttnSeq& sq = a.seq[u.seq];
         const KeyWeights& kw = a.w[Args::VIEWS == 1 ? 0 : sq.view];
         auto finish = [&](int key, float sum) {
             if (key >= sq.k_len) return;
             const int64_t r = sq.k_row0 + key;
-            if (kw.before) sum += kw.before[u.head * kw.before_stride + r];   // (maybe where `after` is written)
-            kw.after[u.head * kw.after_stride + r] = sum;
+            kw.after[u.head * kw.after_stride + r] = kw_had(kw, u.more, u.head, r) + sum;
         };
         if (u.kind == KW_NONE) {
             for (int64_t key = (int64_t)u.j0 * TILE_ROWS + TILE_ROWS * wg + row; key < min((int64_t)sq.k_len, (int64_t)u.j1 * TILE_ROWS); key += 4 * TILE_ROWS)
@@ -404,8 +392,18 @@ FQ_DEV void kw_sum(const Args& a, KwShared* sh, const uint8_t* stay, int units, 
             ++tile;
             tc_fence_after();
             const float* neg = sh->neg[y][s];
-            return __any_sync(0xFFFFFFFFu, lo > 0 || hi < columns) ? kw_row<true>(tS, s_free, neg, c2, columns, lo, hi, lane)
-                                                                 : kw_row<false>(tS, s_free, neg, c2, columns, lo, hi, lane);
+            // (keys that see none of these rows beside keys that see all of them: a window's sinks)
+            const bool all = lo <= 0 && hi >= columns, none = lo >= min(hi, columns) || hi <= 0;
+            if (__all_sync(0xFFFFFFFFu, none)) {
+                if (s_free) {
+                    tc_fence_before();
+                    if (lane == 0) mbar_arrive(s_free);
+                }
+                return 0.f;
+            }
+            if (__any_sync(0xFFFFFFFFu, !all && !none)) return kw_row<true>(tS, s_free, neg, c2, columns, lo, hi, lane);
+            const float sum = kw_row<false>(tS, s_free, neg, c2, columns, lo, hi, lane);
+            return none ? 0.f : sum;
         };
         if (u.kind == KW_ROWS) {
             ++un;
@@ -480,7 +478,7 @@ FQ_DEV void kw_sum(const Args& a, KwShared* sh, const uint8_t* stay, int units, 
             continue;
         }
         if (u.slot < 0) finish(key, total.sum);
-        else a.part[((int64_t)u.slot * a.Hkv + u.head) * (KW_KEY_TILES * TILE_ROWS) + x * TILE_ROWS + row] = total.sum;
+        else a.part[(int64_t)u.slot * (KW_KEY_TILES * TILE_ROWS) + x * TILE_ROWS + row] = total.sum;
     }
 }
 
@@ -491,7 +489,6 @@ __global__ void __launch_bounds__(KW_THREADS, 1) key_weights_kernel(const __grid
     uint8_t* ring = smem + 4 * KW_TILE_BYTES;
     KwShared* sh = reinterpret_cast<KwShared*>(ring + KW_RING * KW_TILE_BYTES);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int units = a.n_entries * a.Hkv;
     pdl_trigger();
     if (warp == 16) {
         if (lane == 0) {
@@ -525,10 +522,10 @@ __global__ void __launch_bounds__(KW_THREADS, 1) key_weights_kernel(const __grid
     tc_fence_after();
     const uint32_t tm = sh->tmem;
     if (wait_limit(sh) != 0) {   // (not with a misaligned base)
-        if (warp < 16) kw_sum(a, sh, stay, units, tm, warp >> 2, tid & 127, lane);
-        else if (warp == 16) kw_load(a, sh, stay, ring, units);
-        else if (warp == 18) kw_statistics(a, sh, units, lane);
-        else if (elect_one()) kw_products(a, sh, stay, ring, units, tm);
+        if (warp < 16) kw_sum(a, sh, stay, tm, warp >> 2, tid & 127, lane);
+        else if (warp == 16) kw_load(a, sh, stay, ring);
+        else if (warp == 18) kw_statistics(a, sh, lane);
+        else if (elect_one()) kw_products(a, sh, stay, ring, tm);
         __syncwarp();
     }
     tc_fence_before();
@@ -538,19 +535,25 @@ __global__ void __launch_bounds__(KW_THREADS, 1) key_weights_kernel(const __grid
     if (tid == 0 && wait_limit(sh) == 0) atomicAdd(a.waits.record, 1u);
 }
 
-// Sums of keys whose query blocks were cut into several units.
-__global__ void __launch_bounds__(KW_KEY_TILES* TILE_ROWS) key_weights_join_kernel(const __grid_constant__ KwJoinArgs a) {
-    const KwJoin e = a.e[blockIdx.x / a.Hkv];
-    const int head = blockIdx.x % a.Hkv;
-    const AttnSeq& sq = a.seq[e.seq];
-    const KeyWeights& kw = a.w[e.seq];
-    const int64_t key = (int64_t)e.j0 * TILE_ROWS + threadIdx.x;
+// Sums of keys that several thread blocks have parts of.
+template <class Args>
+__global__ void __launch_bounds__(KW_KEY_TILES* TILE_ROWS) key_weights_join_kernel(const __grid_constant__ Args a) {
+    const int i = blockIdx.x / a.Hkv, head = blockIdx.x - i * a.Hkv;
+    const KwEntry& e = a.e[i];
+    int c0 = 0, c1 = 0;
+    if (!(e.info & (KW_ROWS | KW_NONE))) kw_parts(a, i, head, c0, c1);
     pdl_wait();   // the partial sums are written
+    if (c0 == c1) return;
+    const AttnSeq& sq = a.seq[e.info & 127];
+    const KeyWeights& kw = a.w[Args::VIEWS == 1 ? 0 : sq.view];
+    const int64_t key = (int64_t)e.j0 * TILE_ROWS + threadIdx.x;
     if (key >= sq.k_len || key >= (int64_t)e.j1 * TILE_ROWS) return;
-    float sum = kw.before ? kw.before[head * kw.before_stride + sq.k_row0 + key] : 0.f;
-    float part = 0.f;
-    for (int i = 0; i < e.n; ++i) part += a.part[((int64_t)(e.slot + i) * a.Hkv + head) * (KW_KEY_TILES * TILE_ROWS) + threadIdx.x];
-    kw.after[head * kw.after_stride + sq.k_row0 + key] = sum + part;
+    const int64_t row = sq.k_row0 + key;
+    const float had = kw_had(kw, e.info & KW_MORE, head, row);
+    float sum = 0.f;
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) sum += a.part[(int64_t)(2 * c + (c == c0)) * (KW_KEY_TILES * TILE_ROWS) + threadIdx.x];
+    kw.after[head * kw.after_stride + row] = had + sum;
 }
 
 }  // namespace
@@ -567,17 +570,16 @@ cudaError_t key_weights_prepare() {
 }
 
 template <class Args>
-void launch_key_weights(const Args& a, cudaStream_t s) {
-    const int64_t units = (int64_t)a.n_entries * a.Hkv;
-    const int grid = (int)(units < ATTN_SMS ? units : ATTN_SMS);
+void launch_key_weights(const Args& a, int grid, cudaStream_t s) {
     key_weights_kernel<Args><<<grid, KW_THREADS, KW_SMEM, s>>>(a);
 }
-template void launch_key_weights<KwArgs1S>(const KwArgs1S&, cudaStream_t);
-template void launch_key_weights<KwArgs1M>(const KwArgs1M&, cudaStream_t);
-template void launch_key_weights<KwArgs1>(const KwArgs1&, cudaStream_t);
-template void launch_key_weights<KwArgsN>(const KwArgsN&, cudaStream_t);
+template void launch_key_weights<KwArgs1S>(const KwArgs1S&, int, cudaStream_t);
+template void launch_key_weights<KwArgs1M>(const KwArgs1M&, int, cudaStream_t);
+template void launch_key_weights<KwArgs1>(const KwArgs1&, int, cudaStream_t);
+template void launch_key_weights<KwArgsN>(const KwArgsN&, int, cudaStream_t);
 
-void launch_key_weights_join(const KwJoinArgs& a, cudaStream_t s) {
+template <class Args>
+void launch_key_weights_join(const Args& a, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3((unsigned)((int64_t)a.n_entries * a.Hkv));
@@ -587,7 +589,11 @@ void launch_key_weights_join(const KwJoinArgs& a, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, key_weights_join_kernel, a);
+    cudaLaunchKernelEx(&cfg, key_weights_join_kernel<Args>, a);
 }
+template void launch_key_weights_join<KwArgs1S>(const KwArgs1S&, cudaStream_t);
+template void launch_key_weights_join<KwArgs1M>(const KwArgs1M&, cudaStream_t);
+template void launch_key_weights_join<KwArgs1>(const KwArgs1&, cudaStream_t);
+template void launch_key_weights_join<KwArgsN>(const KwArgsN&, cudaStream_t);
 
 }  // namespace fq

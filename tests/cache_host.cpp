@@ -90,26 +90,43 @@ template void launch_attn_join<JoinArgsL>(const JoinArgsL&, cudaStream_t);
 
 void launch_qk_paged(const QkPagedArgs& a, cudaStream_t) { g_launches.push_back({3, a.rows, a.pages.shift, a.pages.n_pages, a.pages.table_stride}); }
 
-// 4, entries of the type, views of the type, Hq, Hkv, window, sinks, n, n x (info, j0, j1, b0, b1, slot), 64 sequences
+// 4, entries of the type, views of the type, Hq, Hkv, window, sinks, thread blocks, entries, units, units x (sequence, head, kind,
+// more, j0, j1, b0, b1, slot), 64 sequences
 template <class Args>
-void launch_key_weights(const Args& a, cudaStream_t) {
+void launch_key_weights(const Args& a, int grid, cudaStream_t) {
     std::vector<long long> v;
-    put(v, 4, Args::ENTRIES, Args::VIEWS, a.Hq, a.Hkv, a.mask.window, a.mask.sinks, a.n_entries);
-    for (int i = 0; i < a.n_entries; ++i) put(v, a.e[i].info, a.e[i].j0, a.e[i].j1, a.e[i].b0, a.e[i].b1, a.e[i].slot);
+    put(v, 4, Args::ENTRIES, Args::VIEWS, a.Hq, a.Hkv, a.mask.window, a.mask.sinks, grid, a.n_entries, 0);
+    for (int c = 0; c < grid; ++c) {
+        KwUnit u;
+        for (KwLine l = kw_line(a, c); kw_next(a, l, u); ++v[9])
+            put(v, u.seq, u.head, u.kind >> 7, (int)u.more, u.j0, u.j1, u.b0, u.b1, u.slot);
+    }
     put_seqs(v, a.seq, MAX_SEQ);
     g_launches.push_back(v);
 }
-template void launch_key_weights<KwArgs1S>(const KwArgs1S&, cudaStream_t);
-template void launch_key_weights<KwArgs1M>(const KwArgs1M&, cudaStream_t);
-template void launch_key_weights<KwArgs1>(const KwArgs1&, cudaStream_t);
-template void launch_key_weights<KwArgsN>(const KwArgsN&, cudaStream_t);
-// 5, n, n x (sequence, j0, j1, slot, parts)
-void launch_key_weights_join(const KwJoinArgs& a, cudaStream_t) {
+template void launch_key_weights<KwArgs1S>(const KwArgs1S&, int, cudaStream_t);
+template void launch_key_weights<KwArgs1M>(const KwArgs1M&, int, cudaStream_t);
+template void launch_key_weights<KwArgs1>(const KwArgs1&, int, cudaStream_t);
+template void launch_key_weights<KwArgsN>(const KwArgsN&, int, cudaStream_t);
+// 5, n, n x (sequence, head, more, j0, j1, first slot, first of the others' slots, others: two slots apart) of the sums that are joined
+template <class Args>
+void launch_key_weights_join(const Args& a, cudaStream_t) {
     std::vector<long long> v;
-    put(v, 5, a.n_entries);
-    for (int i = 0; i < a.n_entries; ++i) put(v, a.e[i].seq, a.e[i].j0, a.e[i].j1, a.e[i].slot, a.e[i].n);
+    put(v, 5, 0);
+    for (int i = 0; i < a.n_entries; ++i)
+        for (int h = 0; h < a.Hkv && !(a.e[i].info & (KW_ROWS | KW_NONE)); ++h) {
+            int c0, c1;
+            kw_parts(a, i, h, c0, c1);
+            if (c0 == c1) continue;
+            put(v, a.e[i].info & 127, h, (a.e[i].info & KW_MORE) != 0, a.e[i].j0, a.e[i].j1, 2 * c0 + 1, 2 * (c0 + 1), c1 - c0);
+            ++v[1];
+        }
     g_launches.push_back(v);
 }
+template void launch_key_weights_join<KwArgs1S>(const KwArgs1S&, cudaStream_t);
+template void launch_key_weights_join<KwArgs1M>(const KwArgs1M&, cudaStream_t);
+template void launch_key_weights_join<KwArgs1>(const KwArgs1&, cudaStream_t);
+template void launch_key_weights_join<KwArgsN>(const KwArgsN&, cudaStream_t);
 // 6, longest, blocks, n, n x (rows, rows that stay, first number, first block)
 void launch_evict(const EvictArgs& a, int max_len, int blocks, cudaStream_t) {
     std::vector<long long> v;

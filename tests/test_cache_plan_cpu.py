@@ -246,50 +246,60 @@ def check_weights(host, q_len, k_len, hq, hkv, window, sinks, own_views):
         fq.fq_attn_key_weights(P, P, views, q_len, k_len, hq, hkv, window, sinks, 0.1, None, after, P if ws else 0, ws)
         raw = launches()
     G = hq // hkv
-    units, joins = [], {}
-    for v in raw:
-        if v[0] == 4:
-            assert v[7] <= v[1] and tuple(v[5:7]) == (window or 1 << 30, sinks)
-            units += [tuple(v[8 + 6 * i:14 + 6 * i]) for i in range(v[7])]
-        else:
-            for i in range(v[1]):
-                s, j0, j1, slot, n = v[2 + 5 * i:7 + 5 * i]
-                for p in range(n):
-                    assert slot + p not in joins
-                    joins[slot + p] = s, j0, j1
-    written, met = {}, {}
-    slots = set()
-    for info, j0, j1, b0, b1, slot in units:
-        s, kind = info & 127, info >> 7
-        assert 0 <= j0 < j1 and j1 - j0 <= 4096 and b1 - b0 <= 4096
-        if slot >= 0:
-            assert slot not in slots and joins[slot] == (s, j0, j1) and kind == 0
-            assert (slot + 1) * hkv * 256 * 4 <= ws
-            slots.add(slot)
-        for j in range(j0, j1):
-            if slot < 0:
-                assert (s, j) not in written, "a key is written twice"
-                written[s, j] = True
-            elif joins[slot] == (s, j0, j1):
-                written[s, j] = True
-            if kind < 2:
-                for b in range(b0, b1):
-                    assert (s, j, b) not in met
-                    met[s, j, b] = True
-        if kind == 0:
-            assert j1 - j0 <= 2
-        if kind == 1:
-            assert (b0, b1) == (0, 1)
-    assert slots == set(joins)
+    written, met = {}, set()       # (sequence, head, key tile): how often; (sequence, head, key tile, query block)
+
+    def write(s, h, j, more):      # the first time what was there before is added to, then what has been written
+        assert more == ((s, h, j) in written), "a key's earlier sums are lost"
+        written[s, h, j] = True
+
+    def joined(units, join):
+        """One launch: its unfinished sums against the list of those that are joined."""
+        parts = {}
+        for s, h, kind, more, j0, j1, b0, b1, slot in units:
+            if slot >= 0:
+                assert kind == 0 and slot not in parts and (slot + 1) * 256 * 4 <= ws
+                parts[slot] = s, h, more, j0, j1
+        for s, h, more, j0, j1, first, others, n in join:
+            for slot in [first] + [others + 2 * i for i in range(n)]:
+                assert parts.pop(slot) == (s, h, more, j0, j1)
+            for j in range(j0, j1):
+                write(s, h, j, more)
+        assert not parts, "sums that nobody adds up"
+
+    i = 0
+    while i < len(raw):
+        v = raw[i]
+        assert v[0] == 4 and v[8] <= v[1] and v[7] <= 152 and tuple(v[5:7]) == (window or 1 << 30, sinks)
+        units = [tuple(v[10 + 9 * u:19 + 9 * u]) for u in range(v[9])]
+        join = []
+        if i + 1 < len(raw) and raw[i + 1][0] == 5:
+            i += 1
+            join = [tuple(raw[i][2 + 8 * e:10 + 8 * e]) for e in range(raw[i][1])]
+        i += 1
+        for s, h, kind, more, j0, j1, b0, b1, slot in units:
+            assert 0 <= j0 < j1 and 0 <= b0 < b1 and b1 - b0 <= 4096
+            if kind == 0:
+                assert j1 - j0 <= 2
+            if kind == 1:
+                assert (b0, b1) == (0, 1) and j1 - j0 <= 4096
+            for j in range(j0, j1):
+                if slot < 0:
+                    write(s, h, j, more)
+                for b in range(b0, b1) if kind < 2 else ():
+                    assert (s, h, j, b) not in met
+                    met.add((s, h, j, b))
+        joined(units, join)
     for s, (L, K) in enumerate(zip(q_len, k_len)):
-        for j in range(-(-K // TILE)):
-            assert (s, j) in written, f"keys of tile {j} of sequence {s} are not written"
+        for h in range(hkv):
+            for j in range(-(-K // TILE)):
+                assert (s, h, j) in written, f"keys of tile {j} of sequence {s} are not written"
         step = max(1, L // 40)
         for i in list(range(0, L, step)) + [L - 1] * (L > 0):
             for lo, hi in visible(i, L, K, window, sinks):
                 for j in range(lo // TILE, -(-hi // TILE)):
                     for b in {i * G // BLOCK, (i * G + G - 1) // BLOCK}:
-                        assert (s, j, b) in met, f"row {i} and key tile {j} of sequence {s} do not meet"
+                        for h in {0, hkv // 2, hkv - 1}:
+                            assert (s, h, j, b) in met, f"row {i} and key tile {j} of sequence {s} do not meet"
 
 
 @pytest.mark.parametrize("seed", range(4))
@@ -308,6 +318,9 @@ def test_weights_of_long_sequences(host):
     check_weights(host, [8192], [8192], 32, 8, 1000, 4, False)
     check_weights(host, [1] * 64, [300] * 63 + [60000], 8, 1, 100, 4, True)
     check_weights(host, [70] * 3, [50000] * 3, 32, 4, 0, 0, False)
+    check_weights(host, [60000, 1, 50], [500, 600000, 1000], 8, 1, 0, 0, False)    # more query blocks, key tiles than an entry has
+    check_weights(host, [400000] * 2, [300, 256], 4, 4, 0, 0, True)
+    check_weights(host, [0, 0], [1 << 25, 100], 4, 4, 0, 0, False)
 
 
 def test_evict_blocks_and_numbers(host):
