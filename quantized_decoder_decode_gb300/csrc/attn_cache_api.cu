@@ -191,7 +191,13 @@ fq_status run_groups(const Plan& p, const Call& c, cudaStream_t s) {
         } else {
             a.kv[g] = c.use[c.seq[p.groups[g].seq].view].rows;
         }
-        for (int i = 0; i < chunks(p, g); ++i) a.group[p.groups[g].item0 + i] = (uint8_t)g;
+        a.pos[g] = p.pos[g];
+    }
+    a.n_groups = (int)p.groups.size();
+    a.share = p.share;
+    for (int i = 0, g = 0; i < p.items; ++i) {   // the first group that ends behind the part's beginning
+        while (g + 1 < a.n_groups && a.pos[g + 1] <= i * a.share) ++g;
+        a.group[i] = (uint8_t)g;
     }
     launch_attn_window_rows(a, !p.tiles.empty(), s);
     CK(cudaGetLastError());

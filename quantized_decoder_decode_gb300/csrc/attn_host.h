@@ -183,8 +183,11 @@ struct Plan {
     std::vector<RowGroup> groups;
     std::vector<JoinEntry> join;
     int64_t a_slots = 0, b_slots = 0;   // partial blocks of 128 and of 8 rows
-    int items = 0;                      // chunks of the groups
-    bool even = false;                  // long sequences beside many short ones are cut as well (see choose and plan_groups)
+    int items = 0;                      // chunks of the groups; parts of their line
+    std::vector<int64_t> pos;           // on the line: of the groups
+    std::vector<int> parts;             // .. items that have a part of them
+    int64_t share = 0;                  // .. an item's part
+    bool even = false;                  // work in equal parts: groups on a line, long units beside many short ones cut as well
 
     size_t a_bytes(uint32_t Hkv) const { return (size_t)a_slots * Hkv * TILE_ROWS * HEAD_DIM * 4; }
     size_t b_bytes(uint32_t Hkv) const { return (size_t)b_slots * Hkv * SMALL_ROWS * HEAD_DIM * 4; }
@@ -326,10 +329,37 @@ void add_group(Plan& p, const AttnSeq& q, int s, const AttnMask& m = AttnMask())
     p.groups.push_back(RowGroup{q.q_row0, q.q_len, q.k_row0, q.k_len, q.off, s, 0, 0, -1, key_span(m, q.k_len, q.off, q.q_len).n});
 }
 
+// An item's part of the line, at least, beside tiles, which leave fewer SMs (seven tokens and a chunk of 333 25.9 us, 27.0 with the 192
+// of rows alone).
+constexpr int64_t ROWS_BESIDE = 288;
+
+// Lays the groups on a line and cuts it into equal parts, whose CTAs run all at once.
+void plan_line(Plan& p, uint32_t Hkv, bool tiled) {
+    int64_t line = 0;
+    for (auto& g : p.groups) {
+        p.pos.push_back(line);
+        line += rows_line(g.keys);
+    }
+    const int64_t items = std::max<int64_t>(1, ROWS_CTAS / Hkv);
+    p.share = std::max<int64_t>(tiled ? ROWS_BESIDE : ROWS_CHUNK + ROWS_START, (line + items - 1) / items);
+    p.items = ceil_div(line, p.share);
+    for (size_t i = 0; i < p.groups.size(); ++i) {
+        RowGroup& g = p.groups[i];
+        const int64_t first = p.pos[i] + ROWS_START;
+        int last;
+        rows_items(p.share, first, g.keys, g.item0, last);
+        p.parts.push_back(last - g.item0 + 1);
+        if (p.parts[i] > 1) {
+            g.slot0 = (int)p.b_slots;
+            p.b_slots += p.parts[i];
+        }
+    }
+}
+
 // Chunks the keys of the groups: the shortest chunks whose CTAs still run all at once, the longest chunks
 // first (behind tiles, CTAs start as SMs become free).  Chosen at 16 sequences, 32 / 8 heads, 512 to 4096 keys (38 us
 // cold, floor 22; 48: 96, floor 67; 64: 114, floor 89); where the sequences alone fill a wave the longest is hardly
-// split any more (55 over 500 keys and one over 30000: 268 us, floor 35; 63 and one: 513).
+// split any more (55 over 500 keys and one over 30000: 268 us, floor 35; 63 and one: 513), unlike on a line.
 void plan_groups(Plan& p, uint32_t Hkv, bool partial) {
     auto ctas = [&](int64_t per) {
         int64_t n = 0;
@@ -343,9 +373,6 @@ void plan_groups(Plan& p, uint32_t Hkv, bool partial) {
     }
     int64_t per = std::max(ROWS_CHUNK, (keys * Hkv + ROWS_CTAS - 1) / ROWS_CTAS / 64 * 64);
     while (per < longest && ctas(per) > ROWS_CTAS) per += std::max<int64_t>(64, per / 32 / 64 * 64);
-    // one wave of very uneven chunks: a second wave of short ones costs less (rounded up, the chunks are at most MAX_ITEMS)
-    const int64_t share = std::max(ROWS_CHUNK, (keys * Hkv + ROWS_CTAS - 1) / ROWS_CTAS + 63) / 64 * 64;
-    if (p.even && per > 2 * share) per = share;
     for (auto& g : p.groups) {
         const int splits = std::max(1, ceil_div(g.keys, per));
         g.chunk = std::max(64, ceil_div(ceil_div(g.keys, splits), 64) * 64);
@@ -364,7 +391,10 @@ void plan_groups(Plan& p, uint32_t Hkv, bool partial) {
         }
     }
 }
-int chunks(const Plan& p, size_t g) { return (g + 1 < p.groups.size() ? p.groups[g + 1].item0 : p.items) - p.groups[g].item0; }
+int chunks(const Plan& p, size_t g) {
+    if (p.even) return p.parts[g];
+    return (g + 1 < p.groups.size() ? p.groups[g + 1].item0 : p.items) - p.groups[g].item0;
+}
 
 void plan_prompt(Plan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G, uint32_t Hkv, const AttnMask& m = AttnMask()) {
     const int tpt = TILE_ROWS / (int)G;
@@ -385,7 +415,8 @@ void plan_prompt(Plan& p, uint32_t n_seq, const AttnSeq* seq, uint32_t G, uint32
             add_group(p, seq[s], (int)s, m);
         }
     }
-    plan_groups(p, Hkv, false);
+    if (p.even) plan_line(p, Hkv, tiled);
+    else plan_groups(p, Hkv, false);
     for (size_t g = 0; g < p.groups.size(); ++g) {
         const RowGroup& r = p.groups[g];
         if (r.slot0 >= 0) p.join.push_back(JoinEntry{r.q_row0, r.n_tok, r.k_len, r.off, 0, 0, 0, 0, r.slot0, chunks(p, g), 0, 0, 0});

@@ -229,12 +229,56 @@ struct RowsArgs {
     RowGroup g[MAX_GROUPS];
     KvRows kv[MAX_GROUPS];
 };
+// Windows and pages: the groups' keys lie on a line, of which an item (a CTA per kv head) takes an equal part, whatever groups that
+// meets.  group: the first group of an item's part.  (A chunk of one group per item left some SMs three long ones and
+// others two: window of 2048, 16 single tokens, 32 / 8 heads, 25 % above the mean.)
 template <bool PAGES>
 struct WindowRowsArgs : RowsArgs {
     static constexpr bool WINDOW = true, PAGED = PAGES;
     AttnMask mask;
     KvPages pages;
+    int n_groups;
+    int64_t share;              // an item's part of the line
+    int64_t pos[MAX_GROUPS];    // where a group begins on it: ROWS_START, then its keys
 };
+// What the beginning of a group costs in keys (32: 32 tokens over pages 50.9 us, four tokens over 100 keys 9.0; 64: 49.8 and
+// 5.4; 128: 51.0 and 5.3).
+constexpr int ROWS_START = 64;
+constexpr int ROWS_WHOLE = 128;   // keys of a group that is not cut, at most: the item with the first of them takes all
+// Keys that a CTA's warps take at a time: cuts are whole ones from a group's first key on (60000 keys, one token 47.7 us, cut
+// at any 16 keys 48.3).
+constexpr int ROWS_STEP = 64;
+FQ_HD inline int64_t rows_line(int keys) { return ROWS_START + (keys > 0 ? ((int64_t)keys + ROWS_STEP - 1) / ROWS_STEP * ROWS_STEP : ROWS_STEP); }
+// Where a cut of the line falls in a group that begins at `first`, in keys.
+FQ_HD inline int rows_cut(int64_t cut, int64_t first, int keys) {
+    if (cut <= first) return 0;
+    const int64_t at = (cut - first) / ROWS_STEP * ROWS_STEP;
+    return at < keys ? (int)at : keys;
+}
+// The items that have a part of it: [i0, i1].
+FQ_HD inline void rows_items(int64_t share, int64_t first, int keys, int& i0, int& i1) {
+    i0 = (int)((first + (keys > ROWS_WHOLE ? ROWS_STEP - 1 : 0)) / share);
+    i1 = keys > ROWS_WHOLE ? (int)((first + ((int64_t)keys + ROWS_STEP - 1) / ROWS_STEP * ROWS_STEP - 1) / share) : i0;
+}
+// The next group from g on of which the item has a part, and the numbers [c0, c1) of its keys; false: there is none.
+template <class Args>
+FQ_HD inline bool rows_part(const Args& a, int item, int& g, int& c0, int& c1) {
+    const int64_t begin = item * a.share, end = begin + a.share;
+    for (; g < a.n_groups && a.pos[g] < end; ++g) {
+        const int keys = a.g[g].keys;
+        const int64_t first = a.pos[g] + ROWS_START;
+        c0 = rows_cut(begin, first, keys);
+        c1 = rows_cut(end, first, keys);
+        if (keys <= ROWS_WHOLE) {
+            c0 = 0;
+            c1 = keys;
+            if (first >= begin && first < end) return true;
+        } else if (c0 < c1) {
+            return true;
+        }
+    }
+    return false;
+}
 cudaError_t attn_rows_prepare();      // per device, before the first launch
 cudaError_t attn_window_rows_prepare();
 // beside: it may run beside launch_tiles of the same call, launched just before

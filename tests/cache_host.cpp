@@ -62,13 +62,13 @@ template void launch_tiles<PagedArgsL>(const PagedArgsL&, cudaStream_t);
 template <bool PAGED>
 void rows(const WindowRowsArgs<PAGED>& a, bool beside) {
     std::vector<long long> v;
-    put(v, 1, beside, a.io.Hq, a.io.Hkv, a.mask.window, a.mask.sinks, a.n_items);
+    put(v, 1, beside, a.io.Hq, a.io.Hkv, a.mask.window, a.mask.sinks, 0);
     if (a.n_items > MAX_ITEMS) abort();
-    for (int i = 0; i < a.n_items; ++i) {
-        const RowGroup& g = a.g[a.group[i]];
-        const int c = i - g.item0;
-        put(v, g.q_row0, g.n_tok, g.k_row0, g.k_len, g.off, (long long)c * g.chunk, g.chunk, g.slot0 < 0 ? -1 : g.slot0 + c, g.seq);
-    }
+    for (int i = 0; i < a.n_items; ++i)
+        for (int n = a.group[i], c0, c1; rows_part(a, i, n, c0, c1); ++n, ++v[6]) {
+            const RowGroup& g = a.g[n];
+            put(v, g.q_row0, g.n_tok, g.k_row0, g.k_len, g.off, c0, c1 - c0, g.slot0 < 0 ? -1 : g.slot0 + i - g.item0, g.seq);
+        }
     g_launches.push_back(v);
 }
 void launch_attn_window_rows(const WindowRowsArgs<false>& a, bool beside, cudaStream_t) { rows(a, beside); }

@@ -69,7 +69,9 @@ def test_paged(hq, hkv, q_len, k_len, page, layout):
 
 
 def test_without_a_window_is_prompt_attention():
-    """window 0, and one that reaches every key: the same numbers as fq_attn_prompt, bit for bit."""
+    """window 0, and one that reaches every key: the same numbers as fq_attn_prompt, bit for bit.  But for the single token
+    over 3000 keys (row 700), whose keys the two calls cut at other places: the weights of a cut are rounded to 8 bits
+    against its own largest score, so both are within the bound of their roundings and need not be equal."""
     g, hq, hkv, q_len, k_len = gen(3), 8, 2, [700, 1, 40, 9], [700, 3000, 1040, 9]
     q = normal(g, sum(q_len), hq, D)
     k, v = cache(g, sum(k_len), hkv), cache(g, sum(k_len), hkv)
@@ -78,7 +80,10 @@ def test_without_a_window_is_prompt_attention():
     fq.fq_attn_prompt(q.data_ptr(), view(k, v), q_len, k_len, hq, hkv, SCALE, want.data_ptr(), ws.data_ptr(), ws.numel() * 4, stream())
     for window, sinks in ((0, 0), (0, 7), (5000, 0), (2 ** 32 - 1, 2 ** 32 - 1)):
         got, _ = run_window(q, view(k, v), q_len, k_len, hq, hkv, window, sinks, lse=False)
-        assert bool((got == want).all()), (window, sinks)
+        same = [r for r in range(sum(q_len)) if r != 700]
+        assert bool((got[same] == want[same]).all()), (window, sinks)
+        ref, bound, _, _ = reference(q, packed(k, v, k_len), q_len, k_len, hq, hkv, 0, 0)
+        assert_within(got, ref, bound, True, f"window {window} {sinks}")
 
 
 @pytest.mark.parametrize("paged", [False, True])
