@@ -212,7 +212,9 @@ def test_every_visible_key_once(host, seed):
 
 
 def test_long_beside_many_short(host):
-    """Calls with so many units or groups that whole ones fill the SMs: the long one is cut all the same."""
+    """Calls with so many units or groups that whole ones fill the SMs: the long one is cut all the same.  And more heads than
+    thread blocks."""
+    check_window(host, [1, 2, 0, 30], [3000, 64, 5, 100], 1000, 1000, 0, 0, False)
     for q, k in (([1] * 56, [500] * 55 + [30000]), ([20] * 60 + [200], [20] * 60 + [30200]), ([1] * 64, [1] * 63 + [1 << 20])):
         for paged in (False, True):
             check_window(host, q, k, 32, 8, 0, 0, paged)
@@ -321,6 +323,7 @@ def test_weights_of_long_sequences(host):
     check_weights(host, [60000, 1, 50], [500, 600000, 1000], 8, 1, 0, 0, False)    # more query blocks, key tiles than an entry has
     check_weights(host, [400000] * 2, [300, 256], 4, 4, 0, 0, True)
     check_weights(host, [0, 0], [1 << 25, 100], 4, 4, 0, 0, False)
+    check_weights(host, [300, 1], [200, 900], 1000, 1000, 0, 0, False)
 
 
 def test_evict_blocks_and_numbers(host):

@@ -43,7 +43,7 @@ def gathered(q, lse, k, seen, scale):
     A weight 2^x, x = c q.k - log2(e) lse: the dot product carries at most 128 2^-24 sum_d |q_d k_d| scale, c and the
     product with it three roundings of the score, lse's product two of lse, the subtraction one of both; exp2 2^-21.  The
     weights of a tile are added up in 8 sums of 16 and these in 3 steps; tiles by compensated addition, whose error is 2 steps; 16
-    partial sums of units and what the key had at most, a step each."""
+    partial sums of thread blocks and what the key had at most, a step each."""
     out, bound = (torch.zeros(k.shape[0], dtype=torch.float64, device=DEV) for _ in range(2))
     k = torch.where(seen.any(dim=0)[:, None], k.double(), 0.0)
     for g in range(q.shape[1]):
@@ -100,6 +100,31 @@ def test_key_weights(hq, hkv, q_len, k_len, window, sinks):
     assert bool((got[:, rows:] == 5).all())
     run(q, lse, view(k), q_len, k_len, hq, hkv, window, sinks, weights(was), weights(was))   # in place, the same bits
     assert bool((was[:, :rows] == got[:, :rows]).all())
+
+
+@pytest.mark.parametrize("hq,hkv,q_len,k_len", [(520, 520, [200, 1], [300, 700]), (1, 1, [9000, 3], [700, 90000]),
+                                                (8, 1, [12] * 40, [30 * i for i in range(40)])])
+def test_key_weights_many_and_few_heads(hq, hkv, q_len, k_len):
+    """More kv heads than thread blocks; one, whose work all of them share out."""
+    g = gen(33)
+    q, rows = normal(g, sum(q_len), hq, D), sum(k_len)
+    k = normal(g, hkv, rows, D)
+    first = [sum(k_len[:s]) for s in range(len(k_len))]
+    k_of = lambda s, h: k[h, first[s]:first[s] + k_len[s]]  # noqa: E731
+    lse = log_sums(q, k_of, q_len, k_len, hq, hkv, 0, 0)
+    w, again = torch.empty(hkv, rows, device=DEV), torch.empty(hkv, rows, device=DEV)
+    run(q, lse, view(k), q_len, k_len, hq, hkv, 0, 0, None, weights(w))
+    run(q, lse, view(k), q_len, k_len, hq, hkv, 0, 0, None, weights(again))
+    assert bool((w == again).all())
+    r, G = 0, hq // hkv
+    for s, (L, K) in enumerate(zip(q_len, k_len)):
+        seen = visible(L, K, 0, 0)
+        at = slice(first[s], first[s] + K)
+        for h in range(0, hkv, max(1, hkv // 40)):
+            ref, bound = gathered(q[r:r + L, h * G:(h + 1) * G], lse[r:r + L, h * G:(h + 1) * G], k_of(s, h), seen, SCALE)
+            # (the sums of up to 152 parts of a line, a step each)
+            assert_weights(w[h, at], torch.zeros_like(w[h, at]), ref, bound + ref * 152 * 2.0 ** -24, f"sequence {s} head {h}")
+        r += L
 
 
 def test_key_weights_of_one_row_sum_to_one():

@@ -53,6 +53,22 @@ def test_window(hq, hkv, q_len, k_len, window, sinks):
     assert_lse(e, lse, lse_bound)
 
 
+@pytest.mark.parametrize("hq,hkv,q_len,k_len", [(520, 520, [1, 3, 40], [300, 500, 200]), (2, 1, [1] * 64, [64 * i for i in range(64)]),
+                                                (1, 1, [1, 1, 8], [70000, 1, 129])])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (150, 3)])
+def test_many_and_few_heads(hq, hkv, q_len, k_len, window, sinks):
+    """More kv heads than thread blocks run at once; one, whose keys all of them share out."""
+    g = gen(31)
+    q = normal(g, sum(q_len), hq, D)
+    k, v = cache(g, sum(k_len), hkv), cache(g, sum(k_len), hkv)
+    ref, bound, lse, lse_bound = reference(q, packed(k, v, k_len), q_len, k_len, hq, hkv, window, sinks)
+    got, e = run_window(q, view(k, v), q_len, k_len, hq, hkv, window, sinks)
+    assert_within(got, ref, bound, True, f"{hq}/{hkv} {window} {sinks}")
+    assert_lse(e, lse, lse_bound)
+    again, _ = run_window(q, view(k, v), q_len, k_len, hq, hkv, window, sinks)
+    assert bool((got == again).all())
+
+
 @pytest.mark.parametrize("hq,hkv", HEADS)
 @pytest.mark.parametrize("q_len,k_len", LENGTHS)
 @pytest.mark.parametrize("page,layout", [(16, "head"), (32, "row"), (64, "head"), (128, "row"), (256, "head")])
