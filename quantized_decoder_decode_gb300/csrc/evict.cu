@@ -249,7 +249,8 @@ void launch_evict(const EvictArgs& a, int max_len, int blocks, cudaStream_t s) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
+    // Without a selection nothing may move: `kept` would hold anything.  (The caller reads the error, cudaGetLastError.)
+    if (cudaLaunchKernelEx(&cfg, evict_select_kernel, a) != cudaSuccess) return;
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(EV_MOVE_WARPS * 32);
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
