@@ -366,7 +366,8 @@ fq_status fq_attn_paged(const void* q, uint64_t q_stride, const fq_kv_pages* pag
 
 /* fq_qk_norm_rope into pages: k and v of row i of sequence s go to row kv_row0[s] + i of its pages.  A page that
  * a call writes into belongs to one sequence: rows that are written twice through a shared page end up with
- * elements of either.  Errors: as there, and those of fq_attn_paged's table (KV_CACHE_OVERFLOW: rows beyond the table). */
+ * elements of either.  Errors: as there, those of fq_attn_paged's table (KV_CACHE_OVERFLOW: rows beyond the table), and
+ * INVALID_ARGUMENT for a pool whose pages, rows, heads, K or V share elements. */
 fq_status fq_qk_norm_rope_paged(const float* qkv, uint64_t qkv_stride, uint32_t n_seq, const uint32_t* len,
                                 const uint32_t* pos0, const fq_kv_pages* pages, const int32_t* page_table,
                                 uint64_t table_stride, const uint32_t* kv_row0, uint32_t num_attention_heads,

@@ -83,6 +83,33 @@ fq_status check_pages(const fq_kv_pages* pages, const int32_t* table, uint64_t t
     return FQ_OK;
 }
 
+// Rows of a pool that share elements would be written twice in one call, or one over the other.  Pages, rows, heads and the
+// way from K to V in the order of their strides: where each stride is at least as long as what the ones below it span (any
+// nest of them; every layout that keeps K and V alike), no two rows meet.  Else the pages are looked at for every
+// difference of rows and heads: 0.2 ms for 256 rows of 8 heads, 20 ms at most.
+bool pool_rows_meet(const KvPages& p, int64_t Hkv) {
+    const int64_t R = 1ll << p.shift, N = p.n_pages;
+    const int64_t to_v = (int64_t)(reinterpret_cast<uintptr_t>(p.v) / 2) - (int64_t)(reinterpret_cast<uintptr_t>(p.k) / 2);
+    struct Dim {
+        int64_t stride, n;
+    } d[4] = {{p.row_stride, R}, {p.head_stride, Hkv}, {p.page_stride, N}, {std::llabs(to_v), 2}};
+    std::sort(d, d + 4, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+    int64_t span = HEAD_DIM;
+    bool nest = true;
+    for (const Dim& x : d) {
+        if (x.n == 1) continue;
+        nest = nest && x.stride >= span;
+        span += (x.n - 1) * x.stride;
+    }
+    if (nest) return false;
+    for (int64_t r = 1 - R; r < R; ++r)
+        for (int64_t h = 1 - Hkv; h < Hkv; ++h) {
+            const int64_t c = r * p.row_stride + h * p.head_stride;
+            if (rows_near(c, p.page_stride, N, N, r == 0 && h == 0) || rows_near(to_v + c, p.page_stride, N, N, false)) return true;
+        }
+    return false;
+}
+
 // What the calls over views and over pages share.
 struct Call {
     AttnIo io;
@@ -512,6 +539,7 @@ fq_status fq_qk_norm_rope_paged(const float* qkv, uint64_t qkv_stride, uint32_t 
         qkv, qkv_stride, n_seq, len, pos0, kv_row0, Hq, Hkv, q_norm, k_norm, eps, rope, rope_rows, q_out, q_stride, a, &rows,
         [](uint32_t) { return FQ_OK; }));
     if (rows == 0) return FQ_OK;
+    if (pool_rows_meet(a.pages, Hkv)) return fail(FQ_ERR_INVALID_ARGUMENT, "pages, rows or heads of the pool, or its K and V, share elements");
     uint32_t* waits;
     TRY(prepare_device(&waits, &a.pages.bad));
     launch_qk_paged(a, (cudaStream_t)stream);
