@@ -390,8 +390,8 @@ typedef struct fq_key_weights {
  * way.  Keys that no row sees get before's value.  Products, exponentials and sums are f32 (the sums of many
  * rows are compensated), and the result does not depend on the order in which thread blocks run.
  * workspace: as there, fq_attn_key_weights_workspace.  Errors: as fq_attn_window, and INVALID_ARGUMENT (null lse or
- * weights, a head_stride too short, two sequences of a call that write the same weights; weights of different strides that lie in
- * between one another are taken for such; more than 2^22 units of work, each 256 keys by up to 4096 x 96 query rows of a
+ * weights, a head_stride too short, two sequences of a call that write the same weights, `before` and `after` that
+ * overlap in another way than above; more than 2^22 units of work, each 256 keys by up to 4096 x 96 query rows of a
  * kv head). */
 fq_status fq_attn_key_weights(const void* q, uint64_t q_stride, const float* lse, const fq_kv_view* views, uint32_t n_views,
                               uint32_t n_seq, const uint32_t* q_len, const uint32_t* kv_row0, const uint32_t* k_len,

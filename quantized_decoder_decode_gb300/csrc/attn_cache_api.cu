@@ -343,12 +343,21 @@ fq_status plan_key_weights(KwPlan& p, uint32_t n_seq, const AttnSeq* seq, uint32
 struct WeightRows {
     int64_t lo = 0, stride = 0, n = 0;   // in floats; n of each head
 };
-// Do two sequences' weights share floats?  (Other strides: where their extents meet.)
+// Do two sequences' weights share floats?
 bool weights_meet(const WeightRows& a, const WeightRows& b, int64_t Hkv) {
     if (!a.n || !b.n) return false;
     const int64_t ea = a.lo + (Hkv - 1) * a.stride + a.n, eb = b.lo + (Hkv - 1) * b.stride + b.n;
     if (ea <= b.lo || eb <= a.lo) return false;
-    if (Hkv == 1 || a.stride != b.stride) return true;
+    if (Hkv == 1) return true;
+    if (a.stride != b.stride) {   // heads in the order of their floats (each array's do not overlap)
+        for (int64_t h = 0, g = 0; h < Hkv && g < Hkv;) {
+            const int64_t x = a.lo + h * a.stride, y = b.lo + g * b.stride;
+            if (x + a.n <= y) ++h;
+            else if (y + b.n <= x) ++g;
+            else return true;
+        }
+        return false;
+    }
     const int64_t d = b.lo - a.lo;   // heads h of b and g of a meet where d + (h - g) stride is between -b.n and a.n
     const int64_t below = d >= 0 ? d / a.stride : -((-d + a.stride - 1) / a.stride);
     for (int64_t x = below; x <= below + 1; ++x) {
@@ -387,6 +396,29 @@ fq_status check_weights_apart(const WeightRows* r, uint32_t n_seq, uint32_t Hkv)
     for (uint32_t i = 0; i < n_seq; ++i)
         for (uint32_t j = i + 1; j < n_seq; ++j)
             if (weights_meet(r[i], r[j], Hkv)) return fail(FQ_ERR_INVALID_ARGUMENT, "sequences %u and %u write the same weights", i, j);
+    return FQ_OK;
+}
+
+// What a call adds to is read beside the sums that other thread blocks write: `before` and `after` of a sequence are the same
+// weights, or lie apart; those of two sequences lie apart.
+fq_status check_weights_read(const WeightRows* read, const WeightRows* written, uint32_t n_seq, uint32_t Hkv) {
+    bool place = true;
+    int64_t lo[2] = {INT64_MAX, INT64_MAX}, hi[2] = {INT64_MIN, INT64_MIN};
+    auto same = [&](uint32_t i) { return read[i].lo == written[i].lo && read[i].stride == written[i].stride; };
+    for (uint32_t i = 0; i < n_seq; ++i) {
+        if (!read[i].n) continue;
+        place = place && same(i);
+        for (int k = 0; k < 2; ++k) {
+            const WeightRows& r = k ? written[i] : read[i];
+            lo[k] = std::min(lo[k], r.lo);
+            hi[k] = std::max(hi[k], r.lo + (Hkv - 1) * r.stride + r.n);
+        }
+    }
+    if (place || hi[0] <= lo[1] || hi[1] <= lo[0]) return FQ_OK;   // (in place: written weights lie apart)
+    for (uint32_t i = 0; i < n_seq; ++i)
+        for (uint32_t j = 0; j < n_seq; ++j)
+            if (!(i == j && same(i)) && weights_meet(read[i], written[j], Hkv))
+                return fail(FQ_ERR_INVALID_ARGUMENT, "sequence %u writes weights that sequence %u adds to", j, i);
     return FQ_OK;
 }
 
@@ -586,21 +618,22 @@ fq_status fq_attn_key_weights(const void* q, uint64_t q_stride, const float* lse
     uint64_t q_rows = 0;
     TRY(prompt_sequences(n_seq, q_len, kv_row0, k_len, keys, n_views, Hkv, seq, use, &q_rows));
     KeyWeights w[MAX_SEQ];
-    WeightRows written[MAX_SEQ], read;
+    WeightRows written[MAX_SEQ], read[MAX_SEQ];
     for (uint32_t s = 0; s < n_seq; ++s) {
         const uint32_t v = n_views == 1 ? 0 : s;
         TRY(check_weights(after[v], Hkv, (uint64_t)seq[s].k_row0, k_len[s], "after", s, written[s]));
         w[v].after = after[v].w;
         w[v].after_stride = written[s].stride;
         if (!before || !k_len[s]) continue;
-        TRY(check_weights(before[v], Hkv, (uint64_t)seq[s].k_row0, k_len[s], "before", s, read));
+        TRY(check_weights(before[v], Hkv, (uint64_t)seq[s].k_row0, k_len[s], "before", s, read[s]));
         w[v].before = before[v].w;
-        w[v].before_stride = read.stride;
+        w[v].before_stride = read[s].stride;
     }
     // (strides come from sequences with keys)
     for (uint32_t s = 0; s < n_seq; ++s)
         if (written[s].n) w[n_views == 1 ? 0 : s].after_stride = written[s].stride;
     TRY(check_weights_apart(written, n_seq, Hkv));
+    if (before) TRY(check_weights_read(read, written, n_seq, Hkv));
     AttnMask mask = mask_of(window, sinks);
     try {
         KwPlan p;
