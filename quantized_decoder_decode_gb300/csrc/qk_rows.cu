@@ -26,6 +26,9 @@ namespace {
 constexpr int QR_HEADS = 4;      // heads per warp
 constexpr int QR_THREADS = 64;
 
+FQ_DEV const KvRows& cache_of(const QkRowsArgs& a, int s) { return a.kv[s]; }
+FQ_DEV const KvPages& cache_of(const QkPagedArgs& a, int) { return a.pages; }
+
 template <class Args>
 __global__ void __launch_bounds__(QR_THREADS) qk_rows_kernel(const __grid_constant__ Args a, int groups) {
     const int lane = threadIdx.x & 31;
@@ -54,29 +57,22 @@ __global__ void __launch_bounds__(QR_THREADS) qk_rows_kernel(const __grid_consta
     }
     const int i = row - a.row0[lo];
     const float4 cs = __ldg(reinterpret_cast<const float4*>(a.rope + (int64_t)(a.pos0[lo] + i) * (HEAD_DIM / 2) + 2 * lane));
-    // the row of the view, or of a page (where the table names one)
-    uint16_t *k_row, *v_row;
-    int64_t head_stride;
-    bool have = true;
+    // The row in the cache: of a view, or of a page (where the table names one).  (Views' arguments are read where rows are stored: read up
+    // here, 2048 rows of 16 + 2 x 8 heads take 8.4 us instead of 8.1, 8191 of 32 + 2 x 8 47.9 instead of 47.0.)
+    const auto& kv = cache_of(a, lo);
+    int64_t at = 0;
+    [[maybe_unused]] bool have = true;
     if constexpr (Args::PAGED) {
         const KvPages& p = a.pages;
         const int r = a.kv_row0[lo] + i;
-        int64_t at = 0;
         if (h0 + QR_HEADS > a.Hq) {   // (warps of q heads alone need none)
             const int32_t id = __ldg(p.table + (int64_t)lo * p.table_stride + (r >> p.shift));
             have = (uint32_t)id < (uint32_t)p.n_pages;
             if (have) at = id * p.page_stride + (r & ((1 << p.shift) - 1)) * p.row_stride;
             else if (lane == 0) atomicAdd(p.bad, 1u);
         }
-        k_row = p.k + at;
-        v_row = p.v + at;
-        head_stride = p.head_stride;
     } else {
-        const KvRows& kv = a.kv[lo];
-        const int64_t at = (int64_t)(a.kv_row0[lo] + i) * kv.row_stride;
-        k_row = kv.k + at;
-        v_row = kv.v + at;
-        head_stride = kv.head_stride;
+        at = (int64_t)(a.kv_row0[lo] + i) * kv.row_stride;
     }
     // The four sums of squares at once: each exchange halves what a lane still adds up; lanes
     // 8 j .. 8 j + 7 end up with head j's.
@@ -111,9 +107,9 @@ __global__ void __launch_bounds__(QR_THREADS) qk_rows_kernel(const __grid_consta
             y0 = make_float2(z0.x * cs.x - z1.x * cs.y, z0.y * cs.z - z1.y * cs.w);
             y1 = make_float2(z0.x * cs.y + z1.x * cs.x, z0.y * cs.w + z1.y * cs.z);
             dst = is_q ? a.q_out + (int64_t)row * a.q_stride + h * HEAD_DIM
-                       : k_row + (int64_t)(h - a.Hq) * head_stride;
+                       : kv.k + at + (int64_t)(h - a.Hq) * kv.head_stride;
         } else {
-            dst = v_row + (int64_t)(h - a.Hq - a.Hkv) * head_stride;
+            dst = kv.v + at + (int64_t)(h - a.Hq - a.Hkv) * kv.head_stride;
         }
         if (Args::PAGED && !have && h >= a.Hq) continue;
         reinterpret_cast<uint32_t*>(dst)[lane] = bf16x2(y0.x, y0.y);
