@@ -465,17 +465,19 @@ FQ_DEV void load_values(const Args& a, AtShared* sh, uint8_t* ring, int units, i
         if (!more || !(ok = at_wait_warp(&sh->v_empty[s], parity, sh))) break;
         int j = u.j0 + t;
         bool whole = j < u.jm;
-        if constexpr (Args::WINDOW) {
+        if constexpr (!Args::WINDOW) {
+            if (elect_one() && !(a.waits.starve == 2 && it == 0 && t == 1))
+                load_kv(a.map_v[vw], ring + (AT_KS + s) * AT_TILE_BYTES, row0 + t * TILE_ROWS, u.head, whole ? &sh->v_full[s] : &sh->v_raw[s]);
+        } else {
             j = u.kt.at(j);
             whole = whole_tile(a, u, j);
-        }
-        uint64_t* full = whole ? &sh->v_full[s] : &sh->v_raw[s];
-        if constexpr (Args::PAGED) {
-            pages.load(a, u, a.map_v[0], ring + (AT_KS + s) * AT_TILE_BYTES, t, full, !(a.waits.starve == 2 && it == 0 && t == 1), lane);
-        } else {
-            if (elect_one() && !(a.waits.starve == 2 && it == 0 && t == 1))
-                load_kv(a.map_v[vw], ring + (AT_KS + s) * AT_TILE_BYTES, Args::WINDOW ? row0 + (j - u.j0) * TILE_ROWS : row0 + t * TILE_ROWS,
-                        u.head, full);
+            uint64_t* full = whole ? &sh->v_full[s] : &sh->v_raw[s];
+            if constexpr (Args::PAGED) {
+                pages.load(a, u, a.map_v[0], ring + (AT_KS + s) * AT_TILE_BYTES, t, full, !(a.waits.starve == 2 && it == 0 && t == 1), lane);
+            } else {
+                if (elect_one() && !(a.waits.starve == 2 && it == 0 && t == 1))
+                    load_kv(a.map_v[vw], ring + (AT_KS + s) * AT_TILE_BYTES, row0 + (j - u.j0) * TILE_ROWS, u.head, full);
+            }
         }
         __syncwarp();
         if (!whole) {
@@ -918,14 +920,15 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tiles_kernel(const __grid_
             if (!Args::PAGED)
                 load_kv(a.map_k[vw], ring, sq.k_row0 + (Args::WINDOW ? u.kt.at(u.j0) : u.j0) * TILE_ROWS, u.head, &sh->k_full[0]);
         }
-        __syncwarp();
-        if constexpr (Args::PAGED)
+        if constexpr (Args::PAGED) {
+            __syncwarp();
             if (pre) {
                 PageIds<Args> pages;
                 pages.base = 0;
                 pages.ids = PageIds<Args>::fetch(a, u, lane);
                 pages.load(a, u, a.map_k[0], ring, 0, &sh->k_full[0], true, lane);
             }
+        }
         preloaded = pre;
         __syncwarp();
     } else if (warp == 8) {
