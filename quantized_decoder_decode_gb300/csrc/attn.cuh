@@ -46,6 +46,14 @@ FQ_DEV float ex2(float x) {
 // log(sum e^x) of a row from its reference maximum m (base 2) and the sum l of weights held 2^-lift lower
 FQ_DEV float log_sum(float m, float l, float lift) { return (m + (log2f(l) + lift)) * 0.6931471805599453f; }
 
+// Two bf16 values: is one of them not finite; the same with such ones as 0.
+FQ_DEV bool odd_pair(uint32_t w) { return (w & 0x7F800000u) == 0x7F800000u || (w & 0x7F80u) == 0x7F80u; }
+FQ_DEV uint32_t finite_pair(uint32_t w) {
+    if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
+    if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+    return w;
+}
+
 // mbar_try_wait without suspending.
 FQ_DEV bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
     uint32_t ok;

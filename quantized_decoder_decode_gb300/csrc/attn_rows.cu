@@ -51,12 +51,6 @@ FQ_DEV uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-FQ_DEV bool odd_pair(uint32_t w) { return (w & 0x7F800000u) == 0x7F800000u || (w & 0x7F80u) == 0x7F80u; }
-FQ_DEV uint32_t finite_pair(uint32_t w) {
-    if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
-    if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
-    return w;
-}
 FQ_DEV float max_over_rows(float v) {   // over the lanes with the same lane % 4
     v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
     v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));

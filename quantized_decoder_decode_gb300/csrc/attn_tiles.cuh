@@ -367,13 +367,17 @@ FQ_DEV void load_keys(const Args& a, AtShared* sh, uint8_t* q_sm, uint8_t* ring,
 // ---------------- warp 10: V tiles, and the check of those that some row sees in part
 struct PartTile {
     uint32_t it;                   // its unit
-    int s, tile, k_len, first, jm;   // stage, key tile; keys; keys that every row sees; the unit's first such tile
+    // stage, key tile; keys; keys that every row sees; the unit's first such tile (windows: some row sees the keys from `jm` on
+    // and the sinks, below k_len)
+    int s, tile, k_len, first, jm;
 };
 
 // Waits for a V tile and takes values that are not finite out of it.  With windows the rows that see a key are no longer
-// those below a first one: only the fact is noted, and the outputs look the values up again.
+// those below a first one: only the fact is noted, and the outputs look the values up again.  That takes long (333 rows behind
+// 1000, 16 / 8 heads, 0.8 ms instead of 0.02), so values that no row of the unit sees are no reason for it: the rest of a sequence's last
+// page may hold anything (then 30 us).
 template <bool WINDOW>
-FQ_DEV bool check_values(AtShared* sh, uint8_t* ring, const PartTile& p, uint32_t& raw_ph, int lane) {
+FQ_DEV bool check_values(AtShared* sh, uint8_t* ring, const PartTile& p, int sinks, uint32_t& raw_ph, int lane) {
     if (!at_wait_warp(&sh->v_raw[p.s], (raw_ph >> p.s) & 1, sh)) return false;
     raw_ph ^= 1u << p.s;
     uint8_t* tile = ring + (AT_KS + p.s) * AT_TILE_BYTES;
@@ -395,31 +399,47 @@ FQ_DEV bool check_values(AtShared* sh, uint8_t* ring, const PartTile& p, uint32_
 #pragma unroll
     for (int h = 0; h < 4; ++h) odd |= (z[h] & 0x7FFF7FFFu) != 0;
     if (__any_sync(0xFFFFFFFFu, odd)) {
-        if (*(volatile uint32_t*)&sh->poison_unit != p.it + 1) {
+        if (!WINDOW && *(volatile uint32_t*)&sh->poison_unit != p.it + 1) {
             if (!units_done(p.it, lane, sh)) return false;   // the notes before are read
-            if (!WINDOW)
-                for (int i = lane; i < 3 * HEAD_DIM; i += 32) sh->poison[0][i] = 0xFFFFu;
+            for (int i = lane; i < 3 * HEAD_DIM; i += 32) sh->poison[0][i] = 0xFFFFu;
             __syncwarp();
         }
+        [[maybe_unused]] bool note = false;
         // lane l owns columns 4l .. 4l+3: 8 bytes of every row
         uint8_t* col = tile + (lane >> 4) * AT_PANEL;
+        if constexpr (WINDOW) {
 #pragma unroll 1
-        for (int r = from; r < TILE_ROWS; ++r) {
-            uint16_t* v = reinterpret_cast<uint16_t*>(col + sw128_offset(r, (lane & 15) >> 1) + (lane & 1) * 8);
-            const int key = p.tile * TILE_ROWS + r;
+            for (int r = 0; r < TILE_ROWS; ++r) {
+                uint2* v = reinterpret_cast<uint2*>(col + sw128_offset(r, (lane & 15) >> 1) + (lane & 1) * 8);
+                const uint2 x = *v, y = make_uint2(finite_pair(x.x), finite_pair(x.y));
+                if (x.x == y.x && x.y == y.y) continue;
+                *v = y;
+                const int key = p.tile * TILE_ROWS + r;
+                note |= key < p.k_len && (key >= p.jm || key < sinks);
+            }
+            __syncwarp();
+            note = __any_sync(0xFFFFFFFFu, note);
+            // (the notes before are read)
+            if (note && *(volatile uint32_t*)&sh->poison_unit != p.it + 1 && !units_done(p.it, lane, sh)) return false;
+        } else {
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                const uint32_t b = v[c];
-                if ((b & 0x7F80u) != 0x7F80u) continue;
-                v[c] = 0;
-                if (WINDOW || key >= p.k_len) continue;   // seen by no row
-                uint16_t& f = sh->poison[(b & 0x7Fu) ? 2 : (b & 0x8000u) ? 1 : 0][4 * lane + c];
-                const uint16_t k16 = (uint16_t)(key - p.jm * TILE_ROWS);
-                if (k16 < f) f = k16;
+            for (int r = from; r < TILE_ROWS; ++r) {
+                uint16_t* v = reinterpret_cast<uint16_t*>(col + sw128_offset(r, (lane & 15) >> 1) + (lane & 1) * 8);
+                const int key = p.tile * TILE_ROWS + r;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t b = v[c];
+                    if ((b & 0x7F80u) != 0x7F80u) continue;
+                    v[c] = 0;
+                    if (key >= p.k_len) continue;   // seen by no row
+                    uint16_t& f = sh->poison[(b & 0x7Fu) ? 2 : (b & 0x8000u) ? 1 : 0][4 * lane + c];
+                    const uint16_t k16 = (uint16_t)(key - p.jm * TILE_ROWS);
+                    if (k16 < f) f = k16;
+                }
             }
         }
         __syncwarp();
-        if (lane == 0) *(volatile uint32_t*)&sh->poison_unit = p.it + 1;
+        if (lane == 0 && (!WINDOW || note)) *(volatile uint32_t*)&sh->poison_unit = p.it + 1;
         __threadfence_block();
         fence_async_smem();
     }
@@ -457,7 +477,8 @@ FQ_DEV void load_values(const Args& a, AtShared* sh, uint8_t* ring, int units, i
         const uint32_t parity = ((n / AT_VS) & 1) ^ 1;
         // checks wait behind a load that can be issued, not behind one that cannot
         if (pending && !(more && __all_sync(0xFFFFFFFFu, mbar_test_wait(&sh->v_empty[s], parity)))) {
-            ok = check_values<Args::WINDOW>(sh, ring, part[0], raw_ph, lane);
+            if constexpr (Args::WINDOW) ok = check_values<true>(sh, ring, part[0], a.mask.sinks, raw_ph, lane);
+            else ok = check_values<false>(sh, ring, part[0], 0, raw_ph, lane);
             part[0] = part[1];
             --pending;
             continue;
@@ -481,7 +502,7 @@ FQ_DEV void load_values(const Args& a, AtShared* sh, uint8_t* ring, int units, i
         }
         __syncwarp();
         if (!whole) {
-            const PartTile p{(uint32_t)it, s, j, k_len, Args::WINDOW ? 0 : seen, u.jm};
+            const PartTile p = Args::WINDOW ? PartTile{(uint32_t)it, s, j, u.end, 0, u.lo0} : PartTile{(uint32_t)it, s, j, k_len, seen, u.jm};
             if (pending) part[1] = p;
             else part[0] = p;
             ++pending;
