@@ -356,8 +356,8 @@ typedef struct fq_kv_pages {
 } fq_kv_pages;
 
 /* fq_attn_window over pages: sequence s has the k_len[s] rows 0 .. of its pages.  Workspace:
- * fq_attn_window_workspace.  Errors: also INVALID_ARGUMENT (null table, a table_stride that does not hold the rows of a
- * sequence, page_rows, strides). */
+ * fq_attn_window_workspace.  Errors: also INVALID_ARGUMENT (null table, page_rows, strides) and KV_CACHE_OVERFLOW (a
+ * table_stride that does not hold the rows of a sequence, rows in a pool without pages). */
 fq_status fq_attn_paged(const void* q, uint64_t q_stride, const fq_kv_pages* pages, const int32_t* page_table,
                         uint64_t table_stride, uint32_t n_seq, const uint32_t* q_len, const uint32_t* k_len,
                         uint32_t num_attention_heads, uint32_t num_key_value_heads, uint32_t window, uint32_t sinks,
@@ -366,8 +366,8 @@ fq_status fq_attn_paged(const void* q, uint64_t q_stride, const fq_kv_pages* pag
 
 /* fq_qk_norm_rope into pages: k and v of row i of sequence s go to row kv_row0[s] + i of its pages.  A page that
  * a call writes into belongs to one sequence: rows that are written twice through a shared page end up with
- * elements of either.  Errors: as there, those of fq_attn_paged's table (KV_CACHE_OVERFLOW: rows beyond the table), and
- * INVALID_ARGUMENT for a pool whose pages, rows, heads, K or V share elements. */
+ * elements of either.  Errors: as there, those of fq_attn_paged's table and pool, and INVALID_ARGUMENT
+ * for a pool whose pages, rows, heads, K or V share elements. */
 fq_status fq_qk_norm_rope_paged(const float* qkv, uint64_t qkv_stride, uint32_t n_seq, const uint32_t* len,
                                 const uint32_t* pos0, const fq_kv_pages* pages, const int32_t* page_table,
                                 uint64_t table_stride, const uint32_t* kv_row0, uint32_t num_attention_heads,
