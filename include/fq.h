@@ -387,8 +387,9 @@ typedef struct fq_key_weights {
  * for the k_len[s] keys of every sequence (rows, views, window, sinks and who sees what as in fq_attn_window; V is not looked
  * at).  lse: device f32 [rows][Hq], as fq_attn_window gives it for the same rows.  before, after: host arrays of n_views
  * entries, of the views' rows; before NULL: zeros; before and after may be the same weights, and overlap in no other
- * way.  Keys that no row sees get before's value.  Products, exponentials and sums are f32 (the sums of many
- * rows are compensated), and the result does not depend on the order in which thread blocks run.
+ * way.  Keys that no row sees get before's value.  Products, exponentials and sums are f32.  What a thread adds up of many rows is
+ * compensated; the sums of up to 152 thread blocks that share a key's rows are added plainly, always in the same order, so
+ * that the result does not depend on the order in which they run.
  * workspace: as there, fq_attn_key_weights_workspace.  Errors: as fq_attn_window, and INVALID_ARGUMENT (null lse or
  * weights, a head_stride too short, two sequences of a call that write the same weights, `before` and `after` that
  * overlap in another way than above; more than 2^22 units of work, each 256 keys by up to 4096 x 96 query rows of a
