@@ -367,17 +367,16 @@ FQ_DEV void load_keys(const Args& a, AtShared* sh, uint8_t* q_sm, uint8_t* ring,
 // ---------------- warp 10: V tiles, and the check of those that some row sees in part
 struct PartTile {
     uint32_t it;                   // its unit
-    // stage, key tile; keys; keys that every row sees; the unit's first such tile (windows: some row sees the keys from `jm` on
-    // and the sinks, below k_len)
-    int s, tile, k_len, first, jm;
+    int s, tile, k_len, first, jm;   // stage, key tile; keys; keys that every row sees; the unit's first such tile
 };
 
 // Waits for a V tile and takes values that are not finite out of it.  With windows the rows that see a key are no longer
 // those below a first one: only the fact is noted, and the outputs look the values up again.  That takes long (333 rows behind
 // 1000, 16 / 8 heads, 0.8 ms instead of 0.02), so values that no row of the unit sees are no reason for it: the rest of a sequence's last
 // page may hold anything (then 30 us).
-template <bool WINDOW>
-FQ_DEV bool check_values(AtShared* sh, uint8_t* ring, const PartTile& p, int sinks, uint32_t& raw_ph, int lane) {
+template <class Args>
+FQ_DEV bool check_values(const Args& a, AtShared* sh, uint8_t* ring, const PartTile& p, uint32_t& raw_ph, int lane) {
+    constexpr bool WINDOW = Args::WINDOW;
     if (!at_wait_warp(&sh->v_raw[p.s], (raw_ph >> p.s) & 1, sh)) return false;
     raw_ph ^= 1u << p.s;
     uint8_t* tile = ring + (AT_KS + p.s) * AT_TILE_BYTES;
@@ -408,6 +407,8 @@ FQ_DEV bool check_values(AtShared* sh, uint8_t* ring, const PartTile& p, int sin
         // lane l owns columns 4l .. 4l+3: 8 bytes of every row
         uint8_t* col = tile + (lane >> 4) * AT_PANEL;
         if constexpr (WINDOW) {
+            // (made anew: carried to here, its numbers cost calls without such values 1.5 of 12.8 us, 17 rows in a window of 256 over pages)
+            const Unit u = unit_of(a, unit_at(p.it));
 #pragma unroll 1
             for (int r = 0; r < TILE_ROWS; ++r) {
                 uint2* v = reinterpret_cast<uint2*>(col + sw128_offset(r, (lane & 15) >> 1) + (lane & 1) * 8);
@@ -415,7 +416,7 @@ FQ_DEV bool check_values(AtShared* sh, uint8_t* ring, const PartTile& p, int sin
                 if (x.x == y.x && x.y == y.y) continue;
                 *v = y;
                 const int key = p.tile * TILE_ROWS + r;
-                note |= key < p.k_len && (key >= p.jm || key < sinks);
+                note |= key < u.end && (key >= u.lo0 || key < a.mask.sinks);
             }
             __syncwarp();
             note = __any_sync(0xFFFFFFFFu, note);
@@ -477,8 +478,7 @@ FQ_DEV void load_values(const Args& a, AtShared* sh, uint8_t* ring, int units, i
         const uint32_t parity = ((n / AT_VS) & 1) ^ 1;
         // checks wait behind a load that can be issued, not behind one that cannot
         if (pending && !(more && __all_sync(0xFFFFFFFFu, mbar_test_wait(&sh->v_empty[s], parity)))) {
-            if constexpr (Args::WINDOW) ok = check_values<true>(sh, ring, part[0], a.mask.sinks, raw_ph, lane);
-            else ok = check_values<false>(sh, ring, part[0], 0, raw_ph, lane);
+            ok = check_values(a, sh, ring, part[0], raw_ph, lane);
             part[0] = part[1];
             --pending;
             continue;
@@ -502,7 +502,7 @@ FQ_DEV void load_values(const Args& a, AtShared* sh, uint8_t* ring, int units, i
         }
         __syncwarp();
         if (!whole) {
-            const PartTile p = Args::WINDOW ? PartTile{(uint32_t)it, s, j, u.end, 0, u.lo0} : PartTile{(uint32_t)it, s, j, k_len, seen, u.jm};
+            const PartTile p{(uint32_t)it, s, j, k_len, Args::WINDOW ? 0 : seen, u.jm};
             if (pending) part[1] = p;
             else part[0] = p;
             ++pending;
