@@ -321,7 +321,12 @@ fq_status fq_attn_shared_workspace(uint32_t n_seq, uint32_t prefix_len, const ui
  * of the last keys and at the first few (which trained models lean on whatever they hold), a cache whose rows lie in
  * pages, and a cache of which only the keys that queries have looked at stay.  The conventions of the operators
  * above hold: head_dim 128, bf16 rows, groups of 1, 2, 4 or 8, up to 64 sequences a call, nothing allocated but (once per device and process) by
- * the first call's preparation of the kernels, calls may be captured, and outputs do not overlap inputs. */
+ * the first call's preparation of the kernels, calls may be captured, and outputs do not overlap inputs.  Lengths and row
+ * numbers are the host's, so a captured call is one of the same lengths.
+ *
+ * They work on rows that the caller holds.  No step of a model looks through a window or at pages, hands out the q rows and log-sums
+ * that fq_attn_key_weights wants, or goes on behind a cache made shorter: a step's position is the number of the cache's
+ * rows (pos0 == len). */
 
 /* fq_attn_prompt in which query row i of a sequence, whose own key is e - 1, e = i + 1 + k_len - q_len, sees the
  * keys j < e with j >= e - window or j < sinks: its last `window` keys (its own among them) and the first
@@ -419,7 +424,7 @@ fq_status fq_kv_evict(const fq_kv_view* from, uint32_t n_from, const fq_key_weig
                       uint32_t num_key_value_heads, const fq_kv_view* to, uint32_t n_to, const fq_key_weights* to_weights,
                       const uint32_t* to_row0, int32_t* kept, void* stream);
 
-/* Synchronise `stream` and report bounded device waits of the two attentions that gave up on the
+/* Synchronise `stream` and report bounded device waits of the attentions and of fq_attn_key_weights that gave up on the
  * current device since this host thread's last check (a thread's first: since the last check of
  * any).  DEVICE_TIMEOUT: the outputs of the calls since then, of whichever thread and stream, may be
  * invalid.  No check hides a failure from another thread.  The attention inside
