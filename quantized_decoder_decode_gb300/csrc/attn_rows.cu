@@ -21,7 +21,7 @@
 // arguments, the first reads) is 2.5 us, the join in it 0.7 us.  CTAs of two warps, six per SM, balance better but
 // leave twice the partial results: 32.8 us for the call instead of 31.0.
 // With windows and pages (Args::WINDOW) a CTA takes an equal part of all keys instead of a chunk of one group.  16 tokens over a
-// window of 2048 (121 MB) 25.5 us, 32 tokens over pages of 16 rows (281 MB) 49.7, of which the join 4; in chunks 27.1 and 57.4.
+// window of 2048 (121 MB) 25.5 us, 32 tokens over pages of 16 rows (281 MB) 51.0, of which the join 4; in chunks 27.1 and 57.4.
 // Taken out again there, at chunks: K and V through shared memory by copies of 16 bytes (31 and 66 us), of a row (33 and 71) or of
 // 4 KB (28.5 and 59); 128-key tiles by TMA for tcgen05 products with the keys as rows (30 and 62 to 72: all SMs' first tiles
 // take 2.5 us to land, and a tile of small pages is 16 copies); a fourth CTA per SM, in 128 registers (27.9 and 56.2).

@@ -53,7 +53,7 @@
 // The same kernel serves windows with sinks, over views and over pages (Args::WINDOW, Args::PAGED): a unit
 // then counts through the key tiles that its rows look at (KeyTiles), and a tile is masked on both sides, where a row's
 // window begins or the sinks end in it; a tile is copied page by page.  One prompt of 8192 tokens with a window of 4096, 32 / 8
-// heads: 255 us (products alone 217); 2048 tokens behind 6144 in pages of 64 rows: 161 us (126): 256 units on 152 SMs.
+// heads: 260 us (products alone 217); 2048 tokens behind 6144 in pages of 64 rows: 161 us (126): 256 units on 152 SMs.
 #pragma once
 
 #include "attn.cuh"
@@ -250,8 +250,8 @@ template <int N>
 FQ_DEV void set_regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // The page table's entries of a unit's tiles, 32 at a time (one per lane) and the next 32 on their way: a tile waits for its
-// entries only at a unit's start.  Small pages cost copies, two for each page of a tile: 333 tokens behind 1000, 16 / 8 heads, 16.8
-// us from a view, 18.2 from pages of 128 rows, 19.6 of 32, 22.7 of 16 (a lane for each copy: no faster).  Pages that no row sees into (their entries are not read: a program may have given them away), and entries
+// entries only at a unit's start.  Small pages cost copies, two for each page of a tile: 333 tokens behind 1000, 16 / 8 heads, 17.1
+// us from a view, 18.1 from pages of 128 rows, 19.0 of 32, 22.2 of 16 (a lane for each copy: no faster).  Pages that no row sees into (their entries are not read: a program may have given them away), and entries
 // that name no page, get the page behind the last, which reads as zeros.
 template <class Args>
 struct PageIds {

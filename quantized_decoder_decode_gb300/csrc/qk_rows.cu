@@ -13,7 +13,7 @@
 // 36).  8191 rows of 32 + 2 x 8 heads: 50.4 us, 6.0 TB/s; 54 with separate reductions, 52.7 with CTAs
 // of 256 threads, 66 as a loop over rows with the next row's reads ahead.
 //
-// Into pages (Args::PAGED) a warp looks its row's page up while its reads are on their way: 4097 rows of 32 + 2 x 8 heads 21.2 us
+// Into pages (Args::PAGED) a warp looks its row's page up while its reads are on their way: 4097 rows of 32 + 2 x 8 heads 21.6 us
 // (floor 22.5 at the rate of a plain copy).
 
 #include "attn.cuh"
